@@ -181,9 +181,8 @@ def _own(s):
     from mixture_experts_layer_tokens_gb300 import moe
     op = s["op"]
     if op == "linear":
-        ws = _workspace(s, lambda: moe.linear_workspace_size(s["m"], s["n"], s["k"]))
         out = moe.moe_linear(s["x"], s["w"], bias=s["bias_t"], residual=s["res_t"], activation=s["act"],
-                             out=s["out_t"], preact=s["pre_t"], ws=ws)
+                             out=s["out_t"], preact=s["pre_t"])
         return [out, s["pre_t"]]
     if op == "linear_backward":
         ws = _workspace(s, lambda: moe.linear_backward_workspace_size(s["m"], s["n"], s["k"]))
