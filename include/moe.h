@@ -60,7 +60,8 @@ typedef enum {
   MOE_DT_BF16 = 0,
   MOE_DT_FP8_E4M3 = 1, /* OCP E4M3 ("e4m3fn"), saturating                    */
   MOE_DT_NVFP4 = 2,    /* E2M1 pairs + one E4M3 scale per 16 elements        */
-  MOE_DT_FP32 = 3
+  MOE_DT_FP32 = 3,
+  MOE_DT_FP16 = 4 /* moe_linear, moe_linear_backward and the logits of moe_route_grouped only */
 } moe_dtype_t;
 
 typedef enum {
@@ -437,6 +438,131 @@ moe_status_t moe_finalize(void *output, const void *fused_expert_output, const f
                           int apply_router_weight_on_input, moe_dtype_t out_dtype,
                           uint8_t *out_scale, float out_global_scale, void *residual_out,
                           moe_stream_t stream);
+
+/* ------------------------------------------------------------------ linear projection
+ * A dense projection with its epilogue in the same launch -- the router's gate (bf16 hidden
+ * states to fp32 logits) and the dense layers beside the experts:
+ *   z   = x . w^T + bias                     fp32 accumulation
+ *   out = act(z) + residual                  rounded once, to out_dtype
+ *   preact = z in dtype                      (optional: what moe_linear_backward takes)
+ * x [M, K], w [N, K] (K-contiguous) and bias [N] (NULL = none) in dtype (MOE_DT_BF16 or
+ * MOE_DT_FP16); out [M, N] and residual [M, N] (NULL = none) in out_dtype (dtype itself or
+ * MOE_DT_FP32); preact [M, N] in dtype, NULL = not written.  residual may be out itself (the
+ * projection is then added in place); any other overlap of an output with another buffer is
+ * not allowed.  activation: a moe_linear_activation_t.  M >= 0 (0: nothing is done), N >= 1,
+ * K >= 8 and K % 8 == 0; any N (a multiple of 8 is stored by 16-byte vectors).  Every pointer
+ * 16-byte aligned.  A row of x that holds a NaN or an infinity affects that row of out alone.
+ * The sums of a call have a fixed order: the same inputs give the same bits. */
+typedef enum {
+  MOE_LINEAR_NONE = 0,      /* act(z) = z                                            */
+  MOE_LINEAR_SILU = 1,      /* z / (1 + exp(-z))                                     */
+  MOE_LINEAR_GELU = 2,      /* z/2 (1 + erf(z / sqrt 2))                             */
+  MOE_LINEAR_GELU_TANH = 3  /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))         */
+} moe_linear_activation_t;
+
+moe_status_t moe_linear(const void *x, const void *w, const void *bias, const void *residual, int M,
+                        int N, int K, moe_dtype_t dtype, int activation, moe_dtype_t out_dtype,
+                        void *out, void *preact, moe_stream_t stream);
+
+/* Gradients of moe_linear, given dout [M, N], the gradient of out, in dout_dtype (dtype or
+ * MOE_DT_FP32):
+ *   dz    = dout * act'(preact)
+ *   dx    = dz . w          [M, K] in dtype
+ *   dw    = dz^T . x        [N, K] in dtype
+ *   dbias = sum over m of dz  [N] in dtype (summed in fp32 from dz before any rounding)
+ * Each of dx, dw and dbias may be NULL (not computed), not all three.  The gradient of the
+ * residual is dout itself.  preact [M, N] in dtype is what moe_linear wrote (required unless
+ * the activation is MOE_LINEAR_NONE, where it is not read).  The tensor cores take dz in
+ * dtype: where it has to be computed, or dout is fp32, it is rounded to dtype once (with
+ * fp16, the caller's loss scale keeps it in range).  M == 0 sets dw and dbias to zero.
+ * ws: moe_linear_backward_workspace_size(M, N, K) bytes.  Sizes, alignment and the order of
+ * sums as for moe_linear; outputs overlap nothing. */
+moe_status_t moe_linear_backward(const void *dout, moe_dtype_t dout_dtype, const void *x, const void *w,
+                                 const void *preact, int M, int N, int K, moe_dtype_t dtype,
+                                 int activation, void *dx, void *dw, void *dbias, void *ws,
+                                 size_t ws_bytes, moe_stream_t stream);
+size_t moe_linear_backward_workspace_size(int M, int N, int K);
+
+/* ------------------------------------------------------------------ grouped route
+ * Router with scores over all experts, a bias that balances their load, and expert groups:
+ *   s_e = sigmoid(l_e)  or  softmax(l)_e over the E experts       (cfg->score)
+ *   c_e = s_e + bias_e                       (bias [E] fp32, NULL = none: it steers the choice
+ *                                             and does not enter the weights)
+ *   the E experts form n_group groups of E / n_group consecutive ones; a group's score is the
+ *   sum of its group_top largest c (1: its best expert, 2: its two best), and the topk_group
+ *   groups of largest score are kept, equal scores to the lower group index
+ *   topk_ids: the top_k experts of largest c in the kept groups, larger first, equal c to the
+ *   larger logit and then to the lower index
+ *   topk_weights_j = s_j * scale, with renormalize s_j / (sum of the chosen s) * scale (0 when
+ *   that sum is 0)
+ * The choice is the one of exact arithmetic on the given values: scores too close to be
+ * ordered in fp32 are compared in fp64.  (MoE routers of the DeepSeek-V3 kind: sigmoid, bias,
+ * 4 of 8 groups by their two best, top 8, scale 2.5; plain softmax top-k: n_group 1.)
+ * A logit or bias of -inf or NaN masks the expert: s = 0, no share in its group's score (a
+ * group of masked experts alone ranks last), chosen only when the kept groups have fewer than
+ * top_k others, lower index first, with weight 0.  +inf counts as the largest finite number.
+ * logits [T, E] in logits_dtype (MOE_DT_FP32, MOE_DT_BF16 or MOE_DT_FP16); topk_ids [T, top_k]
+ * int32; topk_weights [T, top_k] fp32.  1 <= E <= 1024, 1 <= top_k <= 32, n_group <= 32
+ * divides E, 1 <= topk_group <= n_group, group_top 1 or 2 (at most the group's size), top_k <=
+ * topk_group * E / n_group, scale finite. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+
+typedef struct {
+  int score;       /* a moe_score_t */
+  int n_group;     /* 1: no groups  */
+  int topk_group;
+  int group_top;
+  int renormalize;
+  float scale;
+} moe_route_config;
+
+moe_status_t moe_route_grouped(const void *logits, moe_dtype_t logits_dtype, const float *bias, int T,
+                               int E, int top_k, const moe_route_config *cfg, int32_t *topk_ids,
+                               float *topk_weights, moe_stream_t stream);
+
+/* Gradient of moe_route_grouped's weights with respect to the logits, the choice held fixed
+ * (the bias has none): given dweights [T, top_k] fp32, the logits and the topk_ids of the
+ * forward call, dlogits [T, E] in logits_dtype, every element written:
+ *   renormalize, with p = s / (sum of the chosen s):
+ *     dl_j = scale p_j f_j (dw_j - sum_i p_i dw_i),   f = 1 - s (sigmoid) or 1 (softmax)
+ *   sigmoid otherwise:  dl_j = scale dw_j s_j (1 - s_j)
+ *     (both 0 for the experts that were not chosen)
+ *   softmax otherwise:  dl_e = s_e (g_e - sum_i g_i s_i), g = scale dw on the chosen, else 0
+ * Only score, renormalize and scale of cfg are used (the others are checked as above).  An id
+ * chosen twice in a row adds up; an id outside [0, E) is left out and recorded as
+ * MOE_ERR_INVALID_ARG in the device status word.  A masked (-inf or NaN) logit gets 0. */
+moe_status_t moe_route_grouped_backward(const float *dweights, const void *logits,
+                                        moe_dtype_t logits_dtype, const int32_t *topk_ids, int T, int E,
+                                        int top_k, const moe_route_config *cfg, void *dlogits,
+                                        moe_stream_t stream);
+
+/* ------------------------------------------------------------------ finalize, gradient
+ * Gradients of moe_finalize with its bf16 output.  With o_t the sum that the forward call
+ * normalised and r = 1 / sqrt(mean_h(o^2) + eps):
+ *   G = r (gamma dout - o r^2 mean_h(gamma dout o))    with rms_weight (gamma)
+ *     = dout                                           without
+ *   G += dresidual_out                                 (optional)
+ *   dy[t * top_k + j] = w_tj G                         (bf16 [T * top_k, H]; w = 1 when
+ *                                                       topk_weights is NULL: the weights were
+ *                                                       applied on the input)
+ *   dweights[t, j] = sum_h G_h y[t * top_k + j, h]     (fp32 [T, top_k])
+ *   dsum = G                                           (bf16 [T, H]: the gradient of the shared
+ *                                                       row and of the residual)
+ *   drms_h = sum_t dout o r                            (fp32 [H])
+ * dout and dresidual_out [T, H] bf16 are the gradients of output and residual_out;
+ * residual_out [T, H] bf16 is what the forward call wrote (o in bf16, read only with
+ * rms_weight, then required); fused_expert_output (y) [T * top_k, H] bf16 is read for
+ * dweights alone (may be NULL without it).  dy, dweights (needs topk_weights), dsum and drms
+ * (needs rms_weight) may each be NULL: not computed; not all.  Sums in fp32, in a fixed order;
+ * G stays in fp32 until an output is rounded.  T == 0 sets drms to zero.  H % 8 == 0, H <=
+ * 16384, 1 <= top_k <= 32.  ws: moe_finalize_backward_workspace_size(T, H) bytes (needed for
+ * drms alone).  dsum may be dout or dresidual_out itself; no other overlap. */
+moe_status_t moe_finalize_backward(const void *dout, const void *dresidual_out, const void *residual_out,
+                                   const void *rms_weight, float eps, const void *fused_expert_output,
+                                   const float *topk_weights, int T, int H, int top_k, void *dy,
+                                   float *dweights, void *dsum, float *drms, void *ws, size_t ws_bytes,
+                                   moe_stream_t stream);
+size_t moe_finalize_backward_workspace_size(int T, int H);
 
 /* ------------------------------------------------------------------ status
  * Every device-side wait in the library's kernels gives up after about two

@@ -1,6 +1,8 @@
 // moe_abi: host-side helpers shared by the entry points -- status strings,
 // the device status word, SM counts.
-#include "moe_common.cuh"
+#include "moe_vec.cuh"
+
+#include <initializer_list>
 
 namespace moe {
 
@@ -27,7 +29,11 @@ extern "C" moe_status_t moe_device_status(int clear) {
   const moe_status_t b = align_status(clear);
   const moe_status_t c = prepare_status(clear);
   const moe_status_t d = finalize_status(clear);
-  return a != MOE_OK ? a : (b != MOE_OK ? b : (c != MOE_OK ? c : d));
+  const moe_status_t e = route_grouped_status(clear);
+  const moe_status_t f = linear_status(clear);
+  for (const moe_status_t st : {a, b, c, d, e, f})
+    if (st != MOE_OK) return st;
+  return MOE_OK;
 }
 
 extern "C" const char* moe_status_string(moe_status_t status) {

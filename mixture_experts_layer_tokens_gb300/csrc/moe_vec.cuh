@@ -1,0 +1,135 @@
+// Typed element and vector access of the linear, grouped-route and gradient kernels: fp32,
+// bf16 and fp16 values in and out of fp32 registers.
+#pragma once
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "moe_common.cuh"
+
+namespace moe {
+
+moe_status_t route_grouped_status(int clear);
+moe_status_t linear_status(int clear);
+
+__device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
+__device__ __forceinline__ float load1(const __half* p) { return __half2float(__ldg(p)); }
+
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store1(__half* p, float v) { *p = __float2half_rn(v); }
+
+// 4 bytes of packed values <-> fp32
+template <class T>
+struct Word;
+template <>
+struct Word<float> {
+  static constexpr int N = 1;
+  static __device__ __forceinline__ void get(uint32_t w, float* v) { v[0] = __uint_as_float(w); }
+  static __device__ __forceinline__ uint32_t put(const float* v) { return __float_as_uint(v[0]); }
+};
+template <>
+struct Word<__nv_bfloat16> {
+  static constexpr int N = 2;
+  static __device__ __forceinline__ void get(uint32_t w, float* v) {
+    v[0] = bf16lo(w);
+    v[1] = bf16hi(w);
+  }
+  static __device__ __forceinline__ uint32_t put(const float* v) { return pack_bf16x2(v[0], v[1]); }
+};
+template <>
+struct Word<__half> {
+  static constexpr int N = 2;
+  static __device__ __forceinline__ void get(uint32_t w, float* v) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    v[0] = f.x;
+    v[1] = f.y;
+  }
+  static __device__ __forceinline__ uint32_t put(const float* v) {
+    const __half2 h = __floats2half2_rn(v[0], v[1]);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+// 8 consecutive values (16-byte aligned) <-> fp32
+template <class T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  constexpr int W = 8 / Word<T>::N;  // words
+  uint32_t w[W];
+#pragma unroll
+  for (int i = 0; i < W; i += 4) {
+    const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+    w[i] = q.x;
+    w[i + 1] = q.y;
+    w[i + 2] = q.z;
+    w[i + 3] = q.w;
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) Word<T>::get(w[i], v + i * Word<T>::N);
+}
+template <class T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+  constexpr int W = 8 / Word<T>::N;
+  uint32_t w[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) w[i] = Word<T>::put(v + i * Word<T>::N);
+#pragma unroll
+  for (int i = 0; i < W; i += 4)
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+}
+
+// The NV consecutive elements [lane NV, (lane + 1) NV) of a row of n (0 past its end); by vectors of up to
+// 16 bytes when they tile the row (the row then starts on a vector boundary too).
+template <int NV, class T>
+__device__ __forceinline__ void load_lane(const T* row, int n, int lane, float (&v)[NV]) {
+  constexpr int BYTES = NV * (int)sizeof(T) < 16 ? NV * (int)sizeof(T) : 16;
+  constexpr int PER = BYTES / (int)sizeof(T);  // elements of a vector
+  if constexpr (BYTES >= 4) {
+    if (n % PER == 0) {
+#pragma unroll
+      for (int i = 0; i < NV; i += PER) {
+        uint32_t w[BYTES / 4] = {};
+        if (lane * NV + i < n) {
+          const T* p = row + lane * NV + i;
+          if constexpr (BYTES == 16) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+            w[0] = q.x;
+            w[1] = q.y;
+            w[2] = q.z;
+            w[3] = q.w;
+          } else if constexpr (BYTES == 8) {
+            const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+            w[0] = q.x;
+            w[1] = q.y;
+          } else {
+            w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < BYTES / 4; ++j) Word<T>::get(w[j], v + i + j * Word<T>::N);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = lane * NV + i < n ? load1(row + lane * NV + i) : 0.f;
+}
+
+// A row of n fp32 values in shared memory (16-byte aligned) written by one warp as type T.
+template <class T>
+__device__ __forceinline__ void store_row(T* row, int n, int lane, const float* buf) {
+  constexpr int PER = 16 / (int)sizeof(T);
+  if (n % PER == 0) {
+    for (int i = lane * PER; i < n; i += 32 * PER) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = Word<T>::put(buf + i + j * Word<T>::N);
+      *reinterpret_cast<uint4*>(row + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+    for (int i = lane; i < n; i += 32) store1(row + i, buf[i]);
+  }
+}
+
+}  // namespace moe

@@ -18,11 +18,15 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_TIMEOUT = range(6)
-MOE_DT_BF16, MOE_DT_FP8_E4M3, MOE_DT_NVFP4, MOE_DT_FP32 = range(4)
+MOE_DT_BF16, MOE_DT_FP8_E4M3, MOE_DT_NVFP4, MOE_DT_FP32, MOE_DT_FP16 = range(5)
 MOE_SCORING_SOFTMAX_RENORM, MOE_SCORING_SIGMOID = 0, 1
 MOE_BLOCK_M = 128
 # moe_activation_t, by the names of the "Fused Experts Kernels" table
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "swigluoai": 3, "silu_no_mul": 4, "gelu_no_mul": 5}
+
+# moe_linear_activation_t and moe_score_t, by name
+LINEAR_ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 # (name, argtypes, restype) of every exported entry point
 _P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -68,6 +72,15 @@ class ExpertsProblem(ctypes.Structure):
 
 _EPP = ctypes.POINTER(ExpertsProblem)
 
+
+class RouteConfig(ctypes.Structure):
+    """moe_route_config: how moe_route_grouped scores, groups and weighs the experts."""
+    _fields_ = [("score", ctypes.c_int), ("n_group", ctypes.c_int), ("topk_group", ctypes.c_int),
+                ("group_top", ctypes.c_int), ("renormalize", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+_RCP = ctypes.POINTER(RouteConfig)
+
 SIGNATURES = {
     "moe_route": ([_P, _I, _I, _I, _I, _P, _P, _P], _I),
     "moe_align": ([_P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _Z, _P], _I),
@@ -94,6 +107,13 @@ SIGNATURES = {
     "moe_workspace_size_batched": ([_I, _I, _I, _I, _QCP], _Z),
     "moe_experts_batched": ([_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _QCP, _I, _P, _P, _Z, _P], _I),
     "moe_finalize_batched": ([_P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _F, _I, _I, _I, _I, _I, _P, _F, _P, _P], _I),
+    "moe_linear": ([_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P], _I),
+    "moe_linear_backward": ([_P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _Z, _P], _I),
+    "moe_linear_backward_workspace_size": ([_I, _I, _I], _Z),
+    "moe_route_grouped": ([_P, _I, _P, _I, _I, _I, _RCP, _P, _P, _P], _I),
+    "moe_route_grouped_backward": ([_P, _P, _I, _P, _I, _I, _I, _RCP, _P, _P], _I),
+    "moe_finalize_backward": ([_P, _P, _P, _P, _F, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _Z, _P], _I),
+    "moe_finalize_backward_workspace_size": ([_I, _I], _Z),
     "moe_device_status": ([_I], _I),
     "moe_selftest_wait_timeout": ([ctypes.c_uint64, _P], _I),
     "moe_selftest_row_division": ([ctypes.c_longlong, ctypes.c_uint32, _P, _P], _I),
@@ -570,3 +590,193 @@ def moe_finalize_batched(out_b: torch.Tensor, topk_weights: Optional[torch.Tenso
         _ptr(shared), _ptr(residual), _ptr(rms_weight), eps, T, H, k, int(apply_router_weight_on_input), MOE_DT_BF16,
         None, 1.0, _ptr(residual_out), _stream(stream)))
     return output
+
+
+# ------------------------------------------------------------------ linear projection
+_DT = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_FP16, torch.float32: MOE_DT_FP32}
+
+
+def _tensor(t: Optional[torch.Tensor], dtype, shape, name: str, device: int):
+    """A tensor argument as its pointer: dtype, shape, contiguity and device checked."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device")
+    return t.data_ptr()
+
+
+def _launch(stream: Optional[torch.cuda.Stream]):
+    """(current device index, raw stream) of a call."""
+    if not torch.cuda.is_available():
+        raise RuntimeError("no CUDA device")
+    dev = torch.cuda.current_device()
+    if stream is None:
+        return dev, torch.cuda.current_stream(dev).cuda_stream
+    if stream.device_index != dev:
+        raise ValueError("stream: expected a stream of the current CUDA device")
+    return dev, stream.cuda_stream
+
+
+def _linear_args(x: torch.Tensor, w: torch.Tensor, activation: str):
+    if activation not in LINEAR_ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}")
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"x: expected bfloat16 or float16, got {x.dtype}")
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w: expected [M, K] and [N, K]")
+    (M, K), N = x.shape, w.shape[0]
+    return M, N, K, x.dtype, _DT[x.dtype], LINEAR_ACTIVATIONS[activation]
+
+
+def moe_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, activation: str = "none", out: Optional[torch.Tensor] = None,
+               out_dtype: Optional[torch.dtype] = None, preact: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """out = act(x w^T + bias) + residual (``moe_linear``): x [M, K], w [N, K], bias [N] bf16 or fp16; out and
+    residual [M, N] in that type or fp32 (``out_dtype``); preact [M, N] receives x w^T + bias for the gradients.
+    ``activation``: see ``LINEAR_ACTIVATIONS``."""
+    M, N, K, dt, code, act = _linear_args(x, w, activation)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or dt, device=x.device)
+    odt = out.dtype
+    if odt is not dt and odt is not torch.float32 or out_dtype not in (None, odt):
+        raise TypeError(f"out: expected {dt} or float32 as out_dtype says, got {odt}")
+    dev, s = _launch(stream)
+    _check("moe_linear", lib().moe_linear(
+        _tensor(x, dt, (M, K), "x", dev), _tensor(w, dt, (N, K), "w", dev), _tensor(bias, dt, (N,), "bias", dev),
+        _tensor(residual, odt, (M, N), "residual", dev), M, N, K, code, act, _DT[odt],
+        _tensor(out, odt, (M, N), "out", dev), _tensor(preact, dt, (M, N), "preact", dev), s))
+    return out
+
+
+def linear_backward_workspace_size(M: int, N: int, K: int) -> int:
+    return int(lib().moe_linear_backward_workspace_size(M, N, K))
+
+
+def moe_linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, preact: Optional[torch.Tensor] = None,
+                        activation: str = "none", dx: Optional[torch.Tensor] = None,
+                        dw: Optional[torch.Tensor] = None, dbias: Optional[torch.Tensor] = None,
+                        ws: Optional[torch.Tensor] = None, need_dx: bool = True, need_dw: bool = True,
+                        need_dbias: bool = False, stream=None):
+    """Gradients of moe_linear (``moe_linear_backward``) given dout [M, N] (the operands' type or fp32) and the
+    forward call's preact (unless ``activation`` is "none"): returns (dx [M, K], dw [N, K], dbias [N]) in the
+    operands' type, None where not needed.  The residual's gradient is dout."""
+    M, N, K, dt, code, act = _linear_args(x, w, activation)
+    if dout.dtype is not dt and dout.dtype is not torch.float32:
+        raise TypeError(f"dout: expected {dt} or float32, got {dout.dtype}")
+    if dx is None and need_dx:
+        dx = torch.empty_like(x)
+    if dw is None and need_dw:
+        dw = torch.empty_like(w)
+    if dbias is None and need_dbias:
+        dbias = torch.empty((N,), dtype=dt, device=x.device)
+    if ws is None:
+        ws = torch.empty(max(linear_backward_workspace_size(M, N, K), 16), dtype=torch.uint8, device=x.device)
+    dev, s = _launch(stream)
+    _check("moe_linear_backward", lib().moe_linear_backward(
+        _tensor(dout, dout.dtype, (M, N), "dout", dev), _DT[dout.dtype], _tensor(x, dt, (M, K), "x", dev),
+        _tensor(w, dt, (N, K), "w", dev), _tensor(preact, dt, (M, N), "preact", dev), M, N, K, code, act,
+        _tensor(dx, dt, (M, K), "dx", dev), _tensor(dw, dt, (N, K), "dw", dev), _tensor(dbias, dt, (N,), "dbias", dev),
+        _tensor(ws, torch.uint8, ws.shape, "ws", dev), ws.numel(), s))
+    return dx, dw, dbias
+
+
+# ------------------------------------------------------------------ grouped route
+def route_config(score: str = "sigmoid", n_group: int = 1, topk_group: int = 1, group_top: int = 1,
+                 renormalize: bool = True, scale: float = 1.0) -> RouteConfig:
+    if score not in SCORES:
+        raise ValueError(f"unknown score {score!r}")
+    return RouteConfig(SCORES[score], n_group, topk_group, group_top, int(bool(renormalize)), scale)
+
+
+def moe_route_grouped(logits: torch.Tensor, top_k: int, bias: Optional[torch.Tensor] = None, score: str = "sigmoid",
+                      n_group: int = 1, topk_group: int = 1, group_top: int = 1, renormalize: bool = True,
+                      scale: float = 1.0, topk_ids: Optional[torch.Tensor] = None,
+                      topk_weights: Optional[torch.Tensor] = None,
+                      stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Router with sigmoid or softmax scores, a balance bias [E] fp32 that steers the choice alone, and expert
+    groups (``moe_route_grouped``): logits [T, E] fp32, bf16 or fp16 -> topk_ids [T, top_k] int32 and topk_weights
+    [T, top_k] fp32."""
+    if logits.dtype not in _DT:
+        raise TypeError(f"logits: expected float32, bfloat16 or float16, got {logits.dtype}")
+    T, E = logits.shape
+    cfg = route_config(score, n_group, topk_group, group_top, renormalize, scale)
+    if topk_ids is None:
+        topk_ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+    if topk_weights is None:
+        topk_weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    dev, s = _launch(stream)
+    _check("moe_route_grouped", lib().moe_route_grouped(
+        _tensor(logits, logits.dtype, (T, E), "logits", dev), _DT[logits.dtype],
+        _tensor(bias, torch.float32, (E,), "bias", dev), T, E, top_k, ctypes.byref(cfg),
+        _tensor(topk_ids, torch.int32, (T, top_k), "topk_ids", dev),
+        _tensor(topk_weights, torch.float32, (T, top_k), "topk_weights", dev), s))
+    return topk_ids, topk_weights
+
+
+def moe_route_grouped_backward(dweights: torch.Tensor, logits: torch.Tensor, topk_ids: torch.Tensor,
+                               score: str = "sigmoid", renormalize: bool = True, scale: float = 1.0,
+                               dlogits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of moe_route_grouped's weights with respect to its logits (``moe_route_grouped_backward``), the
+    choice topk_ids held fixed: dweights [T, top_k] fp32 -> dlogits [T, E] in the logits' type."""
+    if logits.dtype not in _DT:
+        raise TypeError(f"logits: expected float32, bfloat16 or float16, got {logits.dtype}")
+    (T, E), top_k = logits.shape, topk_ids.shape[1]
+    cfg = route_config(score, renormalize=renormalize, scale=scale)
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    dev, s = _launch(stream)
+    _check("moe_route_grouped_backward", lib().moe_route_grouped_backward(
+        _tensor(dweights, torch.float32, (T, top_k), "dweights", dev),
+        _tensor(logits, logits.dtype, (T, E), "logits", dev), _DT[logits.dtype],
+        _tensor(topk_ids, torch.int32, (T, top_k), "topk_ids", dev), T, E, top_k, ctypes.byref(cfg),
+        _tensor(dlogits, logits.dtype, (T, E), "dlogits", dev), s))
+    return dlogits
+
+
+# ------------------------------------------------------------------ finalize, gradient
+def finalize_backward_workspace_size(T: int, H: int) -> int:
+    return int(lib().moe_finalize_backward_workspace_size(T, H))
+
+
+def moe_finalize_backward(dout: torch.Tensor, fused_expert_output: Optional[torch.Tensor],
+                          topk_weights: Optional[torch.Tensor], top_k: int,
+                          residual_out: Optional[torch.Tensor] = None, rms_weight: Optional[torch.Tensor] = None,
+                          eps: float = 1e-6, dresidual_out: Optional[torch.Tensor] = None,
+                          dy: Optional[torch.Tensor] = None, dweights: Optional[torch.Tensor] = None,
+                          dsum: Optional[torch.Tensor] = None, drms: Optional[torch.Tensor] = None,
+                          ws: Optional[torch.Tensor] = None, need_dy: bool = True, need_dweights: bool = True,
+                          need_dsum: bool = True, need_drms: bool = True, stream=None):
+    """Gradients of moe_finalize with its bf16 output (``moe_finalize_backward``): given dout [T, H] bf16 (and
+    dresidual_out, the gradient of residual_out), the expert rows and weights of the forward call, and with an
+    RMSNorm its residual_out and rms_weight, returns (dy [T * top_k, H] bf16, dweights [T, top_k] fp32, dsum [T, H]
+    bf16 -- the gradient of the shared row and of the residual --, drms [H] fp32), None where not needed.
+    topk_weights None: the weights were applied on the input (no dweights)."""
+    T, H = dout.shape
+    bf, d = torch.bfloat16, dout.device
+    if dy is None and need_dy:
+        dy = torch.empty((T * top_k, H), dtype=bf, device=d)
+    if dweights is None and need_dweights and topk_weights is not None:
+        dweights = torch.empty((T, top_k), dtype=torch.float32, device=d)
+    if dsum is None and need_dsum:
+        dsum = torch.empty((T, H), dtype=bf, device=d)
+    if drms is None and need_drms and rms_weight is not None:
+        drms = torch.empty((H,), dtype=torch.float32, device=d)
+    if ws is None and drms is not None:
+        ws = torch.empty(max(finalize_backward_workspace_size(T, H), 16), dtype=torch.uint8, device=d)
+    dev, s = _launch(stream)
+    _check("moe_finalize_backward", lib().moe_finalize_backward(
+        _tensor(dout, bf, (T, H), "dout", dev), _tensor(dresidual_out, bf, (T, H), "dresidual_out", dev),
+        _tensor(residual_out, bf, (T, H), "residual_out", dev), _tensor(rms_weight, bf, (H,), "rms_weight", dev), eps,
+        _tensor(fused_expert_output, bf, (T * top_k, H), "fused_expert_output", dev),
+        _tensor(topk_weights, torch.float32, (T, top_k), "topk_weights", dev), T, H, top_k,
+        _tensor(dy, bf, (T * top_k, H), "dy", dev), _tensor(dweights, torch.float32, (T, top_k), "dweights", dev),
+        _tensor(dsum, bf, (T, H), "dsum", dev), _tensor(drms, torch.float32, (H,), "drms", dev),
+        None if ws is None else _tensor(ws, torch.uint8, ws.shape, "ws", dev), 0 if ws is None else ws.numel(), s))
+    return dy, dweights, dsum, drms

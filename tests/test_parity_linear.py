@@ -1,0 +1,211 @@
+"""moe_linear and its gradients against their fp64 definition, element by element.
+
+Tolerances: a product sum over K is accumulated in fp32 by tensor-core steps of 16 products;
+each step's additions lose at most 2^-22 of the terms' magnitudes so far (an fp32 step is 2^-23,
+truncation included, doubled for the alignment of the 16 products), so a sum is within
+2^-22 (K / 16 + 16) sum |x||w|; the epilogue's functions are within 2^-20 (1 + |z|) and have
+slopes below 1.2; an output is rounded once (half a step: finfo.eps / 2 of the value)."""
+import pytest
+import torch
+
+from mixture_experts_layer_tokens_gb300 import moe
+from oracle import router_ref as rr
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def _half_step(ref, dtype):
+    fi = torch.finfo(dtype)
+    return ref.abs() * (fi.eps / 2) + fi.smallest_normal * fi.eps
+
+
+def _within(got, ref, tol, what):
+    got = got.cpu().double()
+    assert torch.isfinite(got).all(), what
+    bad = (got - ref).abs() - tol
+    assert (bad <= 0).all(), f"{what}: {int((bad > 0).sum())} of {bad.numel()} beyond, worst excess {bad.max():.3e}"
+
+
+def _make(M, N, K, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((M, K), generator=g).to(dtype)
+    w = (torch.randn((N, K), generator=g) / K ** 0.5).to(dtype)
+    return g, x, w
+
+
+def _forward(dev, M, N, K, dtype=BF, act="none", bias=False, residual=False, preact=False, out_dtype=None, inplace=False):
+    g, x, w = _make(M, N, K, dtype, M * 7 + N * 3 + K)
+    odt = out_dtype or dtype
+    b = torch.randn((N,), generator=g).to(dtype) if bias else None
+    res = torch.randn((M, N), generator=g).to(odt) if residual else None
+    d = lambda t: None if t is None else t.to(dev)  # noqa: E731
+    pre = torch.full((M, N), 7.0, dtype=dtype, device=dev) if preact else None
+    resd = d(res)
+    # (a guard row behind the output stays as it was)
+    store = torch.full((M + 1, N), 7.0, dtype=odt, device=dev)
+    out = store[:M]
+    if inplace:
+        out.copy_(res)
+        resd = out
+    got = moe.moe_linear(d(x), d(w), d(b), resd, act, out=out, preact=pre)
+    torch.cuda.synchronize()
+    assert moe.moe_device_status() == moe.MOE_OK
+    ref, z, mag = rr.linear(x, w, b, res, act)
+    acc = 2.0 ** -22 * (K / 16 + 16) * mag
+    fun = 0 if act == "none" else 2.0 ** -20 * (1 + z.abs())
+    _within(got, ref, 1.2 * acc + fun + 2.0 ** -23 * ref.abs() + _half_step(ref, odt), "out")
+    if preact:
+        _within(pre, z, acc + _half_step(z, dtype), "preact")
+    assert (store[M] == 7.0).all()
+
+
+# one row to several tiles; N and K beside the tile sizes; few and many K blocks
+SHAPES = [(1, 1, 8), (1, 256, 7168), (2, 77, 264), (3, 130, 1032), (4, 8, 64), (5, 8, 64), (7, 33, 72), (16, 256, 2048),
+          (33, 500, 200), (127, 129, 520), (128, 256, 64), (129, 257, 128), (200, 64, 4096), (300, 1000, 136),
+          (513, 384, 1024), (1030, 72, 640)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_linear_shapes(cuda_dev, M, N, K):
+    _forward(cuda_dev, M, N, K)
+    _forward(cuda_dev, M, N, K, HF, "none", True, True, True, F32)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 256), (3, 41, 256), (40, 264, 512), (150, 41, 96), (150, 200, 3000 // 8 * 8)])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "gelu_tanh"])
+def test_linear_epilogues(cuda_dev, M, N, K, act):
+    _forward(cuda_dev, M, N, K, BF, act, True, True, True)
+    _forward(cuda_dev, M, N, K, HF, act, True, False, False)
+    _forward(cuda_dev, M, N, K, BF, act, False, True, True, F32, inplace=True)
+    _forward(cuda_dev, M, N, K, HF, act, False, True, False, inplace=True)
+
+
+def test_linear_large_grid(cuda_dev):
+    """More tiles than SMs (persistent CTAs run several), ragged in every dimension."""
+    _forward(cuda_dev, 2500, 2050, 328, BF, "silu", True, True, True)
+    _forward(cuda_dev, 2500, 2056, 328, HF, "none", True, False, True, F32)
+
+
+def test_linear_nonfinite_rows_stay_apart(cuda_dev):
+    for M in (4, 40, 300):
+        _, x, w = _make(M, 200, 256, BF, 5)
+        clean = moe.moe_linear(x.to(cuda_dev), w.to(cuda_dev))
+        x[1, 7] = float("nan")
+        x[2, 9] = float("inf")
+        got = moe.moe_linear(x.to(cuda_dev), w.to(cuda_dev))
+        assert torch.isnan(got[1]).all()
+        assert not torch.isfinite(got[2]).any()
+        keep = [r for r in range(M) if r not in (1, 2)]
+        assert torch.equal(got[keep], clean[keep])
+
+
+def _backward(dev, M, N, K, dtype=BF, act="none", ddt=None, need=(True, True, True)):
+    g, x, w = _make(M, N, K, dtype, M * 5 + N * 3 + K + 1)
+    ddt = ddt or dtype
+    dout = (torch.randn((M, N), generator=g) * 0.5).to(ddt)
+    pre = None if act == "none" else (torch.randn((M, N), generator=g) * 2).to(dtype)
+    d = lambda t: None if t is None else t.to(dev)  # noqa: E731
+    got = moe.moe_linear_backward(d(dout), d(x), d(w), d(pre), act, need_dx=need[0], need_dw=need[1], need_dbias=need[2])
+    torch.cuda.synchronize()
+    assert moe.moe_device_status() == moe.MOE_OK
+    refs, mags = rr.linear_backward(dout, x, w, pre, act)
+    # dz is rounded to the operands' type where it is computed or comes in fp32; act' is within 2^-20
+    rounded = act != "none" or ddt != dtype
+    dz_err = (torch.finfo(dtype).eps / 2 if rounded else 0) + (2.0 ** -19 if act != "none" else 0)
+    sub = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps if rounded else 0
+    for name, v, ref, mag, n, needed in zip(("dx", "dw", "dbias"), got, refs, mags, (N, M, M), need):
+        if not needed:
+            assert v is None
+            continue
+        if name == "dbias":  # 8 rows a thread, 8 threads, then one sum in 8 of all chunks
+            tol = (2.0 ** -24 * (32 + M / 64 / 8) + (2.0 ** -19 if act != "none" else 0)) * mag
+        else:
+            other = x.double().abs().sum(0)[None] if name == "dw" else w.double().abs().sum(0)[None]
+            tol = (2.0 ** -22 * (n / 16 + 16) + dz_err) * mag + sub * other
+        _within(v, ref, tol + _half_step(ref, dtype), name)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 8), (1, 256, 512), (5, 33, 72), (64, 8, 64), (100, 64, 256), (129, 130, 136),
+                                   (300, 257, 520), (1000, 256, 1024), (70, 1000, 2048)])
+def test_linear_backward_shapes(cuda_dev, M, N, K):
+    _backward(cuda_dev, M, N, K)
+    _backward(cuda_dev, M, N, K, HF, "silu", F32)
+    _backward(cuda_dev, M, N, K, BF, "none", F32)
+
+
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_linear_backward_activations(cuda_dev, act, dtype):
+    _backward(cuda_dev, 150, 200, 264, dtype, act)
+    _backward(cuda_dev, 150, 201, 264, dtype, act, F32)
+
+
+def test_linear_backward_parts_and_large_grid(cuda_dev):
+    for need in ((True, False, False), (False, True, False), (False, False, True), (True, False, True)):
+        _backward(cuda_dev, 90, 96, 128, BF, "gelu", None, need)
+        _backward(cuda_dev, 90, 96, 128, BF, "none", None, need)
+    _backward(cuda_dev, 2100, 1100, 1800, BF, "silu")
+
+
+def test_linear_gradients_are_the_differences_of_the_projection(cuda_dev):
+    """d/dt <dout, linear(x + t u)> against <dx, u>, in fp32 outputs: the tensor cores' sums of bf16
+    products are good to 2^-22 (K/16 + 16) of their magnitudes and dx to half a bf16 step, random over
+    its elements; the step of 2^-3 of a linear map has no truncation error."""
+    M, N, K = 64, 96, 128
+    g, x, w = _make(M, N, K, BF, 8)
+    u = (torch.randint(-4, 5, (M, K), generator=g).float() * 0.125)
+    x = (x.float() * 16).round().clamp(-64, 64) / 16  # so that x +- u are exact in bf16
+    dout = (torch.randn((M, N), generator=g)).to(BF)
+    f = lambda v: (moe.moe_linear(v.to(BF).to(cuda_dev), w.to(cuda_dev), out_dtype=F32).cpu().double() * dout.double()).sum()  # noqa: E731
+    dx, _, _ = moe.moe_linear_backward(dout.to(cuda_dev), x.to(BF).to(cuda_dev), w.to(cuda_dev))
+    want = (dx.cpu().double() * u.double()).sum()
+    mag = (dx.cpu().double() * u.double()).abs().sum()
+    acc = 2.0 ** -22 * (K / 16 + 16) * (x.abs().double() @ w.double().abs().T * dout.double().abs()).sum()
+    assert abs((f(x + u) - f(x - u)) / 2 - want) <= acc + 2.0 ** -8 * mag
+
+
+def test_linear_empty_batch(cuda_dev):
+    x = torch.empty((0, 64), dtype=BF, device=cuda_dev)
+    w = torch.ones((8, 64), dtype=BF, device=cuda_dev)
+    assert moe.moe_linear(x, w).shape == (0, 8)
+    dw = torch.ones_like(w)
+    _, _, db = moe.moe_linear_backward(torch.empty((0, 8), dtype=BF, device=cuda_dev), x, w, dw=dw, need_dbias=True)
+    assert (dw == 0).all() and (db == 0).all()
+
+
+def test_linear_is_the_same_twice_and_under_a_graph(cuda_dev):
+    for M, N, K in ((1, 256, 2048), (64, 256, 4096), (600, 512, 512)):
+        _, x, w = _make(M, N, K, BF, 2)
+        x, w = x.to(cuda_dev), w.to(cuda_dev)
+        out = torch.empty((M, N), dtype=F32, device=cuda_dev)
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        ws = torch.empty(moe.linear_backward_workspace_size(M, N, K), dtype=torch.uint8, device=cuda_dev)
+
+        def step():
+            moe.moe_linear(x, w, out=out)
+            moe.moe_linear_backward(out, x, w, dx=dx, dw=dw, ws=ws)
+
+        step()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (out, dx, dw)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for t in (out, dx, dw):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((out, dx, dw), want))
+
+
+def test_linear_on_another_stream(cuda_dev):
+    _, x, w = _make(200, 256, 1024, BF, 3)
+    x, w = x.to(cuda_dev), w.to(cuda_dev)
+    want = moe.moe_linear(x, w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = moe.moe_linear(x, w, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
