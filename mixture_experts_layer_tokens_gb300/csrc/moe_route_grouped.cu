@@ -5,17 +5,21 @@
 //   their group_top largest c, the top_k largest c of the kept groups chosen,
 //   w_j = s_j scale (/ sum of the chosen s).
 //
-// Lane i holds the NV consecutive experts [i NV, (i + 1) NV) in registers as keys: 32-bit
-// integers ordered like the floats, so one redux.sync finds the warp's largest, a ballot the
-// lanes that hold it, and the lowest of them holds the lowest index among equals.  A chosen
-// key becomes 0, which is below the key of every float.
+// Layout: the 32 lanes are dealt to the groups, a power of two of them to each, and a lane
+// holds up to NV consecutive experts of its group, so a group's sums need a few shuffles among
+// its own lanes and a lower lane always holds lower experts.  A lane keeps its experts as
+// 32-bit keys ordered like the floats, the low bits replaced by the place within the lane, and
+// sorts them once; a round of the choice is then one redux.sync over the lanes' first keys, a
+// ballot, and a shift of the winner's list.
 //
-// The order is the one of exact arithmetic.  Without a bias (and, with groups, group_top 1)
-// both scores grow with the logit, so the logits themselves are ranked.  With a bias the c
-// are computed in fp32, where each is within a known distance of its exact value; if two
-// neighbours in the chosen order (the best expert left out and the best group left out among
-// them) lie closer than twice that distance and are not equal in logit and bias, the token is
-// ranked again in fp64.
+// The order is the one of exact arithmetic.  Without a bias both scores grow with the logit,
+// so the logits themselves are ranked.  With a bias the c are computed in fp32, where each is
+// within a known distance of its exact value (the replaced bits included); if two neighbours
+// in the chosen order (the best expert left out and the best group left out among them) lie
+// closer than that and are not equal in logit and bias, the token is ranked again from scores
+// held as pairs of floats (2^-39), and if that cannot tell them either, in fp64.  fp64 alone
+// cost about 20 us for such a token (the tensor of 16384 tokens has some 20 of them): this
+// machine does two fp64 FMAs a clock per SM.
 #include "moe_vec.cuh"
 
 namespace moe {
@@ -32,10 +36,6 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
-}
-__device__ __forceinline__ uint64_t order_key64(double x) {
-  const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
-  return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
 }
 
 // A logit as the router counts it: NaN as -inf (masked), +inf as the largest finite number.
@@ -60,9 +60,10 @@ struct RouteArgs {
   int T, E, top_k;
   int score, n_group, topk_group, group_top, renorm;
   float scale;
+  int lpg;  // lanes of a group: the largest power of two that gives every group as many
 };
 
-// The masked state of expert e and its biased score's two inputs.
+// Logit and bias of expert e, the masked state folded into the logit.
 template <class TL>
 __device__ __forceinline__ void expert_inputs(const TL* row, const float* bias, int e, float& l, float& b) {
   l = clean_logit(load1(row + e));
@@ -73,282 +74,477 @@ __device__ __forceinline__ void expert_inputs(const TL* row, const float* bias, 
   }
 }
 
-// ------------------------------------------------------------------ the order in fp64
-// Lane j < top_k gets the j-th choice; called by the whole warp.
-struct Best64 {
-  uint64_t c;
-  uint32_t l;
-  int i;
+// ------------------------------------------------------------------ pairs of floats
+// hi + lo with |lo| at most half a last place of hi; the error terms of sums and products by
+// the classical two-sum (Knuth) and by fma.
+struct FF {
+  float h, l;
 };
-__device__ __forceinline__ bool better64(const Best64& a, const Best64& b) {
-  return a.c != b.c ? a.c > b.c : (a.l != b.l ? a.l > b.l : a.i < b.i);
+__device__ __forceinline__ FF two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
-__device__ __forceinline__ Best64 warp_best64(Best64 v) {
-#pragma unroll 1
-  for (int off = 16; off > 0; off >>= 1) {
-    Best64 o;
-    o.c = __shfl_xor_sync(kFull, v.c, off);
-    o.l = __shfl_xor_sync(kFull, v.l, off);
-    o.i = __shfl_xor_sync(kFull, v.i, off);
-    if (better64(o, v)) v = o;
-  }
-  return v;
+__device__ __forceinline__ FF norm(float h, float l) {
+  const float s = __fadd_rn(h, l);
+  return {s, __fsub_rn(l, __fsub_rn(s, h))};
+}
+__device__ __forceinline__ FF add(FF a, FF b) {
+  const FF s = two_sum(a.h, b.h);
+  return norm(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+}
+__device__ __forceinline__ FF mul(FF a, FF b) {
+  const float p = __fmul_rn(a.h, b.h);
+  return norm(p, __fmaf_rn(a.h, b.l, __fmaf_rn(a.l, b.h, __fmaf_rn(a.h, b.h, -p))));
+}
+__device__ __forceinline__ FF div(FF a, FF b) {
+  const float q = __fdiv_rn(a.h, b.h);
+  const FF r = add(a, mul({-q, 0.f}, b));
+  return norm(q, __fdiv_rn(r.h, b.h));
+}
+// exp of a pair <= 0 to about 2^-45: n ln 2 taken off (ln 2 as 12 + 12 + 24 bits, so that its
+// products with n are exact), Taylor's series for the rest, |r| <= 0.35: the terms from r^8 / 8!
+// in fp32, below them in pairs.
+__device__ __noinline__ FF exp_ff(FF a) {
+  if (!(a.h > -150.f)) return {0.f, 0.f};  // below every fp32 number
+  const float n = rintf(a.h * 1.4426950408889634f);
+  FF r = two_sum(__fmaf_rn(-n, 0.693115234375f, a.h), -n * 3.1948089599609375e-05f);
+  r = norm(r.h, __fadd_rn(r.l, __fmaf_rn(-n, -1.9046542e-09f, a.l)));
+  float q = 1.60590444e-10f;
+  q = __fmaf_rn(q, r.h, 2.08767559e-09f);
+  q = __fmaf_rn(q, r.h, 2.50521079e-08f);
+  q = __fmaf_rn(q, r.h, 2.755732e-07f);
+  q = __fmaf_rn(q, r.h, 2.75573188e-06f);
+  q = __fmaf_rn(q, r.h, 2.48015876e-05f);
+  FF s = add({0.000198412701f, -2.72559687e-12f}, mul(r, {q, 0.f}));
+  s = add({0.00138888892f, -3.36310944e-11f}, mul(r, s));
+  s = add({0.00833333377f, -4.34617203e-10f}, mul(r, s));
+  s = add({0.0416666679f, -1.24176347e-09f}, mul(r, s));
+  s = add({0.166666672f, -4.96705388e-09f}, mul(r, s));
+  s = add({0.5f, 0.f}, mul(r, s));
+  s = add({1.f, 0.f}, mul(r, s));
+  s = add({1.f, 0.f}, mul(r, s));
+  return {ldexpf(s.h, (int)n), ldexpf(s.l, (int)n)};
 }
 
-template <int NV, class TL>
-__device__ __noinline__ int rank64(const TL* row, const RouteArgs& a) {
+// ------------------------------------------------------------------ the order from exact scores
+// The two precisions of the second ranking: a value type, the score, and keys ordered like it.
+struct PairScores {
+  using V = FF;
+  static __device__ __forceinline__ V of(float x) { return {x, 0.f}; }
+  static __device__ __forceinline__ V plus(V a, V b) { return add(a, b); }
+  static __device__ V exp_diff(float l, float m) { return exp_ff(two_sum(l, -m)); }
+  static __device__ V quotient(V a, V b) { return div(a, b); }
+  static __device__ __forceinline__ V shfl(V v, int off) {
+    return {__shfl_xor_sync(kFull, v.h, off), __shfl_xor_sync(kFull, v.l, off)};
+  }
+  static __device__ __forceinline__ uint64_t key(V v) { return ((uint64_t)order_key(v.h) << 32) | order_key(v.l); }
+  static __device__ __forceinline__ V value(uint64_t k) { return {key_value((uint32_t)(k >> 32)), key_value((uint32_t)k)}; }
+  // x >= y cannot be told from y (the scores are within 2^-42 or so of the exact ones)
+  static __device__ bool near(uint64_t kx, uint64_t ky) {
+    const FF x = value(kx), y = value(ky);
+    return !((x.h - y.h) + (x.l - y.l) > 0x1p-39f + 0x1p-40f * (fabsf(x.h) + fabsf(y.h)));
+  }
+};
+struct DoubleScores {
+  using V = double;
+  static __device__ __forceinline__ V of(float x) { return x; }
+  static __device__ __forceinline__ V plus(V a, V b) { return a + b; }
+  static __device__ V exp_diff(float l, float m) { return exp((double)l - (double)m); }
+  static __device__ V quotient(V a, V b) { return a / b; }
+  static __device__ __forceinline__ V shfl(V v, int off) { return __shfl_xor_sync(kFull, v, off); }
+  static __device__ __forceinline__ uint64_t key(V v) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
+    return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
+  }
+  static __device__ __forceinline__ V value(uint64_t k) {
+    return __longlong_as_double((long long)(k ^ ((k >> 63) ? 0x8000000000000000ull : ~0ull)));
+  }
+  static __device__ bool near(uint64_t, uint64_t) { return false; }  // equal ones go by logit and index
+};
+
+constexpr uint64_t kMasked64 = 1;  // below the key of every number, above a chosen expert's 0
+
+// The lanes that hold the largest (c, then l) key of the warp.
+__device__ __forceinline__ uint32_t best_lanes(uint64_t c, uint32_t l) {
+  const uint32_t hi = (uint32_t)(c >> 32), lo = (uint32_t)c;
+  const uint32_t mh = __reduce_max_sync(kFull, hi);
+  const uint32_t ml = __reduce_max_sync(kFull, hi == mh ? lo : 0u);
+  const bool in = hi == mh && lo == ml;
+  const uint32_t mk = __reduce_max_sync(kFull, in ? l : 0u);
+  return __ballot_sync(kFull, in && l == mk);
+}
+
+// Lane j < top_k gets the j-th choice; called by the whole warp.  unsure: the precision could
+// not order two scores.
+template <class S, int NV, class TL>
+__device__ __noinline__ int rank_again(const TL* row, const RouteArgs& a, bool* unsure) {
   const int lane = threadIdx.x & 31;
+  const int size = a.E / a.n_group, grp = lane / a.lpg, in = (lane % a.lpg) * NV;
+  const int base = grp * size + in;
+  const int cnt = grp < a.n_group ? max(0, min(NV, size - in)) : 0;
   uint64_t c[NV];
   uint32_t lk[NV];
+  bool doubt = false;
+
   float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = lane * NV + i;
-    if (e < a.E) m = fmaxf(m, clean_logit(load1(row + e)));
-  }
+  for (int i = 0; i < cnt; ++i) m = fmaxf(m, clean_logit(load1(row + base + i)));
   m = warp_max(m);
-  // the softmax's common denominator, in fp64 (sigmoid scores need none)
-  double den = 1.0;
+  typename S::V den = S::of(0.f);  // the softmax's denominator
   if (a.score == MOE_SCORE_SOFTMAX) {
-    den = 0.0;
-#pragma unroll 1
-    for (int i = 0; i < NV; ++i) {
-      const int e = lane * NV + i;
-      const float l = e < a.E ? clean_logit(load1(row + e)) : -INFINITY;
-      if (l > -INFINITY) den += exp((double)l - (double)m);
+    for (int i = 0; i < cnt; ++i) {
+      const float l = clean_logit(load1(row + base + i));
+      if (l > -INFINITY) den = S::plus(den, S::exp_diff(l, m));
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(kFull, den, off);
+    for (int off = 16; off > 0; off >>= 1) den = S::plus(den, S::shfl(den, off));
   }
-#pragma unroll
+  auto score_of = [&](float l) {
+    if (a.score == MOE_SCORE_SOFTMAX) return S::quotient(S::exp_diff(l, m), den);
+    const typename S::V e = S::exp_diff(-fabsf(l), 0.f);
+    return S::quotient(l < 0.f ? e : S::of(1.f), S::plus(S::of(1.f), e));
+  };
+  const bool by_logit = a.bias == nullptr;  // the logits' order is the scores'
+#pragma unroll 1
   for (int i = 0; i < NV; ++i) {
-    const int e = lane * NV + i;
     c[i] = 0;
     lk[i] = 0;
-    if (e < a.E) {
-      float l, b;
-      expert_inputs(row, a.bias, e, l, b);
-      lk[i] = order_key(l);
-      if (l == -INFINITY) {
-        c[i] = order_key64(-INFINITY);
-      } else {
-        const double s = a.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-(double)l))
-                                                      : exp((double)l - (double)m) / den;
-        c[i] = order_key64(s + (double)b);
+    if (i >= cnt) continue;
+    float l, b;
+    expert_inputs(row, a.bias, base + i, l, b);
+    if (l == -INFINITY) {
+      c[i] = kMasked64;
+      continue;
+    }
+    lk[i] = order_key(l);
+    if (by_logit)
+      c[i] = (uint64_t)lk[i] << 32;
+    else
+      c[i] = S::key(b == INFINITY ? S::of(b) : S::plus(score_of(l), S::of(b)));
+  }
+  if (a.n_group > 1) {
+    uint64_t top = 0, second = 0;
+#pragma unroll 1
+    for (int i = 0; i < NV; ++i) {
+      if (c[i] > top) {
+        second = top;
+        top = c[i];
+      } else if (c[i] > second) {
+        second = c[i];
       }
     }
-  }
-  const uint64_t masked = order_key64(-INFINITY);
-  if (a.n_group > 1) {
-    const int size = a.E / a.n_group;
-    Best64 mine{0, 0, 0x7fffffff};  // lane g: the score of group g
+    for (int off = 1; off < a.lpg; off <<= 1) {
+      const uint64_t t = __shfl_xor_sync(kFull, top, off), u = __shfl_xor_sync(kFull, second, off);
+      second = max(min(top, t), max(second, u));
+      top = max(top, t);
+    }
+    uint64_t score = top;
+    const bool sums = a.group_top == 2;
+    if (sums && top > kMasked64) {
+      auto value = [&](uint64_t k) { return by_logit ? score_of(key_value((uint32_t)(k >> 32))) : S::value(k); };
+      typename S::V x = value(top);
+      if (second > kMasked64 && top != S::key(S::of(INFINITY))) x = S::plus(x, value(second));
+      score = S::key(x);
+    }
+    int rank = 0;
 #pragma unroll 1
     for (int g = 0; g < a.n_group; ++g) {
-      Best64 first{0, 0, 0x7fffffff}, second;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e = lane * NV + i;
-        const Best64 v{c[i], 0, e};
-        if (e >= g * size && e < (g + 1) * size && better64(v, first)) first = v;
-      }
-      first = warp_best64(first);
-      uint64_t key = first.c;
-      if (a.group_top == 2 && first.c != masked) {
-        second = Best64{0, 0, 0x7fffffff};
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int e = lane * NV + i;
-          const Best64 v{c[i], 0, e};
-          if (e >= g * size && e < (g + 1) * size && e != first.i && better64(v, second)) second = v;
-        }
-        second = warp_best64(second);
-        if (second.c != masked) {
-          auto val = [](uint64_t k) {
-            return __longlong_as_double((long long)(k ^ ((k >> 63) ? 0x8000000000000000ull : ~0ull)));
-          };
-          key = order_key64(val(first.c) + val(second.c));
-        }
-      }
-      if (lane == g) mine = Best64{key, 0, g};
+      const uint64_t o = __shfl_sync(kFull, score, g * a.lpg);
+      rank += o > score || (o == score && g < grp);
     }
-    uint32_t keep = 0;
+    const bool keep = grp < a.n_group && rank < a.topk_group;
+    if (a.topk_group < a.n_group) {
+      // the last group kept and the first left out
+      const int last = __ffs(__ballot_sync(kFull, grp < a.n_group && rank == a.topk_group - 1)) - 1;
+      const int next = __ffs(__ballot_sync(kFull, grp < a.n_group && rank == a.topk_group)) - 1;
+      const uint64_t x = __shfl_sync(kFull, score, last), y = __shfl_sync(kFull, score, next);
+      doubt = y > kMasked64 && (sums || !by_logit) && S::near(x, y);
+    }
+    if (!keep) {
 #pragma unroll 1
-    for (int r = 0; r < a.topk_group; ++r) {
-      const Best64 b = warp_best64(mine);
-      keep |= 1u << b.i;
-      if (lane == b.i) mine = Best64{0, 0, 0x7fffffff};
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = lane * NV + i;
-      if (e < a.E && !((keep >> (e / size)) & 1u)) c[i] = 0;
+      for (int i = 0; i < NV; ++i) c[i] = 0;
     }
   }
-  int mine = 0;
+  int mine = 0, prev_id = 0;
+  uint64_t prev = 0;
 #pragma unroll 1
-  for (int r = 0; r < a.top_k; ++r) {
-    Best64 b{0, 0, 0x7fffffff};
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const Best64 v{c[i], lk[i], lane * NV + i};
-      if (c[i] && better64(v, b)) b = v;
-    }
-    b = warp_best64(b);
-#pragma unroll
+  for (int r = 0; r <= a.top_k; ++r) {
+    uint64_t bc = 0;
+    uint32_t bl = 0;
+    int at = 0;
+#pragma unroll 1
     for (int i = 0; i < NV; ++i)
-      if (lane * NV + i == b.i) c[i] = 0;
-    if (lane == r) mine = b.i;
+      if (c[i] > bc || (c[i] == bc && lk[i] > bl)) {
+        bc = c[i];
+        bl = lk[i];
+        at = i;
+      }
+    const int w = __ffs(best_lanes(bc, bl)) - 1;
+    const uint64_t top = __shfl_sync(kFull, bc, w);
+    const int id = __shfl_sync(kFull, base + at, w);
+    if (r > 0 && top > kMasked64 && !by_logit && S::near(prev, top)) {
+      float lx, bx, ly, by;
+      expert_inputs(row, a.bias, prev_id, lx, bx);
+      expert_inputs(row, a.bias, id, ly, by);
+      doubt |= !(lx == ly && bx == by);
+    }
+    if (lane == w) c[at] = 0;
+    if (lane == w) lk[at] = 0;
+    if (lane == r) mine = id;
+    prev = top;
+    prev_id = id;
   }
+  *unsure = doubt;
   return mine;
 }
 
+// Lane i < n has candidate id: lane j gets the j-th of them (n <= 32) by the scores in pairs of
+// floats, of a sigmoid router or of one without a bias (softmax scores under a bias need the
+// denominator in pairs too: rank_again).
+template <class TL>
+__device__ __noinline__ int rank_candidates(const TL* row, const RouteArgs& a, int id, int n, bool* unsure) {
+  const int lane = threadIdx.x & 31;
+  float l = -INFINITY, b = 0.f;
+  if (lane < n) expert_inputs(row, a.bias, id, l, b);
+  uint64_t c = 0;
+  if (a.bias == nullptr) {
+    c = (uint64_t)order_key(l) << 32;
+  } else {
+    const FF e = exp_ff({-fabsf(l), 0.f});
+    const FF s = div(l < 0.f ? e : FF{1.f, 0.f}, add({1.f, 0.f}, e));
+    c = l == -INFINITY ? kMasked64 : PairScores::key(b == INFINITY ? FF{b, 0.f} : add(s, {b, 0.f}));
+  }
+  int rank = 0;
+  bool doubt = false;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const uint64_t o = __shfl_sync(kFull, c, j);
+    const float ol = __shfl_sync(kFull, l, j), ob = __shfl_sync(kFull, b, j);
+    const int oid = __shfl_sync(kFull, id, j);
+    const bool same = ol == l && ob == b;  // equal scores: the lower index first
+    rank += same ? oid < id : o > c;
+    doubt |= a.bias != nullptr && !same && lane < n && min(o, c) > kMasked64 && PairScores::near(max(o, c), min(o, c));
+  }
+  *unsure = __any_sync(kFull, doubt);
+  int got = 0;
+  for (int j = 0; j < n; ++j) {
+    const int at = __shfl_sync(kFull, rank, j), v = __shfl_sync(kFull, id, j);
+    if (lane == at) got = v;
+  }
+  return got;
+}
+
 // ------------------------------------------------------------------ forward
-// NV: experts held by a lane (E <= 32 NV).  TL: type of the logits.
+__device__ __forceinline__ void order2(uint32_t& a, uint32_t& b) {
+  const uint32_t x = max(a, b), y = min(a, b);
+  a = x;
+  b = y;
+}
+// Batcher's odd-even merge sort, descending.
+template <int NV>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[NV]) {
+#pragma unroll
+  for (int p = 1; p < NV; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j <= NV - 1 - k; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < NV && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order2(key[i + j], key[i + j + k]);
+}
+
+// NV: experts held by a lane, a power of two.  TL: type of the logits.
 template <int NV, class TL>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     route_grouped_kernel(const RouteArgs a, int32_t* __restrict__ topk_ids, float* __restrict__ topk_weights) {
+  constexpr uint32_t kPlace = NV - 1;             // the key bits that hold NV - 1 - place
+  constexpr uint32_t kNone = kMaskedKey & ~kPlace;  // a masked expert's key without its place
+  constexpr bool kSorted = NV <= 16;              // (longer lists are searched again each round)
   const int t = blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5);
   if (t >= a.T) return;
   const int lane = threadIdx.x & 31;
   const TL* row = static_cast<const TL*>(a.logits) + (size_t)t * a.E;
-  const bool by_logit = a.bias == nullptr;
+  const bool by_logit = a.bias == nullptr, softmax = a.score == MOE_SCORE_SOFTMAX;
+  const int size = a.E / a.n_group, grp = lane / a.lpg, in = (lane % a.lpg) * NV;
+  const int base = grp * size + in;
+  const int cnt = grp < a.n_group ? min(NV, size - in) : 0;  // (may be negative: none)
 
-  uint32_t key[NV];
   float l[NV];
-  load_lane<NV>(row, a.E, lane, l);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) l[i] = clean_logit(l[i]);
-
-  // softmax: the row's maximum and denominator (a bias does not enter them; without renormalising the
-  // weights need them too)
+  load_lane<NV>(row + base, cnt, size, l);
+  uint32_t key[NV];
+  float b[NV];
+  if (!by_logit) load_lane<NV>(a.bias + base, cnt, size, b);
+  // the row's largest logit and the softmax's denominator, where a score is needed
   float m = 0.f, den = 1.f;
-  if (a.score == MOE_SCORE_SOFTMAX && (!by_logit || !a.renorm || a.n_group > 1)) {
+  if (softmax && (!by_logit || !a.renorm || (a.n_group > 1 && a.group_top == 2))) {
     m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (lane * NV + i < a.E) m = fmaxf(m, l[i]);
+    for (int i = 0; i < NV; ++i) m = fmaxf(m, clean_logit(l[i]));
     m = warp_max(m);
     den = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (lane * NV + i < a.E && l[i] > -INFINITY) den += expf(l[i] - m);
+    for (int i = 0; i < NV; ++i) {
+      const float x = clean_logit(l[i]);
+      if (x > -INFINITY) den += __expf(x - m);
+    }
     den = warp_sum(den);
   }
-  auto score32 = [&](float x) {  // s of an unmasked logit
-    return a.score == MOE_SCORE_SIGMOID ? sigmoid32(x) : __fdiv_rn(expf(x - m), den);
+  const float rden = __fdividef(1.0f, den);
+  // A score for ranking alone, by the fast exponential and division (see tol0 below).
+  auto rank_score = [&](float x) {
+    const float e = __expf(softmax ? x - m : -fabsf(x));
+    return softmax ? e * rden : __fdividef(x < 0.f ? e : 1.0f, 1.0f + e);
   };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = lane * NV + i;
-    key[i] = 0;
-    if (e < a.E) {
-      if (by_logit) {
-        key[i] = order_key(l[i]);
-      } else {
-        const float b = __ldg(a.bias + e);
-        const bool gone = l[i] == -INFINITY || b != b || b == -INFINITY;
-        key[i] = gone ? kMaskedKey : order_key(score32(l[i]) + b);
-      }
+    const float x = clean_logit(l[i]);
+    uint32_t k;
+    if (by_logit) {
+      k = order_key(x);
+    } else {
+      const bool gone = x == -INFINITY || b[i] != b[i] || b[i] == -INFINITY;
+      k = gone ? kMaskedKey : order_key(rank_score(x) + b[i]);
     }
+    key[i] = i < cnt ? (k & ~kPlace) | (kPlace - i) : 0u;
   }
-  // Distance below which two fp32 scores may be in the wrong order.  sigmoid: expf is within 1
-  // ulp, the sum and the division round once each, so s is within 2^-22 s (s <= 1) and c =
-  // s + b within 2^-22 + 2^-24 |c|; two of them, doubled once more for margin.  softmax: the
-  // denominator's rounding (up to NV + 5 additions) moves all scores of a row by one common
-  // factor within (NV + 6) 2^-24 <= 2^-18.7.
-  const float tol0 = a.score == MOE_SCORE_SIGMOID ? 0x1p-20f : 0x1p-17f;
+  if (kSorted) sort_keys(key);
+
+  // Distances below which two ranking scores may be in the wrong order.  __expf(-x) is within
+  // (2 + 1.2 x) 2^-23 of its value.  Sigmoid: that moves s by at most 0.65 2^-23, the sum and the
+  // division (2 ulp) by 2.5 2^-23: two scores are within 2^-20.3.  Softmax: a score's own exponential
+  // and division give 2^-21; the denominator moves all scores of a row by one common factor, within
+  // 2^-18.2 (its terms' errors weighed by the terms, whose mean x is at most ln E, and up to 69
+  // additions): 2^-17.6 for two.  Adding the bias rounds by 2^-24 |c| and cutting the places off the
+  // keys by NV 2^-23 |c|.
+  const float tol0 = softmax ? 0x1p-17f : 0x1p-20f;
+  constexpr float kCut = (NV + 2) * 0x1p-23f;
   bool unsure = false;
 
   if (a.n_group > 1) {
-    const int size = a.E / a.n_group;
-    uint32_t gkey = 0;  // lane g: the score of group g
-#pragma unroll 1
-    for (int g = 0; g < a.n_group; ++g) {
-      const int e0 = g * size - lane * NV;  // this lane's experts of the group: i in [e0, e0 + size)
-      uint32_t k1 = 0, k2 = 0;
+    uint32_t top = 0, second = 0;
+    const bool exact = by_logit && a.group_top == 1;  // whole logits: nothing cut off
+    if (exact) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (i < cnt) top = max(top, order_key(clean_logit(l[i])));
+    } else if (kSorted) {
+      top = key[0] & ~kPlace;
+      second = NV > 1 ? key[NV > 1 ? 1 : 0] & ~kPlace : 0u;
+    } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const uint32_t k = (i >= e0 && i < e0 + size) ? key[i] : 0u;
-        k2 = max(k2, min(k, k1));
-        k1 = max(k1, k);
+        const uint32_t k = key[i] & ~kPlace;
+        second = max(second, min(top, k));
+        top = max(top, k);
       }
-      const uint32_t top = __reduce_max_sync(kFull, k1);
-      uint32_t gk = top;
-      if (a.group_top == 2) {
-        const uint32_t have = __ballot_sync(kFull, k1 == top);
-        const bool owner = lane == __ffs(have) - 1;
-        const uint32_t next = __reduce_max_sync(kFull, owner ? k2 : k1);
-        if (top != kMaskedKey) {
-          float s = key_value(top);
-          if (by_logit) s = score32(s);
-          if (next > kMaskedKey) s += by_logit ? score32(key_value(next)) : key_value(next);
-          gk = order_key(s);
-        }
+    }
+    for (int off = 1; off < a.lpg; off <<= 1) {
+      const uint32_t x = __shfl_xor_sync(kFull, top, off), y = __shfl_xor_sync(kFull, second, off);
+      second = max(min(top, x), max(second, y));
+      top = max(top, x);
+    }
+    uint32_t score = top;
+    float err = 0.f;  // how far the group's score may be off
+    if (a.group_top == 2 && top > kNone) {  // (a masked group keeps the masked key)
+      float x = key_value(top), y = second > kNone ? key_value(second) : 0.f;
+      err = kCut * (fabsf(x) + fabsf(y));
+      if (by_logit) {
+        // the cut logits' distance moves a sigmoid by less than 0.3 of its relative size, a softmax
+        // numerator by all of it
+        x = rank_score(x);
+        y = second > kNone ? rank_score(y) : 0.f;
       }
-      if (lane == g) gkey = gk;
+      score = order_key(x + y);
+    } else if (top > kNone) {
+      err = by_logit ? 0.f : kCut * fabsf(key_value(top));
     }
-    uint32_t keep = 0, last = 0, left = 0;
-#pragma unroll 1
-    for (int r = 0; r < a.topk_group; ++r) {
-      last = __reduce_max_sync(kFull, gkey);
-      const int w = __ffs(__ballot_sync(kFull, gkey == last)) - 1;
-      keep |= 1u << w;
-      if (lane == w) gkey = 0;
+    int rank = 0;
+#pragma unroll 4
+    for (int g = 0; g < a.n_group; ++g) {
+      const uint32_t o = __shfl_sync(kFull, score, g * a.lpg);
+      rank += o > score || (o == score && g < grp);
     }
-    left = __reduce_max_sync(kFull, gkey);  // the best group left out (0: none)
-    if (!(by_logit && a.group_top == 1) && left != 0 && last != kMaskedKey && left != kMaskedKey) {
+    const bool keep = rank < a.topk_group && grp < a.n_group;
+    const uint32_t last = __reduce_min_sync(kFull, keep ? score : kFull);
+    const uint32_t left = __reduce_max_sync(kFull, keep || grp >= a.n_group ? 0u : score);  // 0: none left out
+    if (left > kNone && !exact) {
       const float x = key_value(last), y = key_value(left);
-      unsure |= !(x - y > 2 * tol0 + 0x1p-20f * (fabsf(x) + fabsf(y)));
+      const float e = warp_max(err);
+      unsure = !(x - y > 2.f * (tol0 + e) + 0x1p-22f * (fabsf(x) + fabsf(y)));
     }
+    if (!keep) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = lane * NV + i;
-      if (e < a.E && !((keep >> (e / size)) & 1u)) key[i] = 0;
+      for (int i = 0; i < NV; ++i) key[i] = 0;
     }
   }
 
-  // top_k rounds, and one more for the best expert left out
-  uint32_t my_key = 0;
+  // top_k rounds, then one for the best expert left out; where some order is in doubt (near), more
+  // until the rest is surely below the last choice.  Lane r keeps the r-th.
   int my_id = 0;
-  const int rounds = by_logit ? a.top_k : a.top_k + 1;
-  uint32_t prev_key = 0;
-  int prev_id = 0;
+  uint32_t prev_key = 0, last_key = 0;
+  int prev_id = 0, r = 0;
+  bool near = false;
+  auto head = [&]() {
+    if (kSorted) return key[0];
+    uint32_t h = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) h = max(h, key[i]);
+    return h;
+  };
+  uint32_t h = head();
+  // x >= y are two keys: may the experts be in the other order?
+  auto in_doubt = [&](uint32_t kx, uint32_t ky) {
+    if (ky <= kNone) return false;
+    if (by_logit) return sizeof(TL) == 4 && kx == ky;  // (16-bit logits fit the key: equal ones are equal)
+    const float x = key_value(kx), y = key_value(ky);
+    return !(x - y > tol0 + kCut * (fabsf(x) + fabsf(y)));
+  };
 #pragma unroll 1
-  for (int r = 0; r < rounds; ++r) {
-    uint32_t k1 = 0;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (key[i] > k1) {
-        k1 = key[i];
-        at = i;
+  for (;; ++r) {
+    const uint32_t top = __reduce_max_sync(kFull, h & ~kPlace);
+    if (r >= a.top_k) {
+      near |= in_doubt(prev_key, top);
+      if (!near || !in_doubt(last_key, top)) break;
+      if (r == 32) {  // more candidates than lanes
+        unsure = true;
+        break;
       }
-    const uint32_t top = __reduce_max_sync(kFull, k1);
-    const int w = __ffs(__ballot_sync(kFull, k1 == top)) - 1;
-    const int id = w * NV + __shfl_sync(kFull, at, w);
-    if (lane == w)
+    }
+    const int w = __ffs(__ballot_sync(kFull, (h & ~kPlace) == top)) - 1;
+    const int id = __shfl_sync(kFull, base + (int)(kPlace - (h & kPlace)), w);
+    if (lane == w) {
+      if (kSorted) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (i == at) key[i] = 0;
-    if (!by_logit && r > 0 && top > kMaskedKey) {
-      const float x = key_value(prev_key), y = key_value(top);
-      if (!(x - y > tol0 + 0x1p-21f * (fabsf(x) + fabsf(y)))) {
-        // equal logit and bias: equal scores, and the lower index came first
-        float lx, bx, ly, by;
-        expert_inputs(row, a.bias, prev_id, lx, bx);
-        expert_inputs(row, a.bias, id, ly, by);
-        unsure |= !(lx == ly && bx == by);
+        for (int i = 0; i + 1 < NV; ++i) key[i] = key[i + 1];
+        key[NV - 1] = 0;
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (key[i] == h) key[i] = 0;
       }
+      h = head();
+    }
+    if (r > 0 && !near && in_doubt(prev_key, top)) {
+      // equal logit and bias: equal scores, and the lower index came first
+      float lx, bx, ly, by;
+      expert_inputs(row, a.bias, prev_id, lx, bx);
+      expert_inputs(row, a.bias, id, ly, by);
+      near = !(lx == ly && bx == by);
     }
     prev_key = top;
     prev_id = id;
-    if (lane == r && r < a.top_k) {
-      my_key = top;
-      my_id = id;
-    }
+    if (r == a.top_k - 1) last_key = top;
+    if (lane == r) my_id = id;
   }
-  (void)my_key;
-  if (unsure) my_id = rank64<NV, TL>(row, a);
+  if (near && softmax && !by_logit) unsure = true;
+  if (near && !unsure) {
+    // the r candidates, one a lane, ranked by their exact scores
+    my_id = rank_candidates(row, a, my_id, r, &unsure);
+  }
+  if (unsure) {
+    my_id = rank_again<PairScores, NV, TL>(row, a, &unsure);
+    if (unsure) my_id = rank_again<DoubleScores, NV, TL>(row, a, &unsure);
+  }
 
   // weights: lane j has the j-th choice
   float lj = -INFINITY, bj = 0.f;
@@ -362,15 +558,25 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     const float top = warp_max(lj);
     float s = 0.f;
     if (live) {
-      if (a.score == MOE_SCORE_SOFTMAX)
+      if (softmax)
         s = expf(lj - top);
       else
         s = top < 0.f ? __fdiv_rn(expf(lj - top), 1.0f + expf(lj)) : sigmoid32(lj);
     }
     const float sum = warp_sum(s);
     w = sum > 0.f ? __fdiv_rn(s, sum) : 0.f;
+  } else if (softmax) {
+    // the denominator again, by the accurate exponential
+    den = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float x = clean_logit(l[i]);
+      if (x > -INFINITY) den += expf(x - m);
+    }
+    den = warp_sum(den);
+    w = live ? __fdiv_rn(expf(lj - m), den) : 0.f;
   } else {
-    w = live ? score32(lj) : 0.f;
+    w = live ? sigmoid32(lj) : 0.f;
   }
   if (lane < a.top_k) {
     topk_ids[(size_t)t * a.top_k + lane] = my_id;
@@ -427,7 +633,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
   }
   float s[NV], dot = 0.f;
   if (!a.renorm && a.score == MOE_SCORE_SOFTMAX) {
-    load_lane<NV>(row, a.E, lane, s);
+    load_lane<NV>(row + lane * NV, a.E - lane * NV, a.E, s);
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -469,15 +675,22 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
   store_row(dlogits + (size_t)t * a.E, a.E, lane, buf);
 }
 
+// Lanes of a group, and the experts a lane then holds (at most 64: 17 groups of 60 on a lane each).
+int lanes_per_group(int n_group) {
+  int lpg = 32;
+  while (lpg * n_group > 32) lpg /= 2;
+  return lpg;
+}
+
 template <class F>
-cudaError_t for_nv(int E, F f) {
-  const int nv = (E + 31) / 32;
+void for_nv(int nv, F f) {
   if (nv <= 1) return f(std::integral_constant<int, 1>());
   if (nv <= 2) return f(std::integral_constant<int, 2>());
   if (nv <= 4) return f(std::integral_constant<int, 4>());
   if (nv <= 8) return f(std::integral_constant<int, 8>());
   if (nv <= 16) return f(std::integral_constant<int, 16>());
-  return f(std::integral_constant<int, 32>());
+  if (nv <= 32) return f(std::integral_constant<int, 32>());
+  return f(std::integral_constant<int, 64>());
 }
 
 moe_status_t check_route(moe_dtype_t dt, int T, int E, int top_k, const moe_route_config* c) {
@@ -508,11 +721,13 @@ extern "C" moe_status_t moe_route_grouped(const void* logits, moe_dtype_t logits
   if (T == 0) return MOE_OK;
   MOE_CHECK_ARG(logits && topk_ids && topk_weights);
   MOE_CHECK_ARG(aligned16(logits) && aligned16(bias) && aligned16(topk_ids) && aligned16(topk_weights));
-  const RouteArgs a{logits,          bias,           T,              E,               top_k,     cfg->score,
-                    cfg->n_group, cfg->topk_group, cfg->group_top, cfg->renormalize, cfg->scale};
+  RouteArgs a{logits,          bias,           T,              E,               top_k,     cfg->score,
+                    cfg->n_group, cfg->topk_group, cfg->group_top, cfg->renormalize, cfg->scale, 32};
   const dim3 grid((unsigned)((T + kWarpsPerBlock - 1) / kWarpsPerBlock)), block(kWarpsPerBlock * 32);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  for_nv(E, [&](auto nv) {
+  a.lpg = lanes_per_group(cfg->n_group);
+  const int size = E / cfg->n_group;
+  for_nv((size + a.lpg - 1) / a.lpg, [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
     if (logits_dtype == MOE_DT_FP32)
       route_grouped_kernel<NV, float><<<grid, block, 0, s>>>(a, topk_ids, topk_weights);
@@ -520,7 +735,6 @@ extern "C" moe_status_t moe_route_grouped(const void* logits, moe_dtype_t logits
       route_grouped_kernel<NV, __nv_bfloat16><<<grid, block, 0, s>>>(a, topk_ids, topk_weights);
     else
       route_grouped_kernel<NV, __half><<<grid, block, 0, s>>>(a, topk_ids, topk_weights);
-    return cudaSuccess;
   });
   return launch_status();
 }
@@ -534,12 +748,13 @@ extern "C" moe_status_t moe_route_grouped_backward(const float* dweights, const 
   MOE_CHECK_ARG(dweights && logits && topk_ids && dlogits);
   MOE_CHECK_ARG(aligned16(dweights) && aligned16(logits) && aligned16(topk_ids) && aligned16(dlogits));
   const RouteArgs a{logits,          nullptr,        T,              E,               top_k,     cfg->score,
-                    cfg->n_group, cfg->topk_group, cfg->group_top, cfg->renormalize, cfg->scale};
+                    cfg->n_group, cfg->topk_group, cfg->group_top, cfg->renormalize, cfg->scale, 32};
   const dim3 grid((unsigned)((T + kWarpsPerBlock - 1) / kWarpsPerBlock)), block(kWarpsPerBlock * 32);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  for_nv(E, [&](auto nv) {
+  for_nv((E + 31) / 32, [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
-    if (logits_dtype == MOE_DT_FP32)
+    if constexpr (NV > 32) return;  // E <= 1024
+    else if (logits_dtype == MOE_DT_FP32)
       route_grouped_backward_kernel<NV, float>
           <<<grid, block, 0, s>>>(a, dweights, topk_ids, static_cast<float*>(dlogits));
     else if (logits_dtype == MOE_DT_BF16)
@@ -548,7 +763,6 @@ extern "C" moe_status_t moe_route_grouped_backward(const float* dweights, const 
     else
       route_grouped_backward_kernel<NV, __half>
           <<<grid, block, 0, s>>>(a, dweights, topk_ids, static_cast<__half*>(dlogits));
-    return cudaSuccess;
   });
   return launch_status();
 }

@@ -79,41 +79,43 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
     *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
 }
 
-// The NV consecutive elements [lane NV, (lane + 1) NV) of a row of n (0 past its end); by vectors of up to
-// 16 bytes when they tile the row (the row then starts on a vector boundary too).
+// NV consecutive elements at p, of which the first cnt exist (-inf for the rest); by vectors of
+// up to 16 bytes when they tile `period`, the distance that p's offset and cnt are made of.
 template <int NV, class T>
-__device__ __forceinline__ void load_lane(const T* row, int n, int lane, float (&v)[NV]) {
+__device__ __forceinline__ void load_lane(const T* p, int cnt, int period, float (&v)[NV]) {
   constexpr int BYTES = NV * (int)sizeof(T) < 16 ? NV * (int)sizeof(T) : 16;
   constexpr int PER = BYTES / (int)sizeof(T);  // elements of a vector
   if constexpr (BYTES >= 4) {
-    if (n % PER == 0) {
+    if (period % PER == 0) {
 #pragma unroll
       for (int i = 0; i < NV; i += PER) {
-        uint32_t w[BYTES / 4] = {};
-        if (lane * NV + i < n) {
-          const T* p = row + lane * NV + i;
+        if (i < cnt) {
+          uint32_t w[BYTES / 4];
           if constexpr (BYTES == 16) {
-            const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+            const uint4 q = __ldg(reinterpret_cast<const uint4*>(p + i));
             w[0] = q.x;
             w[1] = q.y;
             w[2] = q.z;
             w[3] = q.w;
           } else if constexpr (BYTES == 8) {
-            const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+            const uint2 q = __ldg(reinterpret_cast<const uint2*>(p + i));
             w[0] = q.x;
             w[1] = q.y;
           } else {
-            w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            w[0] = __ldg(reinterpret_cast<const uint32_t*>(p + i));
           }
-        }
 #pragma unroll
-        for (int j = 0; j < BYTES / 4; ++j) Word<T>::get(w[j], v + i + j * Word<T>::N);
+          for (int j = 0; j < BYTES / 4; ++j) Word<T>::get(w[j], v + i + j * Word<T>::N);
+        } else {
+#pragma unroll
+          for (int j = 0; j < PER; ++j) v[i + j] = -INFINITY;
+        }
       }
       return;
     }
   }
 #pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = lane * NV + i < n ? load1(row + lane * NV + i) : 0.f;
+  for (int i = 0; i < NV; ++i) v[i] = i < cnt ? load1(p + i) : -INFINITY;
 }
 
 // A row of n fp32 values in shared memory (16-byte aligned) written by one warp as type T.
