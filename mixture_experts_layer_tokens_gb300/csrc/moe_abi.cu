@@ -31,7 +31,8 @@ extern "C" moe_status_t moe_device_status(int clear) {
   const moe_status_t d = finalize_status(clear);
   const moe_status_t e = route_grouped_status(clear);
   const moe_status_t f = linear_status(clear);
-  for (const moe_status_t st : {a, b, c, d, e, f})
+  const moe_status_t g = finalize_backward_status(clear);
+  for (const moe_status_t st : {a, b, c, d, e, f, g})
     if (st != MOE_OK) return st;
   return MOE_OK;
 }

@@ -5,141 +5,245 @@
 //   dy_j = w_j G,  dw_j = <G, y_j>,  dsum = G,  drms = sum_t dn o r
 //
 // Bound by HBM: a token moves 2 H (4 + 2 top_k) bytes and computes a few operations per
-// element.  A CTA takes whole tokens, G stays in registers between the norm's two sums and the
-// top_k rows, and each element is read once.  drms: every thread owns the same columns for all
-// tokens of its CTA and adds them in shared memory; one row of partial sums per CTA goes to the
+// element.  One CTA per SM takes whole tokens; a producer thread streams the token's rows (dn, o,
+// dres, then the top_k expert rows) by bulk copies into a ring of row slots, so that the next
+// rows are on their way through the two block-wide sums of a token, and G stays in registers
+// between them.  (Rows loaded by the threads themselves, two CTAs a SM: 28 KB in flight a SM and
+// 3.0 TB/s; the ring has about 170 KB.)  drms: every thread owns the same columns for all tokens
+// of its CTA and adds them in shared memory; one row of partial sums per CTA goes to the
 // workspace and a second launch adds the rows in order (a fixed order: the same bits each time).
 #include "moe_vec.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kMaxThreads = 512;
+constexpr int kMaxConsumers = 512;
 constexpr int kMaxK = 32;
+constexpr int kMaxSlots = 16;
+constexpr int kSmemMost = 220 * 1024;
 
 struct FinBwd {
   const __nv_bfloat16 *dout, *dres, *o, *gamma, *y;
   const float* w;
   float eps;
-  int T, H, k;
+  int T, H, k, slots;
   __nv_bfloat16 *dy, *dsum;
   float *dw, *partial;
 };
 
-// NV: 8-element vectors of a row held by a thread.
-template <int NV>
-__global__ void __launch_bounds__(kMaxThreads)
-    finalize_backward_kernel(const FinBwd a) {
-  extern __shared__ __align__(16) float drms_sum[];  // [H] when partial
-  __shared__ float red[2][kMaxThreads / 32];
-  __shared__ float dots[kMaxK][kMaxThreads / 32];
-  const int nvec = a.H / 8, warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(smem_dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
 
+// blockDim.x = consumers + 32; consumers hold NV 8-element vectors of a row each.
+template <int NV>
+__global__ void __launch_bounds__(kMaxConsumers + 32, 1)
+    finalize_backward_kernel(const FinBwd a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kMaxSlots], empty[kMaxSlots];
+  __shared__ float red[2][kMaxConsumers / 32];
+  __shared__ float dots[2][kMaxK][kMaxConsumers / 32];
+  const int nvec = a.H / 8, consumers = blockDim.x - 32, warps = consumers >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t row_bytes = a.H * 2;
+  float* drms_sum = reinterpret_cast<float*>(smem + (size_t)a.slots * row_bytes);  // [H] when partial
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.slots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], warps);
+    }
+    fence_mbar_init();
+  }
   if (a.partial)
     for (int i = threadIdx.x; i < a.H; i += blockDim.x) drms_sum[i] = 0.f;
   __syncthreads();
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    float g[NV][8];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < nvec) load8(a.dout + (size_t)t * a.H + v * 8, g[i]);
+
+  if (warp == warps) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int slot = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      auto push = [&](const __nv_bfloat16* row) {
+        if (!ok || !(ok = mbar_wait(&empty[slot], phase ^ 1))) return;
+        mbar_arrive_expect_tx(&full[slot], row_bytes);
+        bulk_load(smem + (size_t)slot * row_bytes, row, row_bytes, &full[slot]);
+        if (++slot == a.slots) {
+          slot = 0;
+          phase ^= 1;
+        }
+      };
+      for (int t = blockIdx.x; t < a.T && ok; t += gridDim.x) {
+        push(a.dout + (size_t)t * a.H);
+        if (a.gamma) push(a.o + (size_t)t * a.H);
+        if (a.dres) push(a.dres + (size_t)t * a.H);
+        if (a.dw)
+          for (int j = 0; j < a.k; ++j) push(a.y + ((size_t)t * a.k + j) * a.H);
+      }
+      if (!ok)  // wait (bounded) for the copies still in flight before the shared memory goes
+        for (int i = 0; i < a.slots; ++i) mbar_wait(&full[i], i < slot ? phase : phase ^ 1, false, 100000000ull);
     }
-    if (a.gamma) {
-      float o[NV][8], sq = 0.f, gd = 0.f;
+  } else {
+    // ------------------------------------------------------------ consumers
+    // A wait that gives up (after two seconds, recorded) leaves wrong values but every barrier is
+    // still met, so that all threads come to the end.
+    int slot = 0;
+    uint32_t phase = 0;
+    auto take = [&]() {  // the next row, once it is there
+      mbar_wait(&full[slot], phase);
+      __syncwarp();
+      return reinterpret_cast<const __nv_bfloat16*>(smem + (size_t)slot * row_bytes);
+    };
+    auto step = [&]() {
+      if (++slot == a.slots) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+    auto done = [&](int s) {  // this warp has read slot s
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    };
+    int par = 0;
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x, par ^= 1) {
+      float g[NV][8];
+      const int s_dn = slot;
+      const __nv_bfloat16* dn = take();
+      step();
+      if (a.gamma) {
+        const int s_o = slot;
+        const __nv_bfloat16* o = take();
+        step();
+        float sq = 0.f, gd = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (v >= nvec) continue;
-        float gm[8];
-        load8(a.o + (size_t)t * a.H + v * 8, o[i]);
-        load8(a.gamma + v * 8, gm);
+        for (int i = 0; i < NV; ++i) {
+          const int v = threadIdx.x + i * consumers;
+          if (v >= nvec) continue;
+          float d[8], x[8], gm[8];
+          load8(dn + v * 8, d);
+          load8(o + v * 8, x);
+          load_bf16x8(a.gamma + v * 8, gm);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          sq += o[i][e] * o[i][e];
-          gd += g[i][e] * gm[e] * o[i][e];
+          for (int e = 0; e < 8; ++e) {
+            sq += x[e] * x[e];
+            gd += d[e] * gm[e] * x[e];
+          }
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+          sq += __shfl_xor_sync(0xffffffffu, sq, off);
+          gd += __shfl_xor_sync(0xffffffffu, gd, off);
+        }
+        if (lane == 0) {
+          red[0][warp] = sq;
+          red[1][warp] = gd;
+        }
+        named_bar_sync(1, consumers);
+        sq = gd = 0.f;
+        for (int i = 0; i < warps; ++i) {
+          sq += red[0][i];
+          gd += red[1][i];
+        }
+        const float r = __frsqrt_rn(sq / a.H + a.eps);
+        const float c = r * r * (gd / a.H);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int v = threadIdx.x + i * consumers;
+          if (v >= nvec) continue;
+          float d[8], x[8], gm[8];
+          load8(dn + v * 8, d);
+          load8(o + v * 8, x);
+          load_bf16x8(a.gamma + v * 8, gm);
+          if (a.partial) {
+            float4* m = reinterpret_cast<float4*>(drms_sum + v * 8);
+            float4 lo = m[0], hi = m[1];
+            lo.x += d[0] * x[0] * r, lo.y += d[1] * x[1] * r, lo.z += d[2] * x[2] * r, lo.w += d[3] * x[3] * r;
+            hi.x += d[4] * x[4] * r, hi.y += d[5] * x[5] * r, hi.z += d[6] * x[6] * r, hi.w += d[7] * x[7] * r;
+            m[0] = lo;
+            m[1] = hi;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[i][e] = r * (d[e] * gm[e] - x[e] * c);
+        }
+        done(s_o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int v = threadIdx.x + i * consumers;
+          if (v < nvec) load8(dn + v * 8, g[i]);
         }
       }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        sq += __shfl_xor_sync(0xffffffffu, sq, off);
-        gd += __shfl_xor_sync(0xffffffffu, gd, off);
-      }
-      if (lane == 0) {
-        red[0][warp] = sq;
-        red[1][warp] = gd;
-      }
-      __syncthreads();
-      sq = gd = 0.f;
-      for (int i = 0; i < warps; ++i) {
-        sq += red[0][i];
-        gd += red[1][i];
-      }
-      const float r = __frsqrt_rn(sq / a.H + a.eps);
-      const float c = r * r * (gd / a.H);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (v >= nvec) continue;
-        float gm[8];
-        load8(a.gamma + v * 8, gm);
-        if (a.partial) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) drms_sum[v * 8 + e] += g[i][e] * o[i][e] * r;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[i][e] = r * (g[i][e] * gm[e] - o[i][e] * c);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v >= nvec) continue;
+      done(s_dn);
       if (a.dres) {
-        float d[8];
-        load8(a.dres + (size_t)t * a.H + v * 8, d);
+        const int s_d = slot;
+        const __nv_bfloat16* dr = take();
+        step();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[i][e] += d[e];
-      }
-      if (a.dsum) store8(a.dsum + (size_t)t * a.H + v * 8, g[i]);
-    }
-    for (int j = 0; j < a.k; ++j) {
-      const size_t row = ((size_t)t * a.k + j) * a.H;
-      const float w = a.w ? __ldg(a.w + (size_t)t * a.k + j) : 1.f;
-      float dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (v >= nvec) continue;
-        if (a.dw) {
-          float y[8];
-          load8(a.y + row + v * 8, y);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dot += g[i][e] * y[e];
-        }
-        if (a.dy) {
+        for (int i = 0; i < NV; ++i) {
+          const int v = threadIdx.x + i * consumers;
+          if (v >= nvec) continue;
           float d[8];
+          load8(dr + v * 8, d);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] = w * g[i][e];
-          store8(a.dy + row + v * 8, d);
+          for (int e = 0; e < 8; ++e) g[i][e] += d[e];
+        }
+        done(s_d);
+      }
+      if (a.dsum) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int v = threadIdx.x + i * consumers;
+          if (v < nvec) store8(a.dsum + (size_t)t * a.H + v * 8, g[i]);
         }
       }
-      if (a.dw) {
+      for (int j = 0; j < a.k; ++j) {
+        const size_t row = ((size_t)t * a.k + j) * a.H;
+        if (a.dy) {
+          const float w = a.w ? __ldg(a.w + (size_t)t * a.k + j) : 1.f;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-        if (lane == 0) dots[j][warp] = dot;
+          for (int i = 0; i < NV; ++i) {
+            const int v = threadIdx.x + i * consumers;
+            if (v >= nvec) continue;
+            float d[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] = w * g[i][e];
+            store8(a.dy + row + v * 8, d);
+          }
+        }
+        if (a.dw) {
+          const __nv_bfloat16* y = take();
+          float dot = 0.f;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            const int v = threadIdx.x + i * consumers;
+            if (v >= nvec) continue;
+            float x[8];
+            load8(y + v * 8, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot += g[i][e] * x[e];
+          }
+          done(slot);
+          step();
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+          if (lane == 0) dots[par][j][warp] = dot;
+        }
+      }
+      if (a.dw || a.gamma) named_bar_sync(1, consumers);  // (red is free again, dots are complete)
+      if (a.dw && threadIdx.x < a.k) {
+        float s = 0.f;
+        for (int i = 0; i < warps; ++i) s += dots[par][threadIdx.x][i];
+        a.dw[(size_t)t * a.k + threadIdx.x] = s;
       }
     }
-    __syncthreads();
-    if (a.dw && threadIdx.x < a.k) {
-      float s = 0.f;
-      for (int i = 0; i < warps; ++i) s += dots[threadIdx.x][i];
-      a.dw[(size_t)t * a.k + threadIdx.x] = s;
+    if (a.partial) {
+      named_bar_sync(1, consumers);
+      for (int i = threadIdx.x; i < a.H; i += consumers) a.partial[(size_t)blockIdx.x * a.H + i] = drms_sum[i];
     }
-    __syncthreads();
   }
-  if (a.partial)
-    for (int i = threadIdx.x; i < a.H; i += blockDim.x) a.partial[(size_t)blockIdx.x * a.H + i] = drms_sum[i];
 }
 
 // out[h] = sum over p of partial[p][h], p in ascending order within each of 8 interleaved sums.
@@ -160,16 +264,20 @@ __global__ void __launch_bounds__(256) drms_kernel(const float* __restrict__ par
 constexpr int kMaxH = 16384;
 
 // Threads a token and vectors a thread: the fewest vectors (up to 4) that keep a row within
-// kMaxThreads threads.
-void shape(int H, int* threads, int* nv) {
+// kMaxConsumers threads.
+void shape(int H, int* consumers, int* nv) {
   const int nvec = H / 8;
-  *nv = nvec <= 256 ? 1 : nvec <= 512 ? 2 : 4;
-  *threads = ((nvec + *nv - 1) / *nv + 31) / 32 * 32;
+  *nv = 1;
+  while (nvec > *nv * kMaxConsumers) *nv *= 2;
+  *consumers = ((nvec + *nv - 1) / *nv + 31) / 32 * 32;
 }
 
-int grid_ctas(int T) { return (int)((long long)T < 4LL * num_sms() ? T : 4LL * num_sms()); }
+int grid_ctas(int T) { return T < num_sms() ? T : num_sms(); }
 
 }  // namespace
+
+MOE_DEFINE_STATUS_READER(finalize_backward_status)
+
 }  // namespace moe
 
 using namespace moe;
@@ -214,15 +322,16 @@ extern "C" moe_status_t moe_finalize_backward(const void* dout, const void* dres
   a.dsum = static_cast<__nv_bfloat16*>(dsum);
   a.dw = dweights;
   a.partial = drms ? static_cast<float*>(ws) : nullptr;
-  int threads, nv;
-  shape(H, &threads, &nv);
+  int consumers, nv;
+  shape(H, &consumers, &nv);
   const int grid = grid_ctas(T);
-  const size_t smem = drms ? (size_t)H * sizeof(float) : 0;
+  const size_t sums = drms ? (size_t)H * sizeof(float) : 0;
+  a.slots = (int)((kSmemMost - sums) / ((size_t)H * 2));
+  if (a.slots > kMaxSlots) a.slots = kMaxSlots;
+  const size_t smem = sums + (size_t)a.slots * H * 2;
   auto run = [&](auto kern) {
-    if (smem > 40 * 1024 &&
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kMaxH * sizeof(float))) != cudaSuccess)
-      return false;
-    kern<<<grid, threads, smem, s>>>(a);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) != cudaSuccess) return false;
+    kern<<<grid, consumers + 32, smem, s>>>(a);
     return true;
   };
   const bool ok = nv == 1 ? run(finalize_backward_kernel<1>)

@@ -11,7 +11,7 @@
 //
 // Persistent, warp-specialised: warp 0 copies 64-deep K blocks of A and B by TMA into a ring
 // of stages, warp 1 issues the MMAs from one lane into one of two accumulators in tensor
-// memory, warps 2-5 (one per 32 TMEM lanes) take the other accumulator through the epilogue.
+// memory, warps 4-11 (two per 32 TMEM lanes) take the other accumulator through the epilogue.
 // Problems with fewer tiles than SMs split K over the CTAs of a thread-block cluster: each
 // leaves its fp32 partial tile in its own shared memory, and after one cluster barrier every
 // CTA adds its share of the elements over distributed shared memory, in rank order.
@@ -24,21 +24,34 @@ namespace {
 
 constexpr int BM = 128;           // accumulator rows of a CTA = TMEM lanes
 constexpr int BK = 64;            // contraction elements of a stage: one 128-byte swizzle row
-constexpr int kThreads = 192;     // producer, MMA issuer, 4 epilogue warps
-constexpr int kEpiWarps = 4;
-constexpr int kMaxStages = 8;
+constexpr int kThreads = 384;     // three warpgroups: producer and MMA issuer (2 warps idle), 8 epilogue warps
+constexpr int kFirstEpi = 4;
+constexpr int kEpiWarps = 8;
+constexpr int kMaxStages = 16;
 constexpr int kStageBudget = 192 * 1024;
-constexpr int kBufStride = 36;    // floats: 32 columns of a row, padded so that 16-byte accesses hit distinct banks
-constexpr int kBufBytes = kEpiWarps * 32 * kBufStride * 4;
-constexpr int kSmemBytes = 1024 + kStageBudget + kBufBytes + 1024;
+constexpr int kCtrlBytes = 512;
+constexpr int kSmemBytes = 1024 + kStageBudget + kCtrlBytes + kEpiWarps * 32 * 32 * 4;
+constexpr int kPromoteKB = 8;     // K blocks between two roundings of an fp32 output's sums
+// kPromote: the epilogue holds up to 128 sums a thread, so the first warpgroup hands it registers
+constexpr int kLaunchRegs = 168, kLowRegs = 40, kHighRegs = 232;
+static_assert(128 * kLowRegs + 256 * kHighRegs == kThreads * kLaunchRegs, "register split must balance");
+static_assert((2 * kMaxStages + 5) * 8 + 4 <= kCtrlBytes && kSmemBytes <= 232448, "shared memory layout");
 constexpr int kTmemCols = 512;
 constexpr int kAccCols = 256;     // columns between the two accumulators
 
+// 1 / (1 + exp(-x)) by the fast exponential and division: within 2^-21 (the exponential's
+// (2 + 1.2 |x|) 2^-23 is weighed by at most 0.65 / (2 + 1.2 |x|), the division adds 2 ulp), and 0
+// or 1 where exp overflows or vanishes.
+__device__ __forceinline__ float fast_sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+
+// sqrt(2/pi) (z + 0.044715 z^3): (1 + tanh(u)) / 2 is the sigmoid of 2 u
+__device__ __forceinline__ float gelu_u(float z) { return 0.79788456f * z * fmaf(0.044715f * z, z, 1.0f); }
+
 __device__ __forceinline__ float act_fwd(float z, int act) {
   switch (act) {
-    case MOE_LINEAR_SILU: return __fdividef(z, 1.0f + expf(-z));
+    case MOE_LINEAR_SILU: return __fdividef(z, 1.0f + __expf(-z));
     case MOE_LINEAR_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    case MOE_LINEAR_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.79788456f * (z + 0.044715f * z * z * z)));
+    case MOE_LINEAR_GELU_TANH: return __fdividef(z, 1.0f + __expf(-2.0f * gelu_u(z)));
   }
   return z;
 }
@@ -46,14 +59,15 @@ __device__ __forceinline__ float act_fwd(float z, int act) {
 __device__ __forceinline__ float act_grad(float z, int act) {
   switch (act) {
     case MOE_LINEAR_SILU: {
-      const float q = __fdiv_rn(1.0f, 1.0f + expf(-z));
-      return q * (1.0f + z * (1.0f - q));
+      const float q = fast_sigmoid(z);
+      return q * fmaf(z, 1.0f - q, 1.0f);
     }
     case MOE_LINEAR_GELU:
-      return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * expf(-0.5f * z * z);
+      return fmaf(z * 0.39894228f, __expf(-0.5f * z * z), 0.5f * (1.0f + erff(z * 0.70710678f)));
     case MOE_LINEAR_GELU_TANH: {
-      const float t = tanhf(0.79788456f * (z + 0.044715f * z * z * z));
-      return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.79788456f * (1.0f + 0.134145f * z * z);
+      const float q = fast_sigmoid(2.0f * gelu_u(z));
+      // z q (1 - q) 2 u'
+      return fmaf(z * q * (1.0f - q), 1.59576912f * fmaf(0.134145f * z, z, 1.0f), q);
     }
   }
   return 1.0f;
@@ -141,29 +155,53 @@ __device__ __forceinline__ void finish8(const Epilogue& e, int row, int col, flo
 struct Gemm {
   Epilogue e;
   int KB;               // K blocks
-  int splits;           // CTAs (of a cluster) that share a tile's K blocks
+  int splits;           // CTAs (CTA pairs) of a cluster that share a tile's K blocks
   int BN;               // tile columns
   int stages;
-  int a_rows;           // rows of the A box (K-major A)
+  int a_rows;           // rows of the A box (K-major A): with fewer than 128 a stage is smaller and more of
+                        // them fit; the MMA reads what lies behind for the other rows, whose
+                        // accumulators nobody looks at
   int tiles_m, tiles_n;
   uint32_t idesc;
 };
 
-// Shared-memory descriptor of an MN-major operand as TMA boxes of 64 MN elements x 64 K
-// elements write it with 128-byte swizzle: rows of 128 bytes along MN, 8 K rows per 1024-byte
-// atom (stride offset), consecutive 64-element MN groups 8 KB apart (leading offset).
-__device__ __forceinline__ uint64_t mn_desc(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_addr & 0x3FFFF) >> 4);
-  d |= (uint64_t)(8192 >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// Shared-memory matrix descriptors of 128-byte-swizzled operands (see sw128_desc): 8-row atoms of
+// 1024 bytes (stride offset) along M/N for a K-major operand, along K for an MN-major one, which
+// lies as TMA boxes of 64 MN elements x 64 K elements write it, so that consecutive 64-element MN
+// groups are 8 KB apart (leading offset; unused by K-major).  The upper word is a constant and an
+// offset in shared memory stays below 2^18, so steps are added to the lower word alone.
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;  // stride offset, version, 128-byte swizzle
+template <bool kMN>
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr) {
+  return (smem_addr & 0x3FFFF) >> 4 | (kMN ? 8192u >> 4 : 1u) << 16;  // (in a cluster the upper bits hold the rank)
 }
+__device__ __forceinline__ uint64_t desc(uint32_t lo) { return (uint64_t)kDescHi << 32 | lo; }
 
+// mbar_wait that looks at the clock only after a while: reading the global timer costs several
+// hundred clocks, and in short K loops most waits miss their first test.  For one thread.
+__device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity);
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+// One thread of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(one));
+  return one != 0;
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -187,6 +225,80 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// The forms for a pair of CTAs that share an MMA (cta_group::2), beside the plain ones.
+template <int CG>
+__device__ __forceinline__ void tma_load(void* smem_dst, const CUtensorMap* map, int x, int y, uint32_t bar,
+                                         uint64_t policy) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CG == 1)
+    mma_bf16(d_tmem, adesc, bdesc, idesc, accumulate);
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on `bar` (CG 2: at its place in both CTAs of the pair, ranks in mask) when this
+// thread's MMAs so far complete.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar, uint16_t mask) {
+  if constexpr (CG == 1)
+    tc_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(mask)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void tmem_take(uint32_t* slot) {
+  if constexpr (CG == 1) {
+    tmem_alloc(slot, kTmemCols);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_release(uint32_t taddr) {
+  if constexpr (CG == 1)
+    tmem_dealloc(taddr, kTmemCols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(kTmemCols) : "memory");
+}
+
+// 32 lanes x 16 consecutive fp32 columns from tensor memory.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 
 // The tile of a unit: blocks of kRaster tile rows run through all tile columns, so that the
 // CTAs that work at the same time share A rows and B rows in L2.
@@ -198,8 +310,84 @@ __device__ __forceinline__ void tile_of(int u, int tiles_m, int tiles_n, int& m,
   n = in / rows;
 }
 
+// 32 columns x 32 rows of fp32 sums in a warp's shared buffer; 16-byte pieces are placed by
+// their index xor the row's low bits, which keeps both the row-per-lane writes and the
+// 4-lanes-per-row reads free of bank conflicts.
+__device__ __forceinline__ float* buf_at(float* buf, int row, int piece) { return buf + row * 32 + ((piece ^ (row & 7)) << 2); }
+
+// The epilogue of one 32-column chunk whose sums lane r holds for row row0 + r.
+__device__ __forceinline__ void finish_chunk(const Epilogue& e, float* buf, const float* v, int row0, int col0, int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<float4*>(buf_at(buf, lane, i)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  __syncwarp();
+  if (e.Q % 8 == 0) {
+    // 4 lanes to the 32 columns of a row: 64-byte pieces (of 16-bit outputs) of 8 rows at a time
+    const int col = col0 + (lane & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2);
+      if (row0 + r < e.P && col < e.Q) {
+        const float4 lo = *reinterpret_cast<const float4*>(buf_at(buf, r, (lane & 3) * 2));
+        const float4 hi = *reinterpret_cast<const float4*>(buf_at(buf, r, (lane & 3) * 2 + 1));
+        float z[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        finish8(e, row0 + r, col, z);
+      }
+    }
+  } else {
+    for (int r = 0; r < 32 && row0 + r < e.P; ++r)
+      if (col0 + lane < e.Q) finish1(e, row0 + r, col0 + lane, buf_at(buf, r, lane >> 2)[lane & 3]);
+  }
+  __syncwarp();
+}
+
+// The share of CTA (pair) `split` of a split tile: its elements summed over the S partial tiles,
+// in rank order, through the epilogue.  Called by the epilogue warps.
+template <int S, int CG>
+__device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int unit, int split, int half) {
+  int tm, tn;
+  tile_of(unit, p.tiles_m, p.tiles_n, tm, tn);
+  const int row0 = (tm * CG + half) * BM;
+  const int rows = max(0, min(BM, p.e.P - row0)), cols = min(p.BN, p.e.Q - tn * p.BN);
+  const int groups = (cols + 7) / 8, items = rows * groups;
+  const uint32_t base = smem_u32(smem);
+  const int i1 = (int)((long long)items * (split + 1) / S);
+  if (status_failed()) return;
+  for (int i = (int)((long long)items * split / S) + threadIdx.x - kFirstEpi * 32; i < i1; i += kEpiWarps * 32) {
+    const int r = i / groups, c = (i - r * groups) * 8;
+    const uint32_t at = base + (uint32_t)((r * (p.BN + 4) + c) * 4);
+    float4 lo[S], hi[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const uint32_t src = map_to_rank(at, s * CG + half);
+      lo[s] = ld_cluster(src);
+      hi[s] = ld_cluster(src + 16);
+    }
+    float z[8] = {};
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      z[0] += lo[s].x, z[1] += lo[s].y, z[2] += lo[s].z, z[3] += lo[s].w;
+      z[4] += hi[s].x, z[5] += hi[s].y, z[6] += hi[s].z, z[7] += hi[s].w;
+    }
+    const int row = row0 + r, col = tn * p.BN + c;
+    if (p.e.Q % 8 == 0) {
+      finish8(p.e, row, col, z);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (col + j < p.e.Q) finish1(p.e, row, col + j, z[j]);
+    }
+  }
+}
+
 // kAMN / kBMN: the operand is MN-major (its contraction dimension is the row of its tensor).
-template <bool kAMN, bool kBMN>
+// CG: CTAs that share an MMA.  2: a tile has 256 rows, each CTA of the pair copies its 128 rows
+//   of A and half of the B rows and holds its rows' accumulators; the even CTA issues the MMAs.
+// kPromote: fp32 outputs.  The tensor core adds to its fp32 accumulator by truncation, which
+//   over K = 7168 left outputs 8e-6 off (2-norm); so every kPromoteKB K blocks the accumulator
+//   is added, with rounding, to fp32 sums in the epilogue's registers, and the next block starts
+//   from zero in the other accumulator.
+template <bool kAMN, bool kBMN, int CG, bool kPromote>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ Gemm p) {
@@ -212,12 +400,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* tempty = tfull + 2;          // [2] accumulator read
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  float* bufs = reinterpret_cast<float*>(ctrl + 1024);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* bufs = reinterpret_cast<float*>(ctrl + kCtrlBytes);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform to the compiler)
   const int stages = p.stages;
+  const int bn_cta = p.BN / CG;  // B rows this CTA copies
   const uint32_t a_bytes = kAMN ? 128 * BK * 2 : p.a_rows * 128;
-  const uint32_t b_bytes = p.BN * 128;
-  const int stage_bytes = 128 * 128 + p.BN * 128;
+  const uint32_t b_bytes = bn_cta * 128;
+  const int a_stage = kAMN ? 128 * 128 : p.a_rows * 128;
+  const int stage_bytes = a_stage + bn_cta * 128;
+  const int splits = p.splits;
+  const int rank = (CG > 1 || splits > 1) ? (int)cluster_rank() : 0;
+  const int half = CG > 1 ? rank & 1 : 0;  // this CTA within its pair
+  const int split = rank / CG;
+  const uint32_t leader = rank - half;
+  const uint16_t pair_mask = (uint16_t)(3u << leader);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -226,217 +422,231 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], kEpiWarps);
+      mbar_init(&tempty[a], kEpiWarps * CG);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
     prefetch_tensormap(&tmA);
     prefetch_tensormap(&tmB);
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
-  }
+  if (warp == 1) tmem_take<CG>(tmem_slot);
   tc_fence_before();
   __syncthreads();
+  if (CG > 1) cluster_sync();  // the pair's barriers are set up
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int splits = p.splits;
-  const int rank = splits > 1 ? (int)cluster_rank() : 0;
-  const int kb0 = (int)((long long)p.KB * rank / splits), kb1 = (int)((long long)p.KB * (rank + 1) / splits);
+  const int kb0 = (int)((long long)p.KB * split / splits), kb1 = (int)((long long)p.KB * (split + 1) / splits);
   const int units = p.tiles_m * p.tiles_n;
-  const int first = splits > 1 ? blockIdx.x / splits : blockIdx.x;
-  const int step = splits > 1 ? units : gridDim.x;  // a split tile is its cluster's only work
+  const int first = blockIdx.x / (splits * CG);
+  const int step = splits > 1 ? units : gridDim.x / CG;  // a split tile is its cluster's only work
+  const int chunk = kPromote ? kPromoteKB : kb1 - kb0;   // K blocks added up in the tensor memory
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
-    const uint64_t pol = policy_evict_normal();
+  if (warp < kFirstEpi) {
+    if (kPromote) setmaxnreg_dec<kLowRegs>();
+    // The producer's and the MMA issuer's K loops run in one thread chosen by elect.sync, what
+    // they need computed outside by the whole warp: with the loop in the warp and its body under
+    // `lane == 0` a K block took 640 clocks however narrow the tile (votes each turn, and every
+    // operand that copies and MMAs want in uniform registers moved there anew), like this 300.
     int stage = 0;
     uint32_t phase = 0;
-    long long fills = 0;
-    bool ok = true;
-    for (int u = first; ok && u < units; u += step) {
-      int tm, tn;
-      tile_of(u, p.tiles_m, p.tiles_n, tm, tn);
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!(ok = warp_wait(&empty[stage], phase ^ 1))) break;
-        if (lane == 0) {
-          uint8_t* sA = smem + stage * stage_bytes;
-          uint8_t* sB = sA + 128 * 128;
-          mbar_arrive_expect_tx(&full[stage], a_bytes + b_bytes);
-          if (kAMN) {
-            tma_load_2d(sA, &tmA, tm * BM, kb * BK, &full[stage], pol);
-            tma_load_2d(sA + 8192, &tmA, tm * BM + 64, kb * BK, &full[stage], pol);
-          } else {
-            tma_load_2d(sA, &tmA, kb * BK, tm * BM, &full[stage], pol);
+    bool failed = false;
+    auto advance = [&](int n) {  // n stages on
+      stage += n;
+      phase ^= (uint32_t)(stage / stages) & 1;
+      stage %= stages;
+    };
+    if (warp == 0) {
+      // ---------------------------------------------------------- TMA producer
+      const uint64_t pol = policy_evict_normal();
+      const uint32_t full0 = CG > 1 ? map_to_rank(smem_u32(full), leader) : smem_u32(full);  // (both CTAs' copies
+      for (int u = first; u < units; u += step) {                                           // complete there)
+        int tm, tn;
+        tile_of(u, p.tiles_m, p.tiles_n, tm, tn);
+        const int arow = (tm * CG + half) * BM, brow = tn * p.BN + half * bn_cta;
+        if (elect_one()) {
+          int st = stage;
+          uint32_t ph = phase;
+          for (int kb = kb0; kb < kb1; ++kb) {
+            if (!lane_wait(&empty[st], ph ^ 1)) {
+              failed = true;
+              break;
+            }
+            uint8_t* sA = smem + st * stage_bytes;
+            uint8_t* sB = sA + a_stage;
+            const uint32_t bar = full0 + st * 8;
+            if (half == 0) mbar_arrive_expect_tx(&full[st], CG * (a_bytes + b_bytes));
+            if (kAMN) {
+              tma_load<CG>(sA, &tmA, arow, kb * BK, bar, pol);
+              tma_load<CG>(sA + 8192, &tmA, arow + 64, kb * BK, bar, pol);
+            } else {
+              tma_load<CG>(sA, &tmA, kb * BK, arow, bar, pol);
+            }
+            if (kBMN) {
+              for (int g = 0; g < bn_cta / 64; ++g)
+                tma_load<CG>(sB + g * 8192, &tmB, brow + g * 64, kb * BK, bar, pol);
+            } else {
+              tma_load<CG>(sB, &tmB, kb * BK, brow, bar, pol);
+            }
+            if (++st == stages) {
+              st = 0;
+              ph ^= 1;
+            }
           }
-          if (kBMN) {
-            for (int g = 0; g < p.BN / 64; ++g)
-              tma_load_2d(sB + g * 8192, &tmB, tn * p.BN + g * 64, kb * BK, &full[stage], pol);
-          } else {
-            tma_load_2d(sB, &tmB, kb * BK, tn * p.BN, &full[stage], pol);
-          }
+          if (failed && half == 0)
+            // wait (bounded) for the copies still in flight, of this unit and of the last: each
+            // stage's phase that the ring was in
+            for (int i = 0; i < stages; ++i)
+              mbar_wait(&full[i], i < st ? ph : ph ^ 1, false, 100000000ull);
         }
         __syncwarp();
-        ++fills;
-        if (++stage == stages) {
-          stage = 0;
-          phase ^= 1;
+        if (__any_sync(0xffffffffu, failed)) break;
+        advance(kb1 - kb0);
+      }
+    } else if (warp == 1 && half == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      const uint32_t a0 = smem_u32(smem), b0 = a0 + a_stage;
+      const uint32_t ad0 = desc_lo<kAMN>(a0), bd0 = desc_lo<kBMN>(b0);
+      constexpr uint32_t kStepA = (kAMN ? 2048 : 32) >> 4, kStepB = (kBMN ? 2048 : 32) >> 4;  // 16 K elements on
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      for (int u = first; u < units && !failed; u += step) {
+        for (int kc = kb0; kc < kb1; kc += chunk) {
+          const uint32_t d = tmem + acc * kAccCols;
+          const int ke = min(kb1, kc + chunk);
+          if (elect_one()) {
+            int st = stage;
+            uint32_t ph = phase;
+            failed = !lane_wait(&tempty[acc], acc_phase ^ 1);
+            tc_fence_after();
+            for (int kb = kc; kb < ke && !failed; ++kb) {
+              if (!lane_wait(&full[st], ph)) {
+                failed = true;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t at = (uint32_t)(st * stage_bytes) >> 4;
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk)
+                mma<CG>(d, desc(ad0 + at + kk * kStepA), desc(bd0 + at + kk * kStepB), p.idesc, kb > kc || kk > 0);
+              commit<CG>(&empty[st], pair_mask);
+              if (++st == stages) {
+                st = 0;
+                ph ^= 1;
+              }
+            }
+            if (!failed) {
+              commit<CG>(&tfull[acc], pair_mask);
+            } else {
+              // a wait gave up: let the MMAs issued so far finish (bounded) before the tensor memory goes
+              commit<CG>(drain, pair_mask);
+              mbar_wait(drain, 0, false, 100000000ull);
+            }
+          }
+          __syncwarp();
+          if ((failed = __any_sync(0xffffffffu, failed))) break;
+          advance(ke - kc);
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1;
         }
       }
-    }
-    if (status_failed() && lane == 0) {
-      // wait (bounded) for the copies still in flight: the last fill of each stage
-      for (long long i = fills - 1; i >= 0 && i >= fills - stages; --i)
-        mbar_wait(&full[i % stages], (uint32_t)((i / stages) & 1), false, 100000000ull);
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    int stage = 0, acc = 0;
-    uint32_t phase = 0, acc_phase = 0;
-    bool ok = true;
-    for (int u = first; ok && u < units; u += step) {
-      if (!(ok = warp_wait(&tempty[acc], acc_phase ^ 1))) break;
-      tc_fence_after();
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!(ok = warp_wait(&full[stage], phase))) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t a0 = smem_u32(smem + stage * stage_bytes), b0 = a0 + 128 * 128;
-          const uint32_t d = tmem + acc * kAccCols;
-#pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = kAMN ? mn_desc(a0 + kk * 2048) : sw128_desc(a0 + kk * 32);
-            const uint64_t bd = kBMN ? mn_desc(b0 + kk * 2048) : sw128_desc(b0 + kk * 32);
-            mma_bf16(d, ad, bd, p.idesc, kb > kb0 || kk > 0);
-          }
-          tc_commit(&empty[stage]);
-        }
-        __syncwarp();
-        if (++stage == stages) {
-          stage = 0;
-          phase ^= 1;
-        }
-      }
-      if (ok) {
-        if (lane == 0) tc_commit(&tfull[acc]);
-        __syncwarp();
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1;
-      }
-    }
-    if (!ok) {
-      // a wait gave up: let the MMAs issued so far finish (bounded) before the tensor memory goes
-      if (lane == 0) {
-        tc_commit(drain);
-        mbar_wait(drain, 0, false, 100000000ull);
-      }
-      __syncwarp();
-    }
+    if (splits > 1) cluster_sync();  // (the partial tiles are in shared memory)
   } else {
     // ------------------------------------------------------------ epilogue
-    const int quarter = warp & 3;  // TMEM lanes this warp may access
-    const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-    float* buf = bufs + (warp - 2) * 32 * kBufStride;
+    if (kPromote) setmaxnreg_inc<kHighRegs>();
+    const int quarter = warp & 3;              // TMEM lanes this warp may access
+    const int side = (warp - kFirstEpi) >> 2;  // column half
+    const int ncol = p.BN / 2;
+    float* buf = bufs + (warp - kFirstEpi) * 1024;
+    const uint32_t tb = tmem + ((uint32_t)(quarter * 32) << 16) + side * ncol;
+    const uint32_t freed = CG > 1 ? map_to_rank(smem_u32(tempty), leader) : 0;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int u = first; u < units; u += step) {
-      int tm, tn;
-      tile_of(u, p.tiles_m, p.tiles_n, tm, tn);
-      if (!warp_wait(&tfull[acc], acc_phase)) break;
-      tc_fence_after();
-      const uint32_t tb = tmem + lane_addr + acc * kAccCols;
-      const int row0 = tm * BM + quarter * 32, col0 = tn * p.BN;
-      const int cols = min(p.BN, p.e.Q - col0);
-      if (splits > 1) {
-        // the whole partial tile into this CTA's stages: every copy has landed and every MMA
-        // has read it
-        float* part = reinterpret_cast<float*>(smem) + (quarter * 32 + lane) * (p.BN + 4);
-        if (row0 < p.e.P)
-          for (int c = 0; c < cols; c += 32) {
-            float v[32];
-            tmem_ld32(tb + c, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(part + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-          }
-      } else {
-        if (row0 < p.e.P)
-          for (int c = 0; c < cols; c += 32) {
-            float v[32];
-            tmem_ld32(tb + c, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(buf + lane * kBufStride + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            __syncwarp();
-            if (p.e.Q % 8 == 0) {
-              // 4 lanes to the 32 columns of a row: 64-byte pieces of 8 rows at a time
-              const int col = col0 + c + (lane & 3) * 8;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int r = i * 8 + (lane >> 2);
-                if (row0 + r < p.e.P && col < p.e.Q) {
-                  const float4 lo = *reinterpret_cast<const float4*>(buf + r * kBufStride + (lane & 3) * 8);
-                  const float4 hi = *reinterpret_cast<const float4*>(buf + r * kBufStride + (lane & 3) * 8 + 4);
-                  float z[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                  finish8(p.e, row0 + r, col, z);
-                }
-              }
-            } else {
-              for (int r = 0; r < 32 && row0 + r < p.e.P; ++r)
-                if (col0 + c + lane < p.e.Q) finish1(p.e, row0 + r, col0 + c + lane, buf[r * kBufStride + lane]);
-            }
-            __syncwarp();
-          }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[acc]);
+    auto release = [&]() {  // this warp is done with the accumulator
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG > 1)
+          mbar_arrive_cluster(freed + acc * 8);
+        else
+          mbar_arrive(&tempty[acc]);
       }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
+    };
+    bool ok = true;
+    for (int u = first; ok && u < units; u += step) {
+      int tm, tn;
+      tile_of(u, p.tiles_m, p.tiles_n, tm, tn);
+      const int row0 = (tm * CG + half) * BM + quarter * 32, col0 = tn * p.BN + side * ncol;
+      const int cols = row0 < p.e.P ? min(ncol, p.e.Q - col0) : 0;
+      // split: the partial tile goes to this CTA's stages (every copy has landed and every MMA has
+      // read it when the accumulator is complete)
+      float* part = reinterpret_cast<float*>(smem) + (quarter * 32 + lane) * (p.BN + 4) + side * ncol;
+      auto take = [&](const float* v, int c) {
+        if (splits > 1) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(part + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else {
+          finish_chunk(p.e, buf, v, row0, col0 + c, lane);
+        }
+      };
+      if constexpr (kPromote) {
+        float sums[128] = {};
+        for (int kc = kb0; kc < kb1; kc += chunk) {
+          if (!(ok = __all_sync(0xffffffffu, lane_wait(&tfull[acc], acc_phase)))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 128; c += 32)
+            if (c < cols) {
+#pragma unroll
+              for (int h = 0; h < 32; h += 16) {
+                float v[16];
+                tmem_ld16(tb + acc * kAccCols + c + h, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sums[c + h + i] += v[i];
+              }
+            }
+          release();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < 128; c += 32)
+          if (c < cols) take(sums + c, c);
+      } else {
+        if (!(ok = warp_wait(&tfull[acc], acc_phase))) break;
+        tc_fence_after();
+        for (int c = 0; c < cols; c += 32) {
+          float v[32];
+          tmem_ld32(tb + acc * kAccCols + c, v);
+          tmem_ld_wait();
+          take(v, c);
+        }
+        release();
+      }
+    }
+    if (splits > 1) {
+      __syncwarp();
+      cluster_sync();  // every CTA's partial tile is in its shared memory
+      if (splits == 2)
+        join_splits<2, CG>(p, smem, first, split, half);
+      else if (splits == 4)
+        join_splits<4, CG>(p, smem, first, split, half);
+      else
+        join_splits<8, CG>(p, smem, first, split, half);
     }
   }
 
-  if (splits > 1) {
-    __syncwarp();
-    cluster_sync();  // every CTA's partial tile is in its shared memory
-    int tm, tn;
-    tile_of(first, p.tiles_m, p.tiles_n, tm, tn);
-    const int rows = min(BM, p.e.P - tm * BM), cols = min(p.BN, p.e.Q - tn * p.BN);
-    const int groups = (cols + 7) / 8, items = rows * groups;
-    const uint32_t base = smem_u32(smem);
-    const int i1 = (int)((long long)items * (rank + 1) / splits);
-    if (!status_failed())
-      for (int i = (int)((long long)items * rank / splits) + threadIdx.x; i < i1; i += kThreads) {
-        const int r = i / groups, c = (i - r * groups) * 8;
-        const uint32_t at = base + (uint32_t)((r * (p.BN + 4) + c) * 4);
-        float z[8] = {};
-        for (int s = 0; s < splits; ++s) {
-          const uint32_t src = map_to_rank(at, s);
-          const float4 lo = ld_cluster(src), hi = ld_cluster(src + 16);
-          z[0] += lo.x, z[1] += lo.y, z[2] += lo.z, z[3] += lo.w;
-          z[4] += hi.x, z[5] += hi.y, z[6] += hi.z, z[7] += hi.w;
-        }
-        const int row = tm * BM + r, col = tn * p.BN + c;
-        if (p.e.Q % 8 == 0) {
-          finish8(p.e, row, col, z);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (col + j < p.e.Q) finish1(p.e, row, col + j, z[j]);
-        }
-      }
-    __syncwarp();
-    cluster_sync();  // no CTA leaves while another reads its shared memory
-  }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (CG > 1 || splits > 1) cluster_sync();  // no CTA leaves while another uses its memory or barriers
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 1) tmem_release<CG>(tmem);
 }
 
 // ------------------------------------------------------------------ a few rows
@@ -500,6 +710,7 @@ __global__ void __launch_bounds__(256)
   const int r0 = blockIdx.y * rows, r1 = min(M, r0 + rows);
   float sum[V] = {};
   if (col < N)
+#pragma unroll 2
     for (int r = r0 + ry; r < r1; r += 8) {
       const size_t at = (size_t)r * N + col;
       float d[V];
@@ -587,9 +798,9 @@ struct Operand {
 
 int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-template <bool kAMN, bool kBMN>
+template <bool kAMN, bool kBMN, int CG, bool kPromote>
 cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g, int grid, cudaStream_t s) {
-  auto kern = linear_gemm_kernel<kAMN, kBMN>;
+  auto kern = linear_gemm_kernel<kAMN, kBMN, CG, kPromote>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
@@ -599,7 +810,7 @@ cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = g.splits;
+  attr[0].val.clusterDim.x = g.splits * CG;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -607,36 +818,72 @@ cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm
   return cudaLaunchKernelEx(&cfg, kern, ma, mb, g);
 }
 
+template <bool kAMN, bool kBMN, bool kPromote>
+cudaError_t launch_gemm(int cg, const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g, int grid, cudaStream_t s) {
+  return cg == 2 ? launch_gemm<kAMN, kBMN, 2, kPromote>(ma, mb, g, grid, s)
+                 : launch_gemm<kAMN, kBMN, 1, kPromote>(ma, mb, g, grid, s);
+}
+
+// How a product is cut: CTAs per MMA, tile columns, CTAs (pairs) that share a tile's K.
+struct Plan {
+  int cg, bn, splits;
+};
+
+Plan plan_gemm(long long P, long long Q, int KB) {
+  const int nsm = num_sms();
+  Plan best{1, 64, 1};
+  double best_cost = 1e30;
+  for (int cg = 1; cg <= 2; ++cg)
+    for (int bn = 64; bn <= 256; bn *= 2) {
+      if (cg == 2 && (P <= 128 || bn < 128)) continue;
+      const long long tiles = (long long)cdiv(P, BM * cg) * cdiv(Q, bn);
+      for (int s = 1; s * cg <= 8; s *= 2) {
+        if (s > 1 && (KB < 4 * s || tiles * s * cg > nsm)) break;
+        // clocks of one K block (MMA rate; copies into shared memory at about 56 bytes a clock)
+        const double mma = 2.0 * bn, copy = (128 + bn / cg) * 128 / 56.0;
+        const double kb = (double)cdiv(KB, s) * (mma > copy ? mma : copy);
+        const double waves = cdiv(tiles * s * cg, nsm / cg * cg);
+        const double tail = 2500 + 12.0 * bn + (s > 1 ? 1500 : 0);
+        const double cost = waves * kb + tail;
+        if (cost < best_cost) {
+          best_cost = cost;
+          best = {cg, bn, s};
+        }
+      }
+    }
+  return best;
+}
+
 // D [P, Q] = A . B^T over a contraction of C.
 moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue& e, cudaStream_t s) {
   Gemm g;
   g.e = e;
   g.KB = cdiv(C, BK);
-  const int nsm = num_sms();
-  g.tiles_m = cdiv(e.P, BM);
-  int bn = 256;
-  while (bn > 64 && (bn / 2 >= e.Q || g.tiles_m * cdiv(e.Q, bn) * 2 <= nsm)) bn /= 2;
-  g.BN = bn;
-  g.tiles_n = cdiv(e.Q, bn);
+  const bool promote = e.out32 && g.KB > kPromoteKB;  // (the gradients' outputs have 16 bits)
+  const Plan p = plan_gemm(e.P, e.Q, g.KB);
+  g.tiles_m = cdiv(e.P, BM * p.cg);
+  g.tiles_n = cdiv(e.Q, p.bn);
+  g.BN = p.bn;
+  g.splits = p.splits;
   const long long units = (long long)g.tiles_m * g.tiles_n;
-  if (units > 2147483647LL / 8) return MOE_ERR_UNSUPPORTED;
-  int S = 1;
-  while (S < 8 && units * S * 2 <= nsm && g.KB / (2 * S) >= 4) S *= 2;
-  g.splits = S;
-  g.stages = kStageBudget / (128 * 128 + bn * 128);
+  if (units > 2147483647LL / 16) return MOE_ERR_UNSUPPORTED;
+  g.a_rows = A.mn || e.P >= BM ? BM : (e.P + 7) / 8 * 8;
+  g.stages = kStageBudget / ((g.a_rows + p.bn / p.cg) * 128);
   if (g.stages > kMaxStages) g.stages = kMaxStages;
-  g.a_rows = e.P >= BM ? BM : (e.P + 7) / 8 * 8;
-  g.idesc = make_idesc(e.fp16 ? 0 : 1, BM, bn) | (A.mn ? 1u << 15 : 0) | (B.mn ? 1u << 16 : 0);
+  g.idesc = make_idesc(e.fp16 ? 0 : 1, BM * p.cg, p.bn) | (A.mn ? 1u << 15 : 0) | (B.mn ? 1u << 16 : 0);
   CUtensorMap ma, mb;
   const bool ok = (A.mn ? make_map(&ma, A.base, e.fp16, e.P, C, A.ld, BK)
                         : make_map(&ma, A.base, e.fp16, C, e.P, A.ld, g.a_rows)) &&
                   (B.mn ? make_map(&mb, B.base, e.fp16, e.Q, C, B.ld, BK)
-                        : make_map(&mb, B.base, e.fp16, C, e.Q, B.ld, bn));
+                        : make_map(&mb, B.base, e.fp16, C, e.Q, B.ld, p.bn / p.cg));
   if (!ok) return MOE_ERR_CUDA;
-  const int grid = S > 1 ? (int)units * S : (int)(units < nsm ? units : nsm);
-  const cudaError_t err = A.mn ? launch_gemm<true, true>(ma, mb, g, grid, s)
-                          : B.mn ? launch_gemm<false, true>(ma, mb, g, grid, s)
-                                 : launch_gemm<false, false>(ma, mb, g, grid, s);
+  const long long ctas = units * p.splits * p.cg;
+  const int most = num_sms() / p.cg * p.cg;
+  const int grid = (int)(p.splits > 1 || ctas < most ? ctas : most);
+  const cudaError_t err = A.mn      ? launch_gemm<true, true, false>(p.cg, ma, mb, g, grid, s)
+                          : B.mn    ? launch_gemm<false, true, false>(p.cg, ma, mb, g, grid, s)
+                          : promote ? launch_gemm<false, false, true>(p.cg, ma, mb, g, grid, s)
+                                    : launch_gemm<false, false, false>(p.cg, ma, mb, g, grid, s);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

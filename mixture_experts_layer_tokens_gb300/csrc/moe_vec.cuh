@@ -11,6 +11,7 @@ namespace moe {
 
 moe_status_t route_grouped_status(int clear);
 moe_status_t linear_status(int clear);
+moe_status_t finalize_backward_status(int clear);
 
 __device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
