@@ -39,19 +39,30 @@ static_assert((2 * kMaxStages + 5) * 8 + 4 <= kCtrlBytes && kSmemBytes <= 232448
 constexpr int kTmemCols = 512;
 constexpr int kAccCols = 256;     // columns between the two accumulators
 
-// 1 / (1 + exp(-x)) by the fast exponential and division: within 2^-21 (the exponential's
-// (2 + 1.2 |x|) 2^-23 is weighed by at most 0.65 / (2 + 1.2 |x|), the division adds 2 ulp), and 0
-// or 1 where exp overflows or vanishes.
-__device__ __forceinline__ float fast_sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// exp(x) and 1 / x by the special-function unit: within (2 + 1.2 |x|) 2^-23 (the product with
+// log2 e rounds) and 1 ulp; results below 2^-126 are 0.
+__device__ __forceinline__ float fast_exp(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+  return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 1 / (1 + exp(-x)) within 2^-21 (the exponential's error is weighed by at most 0.65 / (2 + 1.2 |x|)),
+// and 0 or 1 where exp overflows or vanishes.
+__device__ __forceinline__ float fast_sigmoid(float x) { return fast_rcp(1.0f + fast_exp(-x)); }
 
 // sqrt(2/pi) (z + 0.044715 z^3): (1 + tanh(u)) / 2 is the sigmoid of 2 u
 __device__ __forceinline__ float gelu_u(float z) { return 0.79788456f * z * fmaf(0.044715f * z, z, 1.0f); }
 
 __device__ __forceinline__ float act_fwd(float z, int act) {
   switch (act) {
-    case MOE_LINEAR_SILU: return __fdividef(z, 1.0f + __expf(-z));
+    case MOE_LINEAR_SILU: return z * fast_sigmoid(z);
     case MOE_LINEAR_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    case MOE_LINEAR_GELU_TANH: return __fdividef(z, 1.0f + __expf(-2.0f * gelu_u(z)));
+    case MOE_LINEAR_GELU_TANH: return z * fast_sigmoid(2.0f * gelu_u(z));
   }
   return z;
 }
@@ -63,7 +74,7 @@ __device__ __forceinline__ float act_grad(float z, int act) {
       return q * fmaf(z, 1.0f - q, 1.0f);
     }
     case MOE_LINEAR_GELU:
-      return fmaf(z * 0.39894228f, __expf(-0.5f * z * z), 0.5f * (1.0f + erff(z * 0.70710678f)));
+      return fmaf(z * 0.39894228f, fast_exp(-0.5f * z * z), 0.5f * (1.0f + erff(z * 0.70710678f)));
     case MOE_LINEAR_GELU_TANH: {
       const float q = fast_sigmoid(2.0f * gelu_u(z));
       // z q (1 - q) 2 u'
@@ -83,6 +94,10 @@ struct Epilogue {
   int act;
   int fp16;   // 16-bit values are fp16 (else bf16)
   int out32;  // out and residual are fp32
+  // the sums rounded to 16 bits and nothing else, by vectors
+  __device__ __forceinline__ bool plain() const {
+    return !bias && !residual && !preact && act == MOE_LINEAR_NONE && !out32 && Q % 8 == 0;
+  }
 };
 
 __device__ __forceinline__ float load16(const void* p, size_t i, int fp16) {
@@ -112,43 +127,63 @@ __device__ __forceinline__ void finish1(const Epilogue& e, int row, int col, flo
   }
 }
 
-template <class T>
-__device__ __forceinline__ void add8(const void* p, size_t at, float (&z)[8]) {
-  float v[8];
-  load8(static_cast<const T*>(p) + at, v);
+// 8 consecutive columns (Q % 8 == 0) of R rows, R independent chains of loads and stores;
+// `valid` says which rows exist.
+template <class T, int R>
+__device__ __forceinline__ void add_rows(const void* p, const size_t (&at)[R], const bool (&valid)[R], float (&z)[R][8]) {
+  float v[R][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] += v[i];
+  for (int r = 0; r < R; ++r)
+    if (valid[r]) load8(static_cast<const T*>(p) + at[r], v[r]);
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (valid[r]) z[r][i] += v[r][i];
 }
-
-// 8 consecutive columns of a row (Q % 8 == 0).
-__device__ __forceinline__ void finish8(const Epilogue& e, int row, int col, float (&z)[8]) {
-  const size_t at = (size_t)row * e.Q + col;
+template <class T, int R>
+__device__ __forceinline__ void store_rows(void* p, const size_t (&at)[R], const bool (&valid)[R], const float (&z)[R][8]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (valid[r]) store8(static_cast<T*>(p) + at[r], z[r]);
+}
+// T: the 16-bit type
+template <class T, int R>
+__device__ __forceinline__ void finish_rows_as(const Epilogue& e, const int (&row)[R], int col, const bool (&valid)[R],
+                                               float (&z)[R][8]) {
+  size_t at[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) at[r] = (size_t)row[r] * e.Q + col;
   if (e.bias) {
-    if (e.fp16)
-      add8<__half>(e.bias, col, z);
-    else
-      add8<__nv_bfloat16>(e.bias, col, z);
+    float b[8];
+    load8(static_cast<const T*>(e.bias) + col, b);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[r][i] += b[i];
   }
-  if (e.preact) {
-    if (e.fp16)
-      store8(static_cast<__half*>(e.preact) + at, z);
-    else
-      store8(static_cast<__nv_bfloat16*>(e.preact) + at, z);
-  }
+  if (e.preact) store_rows<T>(e.preact, at, valid, z);
   if (e.act != MOE_LINEAR_NONE) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = act_fwd(z[i], e.act);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[r][i] = act_fwd(z[r][i], e.act);
   }
   if (e.out32) {
-    if (e.residual) add8<float>(e.residual, at, z);
-    store8(static_cast<float*>(e.out) + at, z);
-  } else if (e.fp16) {
-    if (e.residual) add8<__half>(e.residual, at, z);
-    store8(static_cast<__half*>(e.out) + at, z);
+    if (e.residual) add_rows<float>(e.residual, at, valid, z);
+    store_rows<float>(e.out, at, valid, z);
   } else {
-    if (e.residual) add8<__nv_bfloat16>(e.residual, at, z);
-    store8(static_cast<__nv_bfloat16*>(e.out) + at, z);
+    if (e.residual) add_rows<T>(e.residual, at, valid, z);
+    store_rows<T>(e.out, at, valid, z);
   }
+}
+template <int R>
+__device__ __forceinline__ void finish_rows(const Epilogue& e, const int (&row)[R], int col, const bool (&valid)[R],
+                                            float (&z)[R][8]) {
+  if (e.fp16)
+    finish_rows_as<__half>(e, row, col, valid, z);
+  else
+    finish_rows_as<__nv_bfloat16>(e, row, col, valid, z);
 }
 
 // ------------------------------------------------------------------ tensor-core kernel
@@ -317,21 +352,54 @@ __device__ __forceinline__ float* buf_at(float* buf, int row, int piece) { retur
 
 // The epilogue of one 32-column chunk whose sums lane r holds for row row0 + r.
 __device__ __forceinline__ void finish_chunk(const Epilogue& e, float* buf, const float* v, int row0, int col0, int lane) {
+  // 4 lanes to the 32 columns of a row: 64-byte pieces (of 16-bit outputs) of 8 rows at a time
+  const int q = lane & 3, col = col0 + q * 8;
+  if (e.plain()) {
+    // rounded before the exchange: half the shared-memory traffic, and short enough that the
+    // gate's dx (4 K blocks a tile) went from 38 to XX us
+    char* b16 = reinterpret_cast<char*>(buf);
+    auto at = [&](int row, int piece) { return b16 + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4); };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = e.fp16 ? Word<__half>::put(v + 8 * i + 2 * j) : Word<__nv_bfloat16>::put(v + 8 * i + 2 * j);
+      *reinterpret_cast<uint4*>(at(lane, i)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    uint16_t* out = static_cast<uint16_t*>(e.out) + (size_t)row0 * e.Q + col;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2);
+      const uint4 w = *reinterpret_cast<const uint4*>(at(r, q));
+      if (row0 + r < e.P && col < e.Q) *reinterpret_cast<uint4*>(out + (size_t)r * e.Q) = w;
+    }
+    __syncwarp();
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     *reinterpret_cast<float4*>(buf_at(buf, lane, i)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
   __syncwarp();
   if (e.Q % 8 == 0) {
-    // 4 lanes to the 32 columns of a row: 64-byte pieces (of 16-bit outputs) of 8 rows at a time
-    const int col = col0 + (lane & 3) * 8;
+    if (col < e.Q) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2);
-      if (row0 + r < e.P && col < e.Q) {
-        const float4 lo = *reinterpret_cast<const float4*>(buf_at(buf, r, (lane & 3) * 2));
-        const float4 hi = *reinterpret_cast<const float4*>(buf_at(buf, r, (lane & 3) * 2 + 1));
-        float z[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        finish8(e, row0 + r, col, z);
+      for (int h = 0; h < 4; h += 2) {  // two rows at a time: four spilled registers
+        float z[2][8];
+        int row[2];
+        bool valid[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = (h + i) * 8 + (lane >> 2);
+          const float4 lo = *reinterpret_cast<const float4*>(buf_at(buf, r, q * 2));
+          const float4 hi = *reinterpret_cast<const float4*>(buf_at(buf, r, q * 2 + 1));
+          z[i][0] = lo.x, z[i][1] = lo.y, z[i][2] = lo.z, z[i][3] = lo.w;
+          z[i][4] = hi.x, z[i][5] = hi.y, z[i][6] = hi.z, z[i][7] = hi.w;
+          row[i] = row0 + r;
+          valid[i] = row[i] < e.P;
+        }
+        finish_rows<2>(e, row, col, valid, z);
       }
     }
   } else {
@@ -363,19 +431,20 @@ __device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int un
       lo[s] = ld_cluster(src);
       hi[s] = ld_cluster(src + 16);
     }
-    float z[8] = {};
+    float z[1][8] = {};
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      z[0] += lo[s].x, z[1] += lo[s].y, z[2] += lo[s].z, z[3] += lo[s].w;
-      z[4] += hi[s].x, z[5] += hi[s].y, z[6] += hi[s].z, z[7] += hi[s].w;
+      z[0][0] += lo[s].x, z[0][1] += lo[s].y, z[0][2] += lo[s].z, z[0][3] += lo[s].w;
+      z[0][4] += hi[s].x, z[0][5] += hi[s].y, z[0][6] += hi[s].z, z[0][7] += hi[s].w;
     }
-    const int row = row0 + r, col = tn * p.BN + c;
+    const int row[1] = {row0 + r}, col = tn * p.BN + c;
+    const bool valid[1] = {true};
     if (p.e.Q % 8 == 0) {
-      finish8(p.e, row, col, z);
+      finish_rows<1>(p.e, row, col, valid, z);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (col + j < p.e.Q) finish1(p.e, row, col + j, z[j]);
+        if (col + j < p.e.Q) finish1(p.e, row[0], col + j, z[0][j]);
     }
   }
 }
@@ -696,45 +765,56 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ dz and its column sums
 // dz = dout * act'(preact), in the operand type (row stride ld), and one row of column sums per
 // chunk of rows.  A thread takes 8 columns (or 1 where N % 8) of every 8th row of its chunk.
-constexpr int kDzRows = 64;       // rows of a chunk, more where that would give over
-constexpr int kDzChunks = 1024;   // this many
+constexpr int kDzRows = 64;       // rows of a chunk, fewer where that leaves SMs idle, more where it
+constexpr int kDzChunks = 1024;   // would give over this many chunks
 
-template <class TO, class T, bool kVec>
-__global__ void __launch_bounds__(256)
-    linear_dz_kernel(const TO* __restrict__ dout, const T* __restrict__ preact, int M, int N, int act, T* __restrict__ dz,
+template <class TO, class T, bool kVec, int act>
+__global__ void __launch_bounds__(256, 4)
+    linear_dz_kernel(const TO* __restrict__ dout, const T* __restrict__ preact, int M, int N, T* __restrict__ dz,
                      int ld, int rows, float* __restrict__ partial) {
   constexpr int V = kVec ? 8 : 1;
+  constexpr int R = 2;  // rows whose loads are in flight together
   __shared__ float sums[8][32 * V];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int col = (blockIdx.x * 32 + cx) * V;
   const int r0 = blockIdx.y * rows, r1 = min(M, r0 + rows);
   float sum[V] = {};
   if (col < N)
-#pragma unroll 2
-    for (int r = r0 + ry; r < r1; r += 8) {
-      const size_t at = (size_t)r * N + col;
-      float d[V];
-      if constexpr (kVec)
-        load8(dout + at, d);
-      else
-        d[0] = load1(dout + at);
-      if (act != MOE_LINEAR_NONE) {
-        float z[V];
-        if constexpr (kVec)
-          load8(preact + at, z);
-        else
-          z[0] = load1(preact + at);
+    for (int rb = r0 + ry; rb < r1; rb += 8 * R) {
+      float d[R][V], z[R][V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[i] *= act_grad(z[i], act);
-      }
-      if (dz) {
+      for (int j = 0; j < R; ++j) {
+        const int r = rb + 8 * j;
+        if (r >= r1) break;
+        const size_t at = (size_t)r * N + col;
         if constexpr (kVec)
-          store8(dz + (size_t)r * ld + col, d);
+          load8(dout + at, d[j]);
         else
-          store1(dz + (size_t)r * ld + col, d[0]);
+          d[j][0] = load1(dout + at);
+        if (act != MOE_LINEAR_NONE) {
+          if constexpr (kVec)
+            load8(preact + at, z[j]);
+          else
+            z[j][0] = load1(preact + at);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum[i] += d[i];
+      for (int j = 0; j < R; ++j) {
+        const int r = rb + 8 * j;
+        if (r >= r1) break;
+        if (act != MOE_LINEAR_NONE) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) d[j][i] *= act_grad(z[j][i], act);
+        }
+        if (dz) {
+          if constexpr (kVec)
+            store8(dz + (size_t)r * ld + col, d[j]);
+          else
+            store1(dz + (size_t)r * ld + col, d[j][0]);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] += d[j][i];
+      }
     }
   if (!partial) return;
 #pragma unroll
@@ -824,27 +904,68 @@ cudaError_t launch_gemm(int cg, const CUtensorMap& ma, const CUtensorMap& mb, co
                  : launch_gemm<kAMN, kBMN, 1, kPromote>(ma, mb, g, grid, s);
 }
 
+// Clusters of `size` GEMM CTAs that fit the device at once (a cluster lies within one group of
+// SMs, so eight-CTA clusters leave SMs idle); asked once per device and size.
+int cluster_slots(int size) {
+  static int cached[64][4] = {};
+  int dev = 0, log2 = 0;
+  while ((1 << log2) < size) ++log2;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms() / size;
+  if (cached[dev][log2] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    auto kern = linear_gemm_kernel<false, false, 1, false>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      n = num_sms() / size;
+    }
+    cached[dev][log2] = n;
+  }
+  return cached[dev][log2];
+}
+
 // How a product is cut: CTAs per MMA, tile columns, CTAs (pairs) that share a tile's K.
 struct Plan {
   int cg, bn, splits;
 };
 
+// The cheapest cut by a model fitted to measurements (ns, at 1.9 GHz): a K block takes 200 (the
+// turn of the copy and MMA loops) or 1.06 a column (the MMA rate) or 6.5 a KB copied (all SMs
+// reading L2); a tile's epilogue 1200 + 12 a column, overlapped with the next tile's K loop; joining
+// split tiles 1500 and its bytes at 10 a ns.  Measured either side of it: [64, 256] over K 7168 in
+// 64-column tiles, 1 / 2 / 4 / 8 splits 26 / 16 / 11 / 8.9 us; [4096, 256] over 7168, (128 columns,
+// 2 splits) 20 us, (256, 4) 23; [8192, 4096] over 4096, one CTA or a pair per MMA 174 / 152 us;
+// [4096, 7168] over 256, 26 / 29.
 Plan plan_gemm(long long P, long long Q, int KB) {
-  const int nsm = num_sms();
   Plan best{1, 64, 1};
   double best_cost = 1e30;
+  const double rows = P < BM ? (double)P : (double)BM;
   for (int cg = 1; cg <= 2; ++cg)
     for (int bn = 64; bn <= 256; bn *= 2) {
       if (cg == 2 && (P <= 128 || bn < 128)) continue;
       const long long tiles = (long long)cdiv(P, BM * cg) * cdiv(Q, bn);
       for (int s = 1; s * cg <= 8; s *= 2) {
-        if (s > 1 && (KB < 4 * s || tiles * s * cg > nsm)) break;
-        // clocks of one K block (MMA rate; copies into shared memory at about 56 bytes a clock)
-        const double mma = 2.0 * bn, copy = (128 + bn / cg) * 128 / 56.0;
-        const double kb = (double)cdiv(KB, s) * (mma > copy ? mma : copy);
-        const double waves = cdiv(tiles * s * cg, nsm / cg * cg);
-        const double tail = 2500 + 12.0 * bn + (s > 1 ? 1500 : 0);
-        const double cost = waves * kb + tail;
+        const int slots = cluster_slots(s * cg);
+        if (s > 1 && (KB < 4 * s || tiles > slots)) break;
+        const double busy = (double)(tiles < slots ? tiles : slots) * s * cg / num_sms();
+        const double copy = (rows + bn / cg) * 0.125 * 6.5 * (busy > 0.5 ? busy : 0.5);
+        double kb = 1.06 * bn > copy ? 1.06 * bn : copy;
+        if (kb < 200) kb = 200;
+        const double loop = cdiv(KB, s) * kb, epi = 1200 + 12.0 * bn;
+        const double waves = cdiv(tiles, slots);
+        const double join = s > 1 ? 1500 + rows * bn * 4 * (s - 1) / s / 10 : 0;
+        const double cost = waves * (loop > epi ? loop : epi) + (loop > epi ? epi : loop) + join;
         if (cost < best_cost) {
           best_cost = cost;
           best = {cg, bn, s};
@@ -878,7 +999,7 @@ moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue&
                         : make_map(&mb, B.base, e.fp16, C, e.Q, B.ld, p.bn / p.cg));
   if (!ok) return MOE_ERR_CUDA;
   const long long ctas = units * p.splits * p.cg;
-  const int most = num_sms() / p.cg * p.cg;
+  const int most = cluster_slots(p.cg) * p.cg;
   const int grid = (int)(p.splits > 1 || ctas < most ? ctas : most);
   const cudaError_t err = A.mn      ? launch_gemm<true, true, false>(p.cg, ma, mb, g, grid, s)
                           : B.mn    ? launch_gemm<false, true, false>(p.cg, ma, mb, g, grid, s)
@@ -909,6 +1030,8 @@ BwdLayout bwd_layout(int M, int N) {
   BwdLayout l;
   l.ld = ((long long)N + 7) / 8 * 8;
   l.rows = kDzRows;
+  const int blocks = cdiv(N, N % 8 == 0 ? 256 : 32);
+  while (l.rows > 8 && (long long)blocks * cdiv(M, l.rows) < 4LL * num_sms()) l.rows /= 2;
   while (cdiv(M, l.rows) > kDzChunks) l.rows *= 2;
   l.chunks = cdiv(M, l.rows);
   l.partial = ((size_t)M * l.ld * 2 + 255) / 256 * 256;
@@ -916,17 +1039,27 @@ BwdLayout bwd_layout(int M, int N) {
   return l;
 }
 
+template <class TO, class T, int act>
+void launch_dz_act(const TO* d, const T* z, int M, int N, T* dz, const BwdLayout& l, float* partial, cudaStream_t s) {
+  if (N % 8 == 0)
+    linear_dz_kernel<TO, T, true, act>
+        <<<dim3(cdiv(N, 256), l.chunks), 256, 0, s>>>(d, z, M, N, dz, (int)l.ld, l.rows, partial);
+  else
+    linear_dz_kernel<TO, T, false, act>
+        <<<dim3(cdiv(N, 32), l.chunks), 256, 0, s>>>(d, z, M, N, dz, (int)l.ld, l.rows, partial);
+}
 template <class TO, class T>
 void launch_dz(const void* dout, const void* preact, int M, int N, int act, void* dz, const BwdLayout& l, float* partial,
                cudaStream_t s) {
   const TO* d = static_cast<const TO*>(dout);
   const T* z = static_cast<const T*>(preact);
-  if (N % 8 == 0)
-    linear_dz_kernel<TO, T, true><<<dim3(cdiv(N, 256), l.chunks), 256, 0, s>>>(d, z, M, N, act, static_cast<T*>(dz),
-                                                                               (int)l.ld, l.rows, partial);
-  else
-    linear_dz_kernel<TO, T, false><<<dim3(cdiv(N, 32), l.chunks), 256, 0, s>>>(d, z, M, N, act, static_cast<T*>(dz),
-                                                                               (int)l.ld, l.rows, partial);
+  T* o = static_cast<T*>(dz);
+  switch (act) {
+    case MOE_LINEAR_NONE: return launch_dz_act<TO, T, MOE_LINEAR_NONE>(d, z, M, N, o, l, partial, s);
+    case MOE_LINEAR_SILU: return launch_dz_act<TO, T, MOE_LINEAR_SILU>(d, z, M, N, o, l, partial, s);
+    case MOE_LINEAR_GELU: return launch_dz_act<TO, T, MOE_LINEAR_GELU>(d, z, M, N, o, l, partial, s);
+    default: return launch_dz_act<TO, T, MOE_LINEAR_GELU_TANH>(d, z, M, N, o, l, partial, s);
+  }
 }
 
 moe_status_t check_sizes(int M, int N, int K, moe_dtype_t dtype, int activation, moe_dtype_t other) {

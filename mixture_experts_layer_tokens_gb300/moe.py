@@ -9,6 +9,7 @@ and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -600,24 +601,23 @@ def _tensor(t: Optional[torch.Tensor], dtype, shape, name: str, device: int):
     """A tensor argument as its pointer: dtype, shape, contiguity and device checked."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
     if t.get_device() != device:
         raise ValueError(f"{name}: expected a tensor on the current CUDA device")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous tensor")
 
 
 def _launch(stream: Optional[torch.cuda.Stream]):
-    """(current device index, raw stream) of a call."""
-    if not torch.cuda.is_available():
-        raise RuntimeError("no CUDA device")
+    """(current device index, raw stream) of a call.  (A call without outputs to allocate costs the host a few
+    microseconds, so the raw stream is asked for rather than a torch.cuda.Stream built around it.)"""
     dev = torch.cuda.current_device()
     if stream is None:
-        return dev, torch.cuda.current_stream(dev).cuda_stream
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
     if stream.device_index != dev:
         raise ValueError("stream: expected a stream of the current CUDA device")
     return dev, stream.cuda_stream
@@ -688,6 +688,11 @@ def moe_linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pr
 
 
 # ------------------------------------------------------------------ grouped route
+@functools.lru_cache(maxsize=None)
+def _route_config(score, n_group, topk_group, group_top, renormalize, scale):
+    return ctypes.byref(route_config(score, n_group, topk_group, group_top, renormalize, scale))
+
+
 def route_config(score: str = "sigmoid", n_group: int = 1, topk_group: int = 1, group_top: int = 1,
                  renormalize: bool = True, scale: float = 1.0) -> RouteConfig:
     if score not in SCORES:
@@ -706,7 +711,7 @@ def moe_route_grouped(logits: torch.Tensor, top_k: int, bias: Optional[torch.Ten
     if logits.dtype not in _DT:
         raise TypeError(f"logits: expected float32, bfloat16 or float16, got {logits.dtype}")
     T, E = logits.shape
-    cfg = route_config(score, n_group, topk_group, group_top, renormalize, scale)
+    cfg = _route_config(score, n_group, topk_group, group_top, bool(renormalize), scale)
     if topk_ids is None:
         topk_ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
     if topk_weights is None:
@@ -714,7 +719,7 @@ def moe_route_grouped(logits: torch.Tensor, top_k: int, bias: Optional[torch.Ten
     dev, s = _launch(stream)
     _check("moe_route_grouped", lib().moe_route_grouped(
         _tensor(logits, logits.dtype, (T, E), "logits", dev), _DT[logits.dtype],
-        _tensor(bias, torch.float32, (E,), "bias", dev), T, E, top_k, ctypes.byref(cfg),
+        _tensor(bias, torch.float32, (E,), "bias", dev), T, E, top_k, cfg,
         _tensor(topk_ids, torch.int32, (T, top_k), "topk_ids", dev),
         _tensor(topk_weights, torch.float32, (T, top_k), "topk_weights", dev), s))
     return topk_ids, topk_weights
@@ -728,14 +733,14 @@ def moe_route_grouped_backward(dweights: torch.Tensor, logits: torch.Tensor, top
     if logits.dtype not in _DT:
         raise TypeError(f"logits: expected float32, bfloat16 or float16, got {logits.dtype}")
     (T, E), top_k = logits.shape, topk_ids.shape[1]
-    cfg = route_config(score, renormalize=renormalize, scale=scale)
+    cfg = _route_config(score, 1, 1, 1, bool(renormalize), scale)
     if dlogits is None:
         dlogits = torch.empty_like(logits)
     dev, s = _launch(stream)
     _check("moe_route_grouped_backward", lib().moe_route_grouped_backward(
         _tensor(dweights, torch.float32, (T, top_k), "dweights", dev),
         _tensor(logits, logits.dtype, (T, E), "logits", dev), _DT[logits.dtype],
-        _tensor(topk_ids, torch.int32, (T, top_k), "topk_ids", dev), T, E, top_k, ctypes.byref(cfg),
+        _tensor(topk_ids, torch.int32, (T, top_k), "topk_ids", dev), T, E, top_k, cfg,
         _tensor(dlogits, logits.dtype, (T, E), "dlogits", dev), s))
     return dlogits
 

@@ -119,8 +119,10 @@ def _backward(dev, M, N, K, dtype=BF, act="none", ddt=None, need=(True, True, Tr
         if not needed:
             assert v is None
             continue
-        if name == "dbias":  # 8 rows a thread, 8 threads, then one sum in 8 of all chunks
-            tol = (2.0 ** -24 * (32 + M / 64 / 8) + (2.0 ** -19 if act != "none" else 0)) * mag
+        if name == "dbias":
+            # a chunk of 8 to 64 rows: at most 8 rows a thread, then 8 threads; then 8 sums over up to M / 8
+            # chunks, and those: 8 + 8 + M / 64 + 8 additions in a row at most
+            tol = (2.0 ** -24 * (32 + M / 64) + (2.0 ** -19 if act != "none" else 0)) * mag
         else:
             other = x.double().abs().sum(0)[None] if name == "dw" else w.double().abs().sum(0)[None]
             tol = (2.0 ** -22 * (n / 16 + 16) + dz_err) * mag + sub * other
