@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(kMaxConsumers + 32, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t row_bytes = a.H * 2;
   float* drms_sum = reinterpret_cast<float*>(smem + (size_t)a.slots * row_bytes);  // [H] when partial
+  depend_launch();
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.slots; ++i) {
       mbar_init(&full[i], 1);
@@ -250,6 +251,7 @@ __global__ void __launch_bounds__(kMaxConsumers + 32, 1)
 __global__ void __launch_bounds__(256) drms_kernel(const float* __restrict__ partial, int P, int H, float* out) {
   __shared__ float sums[8][32];
   const int h = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+  depend_wait();
   float s = 0.f;
   if (h < H)
     for (int p = part; p < P; p += 8) s += partial[(size_t)p * H + h];
@@ -337,6 +339,7 @@ extern "C" moe_status_t moe_finalize_backward(const void* dout, const void* dres
   const bool ok = nv == 1 ? run(finalize_backward_kernel<1>)
                           : nv == 2 ? run(finalize_backward_kernel<2>) : run(finalize_backward_kernel<4>);
   if (!ok) return MOE_ERR_CUDA;
-  if (drms) drms_kernel<<<(H + 31) / 32, 256, 0, s>>>(a.partial, grid, H, drms);
+  if (drms && launch_overlapped(drms_kernel, (H + 31) / 32, 256, s, a.partial, grid, H, drms) != cudaSuccess)
+    return MOE_ERR_CUDA;
   return launch_status();
 }

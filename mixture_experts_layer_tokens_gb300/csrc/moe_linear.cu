@@ -110,21 +110,41 @@ __device__ __forceinline__ void store16(void* p, size_t i, float v, int fp16) {
     store1(static_cast<__nv_bfloat16*>(p) + i, v);
 }
 
-__device__ __forceinline__ void finish1(const Epilogue& e, int row, int col, float z) {
+// R consecutive rows of a column; the loads and stores of the rows are independent.
+template <int R>
+__device__ __forceinline__ void finish_column(const Epilogue& e, int row, int col, float (&z)[R]) {
   const size_t at = (size_t)row * e.Q + col;
-  if (e.bias) z += load16(e.bias, col, e.fp16);
-  if (e.preact) store16(e.preact, at, z, e.fp16);
-  z = act_fwd(z, e.act);
-  // (residual may be out: a plain load, not the read-only path)
-  if (e.out32) {
-    if (e.residual) z += static_cast<const float*>(e.residual)[at];
-    static_cast<float*>(e.out)[at] = z;
-  } else {
-    if (e.residual)
-      z += e.fp16 ? __half2float(static_cast<const __half*>(e.residual)[at])
-                  : __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[at]);
-    store16(e.out, at, z, e.fp16);
+  const int rows = min(R, e.P - row);
+  const float b = e.bias ? load16(e.bias, col, e.fp16) : 0.f;
+  float res[R];
+  // (residual may be out: plain loads, not the read-only path)
+  if (e.residual) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r < rows) {
+        const size_t i = at + (size_t)r * e.Q;
+        res[r] = e.out32  ? static_cast<const float*>(e.residual)[i]
+                 : e.fp16 ? __half2float(static_cast<const __half*>(e.residual)[i])
+                          : __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[i]);
+      }
   }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (r < rows) {
+      const size_t i = at + (size_t)r * e.Q;
+      float v = z[r] + b;
+      if (e.preact) store16(e.preact, i, v, e.fp16);
+      v = act_fwd(v, e.act);
+      if (e.residual) v += res[r];
+      if (e.out32)
+        static_cast<float*>(e.out)[i] = v;
+      else
+        store16(e.out, i, v, e.fp16);
+    }
+}
+__device__ __forceinline__ void finish1(const Epilogue& e, int row, int col, float z) {
+  float v[1] = {z};
+  finish_column<1>(e, row, col, v);
 }
 
 // 8 consecutive columns (Q % 8 == 0) of R rows, R independent chains of loads and stores;
@@ -196,7 +216,8 @@ struct Gemm {
   int a_rows;           // rows of the A box (K-major A): with fewer than 128 a stage is smaller and more of
                         // them fit; the MMA reads what lies behind for the other rows, whose
                         // accumulators nobody looks at
-  int tiles_m, tiles_n;
+  int tiles_m, tiles_n, raster;
+  int unit0, units;     // the tiles of this launch: [unit0, units)
   uint32_t idesc;
 };
 
@@ -335,13 +356,14 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
       : "r"(taddr));
 }
 
-// The tile of a unit: blocks of kRaster tile rows run through all tile columns, so that the
-// CTAs that work at the same time share A rows and B rows in L2.
-constexpr int kRaster = 8;
-__device__ __forceinline__ void tile_of(int u, int tiles_m, int tiles_n, int& m, int& n) {
-  const int per = kRaster * tiles_n, g = u / per, in = u - g * per;
-  const int rows = min(kRaster, tiles_m - g * kRaster);
-  m = g * kRaster + in % rows;
+// The tile of a unit: blocks of `raster` tile rows run through all tile columns, so that the CTAs
+// that work at the same time share A rows and B rows in L2.
+constexpr int kRaster = 8;  // at most; the host evens the blocks out (9 tile rows: 5 and 4, not 8 and a
+                            // last row that reads all of B again)
+__device__ __forceinline__ void tile_of(const Gemm& p, int u, int& m, int& n) {
+  const int per = p.raster * p.tiles_n, g = u / per, in = u - g * per;
+  const int rows = min(p.raster, p.tiles_m - g * p.raster);
+  m = g * p.raster + in % rows;
   n = in / rows;
 }
 
@@ -403,8 +425,14 @@ __device__ __forceinline__ void finish_chunk(const Epilogue& e, float* buf, cons
       }
     }
   } else {
-    for (int r = 0; r < 32 && row0 + r < e.P; ++r)
-      if (col0 + lane < e.Q) finish1(e, row0 + r, col0 + lane, buf_at(buf, r, lane >> 2)[lane & 3]);
+    // a lane takes a column: 64-byte pieces of rows that start anywhere
+    if (col0 + lane < e.Q)
+      for (int h = 0; h < 32 && row0 + h < e.P; h += 8) {
+        float z[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = buf_at(buf, h + i, lane >> 2)[lane & 3];
+        finish_column<8>(e, row0 + h, col0 + lane, z);
+      }
   }
   __syncwarp();
 }
@@ -414,37 +442,47 @@ __device__ __forceinline__ void finish_chunk(const Epilogue& e, float* buf, cons
 template <int S, int CG>
 __device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int unit, int split, int half) {
   int tm, tn;
-  tile_of(unit, p.tiles_m, p.tiles_n, tm, tn);
+  tile_of(p, unit, tm, tn);
   const int row0 = (tm * CG + half) * BM;
   const int rows = max(0, min(BM, p.e.P - row0)), cols = min(p.BN, p.e.Q - tn * p.BN);
   const int groups = (cols + 7) / 8, items = rows * groups;
   const uint32_t base = smem_u32(smem);
   const int i1 = (int)((long long)items * (split + 1) / S);
   if (status_failed()) return;
-  for (int i = (int)((long long)items * split / S) + threadIdx.x - kFirstEpi * 32; i < i1; i += kEpiWarps * 32) {
-    const int r = i / groups, c = (i - r * groups) * 8;
-    const uint32_t at = base + (uint32_t)((r * (p.BN + 4) + c) * 4);
-    float4 lo[S], hi[S];
+  constexpr int U = S >= 8 ? 1 : 8 / S;  // items whose loads are in flight together
+  constexpr int kStep = kEpiWarps * 32;
+  for (int i0 = (int)((long long)items * split / S) + threadIdx.x - kFirstEpi * 32; i0 < i1; i0 += U * kStep) {
+    float4 lo[U][S], hi[U][S];
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const uint32_t src = map_to_rank(at, s * CG + half);
-      lo[s] = ld_cluster(src);
-      hi[s] = ld_cluster(src + 16);
+    for (int u = 0; u < U; ++u) {
+      const int i = min(i0 + u * kStep, i1 - 1), r = i / groups, c = (i - r * groups) * 8;
+      const uint32_t at = base + (uint32_t)((r * (p.BN + 4) + c) * 4);
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        const uint32_t src = map_to_rank(at, s * CG + half);
+        lo[u][s] = ld_cluster(src);
+        hi[u][s] = ld_cluster(src + 16);
+      }
     }
-    float z[1][8] = {};
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      z[0][0] += lo[s].x, z[0][1] += lo[s].y, z[0][2] += lo[s].z, z[0][3] += lo[s].w;
-      z[0][4] += hi[s].x, z[0][5] += hi[s].y, z[0][6] += hi[s].z, z[0][7] += hi[s].w;
-    }
-    const int row[1] = {row0 + r}, col = tn * p.BN + c;
-    const bool valid[1] = {true};
-    if (p.e.Q % 8 == 0) {
-      finish_rows<1>(p.e, row, col, valid, z);
-    } else {
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kStep, r = i / groups, c = (i - r * groups) * 8;
+      if (i >= i1) break;
+      float z[1][8] = {};
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (col + j < p.e.Q) finish1(p.e, row[0], col + j, z[0][j]);
+      for (int s = 0; s < S; ++s) {
+        z[0][0] += lo[u][s].x, z[0][1] += lo[u][s].y, z[0][2] += lo[u][s].z, z[0][3] += lo[u][s].w;
+        z[0][4] += hi[u][s].x, z[0][5] += hi[u][s].y, z[0][6] += hi[u][s].z, z[0][7] += hi[u][s].w;
+      }
+      const int row[1] = {row0 + r}, col = tn * p.BN + c;
+      const bool valid[1] = {true};
+      if (p.e.Q % 8 == 0) {
+        finish_rows<1>(p.e, row, col, valid, z);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (col + j < p.e.Q) finish1(p.e, row[0], col + j, z[0][j]);
+      }
     }
   }
 }
@@ -484,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t leader = rank - half;
   const uint16_t pair_mask = (uint16_t)(3u << leader);
 
+  depend_launch();
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
@@ -504,10 +543,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (CG > 1) cluster_sync();  // the pair's barriers are set up
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  depend_wait();
 
   const int kb0 = (int)((long long)p.KB * split / splits), kb1 = (int)((long long)p.KB * (split + 1) / splits);
-  const int units = p.tiles_m * p.tiles_n;
-  const int first = blockIdx.x / (splits * CG);
+  const int units = p.units;
+  const int first = p.unit0 + blockIdx.x / (splits * CG);
   const int step = splits > 1 ? units : gridDim.x / CG;  // a split tile is its cluster's only work
   const int chunk = kPromote ? kPromoteKB : kb1 - kb0;   // K blocks added up in the tensor memory
 
@@ -531,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t full0 = CG > 1 ? map_to_rank(smem_u32(full), leader) : smem_u32(full);  // (both CTAs' copies
       for (int u = first; u < units; u += step) {                                           // complete there)
         int tm, tn;
-        tile_of(u, p.tiles_m, p.tiles_n, tm, tn);
+        tile_of(p, u, tm, tn);
         const int arow = (tm * CG + half) * BM, brow = tn * p.BN + half * bn_cta;
         if (elect_one()) {
           int st = stage;
@@ -648,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int u = first; ok && u < units; u += step) {
       int tm, tn;
-      tile_of(u, p.tiles_m, p.tiles_n, tm, tn);
+      tile_of(p, u, tm, tn);
       const int row0 = (tm * CG + half) * BM + quarter * 32, col0 = tn * p.BN + side * ncol;
       const int cols = row0 < p.e.P ? min(ncol, p.e.Q - col0) : 0;
       // split: the partial tile goes to this CTA's stages (every copy has landed and every MMA has
@@ -774,6 +814,7 @@ __global__ void __launch_bounds__(256, 4)
                      int ld, int rows, float* __restrict__ partial) {
   constexpr int V = kVec ? 8 : 1;
   constexpr int R = 2;  // rows whose loads are in flight together
+  depend_launch();
   __shared__ float sums[8][32 * V];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int col = (blockIdx.x * 32 + cx) * V;
@@ -831,6 +872,8 @@ __global__ void __launch_bounds__(256, 4)
 template <class T>
 __global__ void __launch_bounds__(256) linear_dbias_kernel(const float* __restrict__ partial, int P, int N, T* dbias) {
   __shared__ float sums[8][32];
+  depend_launch();
+  depend_wait();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
   float s = 0.f;
   if (c < N)
@@ -879,7 +922,7 @@ struct Operand {
 int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 template <bool kAMN, bool kBMN, int CG, bool kPromote>
-cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g, int grid, cudaStream_t s) {
+cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g, int grid, bool overlap, cudaStream_t s) {
   auto kern = linear_gemm_kernel<kAMN, kBMN, CG, kPromote>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (err != cudaSuccess) return err;
@@ -888,20 +931,21 @@ cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = g.splits * CG;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1] = overlap_attr();
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = overlap ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, ma, mb, g);
 }
 
 template <bool kAMN, bool kBMN, bool kPromote>
-cudaError_t launch_gemm(int cg, const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g, int grid, cudaStream_t s) {
-  return cg == 2 ? launch_gemm<kAMN, kBMN, 2, kPromote>(ma, mb, g, grid, s)
-                 : launch_gemm<kAMN, kBMN, 1, kPromote>(ma, mb, g, grid, s);
+cudaError_t launch_gemm(int cg, const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g, int grid, bool overlap, cudaStream_t s) {
+  return cg == 2 ? launch_gemm<kAMN, kBMN, 2, kPromote>(ma, mb, g, grid, overlap, s)
+                 : launch_gemm<kAMN, kBMN, 1, kPromote>(ma, mb, g, grid, overlap, s);
 }
 
 // Clusters of `size` GEMM CTAs that fit the device at once (a cluster lies within one group of
@@ -942,7 +986,7 @@ struct Plan {
 
 // The cheapest cut by a model fitted to measurements (ns, at 1.9 GHz): a K block takes 200 (the
 // turn of the copy and MMA loops) or 1.06 a column (the MMA rate) or 6.5 a KB copied (all SMs
-// reading L2); a tile's epilogue 1200 + 12 a column, overlapped with the next tile's K loop; joining
+// reading L2); a tile's epilogue 1200 (1800 with pairs) + 12 a column, overlapped with the next tile's K loop; joining
 // split tiles 1500 and its bytes at 10 a ns.  Measured either side of it: [64, 256] over K 7168 in
 // 64-column tiles, 1 / 2 / 4 / 8 splits 26 / 16 / 11 / 8.9 us; [4096, 256] over 7168, (128 columns,
 // 2 splits) 20 us, (256, 4) 23; [8192, 4096] over 4096, one CTA or a pair per MMA 174 / 152 us;
@@ -962,7 +1006,7 @@ Plan plan_gemm(long long P, long long Q, int KB) {
         const double copy = (rows + bn / cg) * 0.125 * 6.5 * (busy > 0.5 ? busy : 0.5);
         double kb = 1.06 * bn > copy ? 1.06 * bn : copy;
         if (kb < 200) kb = 200;
-        const double loop = cdiv(KB, s) * kb, epi = 1200 + 12.0 * bn;
+        const double loop = cdiv(KB, s) * kb, epi = 600 * (1 + cg) + 12.0 * bn;
         const double waves = cdiv(tiles, slots);
         const double join = s > 1 ? 1500 + rows * bn * 4 * (s - 1) / s / 10 : 0;
         const double cost = waves * (loop > epi ? loop : epi) + (loop > epi ? epi : loop) + join;
@@ -975,8 +1019,19 @@ Plan plan_gemm(long long P, long long Q, int KB) {
   return best;
 }
 
-// D [P, Q] = A . B^T over a contraction of C.
-moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue& e, cudaStream_t s) {
+// Splits of the last, partly filled wave of tiles: `rem` tiles that would leave the other slots idle
+// for a whole K loop take a launch of their own, several CTAs (pairs) to a tile, when that saves
+// more than its launch and join cost (about 6 us; the dense dx of 2050 x 5120 over 8192, 152
+// tiles and 28 more on 76 pairs, 122 -> XX us).
+int tail_splits(const Plan& p, long long rem, int KB) {
+  int s = 1;
+  while (2 * s * p.cg <= 8 && rem <= cluster_slots(2 * s * p.cg) && KB >= 16 * s) s *= 2;
+  return (double)KB * (1.0 - 1.0 / s) * 1.06 * p.bn > 8000 ? s : 1;
+}
+
+// D [P, Q] = A . B^T over a contraction of C.  overlap: what ran before on the stream in this call
+// is this library's, so the launch may overlap its end (the kernel waits for its results).
+moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue& e, bool overlap, cudaStream_t s) {
   Gemm g;
   g.e = e;
   g.KB = cdiv(C, BK);
@@ -984,8 +1039,8 @@ moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue&
   const Plan p = plan_gemm(e.P, e.Q, g.KB);
   g.tiles_m = cdiv(e.P, BM * p.cg);
   g.tiles_n = cdiv(e.Q, p.bn);
+  g.raster = cdiv(g.tiles_m, cdiv(g.tiles_m, kRaster));
   g.BN = p.bn;
-  g.splits = p.splits;
   const long long units = (long long)g.tiles_m * g.tiles_n;
   if (units > 2147483647LL / 16) return MOE_ERR_UNSUPPORTED;
   g.a_rows = A.mn || e.P >= BM ? BM : (e.P + 7) / 8 * 8;
@@ -998,14 +1053,26 @@ moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue&
                   (B.mn ? make_map(&mb, B.base, e.fp16, e.Q, C, B.ld, BK)
                         : make_map(&mb, B.base, e.fp16, C, e.Q, B.ld, p.bn / p.cg));
   if (!ok) return MOE_ERR_CUDA;
-  const long long ctas = units * p.splits * p.cg;
-  const int most = cluster_slots(p.cg) * p.cg;
-  const int grid = (int)(p.splits > 1 || ctas < most ? ctas : most);
-  const cudaError_t err = A.mn      ? launch_gemm<true, true, false>(p.cg, ma, mb, g, grid, s)
-                          : B.mn    ? launch_gemm<false, true, false>(p.cg, ma, mb, g, grid, s)
-                          : promote ? launch_gemm<false, false, true>(p.cg, ma, mb, g, grid, s)
-                                    : launch_gemm<false, false, false>(p.cg, ma, mb, g, grid, s);
-  return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  auto launch = [&](long long first, long long last, int splits) {
+    g.unit0 = (int)first;
+    g.units = (int)last;
+    g.splits = splits;
+    const long long ctas = (last - first) * splits * p.cg;
+    const int most = cluster_slots(p.cg) * p.cg;
+    const int grid = (int)(splits > 1 || ctas < most ? ctas : most);
+    const cudaError_t err = A.mn      ? launch_gemm<true, true, false>(p.cg, ma, mb, g, grid, overlap, s)
+                            : B.mn    ? launch_gemm<false, true, false>(p.cg, ma, mb, g, grid, overlap, s)
+                            : promote ? launch_gemm<false, false, true>(p.cg, ma, mb, g, grid, overlap, s)
+                                      : launch_gemm<false, false, false>(p.cg, ma, mb, g, grid, overlap, s);
+    overlap = true;
+    return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  };
+  const int slots = cluster_slots(p.cg);
+  const long long rem = p.splits == 1 && units > slots ? units % slots : 0;
+  const int tail = rem ? tail_splits(p, rem, g.KB) : 1;
+  if (tail == 1) return launch(0, units, p.splits);
+  const moe_status_t st = launch(0, units - rem, 1);
+  return st != MOE_OK ? st : launch(units - rem, units, tail);
 }
 
 template <int kM>
@@ -1099,7 +1166,7 @@ extern "C" moe_status_t moe_linear(const void* x, const void* w, const void* bia
       launch_rows<4>(x, w, M, N, K, e, s);
     return launch_status();
   }
-  return run_gemm({x, false, K}, {w, false, K}, K, e, s);
+  return run_gemm({x, false, K}, {w, false, K}, K, e, false, s);
 }
 
 extern "C" size_t moe_linear_backward_workspace_size(int M, int N, int K) {
@@ -1143,10 +1210,12 @@ extern "C" moe_status_t moe_linear_backward(const void* dout, moe_dtype_t dout_d
         launch_dz<__nv_bfloat16, __nv_bfloat16>(dout, preact, M, N, activation, dz, l, partial, s);
     }
     if (dbias) {
-      if (fp16)
-        linear_dbias_kernel<<<cdiv(N, 32), 256, 0, s>>>(partial, l.chunks, N, static_cast<__half*>(dbias));
-      else
-        linear_dbias_kernel<<<cdiv(N, 32), 256, 0, s>>>(partial, l.chunks, N, static_cast<__nv_bfloat16*>(dbias));
+      const cudaError_t err =
+          fp16 ? launch_overlapped(linear_dbias_kernel<__half>, cdiv(N, 32), 256, s, (const float*)partial, l.chunks, N,
+                                   static_cast<__half*>(dbias))
+               : launch_overlapped(linear_dbias_kernel<__nv_bfloat16>, cdiv(N, 32), 256, s, (const float*)partial,
+                                   l.chunks, N, static_cast<__nv_bfloat16*>(dbias));
+      if (err != cudaSuccess) return MOE_ERR_CUDA;
     }
     if ((st = launch_status()) != MOE_OK) return st;
   }
@@ -1154,11 +1223,11 @@ extern "C" moe_status_t moe_linear_backward(const void* dout, moe_dtype_t dout_d
   const long long ld = direct ? N : l.ld;
   if (dx) {
     const Epilogue e{nullptr, nullptr, dx, nullptr, M, K, MOE_LINEAR_NONE, fp16, 0};
-    if ((st = run_gemm({z, false, ld}, {w, true, K}, N, e, s)) != MOE_OK) return st;
+    if ((st = run_gemm({z, false, ld}, {w, true, K}, N, e, dz || partial, s)) != MOE_OK) return st;
   }
   if (dw) {
     const Epilogue e{nullptr, nullptr, dw, nullptr, N, K, MOE_LINEAR_NONE, fp16, 0};
-    if ((st = run_gemm({z, true, ld}, {x, true, K}, M, e, s)) != MOE_OK) return st;
+    if ((st = run_gemm({z, true, ld}, {x, true, K}, M, e, dz || partial || dx, s)) != MOE_OK) return st;
   }
   return launch_status();
 }

@@ -13,6 +13,33 @@ moe_status_t route_grouped_status(int clear);
 moe_status_t linear_status(int clear);
 moe_status_t finalize_backward_status(int clear);
 
+// ---- launches that overlap the end of the launch before them on the stream
+// A call's second and later kernels are launched with overlap_attr(): the device may start their
+// CTAs when every CTA of the kernel before has called depend_launch() (or ended) and there is room
+// for them.  depend_wait() then waits until that kernel has ended and its writes are visible; each
+// kernel of a call waits before it touches memory, so the whole chain is ordered.  The first
+// kernel of a call is launched plainly and waits for nothing.
+__device__ __forceinline__ void depend_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+inline cudaLaunchAttribute overlap_attr() {
+  cudaLaunchAttribute a;
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+template <class... P, class... A>
+cudaError_t launch_overlapped(void (*kern)(P...), int grid, int block, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1] = {overlap_attr()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 __device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
 __device__ __forceinline__ float load1(const __half* p) { return __half2float(__ldg(p)); }
