@@ -23,7 +23,7 @@ namespace moe {
 namespace {
 
 constexpr int BM = 128;           // accumulator rows of a CTA = TMEM lanes
-constexpr int BK = 64;            // contraction elements of a stage: one 128-byte swizzle row
+constexpr int BK = 64;            // contraction elements of a K block: one 128-byte swizzle row
 constexpr int kThreads = 384;     // three warpgroups: producer and MMA issuer (2 warps idle), 8 epilogue warps
 constexpr int kFirstEpi = 4;
 constexpr int kEpiWarps = 8;
@@ -167,6 +167,13 @@ __device__ __forceinline__ void store_rows(void* p, const size_t (&at)[R], const
   for (int r = 0; r < R; ++r)
     if (valid[r]) store8(static_cast<T*>(p) + at[r], z[r]);
 }
+template <int act, int R>
+__device__ __forceinline__ void act_rows(float (&z)[R][8]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[r][i] = act_fwd(z[r][i], act);
+}
 // T: the 16-bit type
 template <class T, int R>
 __device__ __forceinline__ void finish_rows_as(const Epilogue& e, const int (&row)[R], int col, const bool (&valid)[R],
@@ -183,12 +190,12 @@ __device__ __forceinline__ void finish_rows_as(const Epilogue& e, const int (&ro
       for (int i = 0; i < 8; ++i) z[r][i] += b[i];
   }
   if (e.preact) store_rows<T>(e.preact, at, valid, z);
-  if (e.act != MOE_LINEAR_NONE) {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[r][i] = act_fwd(z[r][i], e.act);
-  }
+  if (e.act == MOE_LINEAR_SILU)
+    act_rows<MOE_LINEAR_SILU>(z);
+  else if (e.act == MOE_LINEAR_GELU)
+    act_rows<MOE_LINEAR_GELU>(z);
+  else if (e.act == MOE_LINEAR_GELU_TANH)
+    act_rows<MOE_LINEAR_GELU_TANH>(z);
   if (e.out32) {
     if (e.residual) add_rows<float>(e.residual, at, valid, z);
     store_rows<float>(e.out, at, valid, z);
@@ -209,7 +216,7 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, const int (&row)[
 // ------------------------------------------------------------------ tensor-core kernel
 struct Gemm {
   Epilogue e;
-  int KB;               // K blocks
+  int KB;               // stages of K
   int splits;           // CTAs (CTA pairs) of a cluster that share a tile's K blocks
   int BN;               // tile columns
   int stages;
@@ -372,13 +379,15 @@ __device__ __forceinline__ void tile_of(const Gemm& p, int u, int& m, int& n) {
 // 4-lanes-per-row reads free of bank conflicts.
 __device__ __forceinline__ float* buf_at(float* buf, int row, int piece) { return buf + row * 32 + ((piece ^ (row & 7)) << 2); }
 
-// The epilogue of one 32-column chunk whose sums lane r holds for row row0 + r.
+// The epilogue of one 32-column chunk whose sums lane r holds for row row0 + r.  kPlain: nothing but
+// the plain form can come (the gradients).
+template <bool kPlain>
 __device__ __forceinline__ void finish_chunk(const Epilogue& e, float* buf, const float* v, int row0, int col0, int lane) {
   // 4 lanes to the 32 columns of a row: 64-byte pieces (of 16-bit outputs) of 8 rows at a time
   const int q = lane & 3, col = col0 + q * 8;
-  if (e.plain()) {
+  if (kPlain || e.plain()) {
     // rounded before the exchange: half the shared-memory traffic, and short enough that the
-    // gate's dx (4 K blocks a tile) went from 38 to XX us
+    // gate's dx (4 K blocks a tile) went from 38 to 26 us
     char* b16 = reinterpret_cast<char*>(buf);
     auto at = [&](int row, int piece) { return b16 + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4); };
 #pragma unroll
@@ -400,46 +409,48 @@ __device__ __forceinline__ void finish_chunk(const Epilogue& e, float* buf, cons
     __syncwarp();
     return;
   }
+  if constexpr (!kPlain) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    *reinterpret_cast<float4*>(buf_at(buf, lane, i)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  __syncwarp();
-  if (e.Q % 8 == 0) {
-    if (col < e.Q) {
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<float4*>(buf_at(buf, lane, i)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    __syncwarp();
+    if (e.Q % 8 == 0) {
+      if (col < e.Q) {
 #pragma unroll
-      for (int h = 0; h < 4; h += 2) {  // two rows at a time: four spilled registers
-        float z[2][8];
-        int row[2];
-        bool valid[2];
+        for (int h = 0; h < 4; h += 2) {  // two rows at a time: four spilled registers
+          float z[2][8];
+          int row[2];
+          bool valid[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = (h + i) * 8 + (lane >> 2);
-          const float4 lo = *reinterpret_cast<const float4*>(buf_at(buf, r, q * 2));
-          const float4 hi = *reinterpret_cast<const float4*>(buf_at(buf, r, q * 2 + 1));
-          z[i][0] = lo.x, z[i][1] = lo.y, z[i][2] = lo.z, z[i][3] = lo.w;
-          z[i][4] = hi.x, z[i][5] = hi.y, z[i][6] = hi.z, z[i][7] = hi.w;
-          row[i] = row0 + r;
-          valid[i] = row[i] < e.P;
+          for (int i = 0; i < 2; ++i) {
+            const int r = (h + i) * 8 + (lane >> 2);
+            const float4 lo = *reinterpret_cast<const float4*>(buf_at(buf, r, q * 2));
+            const float4 hi = *reinterpret_cast<const float4*>(buf_at(buf, r, q * 2 + 1));
+            z[i][0] = lo.x, z[i][1] = lo.y, z[i][2] = lo.z, z[i][3] = lo.w;
+            z[i][4] = hi.x, z[i][5] = hi.y, z[i][6] = hi.z, z[i][7] = hi.w;
+            row[i] = row0 + r;
+            valid[i] = row[i] < e.P;
+          }
+          finish_rows<2>(e, row, col, valid, z);
         }
-        finish_rows<2>(e, row, col, valid, z);
       }
-    }
-  } else {
-    // a lane takes a column: 64-byte pieces of rows that start anywhere
-    if (col0 + lane < e.Q)
-      for (int h = 0; h < 32 && row0 + h < e.P; h += 8) {
-        float z[8];
+    } else {
+      // a lane takes a column: 64-byte pieces of rows that start anywhere
+      if (col0 + lane < e.Q)
+        for (int h = 0; h < 32 && row0 + h < e.P; h += 8) {
+          float z[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = buf_at(buf, h + i, lane >> 2)[lane & 3];
-        finish_column<8>(e, row0 + h, col0 + lane, z);
-      }
+          for (int i = 0; i < 8; ++i) z[i] = buf_at(buf, h + i, lane >> 2)[lane & 3];
+          finish_column<8>(e, row0 + h, col0 + lane, z);
+        }
+    }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
 // The share of CTA (pair) `split` of a split tile: its elements summed over the S partial tiles,
 // in rank order, through the epilogue.  Called by the epilogue warps.
-template <int S, int CG>
+template <int S, int CG, bool kPlain>
 __device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int unit, int split, int half) {
   int tm, tn;
   tile_of(p, unit, tm, tn);
@@ -476,7 +487,13 @@ __device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int un
       }
       const int row[1] = {row0 + r}, col = tn * p.BN + c;
       const bool valid[1] = {true};
-      if (p.e.Q % 8 == 0) {
+      if (kPlain) {
+        uint16_t* out = static_cast<uint16_t*>(p.e.out) + (size_t)row[0] * p.e.Q + col;
+        if (p.e.fp16)
+          store8(reinterpret_cast<__half*>(out), z[0]);
+        else
+          store8(reinterpret_cast<__nv_bfloat16*>(out), z[0]);
+      } else if (p.e.Q % 8 == 0) {
         finish_rows<1>(p.e, row, col, valid, z);
       } else {
 #pragma unroll
@@ -494,7 +511,11 @@ __device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int un
 //   over K = 7168 left outputs 8e-6 off (2-norm); so every kPromoteKB K blocks the accumulator
 //   is added, with rounding, to fp32 sums in the epilogue's registers, and the next block starts
 //   from zero in the other accumulator.
-template <bool kAMN, bool kBMN, int CG, bool kPromote>
+// KS: K blocks of a stage, copied, awaited and multiplied together.  2 where a stage stays at most
+//   64 KB: fewer turns of the two loops, which bound narrow tiles ([16, 4096] over K 4096 in
+//   64-column tiles 16.5 -> 12.6 us; wider stages lose at 256 columns, 129 -> 150 us for
+//   [2050, 8192] over 5120 with one CTA per MMA).
+template <bool kAMN, bool kBMN, int CG, bool kPromote, int KS>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ Gemm p) {
@@ -514,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t a_bytes = kAMN ? 128 * BK * 2 : p.a_rows * 128;
   const uint32_t b_bytes = bn_cta * 128;
   const int a_stage = kAMN ? 128 * 128 : p.a_rows * 128;
-  const int stage_bytes = a_stage + bn_cta * 128;
+  const int stage_bytes = KS * (a_stage + bn_cta * 128);
   const int splits = p.splits;
   const int rank = (CG > 1 || splits > 1) ? (int)cluster_rank() : 0;
   const int half = CG > 1 ? rank & 1 : 0;  // this CTA within its pair
@@ -549,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int units = p.units;
   const int first = p.unit0 + blockIdx.x / (splits * CG);
   const int step = splits > 1 ? units : gridDim.x / CG;  // a split tile is its cluster's only work
-  const int chunk = kPromote ? kPromoteKB : kb1 - kb0;   // K blocks added up in the tensor memory
+  const int chunk = kPromote ? kPromoteKB / KS : kb1 - kb0;  // stages added up in the tensor memory
 
   if (warp < kFirstEpi) {
     if (kPromote) setmaxnreg_dec<kLowRegs>();
@@ -582,20 +603,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             uint8_t* sA = smem + st * stage_bytes;
-            uint8_t* sB = sA + a_stage;
+            uint8_t* sB = sA + KS * a_stage;
             const uint32_t bar = full0 + st * 8;
-            if (half == 0) mbar_arrive_expect_tx(&full[st], CG * (a_bytes + b_bytes));
-            if (kAMN) {
-              tma_load<CG>(sA, &tmA, arow, kb * BK, bar, pol);
-              tma_load<CG>(sA + 8192, &tmA, arow + 64, kb * BK, bar, pol);
-            } else {
-              tma_load<CG>(sA, &tmA, kb * BK, arow, bar, pol);
-            }
-            if (kBMN) {
-              for (int g = 0; g < bn_cta / 64; ++g)
-                tma_load<CG>(sB + g * 8192, &tmB, brow + g * 64, kb * BK, bar, pol);
-            } else {
-              tma_load<CG>(sB, &tmB, kb * BK, brow, bar, pol);
+            if (half == 0) mbar_arrive_expect_tx(&full[st], CG * KS * (a_bytes + b_bytes));
+#pragma unroll
+            for (int i = 0; i < KS; ++i, sA += a_stage, sB += b_bytes) {
+              const int k = (kb * KS + i) * BK;
+              if (kAMN) {
+                tma_load<CG>(sA, &tmA, arow, k, bar, pol);
+                tma_load<CG>(sA + 8192, &tmA, arow + 64, k, bar, pol);
+              } else {
+                tma_load<CG>(sA, &tmA, k, arow, bar, pol);
+              }
+              if (kBMN) {
+                for (int g = 0; g < bn_cta / 64; ++g) tma_load<CG>(sB + g * 8192, &tmB, brow + g * 64, k, bar, pol);
+              } else {
+                tma_load<CG>(sB, &tmB, k, brow, bar, pol);
+              }
             }
             if (++st == stages) {
               st = 0;
@@ -614,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 1 && half == 0) {
       // ---------------------------------------------------------- MMA issuer
-      const uint32_t a0 = smem_u32(smem), b0 = a0 + a_stage;
+      const uint32_t a0 = smem_u32(smem), b0 = a0 + KS * a_stage;
       const uint32_t ad0 = desc_lo<kAMN>(a0), bd0 = desc_lo<kBMN>(b0);
       constexpr uint32_t kStepA = (kAMN ? 2048 : 32) >> 4, kStepB = (kBMN ? 2048 : 32) >> 4;  // 16 K elements on
       int acc = 0;
@@ -636,8 +660,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_after();
               const uint32_t at = (uint32_t)(st * stage_bytes) >> 4;
 #pragma unroll
-              for (int kk = 0; kk < BK / 16; ++kk)
-                mma<CG>(d, desc(ad0 + at + kk * kStepA), desc(bd0 + at + kk * kStepB), p.idesc, kb > kc || kk > 0);
+              for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int kk = 0; kk < BK / 16; ++kk)
+                  mma<CG>(d, desc(ad0 + at + i * (a_stage >> 4) + kk * kStepA),
+                          desc(bd0 + at + i * (b_bytes >> 4) + kk * kStepB), p.idesc, kb > kc || i > 0 || kk > 0);
               commit<CG>(&empty[st], pair_mask);
               if (++st == stages) {
                 st = 0;
@@ -700,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; i += 4)
             *reinterpret_cast<float4*>(part + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         } else {
-          finish_chunk(p.e, buf, v, row0, col0 + c, lane);
+          finish_chunk<kBMN>(p.e, buf, v, row0, col0 + c, lane);
         }
       };
       if constexpr (kPromote) {
@@ -742,11 +769,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       cluster_sync();  // every CTA's partial tile is in its shared memory
       if (splits == 2)
-        join_splits<2, CG>(p, smem, first, split, half);
+        join_splits<2, CG, kBMN>(p, smem, first, split, half);
       else if (splits == 4)
-        join_splits<4, CG>(p, smem, first, split, half);
+        join_splits<4, CG, kBMN>(p, smem, first, split, half);
       else
-        join_splits<8, CG>(p, smem, first, split, half);
+        join_splits<8, CG, kBMN>(p, smem, first, split, half);
     }
   }
 
@@ -921,9 +948,9 @@ struct Operand {
 
 int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-template <bool kAMN, bool kBMN, int CG, bool kPromote>
+template <bool kAMN, bool kBMN, int CG, bool kPromote, int KS>
 cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g, int grid, bool overlap, cudaStream_t s) {
-  auto kern = linear_gemm_kernel<kAMN, kBMN, CG, kPromote>;
+  auto kern = linear_gemm_kernel<kAMN, kBMN, CG, kPromote, KS>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
@@ -943,9 +970,13 @@ cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm
 }
 
 template <bool kAMN, bool kBMN, bool kPromote>
-cudaError_t launch_gemm(int cg, const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g, int grid, bool overlap, cudaStream_t s) {
-  return cg == 2 ? launch_gemm<kAMN, kBMN, 2, kPromote>(ma, mb, g, grid, overlap, s)
-                 : launch_gemm<kAMN, kBMN, 1, kPromote>(ma, mb, g, grid, overlap, s);
+cudaError_t launch_gemm(int cg, int ks, const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g, int grid,
+                        bool overlap, cudaStream_t s) {
+  if (cg == 2)
+    return ks == 2 ? launch_gemm<kAMN, kBMN, 2, kPromote, 2>(ma, mb, g, grid, overlap, s)
+                   : launch_gemm<kAMN, kBMN, 2, kPromote, 1>(ma, mb, g, grid, overlap, s);
+  return ks == 2 ? launch_gemm<kAMN, kBMN, 1, kPromote, 2>(ma, mb, g, grid, overlap, s)
+                 : launch_gemm<kAMN, kBMN, 1, kPromote, 1>(ma, mb, g, grid, overlap, s);
 }
 
 // Clusters of `size` GEMM CTAs that fit the device at once (a cluster lies within one group of
@@ -968,7 +999,7 @@ int cluster_slots(int size) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    auto kern = linear_gemm_kernel<false, false, 1, false>;
+    auto kern = linear_gemm_kernel<false, false, 1, false, 1>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
       (void)cudaGetLastError();
@@ -1022,7 +1053,7 @@ Plan plan_gemm(long long P, long long Q, int KB) {
 // Splits of the last, partly filled wave of tiles: `rem` tiles that would leave the other slots idle
 // for a whole K loop take a launch of their own, several CTAs (pairs) to a tile, when that saves
 // more than its launch and join cost (about 6 us; the dense dx of 2050 x 5120 over 8192, 152
-// tiles and 28 more on 76 pairs, 122 -> XX us).
+// tiles and 28 more on 76 pairs, 122 -> 117 us).
 int tail_splits(const Plan& p, long long rem, int KB) {
   int s = 1;
   while (2 * s * p.cg <= 8 && rem <= cluster_slots(2 * s * p.cg) && KB >= 16 * s) s *= 2;
@@ -1044,7 +1075,10 @@ moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue&
   const long long units = (long long)g.tiles_m * g.tiles_n;
   if (units > 2147483647LL / 16) return MOE_ERR_UNSUPPORTED;
   g.a_rows = A.mn || e.P >= BM ? BM : (e.P + 7) / 8 * 8;
-  g.stages = kStageBudget / ((g.a_rows + p.bn / p.cg) * 128);
+  const int ks = p.bn <= 128 ? 2 : 1;
+  const int blocks = g.KB;
+  g.KB = cdiv(blocks, ks);
+  g.stages = kStageBudget / (ks * (g.a_rows + p.bn / p.cg) * 128);
   if (g.stages > kMaxStages) g.stages = kMaxStages;
   g.idesc = make_idesc(e.fp16 ? 0 : 1, BM * p.cg, p.bn) | (A.mn ? 1u << 15 : 0) | (B.mn ? 1u << 16 : 0);
   CUtensorMap ma, mb;
@@ -1060,16 +1094,16 @@ moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue&
     const long long ctas = (last - first) * splits * p.cg;
     const int most = cluster_slots(p.cg) * p.cg;
     const int grid = (int)(splits > 1 || ctas < most ? ctas : most);
-    const cudaError_t err = A.mn      ? launch_gemm<true, true, false>(p.cg, ma, mb, g, grid, overlap, s)
-                            : B.mn    ? launch_gemm<false, true, false>(p.cg, ma, mb, g, grid, overlap, s)
-                            : promote ? launch_gemm<false, false, true>(p.cg, ma, mb, g, grid, overlap, s)
-                                      : launch_gemm<false, false, false>(p.cg, ma, mb, g, grid, overlap, s);
+    const cudaError_t err = A.mn      ? launch_gemm<true, true, false>(p.cg, ks, ma, mb, g, grid, overlap, s)
+                            : B.mn    ? launch_gemm<false, true, false>(p.cg, ks, ma, mb, g, grid, overlap, s)
+                            : promote ? launch_gemm<false, false, true>(p.cg, ks, ma, mb, g, grid, overlap, s)
+                                      : launch_gemm<false, false, false>(p.cg, ks, ma, mb, g, grid, overlap, s);
     overlap = true;
     return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   };
   const int slots = cluster_slots(p.cg);
   const long long rem = p.splits == 1 && units > slots ? units % slots : 0;
-  const int tail = rem ? tail_splits(p, rem, g.KB) : 1;
+  const int tail = rem ? tail_splits(p, rem, blocks) : 1;
   if (tail == 1) return launch(0, units, p.splits);
   const moe_status_t st = launch(0, units - rem, 1);
   return st != MOE_OK ? st : launch(units - rem, units, tail);
