@@ -32,19 +32,21 @@ constexpr uint32_t kMaskedKey = 0x007fffffu;  // the key of -inf: a masked exper
 // An unsigned integer ordered like the float (never 0 for a number; -0 counts as +0).
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t u = __float_as_uint(x + 0.0f);
-  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
 // A logit as the router counts it: NaN as -inf (masked), +inf as the largest finite number.
-__device__ __forceinline__ float clean_logit(float x) { return x != x ? -INFINITY : fminf(x, 3.402823466e38f); }
+__device__ __forceinline__ float clean_logit(float x) {
+  return fminf(fmaxf(x, -INFINITY), 3.402823466e38f);  // (the maximum of a NaN and a number is the number)
+}
 
 // By exp(-|l|), so that very negative logits keep their relative accuracy.
 __device__ __forceinline__ float sigmoid32(float l) {
   const float e = expf(-fabsf(l));
-  return __fdiv_rn(l < 0.f ? e : 1.0f, 1.0f + e);
+  return __fdividef(l < 0.f ? e : 1.0f, 1.0f + e);  // (the divisor lies in [1, 2])
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -140,9 +142,9 @@ struct PairScores {
   static __device__ __forceinline__ uint64_t key(V v) { return ((uint64_t)order_key(v.h) << 32) | order_key(v.l); }
   static __device__ __forceinline__ V value(uint64_t k) { return {key_value((uint32_t)(k >> 32)), key_value((uint32_t)k)}; }
   // x >= y cannot be told from y (the scores are within 2^-42 or so of the exact ones)
-  static __device__ bool near(uint64_t kx, uint64_t ky) {
+  static __device__ bool near(uint64_t kx, uint64_t ky, float more = 0.f) {
     const FF x = value(kx), y = value(ky);
-    return !((x.h - y.h) + (x.l - y.l) > 0x1p-39f + 0x1p-40f * (fabsf(x.h) + fabsf(y.h)));
+    return !((x.h - y.h) + (x.l - y.l) > more + 0x1p-39f + 0x1p-40f * (fabsf(x.h) + fabsf(y.h)));
   }
 };
 struct DoubleScores {
@@ -159,7 +161,7 @@ struct DoubleScores {
   static __device__ __forceinline__ V value(uint64_t k) {
     return __longlong_as_double((long long)(k ^ ((k >> 63) ? 0x8000000000000000ull : ~0ull)));
   }
-  static __device__ bool near(uint64_t, uint64_t) { return false; }  // equal ones go by logit and index
+  static __device__ bool near(uint64_t, uint64_t, float = 0.f) { return false; }  // equal ones go by logit and index
 };
 
 constexpr uint64_t kMasked64 = 1;  // below the key of every number, above a chosen expert's 0
@@ -297,20 +299,27 @@ __device__ __noinline__ int rank_again(const TL* row, const RouteArgs& a, bool* 
   return mine;
 }
 
+__device__ __forceinline__ FF sigmoid_ff(float l) {
+  const FF e = exp_ff({-fabsf(l), 0.f});
+  return div(l < 0.f ? e : FF{1.f, 0.f}, add({1.f, 0.f}, e));
+}
+
 // Lane i < n has candidate id: lane j gets the j-th of them (n <= 32) by the scores in pairs of
-// floats, of a sigmoid router or of one without a bias (softmax scores under a bias need the
-// denominator in pairs too: rank_again).
+// floats.  m, den: the row's softmax, den within 2^-22 (an error in it moves all scores of the row
+// by one factor, so it counts by the scores' difference).
 template <class TL>
-__device__ __noinline__ int rank_candidates(const TL* row, const RouteArgs& a, int id, int n, bool* unsure) {
+__device__ __noinline__ int rank_candidates(const TL* row, const RouteArgs& a, int id, int n, float m, FF den,
+                                            bool* unsure) {
   const int lane = threadIdx.x & 31;
   float l = -INFINITY, b = 0.f;
   if (lane < n) expert_inputs(row, a.bias, id, l, b);
   uint64_t c = 0;
+  FF s{0.f, 0.f};
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
   if (a.bias == nullptr) {
     c = (uint64_t)order_key(l) << 32;
   } else {
-    const FF e = exp_ff({-fabsf(l), 0.f});
-    const FF s = div(l < 0.f ? e : FF{1.f, 0.f}, add({1.f, 0.f}, e));
+    s = softmax ? div(exp_ff(two_sum(l, -m)), den) : sigmoid_ff(l);
     c = l == -INFINITY ? kMasked64 : PairScores::key(b == INFINITY ? FF{b, 0.f} : add(s, {b, 0.f}));
   }
   int rank = 0;
@@ -322,7 +331,9 @@ __device__ __noinline__ int rank_candidates(const TL* row, const RouteArgs& a, i
     const int oid = __shfl_sync(kFull, id, j);
     const bool same = ol == l && ob == b;  // equal scores: the lower index first
     rank += same ? oid < id : o > c;
-    doubt |= a.bias != nullptr && !same && lane < n && min(o, c) > kMasked64 && PairScores::near(max(o, c), min(o, c));
+    const float apart = softmax ? 0x1p-22f * fabsf(__shfl_sync(kFull, s.h, j) - s.h) : 0.f;
+    doubt |= a.bias != nullptr && !same && lane < n && min(o, c) > kMasked64 &&
+             PairScores::near(max(o, c), min(o, c), apart);
   }
   *unsure = __any_sync(kFull, doubt);
   int got = 0;
@@ -353,7 +364,82 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[NV]) {
           if (i + j + k < NV && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order2(key[i + j], key[i + j + k]);
 }
 
-// NV: experts held by a lane, a power of two.  TL: type of the logits.
+// Distances below which two ranking scores may be in the wrong order.  __expf(-x) is within
+// (2 + 1.2 x) 2^-23 of its value.  Sigmoid: that moves s by at most 0.65 2^-23, the sum and the
+// division (2 ulp) by 2.5 2^-23: two scores are within 2^-20.3.  Softmax: a score's own exponential
+// and division give 2^-21; the denominator moves all scores of a row by one common factor, within
+// 2^-18.2 (its terms' errors weighed by the terms, whose mean x is at most ln E, and up to 69
+// additions): 2^-17.6 for two.  Adding the bias rounds by 2^-24 |c| and cutting the places off the
+// keys by NV 2^-23 |c| (cut).
+struct Doubt {
+  bool by_logit, exact16;  // ranked by logits; they fit the keys whole (16-bit types)
+  float tol0, cut;
+  // x >= y are two keys (without places): may their experts be in the other order?
+  __device__ __forceinline__ bool of(uint32_t kx, uint32_t ky, uint32_t none) const {
+    if (ky <= none) return false;
+    if (by_logit) return !exact16 && kx == ky;
+    const float x = key_value(kx), y = key_value(ky);
+    return !(x - y > tol0 + cut * (fabsf(x) + fabsf(y)));
+  }
+  // the same for the scores of the last group kept and the best left out, err from the cuts
+  __device__ __forceinline__ bool groups(uint32_t kx, uint32_t ky, float err) const {
+    const float x = key_value(kx), y = key_value(ky);
+    float tol = 2.f * (tol0 + err) + 0x1p-22f * (fabsf(x) + fabsf(y));
+    // without a bias the errors are relative too (the exponential's at most (2 + 1.2 88) 2^-23, the
+    // cut logits' err): sums of small scores are told apart by their own size
+    if (by_logit) tol = fminf(tol, (0x1p-15f + 8.f * cut) * (x + y) + 2.f * err * (x + y));
+    return !(x - y > tol);
+  }
+};
+
+// A score for ranking alone, by the fast exponential and division.
+__device__ __forceinline__ float rank_score(float x, bool softmax, float m, float rden) {
+  const float e = __expf(softmax ? x - m : -fabsf(x));
+  return softmax ? e * rden : __fdividef(x < 0.f ? e : 1.0f, 1.0f + e);
+}
+
+// A group's score as an ordered key, from its two best keys (`none`: a masked one); err: how far the
+// places cut off the keys may have moved it.
+__device__ __forceinline__ uint32_t group_score(uint32_t top, uint32_t second, uint32_t none, bool sums, bool by_logit,
+                                                bool softmax, float m, float rden, float cut, float& err) {
+  err = 0.f;
+  if (top <= none) return top;  // (a masked group keeps the masked key)
+  if (!sums) {
+    if (!by_logit) err = cut * fabsf(key_value(top));
+    return top;
+  }
+  float x = key_value(top), y = second > none ? key_value(second) : 0.f;
+  err = cut * (fabsf(x) + fabsf(y));
+  if (by_logit) {
+    // the cut logits' distance moves a sigmoid by less than 0.3 of its relative size, a softmax
+    // numerator by all of it
+    x = rank_score(x, softmax, m, rden);
+    y = second > none ? rank_score(y, softmax, m, rden) : 0.f;
+  }
+  return order_key(x + y);
+}
+
+// The weight (before the scale) of a lane's choice with logit lj (-inf: masked, or no choice); m and
+// den: the row's softmax.  Called by the whole warp.
+__device__ __forceinline__ float choice_weight(const RouteArgs& a, float lj, float m, float den) {
+  const bool live = lj > -INFINITY, softmax = a.score == MOE_SCORE_SOFTMAX;
+  if (!a.renorm) return !live ? 0.f : softmax ? __fdividef(expf(lj - m), den) : sigmoid32(lj);
+  // s_j / sum s is the same for scores scaled by one factor: softmax numerators relative to the
+  // largest chosen, sigmoid scores by e^-m (m = the largest chosen logit when all are negative)
+  // so that none underflows
+  const float top = warp_max(lj);
+  float s = 0.f;
+  if (live) {
+    if (softmax)
+      s = expf(lj - top);
+    else
+      s = top < 0.f ? __fdividef(expf(lj - top), 1.0f + expf(lj)) : sigmoid32(lj);
+  }
+  const float sum = warp_sum(s);
+  return sum > 0.f ? __fdividef(s, sum) : 0.f;  // (the sum lies in [1/2, 32])
+}
+
+// One token by one warp.  NV: experts held by a lane, a power of two.  TL: type of the logits.
 template <int NV, class TL>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     route_grouped_kernel(const RouteArgs a, int32_t* __restrict__ topk_ids, float* __restrict__ topk_weights) {
@@ -390,11 +476,6 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     den = warp_sum(den);
   }
   const float rden = __fdividef(1.0f, den);
-  // A score for ranking alone, by the fast exponential and division (see tol0 below).
-  auto rank_score = [&](float x) {
-    const float e = __expf(softmax ? x - m : -fabsf(x));
-    return softmax ? e * rden : __fdividef(x < 0.f ? e : 1.0f, 1.0f + e);
-  };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const float x = clean_logit(l[i]);
@@ -403,21 +484,13 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
       k = order_key(x);
     } else {
       const bool gone = x == -INFINITY || b[i] != b[i] || b[i] == -INFINITY;
-      k = gone ? kMaskedKey : order_key(rank_score(x) + b[i]);
+      k = gone ? kMaskedKey : order_key(rank_score(x, softmax, m, rden) + b[i]);
     }
     key[i] = i < cnt ? (k & ~kPlace) | (kPlace - i) : 0u;
   }
   if (kSorted) sort_keys(key);
 
-  // Distances below which two ranking scores may be in the wrong order.  __expf(-x) is within
-  // (2 + 1.2 x) 2^-23 of its value.  Sigmoid: that moves s by at most 0.65 2^-23, the sum and the
-  // division (2 ulp) by 2.5 2^-23: two scores are within 2^-20.3.  Softmax: a score's own exponential
-  // and division give 2^-21; the denominator moves all scores of a row by one common factor, within
-  // 2^-18.2 (its terms' errors weighed by the terms, whose mean x is at most ln E, and up to 69
-  // additions): 2^-17.6 for two.  Adding the bias rounds by 2^-24 |c| and cutting the places off the
-  // keys by NV 2^-23 |c|.
-  const float tol0 = softmax ? 0x1p-17f : 0x1p-20f;
-  constexpr float kCut = (NV + 2) * 0x1p-23f;
+  const Doubt doubt{by_logit, sizeof(TL) == 2, softmax ? 0x1p-17f : 0x1p-20f, (NV + 2) * 0x1p-23f};
   bool unsure = false;
 
   if (a.n_group > 1) {
@@ -443,21 +516,8 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
       second = max(min(top, x), max(second, y));
       top = max(top, x);
     }
-    uint32_t score = top;
-    float err = 0.f;  // how far the group's score may be off
-    if (a.group_top == 2 && top > kNone) {  // (a masked group keeps the masked key)
-      float x = key_value(top), y = second > kNone ? key_value(second) : 0.f;
-      err = kCut * (fabsf(x) + fabsf(y));
-      if (by_logit) {
-        // the cut logits' distance moves a sigmoid by less than 0.3 of its relative size, a softmax
-        // numerator by all of it
-        x = rank_score(x);
-        y = second > kNone ? rank_score(y) : 0.f;
-      }
-      score = order_key(x + y);
-    } else if (top > kNone) {
-      err = by_logit ? 0.f : kCut * fabsf(key_value(top));
-    }
+    float err;
+    const uint32_t score = group_score(top, second, kNone, a.group_top == 2, by_logit, softmax, m, rden, doubt.cut, err);
     int rank = 0;
 #pragma unroll 4
     for (int g = 0; g < a.n_group; ++g) {
@@ -467,11 +527,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     const bool keep = rank < a.topk_group && grp < a.n_group;
     const uint32_t last = __reduce_min_sync(kFull, keep ? score : kFull);
     const uint32_t left = __reduce_max_sync(kFull, keep || grp >= a.n_group ? 0u : score);  // 0: none left out
-    if (left > kNone && !exact) {
-      const float x = key_value(last), y = key_value(left);
-      const float e = warp_max(err);
-      unsure = !(x - y > 2.f * (tol0 + e) + 0x1p-22f * (fabsf(x) + fabsf(y)));
-    }
+    if (left > kNone && !exact) unsure = doubt.groups(last, left, warp_max(err));
     if (!keep) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) key[i] = 0;
@@ -492,13 +548,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     return h;
   };
   uint32_t h = head();
-  // x >= y are two keys: may the experts be in the other order?
-  auto in_doubt = [&](uint32_t kx, uint32_t ky) {
-    if (ky <= kNone) return false;
-    if (by_logit) return sizeof(TL) == 4 && kx == ky;  // (16-bit logits fit the key: equal ones are equal)
-    const float x = key_value(kx), y = key_value(ky);
-    return !(x - y > tol0 + kCut * (fabsf(x) + fabsf(y)));
-  };
+  auto in_doubt = [&](uint32_t kx, uint32_t ky) { return doubt.of(kx, ky, kNone); };
 #pragma unroll 1
   for (;; ++r) {
     const uint32_t top = __reduce_max_sync(kFull, h & ~kPlace);
@@ -539,7 +589,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
   if (near && softmax && !by_logit) unsure = true;
   if (near && !unsure) {
     // the r candidates, one a lane, ranked by their exact scores
-    my_id = rank_candidates(row, a, my_id, r, &unsure);
+    my_id = rank_candidates(row, a, my_id, r, m, FF{1.f, 0.f}, &unsure);
   }
   if (unsure) {
     my_id = rank_again<PairScores, NV, TL>(row, a, &unsure);
@@ -549,24 +599,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
   // weights: lane j has the j-th choice
   float lj = -INFINITY, bj = 0.f;
   if (lane < a.top_k) expert_inputs(row, a.bias, my_id, lj, bj);
-  const bool live = lj > -INFINITY;
-  float w;
-  if (a.renorm) {
-    // s_j / sum s is the same for scores scaled by one factor: softmax numerators relative to the
-    // largest chosen, sigmoid scores by e^-m (m = the largest chosen logit when all are negative)
-    // so that none underflows
-    const float top = warp_max(lj);
-    float s = 0.f;
-    if (live) {
-      if (softmax)
-        s = expf(lj - top);
-      else
-        s = top < 0.f ? __fdiv_rn(expf(lj - top), 1.0f + expf(lj)) : sigmoid32(lj);
-    }
-    const float sum = warp_sum(s);
-    w = sum > 0.f ? __fdiv_rn(s, sum) : 0.f;
-  } else if (softmax) {
-    // the denominator again, by the accurate exponential
+  if (softmax && !a.renorm) {  // the denominator again, by the accurate exponential
     den = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -574,10 +607,266 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
       if (x > -INFINITY) den += expf(x - m);
     }
     den = warp_sum(den);
-    w = live ? __fdiv_rn(expf(lj - m), den) : 0.f;
-  } else {
-    w = live ? sigmoid32(lj) : 0.f;
   }
+  const float w = choice_weight(a, lj, m, den);
+  if (lane < a.top_k) {
+    topk_ids[(size_t)t * a.top_k + lane] = my_id;
+    topk_weights[(size_t)t * a.top_k + lane] = w * a.scale;
+  }
+}
+
+// Up to 8 choices among up to 8 experts a lane, one token by one warp, without rounds: every lane
+// sorts its keys, and five butterfly steps merge the lists of two lanes into the best 8 of both,
+// so that all lanes end with the chosen 8 in order.  A merge of two sorted lists of 8 takes 8
+// shuffles, 8 maxima (of one list against the other reversed, which leaves the best 8 as a
+// bitonic sequence) and 12 comparators.  The keys carry the expert's place in the warp in their low
+// bits (8 of them for 256 experts), so a key names its expert; the cut makes a few tokens in a
+// hundred doubtful, whose candidates are ranked exactly.  Against rounds of redux.sync (the
+// kernel above): XX instructions a token instead of 1320, 16384 tokens of 256 experts (4 of 8 groups,
+// bias) XX us instead of 33, one token XX instead of 4.2.
+constexpr int kFew = 8;
+
+// a[0..N) is bitonic: sorted descending
+template <int N, int M>
+__device__ __forceinline__ void bitonic_sort(uint32_t (&a)[M]) {
+#pragma unroll
+  for (int k = N / 2; k >= 1; k /= 2)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((i & k) == 0) order2(a[i], a[i + k]);
+}
+// The best kFew of the warp's lists of LEN sorted keys; OFF: lanes merged so far.
+template <int LEN, int OFF>
+__device__ __forceinline__ void merge_lists(uint32_t (&a)[kFew]) {
+  if constexpr (OFF < 32) {
+    uint32_t o[LEN];
+#pragma unroll
+    for (int i = 0; i < LEN; ++i) o[i] = __shfl_xor_sync(kFull, a[i], OFF);
+    if constexpr (LEN < kFew) {
+#pragma unroll
+      for (int i = 0; i < LEN; ++i) a[LEN + i] = o[LEN - 1 - i];
+      bitonic_sort<2 * LEN>(a);
+      merge_lists<2 * LEN, 2 * OFF>(a);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) a[i] = max(a[i], o[kFew - 1 - i]);
+      bitonic_sort<kFew>(a);
+      merge_lists<kFew, 2 * OFF>(a);
+    }
+  }
+}
+
+template <int NV, class TL>
+__global__ void __launch_bounds__(kWarpsPerBlock * 32)
+    route_grouped_merge_kernel(const RouteArgs a, int32_t* __restrict__ topk_ids, float* __restrict__ topk_weights) {
+  constexpr uint32_t kPlace = 32 * NV - 1;  // the key bits that hold kPlace - (place in the warp)
+  constexpr uint32_t kNone = kMaskedKey & ~kPlace;
+  const int t = blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const int lane = threadIdx.x & 31;
+  const TL* row = static_cast<const TL*>(a.logits) + (size_t)t * a.E;
+  const bool by_logit = a.bias == nullptr, softmax = a.score == MOE_SCORE_SOFTMAX;
+  const int lpg = a.lpg, size = a.E / a.n_group, lane_shift = __ffs(lpg) - 1;
+  const int grp = lane >> lane_shift, in = (lane & (lpg - 1)) * NV;
+  const int base = grp * size + in;
+  const int cnt = grp < a.n_group ? min(NV, size - in) : 0;  // (may be negative: none)
+
+  float m = 0.f, den = 1.f;
+  uint32_t key[NV];
+  {
+    float l[NV];
+    load_lane<NV>(row + base, cnt, size, l);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) l[i] = clean_logit(l[i]);
+    // the row's largest logit and the softmax's denominator, where a score is needed
+    if (softmax && (!by_logit || !a.renorm || (a.n_group > 1 && a.group_top == 2))) {
+      m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) m = fmaxf(m, l[i]);
+      m = warp_max(m);
+      den = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (l[i] > -INFINITY) den += expf(l[i] - m);
+      den = warp_sum(den);
+    }
+    if (by_logit) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) key[i] = order_key(l[i]);
+    } else {
+      float b[NV];
+      load_lane<NV>(a.bias + base, cnt, size, b);
+      const float rden = __fdividef(1.0f, den);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        // (a NaN or -inf bias masks: the sum is then NaN or -inf too)
+        const float c = rank_score(l[i], softmax, m, rden) + b[i];
+        key[i] = l[i] > -INFINITY && c > -INFINITY ? order_key(c) : kMaskedKey;
+      }
+    }
+    if (cnt < NV) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (i >= cnt) key[i] = 0;
+    }
+  }
+  Doubt doubt{by_logit, sizeof(TL) == 2, softmax ? 0x1p-17f : 0x1p-20f, 0x1p-22f};
+  bool unsure = false, dropped = false;
+
+  if (a.n_group > 1) {
+    uint32_t top = 0, second = 0;  // whole keys: the groups' order is hardly ever in doubt
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      second = max(second, min(top, key[i]));
+      top = max(top, key[i]);
+    }
+    for (int off = 1; off < lpg; off <<= 1) {
+      const uint32_t x = __shfl_xor_sync(kFull, top, off), y = __shfl_xor_sync(kFull, second, off);
+      second = max(min(top, x), max(second, y));
+      top = max(top, x);
+    }
+    float err;
+    const uint32_t score = group_score(top, second, kMaskedKey, a.group_top == 2, by_logit, softmax, m,
+                                       __fdividef(1.0f, den), doubt.cut, err);
+    int rank = 0;
+#pragma unroll 4
+    for (int g = 0; g < a.n_group; ++g) {
+      const uint32_t o = __shfl_sync(kFull, score, g << lane_shift);
+      rank += o > score || (o == score && g < grp);
+    }
+    const bool in_use = grp < a.n_group;
+    bool keep = in_use && rank < a.topk_group;
+    const uint32_t last = __reduce_min_sync(kFull, keep ? score : kFull);
+    const uint32_t left = __reduce_max_sync(kFull, keep || !in_use ? 0u : score);  // 0: none left out
+    if (left > kMaskedKey && !(by_logit && a.group_top == 1)) {
+      err = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(err)));
+      if (doubt.groups(last, left, err)) {
+        // Which of two groups?  Exactly, if only they are in doubt, from their group_top best experts
+        // if these are surely the best: one expert a lane, 0 and 1 of the last group kept, 2 and 3
+        // of the first left out.
+        const uint32_t above = __reduce_min_sync(kFull, in_use && rank < a.topk_group - 1 ? score : kFull);
+        const uint32_t below = __reduce_max_sync(kFull, in_use && rank > a.topk_group ? score : 0u);
+        unsure = (softmax && !by_logit) || (above != kFull && doubt.groups(above, left, err)) ||
+                 (below > kMaskedKey && doubt.groups(last, below, err));
+        const int ga = __shfl_sync(kFull, grp, __ffs(__ballot_sync(kFull, in_use && rank == a.topk_group - 1)) - 1);
+        const int gb = __shfl_sync(kFull, grp, __ffs(__ballot_sync(kFull, in_use && rank == a.topk_group)) - 1);
+        int id = -1;
+#pragma unroll 1
+        for (int g = 0; g < 2; ++g) {
+          const int want = g ? gb : ga;
+          uint32_t prev = 0;
+          int first = -1;
+#pragma unroll 1
+          for (int j = 0; j <= a.group_top; ++j) {  // (the last of them: the best expert that does not count)
+            uint32_t v = 0;
+            int at = -1;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+              if (grp == want && (j == 0 || key[i] < prev || (key[i] == prev && base + i > first)) && key[i] > v) {
+                v = key[i];
+                at = base + i;
+              }
+            const uint32_t best_key = __reduce_max_sync(kFull, v);
+            const int w = __ffs(__ballot_sync(kFull, v == best_key)) - 1, e = __shfl_sync(kFull, at, w);
+            if (j == a.group_top)
+              unsure |= !by_logit && best_key > kMaskedKey && doubt.of(prev, best_key, kMaskedKey);
+            else if (lane == 2 * g + j && best_key > kMaskedKey)
+              id = e;
+            prev = best_key;
+            first = e;
+          }
+        }
+        if (!unsure) {
+          FF c{0.f, 0.f};
+          if (id >= 0) {
+            float x, b;
+            expert_inputs(row, a.bias, id, x, b);
+            c = softmax ? exp_ff(two_sum(x, -m)) : sigmoid_ff(x);  // (a softmax's numerators order like its scores)
+            c = b == INFINITY ? FF{b, 0.f} : add(c, {b, 0.f});
+          }
+          const FF o = PairScores::shfl(c, 1);
+          c = c.h == INFINITY || o.h == INFINITY ? FF{fmaxf(c.h, o.h), 0.f} : add(c, o);
+          const uint64_t sa = __shfl_sync(kFull, PairScores::key(c), 0), sb = __shfl_sync(kFull, PairScores::key(c), 2);
+          unsure = PairScores::near(max(sa, sb), min(sa, sb));
+          if (sb > sa) keep = (keep && grp != ga) || (in_use && grp == gb);
+        }
+      }
+    }
+    dropped = !keep;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) key[i] = key[i] && !dropped ? (key[i] & ~kPlace) | (kPlace - (lane * NV + i)) : 0u;
+  doubt.cut = (32 * NV + 2) * 0x1p-23f;
+  sort_keys(key);
+
+  uint32_t best[kFew];
+#pragma unroll
+  for (int i = 0; i < kFew; ++i) best[i] = i < NV ? key[i < NV ? i : 0] : 0u;
+  merge_lists<NV, 1>(best);
+
+  // lane r holds the r-th best; the first left out (none: 0) after them
+  auto next_below = [&](uint32_t bound) {  // the warp's largest key below bound
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v = max(v, key[i] < bound ? key[i] : 0u);
+    return __reduce_max_sync(kFull, v);
+  };
+  uint32_t mine = 0;
+#pragma unroll
+  for (int i = 0; i < kFew; ++i) mine = lane == i ? best[i] : mine;
+  if (a.top_k == kFew) {
+    const uint32_t v = next_below(best[kFew - 1]);
+    if (lane == kFew) mine = v;
+  }
+  auto expert_of = [&](uint32_t k) {
+    const int pos = (int)(kPlace - (k & kPlace)), ln = pos / NV;
+    return k ? (ln >> lane_shift) * size + (ln & (lpg - 1)) * NV + pos % NV : 0;
+  };
+  int my_id = expert_of(mine);
+  float lj = -INFINITY, bj = 0.f;
+  if (lane <= a.top_k && mine) expert_inputs(row, a.bias, my_id, lj, bj);
+  {
+    // doubt between neighbours, unless they are equal in logit and bias
+    const uint32_t next = __shfl_down_sync(kFull, mine, 1) & ~kPlace;
+    const float ln = __shfl_down_sync(kFull, lj, 1), bn = __shfl_down_sync(kFull, bj, 1);
+    const bool near =
+        __any_sync(kFull, lane < a.top_k && doubt.of(mine & ~kPlace, next, kNone) && !(ln == lj && bn == bj));
+    if (near || unsure) {
+      if (!unsure) {
+        // the candidates, one a lane: all that are not surely below the last choice
+        const uint32_t last = __shfl_sync(kFull, mine, a.top_k - 1);
+        uint32_t low = last;
+        int n = a.top_k;
+        while (true) {
+          low = next_below(low);
+          if (!doubt.of(last & ~kPlace, low & ~kPlace, kNone)) break;
+          if (n == 32) {
+            unsure = true;
+            break;
+          }
+          if (lane == n) my_id = expert_of(low);
+          ++n;
+        }
+        FF sum{0.f, 0.f};  // the softmax's denominator: its terms are within 1 ulp, their sum adds nothing
+        if (softmax && !by_logit) {
+#pragma unroll 1
+          for (int i = 0; i < cnt; ++i) {
+            const float x = clean_logit(load1(row + base + i));
+            if (x > -INFINITY) sum = add(sum, {expf(x - m), 0.f});
+          }
+#pragma unroll 1
+          for (int off = 16; off > 0; off >>= 1) sum = add(sum, PairScores::shfl(sum, off));
+        }
+        if (!unsure) my_id = rank_candidates(row, a, my_id, n, m, sum, &unsure);
+      }
+      if (unsure) my_id = rank_again<PairScores, NV, TL>(row, a, &unsure);
+      if (unsure) my_id = rank_again<DoubleScores, NV, TL>(row, a, &unsure);
+      lj = -INFINITY;
+      if (lane < a.top_k) expert_inputs(row, a.bias, my_id, lj, bj);
+    }
+  }
+  if (lane >= a.top_k) lj = -INFINITY;
+  const float w = choice_weight(a, lj, m, den);
   if (lane < a.top_k) {
     topk_ids[(size_t)t * a.top_k + lane] = my_id;
     topk_weights[(size_t)t * a.top_k + lane] = w * a.scale;
@@ -620,45 +909,49 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
       if (a.score == MOE_SCORE_SOFTMAX) {
         s = expf(lj - top);
       } else {
-        s = top < 0.f ? __fdiv_rn(expf(lj - top), 1.0f + expf(lj)) : sigmoid32(lj);
+        s = top < 0.f ? __fdividef(expf(lj - top), 1.0f + expf(lj)) : sigmoid32(lj);
         f = sigmoid32(-lj);  // 1 - s without the cancellation
       }
     }
     const float sum = warp_sum(s);
-    const float p = sum > 0.f ? __fdiv_rn(s, sum) : 0.f;
+    const float p = sum > 0.f ? __fdividef(s, sum) : 0.f;
     const float mean = warp_sum(p * dw);
     d = p * f * (dw - mean);
   } else if (a.score == MOE_SCORE_SIGMOID) {
     if (live) d = dw * sigmoid32(lj) * sigmoid32(-lj);
   }
-  float s[NV], dot = 0.f;
   if (!a.renorm && a.score == MOE_SCORE_SOFTMAX) {
+    float s[NV];
     load_lane<NV>(row + lane * NV, a.E - lane * NV, a.E, s);
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       s[i] = clean_logit(s[i]);
-      if (lane * NV + i < a.E) m = fmaxf(m, s[i]);
+      m = fmaxf(m, s[i]);
     }
     m = warp_max(m);
     float den = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      s[i] = (lane * NV + i < a.E && s[i] > -INFINITY) ? expf(s[i] - m) : 0.f;
+      s[i] = s[i] > -INFINITY ? expf(s[i] - m) : 0.f;
       den += s[i];
     }
     den = warp_sum(den);
-    d = live ? dw * __fdiv_rn(expf(lj - m), den) : 0.f;  // g_j s_j
-    dot = warp_sum(d);
-    const float rden = den > 0.f ? __fdiv_rn(-dot, den) : 0.f;
+    d = live ? dw * __fdividef(expf(lj - m), den) : 0.f;  // g_j s_j
+    const float dot = warp_sum(d), rden = den > 0.f ? __fdividef(-dot, den) : 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) s[i] *= rden;
+    if constexpr (NV >= 4) {
+#pragma unroll
+      for (int i = 0; i < NV; i += 4)
+        *reinterpret_cast<float4*>(buf + lane * NV + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) buf[lane * NV + i] = s[i];
+    }
   } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = 0.f;
+    for (int i = lane * 4; i < 32 * NV; i += 128) *reinterpret_cast<float4*>(buf + i) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) buf[lane * NV + i] = s[i];
   __syncwarp();
   // an id chosen twice adds up, in the order of the choices
   const uint32_t same = __match_any_sync(kFull, id < 0 ? -1 - lane : id);
@@ -727,14 +1020,24 @@ extern "C" moe_status_t moe_route_grouped(const void* logits, moe_dtype_t logits
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   a.lpg = lanes_per_group(cfg->n_group);
   const int size = E / cfg->n_group;
-  for_nv((size + a.lpg - 1) / a.lpg, [&](auto nv) {
-    constexpr int NV = decltype(nv)::value;
+  auto with_type = [&](auto f) {
     if (logits_dtype == MOE_DT_FP32)
-      route_grouped_kernel<NV, float><<<grid, block, 0, s>>>(a, topk_ids, topk_weights);
+      f(float());
     else if (logits_dtype == MOE_DT_BF16)
-      route_grouped_kernel<NV, __nv_bfloat16><<<grid, block, 0, s>>>(a, topk_ids, topk_weights);
+      f(__nv_bfloat16());
     else
-      route_grouped_kernel<NV, __half><<<grid, block, 0, s>>>(a, topk_ids, topk_weights);
+      f(__half());
+  };
+  for_nv((size + a.lpg - 1) / a.lpg, [&](auto n) {
+    constexpr int NV = decltype(n)::value;
+    with_type([&](auto tl) {
+      if constexpr (NV <= 8)
+        if (top_k <= kFew) {
+          route_grouped_merge_kernel<NV, decltype(tl)><<<grid, block, 0, s>>>(a, topk_ids, topk_weights);
+          return;
+        }
+      route_grouped_kernel<NV, decltype(tl)><<<grid, block, 0, s>>>(a, topk_ids, topk_weights);
+    });
   });
   return launch_status();
 }
