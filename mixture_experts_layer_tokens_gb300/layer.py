@@ -10,6 +10,9 @@ promise), it runs on a second stream forked at the start of the step and joined
 before the finalize, so its GEMMs overlap the routing, quantisation, gather and the
 routed experts' GEMMs (which take their units from a counter, so CTAs that start
 late because the shared expert still holds their SMs take fewer units).
+A layer with a MoERouter makes its logits itself (moe_linear on the hidden states, then
+moe_route_grouped in place of moe_route), and its router can be trained beside fixed
+experts: moe_finalize_backward, moe_route_grouped_backward, moe_linear_backward.
 NVFP4 layers use moe_prepare_nvfp4 and moe_experts_nvfp4 (the shared expert
 stays bf16).  Single-launch layers run the whole step as one moe_layer_fused launch.
 
@@ -26,10 +29,66 @@ from . import moe
 from .inputs import LayerConfig, LayerInputs
 
 
+class MoERouter:
+    """The router with its gate: hidden states -> logits (``moe_linear``) -> choice and weights
+    (``moe_route_grouped``), and the gradients back (``moe_route_grouped_backward``,
+    ``moe_linear_backward``), every buffer allocated once.
+
+    gate_w [E, H] and gate_bias [E] (None: none) bf16 or fp16; balance_bias [E] fp32 (None: none) steers the
+    choice alone.  The logits are fp32.  The other arguments are moe_route_grouped's."""
+
+    def __init__(self, T: int, gate_w: torch.Tensor, top_k: int, gate_bias: Optional[torch.Tensor] = None,
+                 balance_bias: Optional[torch.Tensor] = None, score: str = "sigmoid", n_group: int = 1,
+                 topk_group: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0):
+        self.gate_w, self.gate_bias, self.balance_bias = gate_w, gate_bias, balance_bias
+        (E, H), dev = gate_w.shape, gate_w.device
+        self.T, self.E, self.top_k = T, E, top_k
+        self.weigh = dict(score=score, renormalize=renormalize, scale=scale)
+        self.choose = dict(self.weigh, n_group=n_group, topk_group=topk_group, group_top=group_top)
+        self.logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        self.topk_ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        self.topk_weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        self._grads = None
+
+    def forward(self, a1: torch.Tensor, topk_ids: Optional[torch.Tensor] = None,
+                topk_weights: Optional[torch.Tensor] = None, stream=None):
+        """(topk_ids, topk_weights) of the hidden states a1 [T, H]."""
+        ids = self.topk_ids if topk_ids is None else topk_ids
+        w = self.topk_weights if topk_weights is None else topk_weights
+        moe.moe_linear(a1, self.gate_w, self.gate_bias, out=self.logits, stream=stream)
+        return moe.moe_route_grouped(self.logits, self.top_k, self.balance_bias, topk_ids=ids, topk_weights=w,
+                                     stream=stream, **self.choose)
+
+    def backward(self, dweights: torch.Tensor, a1: torch.Tensor, topk_ids: Optional[torch.Tensor] = None, stream=None):
+        """Gradients of the last forward call's weights: (dgate_w, dgate_bias or None, da1, dlogits), the choice
+        (topk_ids, when forward wrote another buffer than its own) held fixed.  Buffers of the router, written
+        again by the next call."""
+        if self._grads is None:
+            E, dev = self.E, self.gate_w.device
+            self._grads = dict(
+                dx=torch.empty_like(a1), dw=torch.empty_like(self.gate_w),
+                dbias=None if self.gate_bias is None else torch.empty_like(self.gate_bias),
+                ws=torch.empty(max(moe.linear_backward_workspace_size(self.T, E, a1.shape[1]), 16), dtype=torch.uint8,
+                               device=dev))
+            self._dlogits = torch.empty_like(self.logits)
+        ids = self.topk_ids if topk_ids is None else topk_ids
+        moe.moe_route_grouped_backward(dweights, self.logits, ids, dlogits=self._dlogits, stream=stream, **self.weigh)
+        da1, dgate_w, dgate_bias = moe.moe_linear_backward(self._dlogits, a1, self.gate_w, stream=stream, **self._grads)
+        return dgate_w, dgate_bias, da1, self._dlogits
+
+
 class MoELayer:
-    def __init__(self, inp: LayerInputs, stream: Optional[torch.cuda.Stream] = None):
+    """router: a MoERouter of the same tokens, experts and top_k that takes the place of moe_route (the
+    forward call's logits are then not read and may be None)."""
+
+    def __init__(self, inp: LayerInputs, stream: Optional[torch.cuda.Stream] = None,
+                 router: Optional[MoERouter] = None):
         cfg = self.cfg = inp.cfg
         assert not cfg.finalize_only
+        self.router = router
+        if router is not None and ((router.T, router.E, router.top_k) != (cfg.T, cfg.E, cfg.top_k) or
+                                   cfg.single_launch):
+            raise ValueError("router: expected one of the layer's tokens, experts and top_k, and separate launches")
         self.inp = inp
         dev = inp.logits.device
         T, H, I, E, k = cfg.T, cfg.H, cfg.I, cfg.E, cfg.top_k
@@ -89,7 +148,7 @@ class MoELayer:
                  moe.experts_problem(a_dummy, None, inp.shared_w13, None, inp.shared_w2, None, self.al_shared,
                                      self.shared, identity=True)], H, "bf16"), 16), dtype=torch.uint8, device=dev)
 
-    def forward(self, logits: torch.Tensor, a1: torch.Tensor, stream=None) -> torch.Tensor:
+    def forward(self, logits: Optional[torch.Tensor], a1: torch.Tensor, stream=None) -> torch.Tensor:
         cfg, inp = self.cfg, self.inp
         if self.single:
             return moe.moe_layer_fused(
@@ -105,7 +164,10 @@ class MoELayer:
             moe.moe_experts(a1, None, inp.shared_w13, None, inp.shared_w2, None, self.al_shared, "bf16",
                             out=self.shared, ws=self.ws_shared, identity=True, stream=self.side)
             self.ev_join.record(self.side)
-        moe.moe_route(logits, cfg.top_k, self.scoring, self.topk_ids, self.topk_weights, stream=stream)
+        if self.router is not None:
+            self.router.forward(a1, self.topk_ids, self.topk_weights, stream=stream)
+        else:
+            moe.moe_route(logits, cfg.top_k, self.scoring, self.topk_ids, self.topk_weights, stream=stream)
         moe.moe_align(self.topk_ids, cfg.E, out=self.al, stream=stream)
         if self.passthrough:
             a1q, a1q_scale = a1, None
@@ -121,6 +183,19 @@ class MoELayer:
         moe.moe_finalize(self.y, self.topk_weights, cfg.top_k, cfg.weight_on_input, shared=shared,
                          residual=inp.residual, rms_weight=inp.rms_weight, output=self.out, stream=stream)
         return self.out
+
+    def router_backward(self, dout: torch.Tensor, a1: torch.Tensor, residual_out: Optional[torch.Tensor] = None,
+                        stream=None):
+        """Gradients that train the router of a layer whose experts are held fixed: dout [T, H] bf16, the
+        gradient of the last forward call's output -> (finalize gradients, router gradients), as
+        moe_finalize_backward and MoERouter.backward return them.  residual_out: the sum before the RMSNorm
+        (layers with one).  The router weights of a layer that applies them on the input have no gradient
+        here."""
+        if self.router is None or self.cfg.weight_on_input:
+            raise ValueError("router_backward needs a MoERouter whose weights are applied in the finalize")
+        fin = moe.moe_finalize_backward(dout, self.y, self.topk_weights, self.cfg.top_k, residual_out=residual_out,
+                                        rms_weight=self.inp.rms_weight, need_dy=False, stream=stream)
+        return fin, self.router.backward(fin[1], a1, self.topk_ids, stream=stream)
 
     def experts(self, a1q, a1q_scale, a1, stream=None, shared_launched=False):
         """The routed experts into self.y and the shared expert (if any) into
