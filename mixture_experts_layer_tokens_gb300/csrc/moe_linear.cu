@@ -230,13 +230,13 @@ struct Gemm {
 
 // Shared-memory matrix descriptors of 128-byte-swizzled operands (see sw128_desc): 8-row atoms of
 // 1024 bytes (stride offset) along M/N for a K-major operand, along K for an MN-major one, which
-// lies as TMA boxes of 64 MN elements x 64 K elements write it, so that consecutive 64-element MN
-// groups are 8 KB apart (leading offset; unused by K-major).  The upper word is a constant and an
+// lies as TMA boxes of 64 MN elements x KS 64 K elements write it, so that consecutive 64-element MN
+// groups are KS 8 KB apart (leading offset; unused by K-major).  The upper word is a constant and an
 // offset in shared memory stays below 2^18, so steps are added to the lower word alone.
 constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;  // stride offset, version, 128-byte swizzle
-template <bool kMN>
+template <bool kMN, int KS>
 __device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr) {
-  return (smem_addr & 0x3FFFF) >> 4 | (kMN ? 8192u >> 4 : 1u) << 16;  // (in a cluster the upper bits hold the rank)
+  return (smem_addr & 0x3FFFF) >> 4 | (kMN ? KS * 8192u >> 4 : 1u) << 16;  // (in a cluster the upper bits hold the rank)
 }
 __device__ __forceinline__ uint64_t desc(uint32_t lo) { return (uint64_t)kDescHi << 32 | lo; }
 
@@ -606,20 +606,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* sB = sA + KS * a_stage;
             const uint32_t bar = full0 + st * 8;
             if (half == 0) mbar_arrive_expect_tx(&full[st], CG * KS * (a_bytes + b_bytes));
+            const int k = kb * KS * BK;
+            if (kAMN) {
+              tma_load<CG>(sA, &tmA, arow, k, bar, pol);
+              tma_load<CG>(sA + KS * 8192, &tmA, arow + 64, k, bar, pol);
+            } else {
 #pragma unroll
-            for (int i = 0; i < KS; ++i, sA += a_stage, sB += b_bytes) {
-              const int k = (kb * KS + i) * BK;
-              if (kAMN) {
-                tma_load<CG>(sA, &tmA, arow, k, bar, pol);
-                tma_load<CG>(sA + 8192, &tmA, arow + 64, k, bar, pol);
-              } else {
-                tma_load<CG>(sA, &tmA, k, arow, bar, pol);
-              }
-              if (kBMN) {
-                for (int g = 0; g < bn_cta / 64; ++g) tma_load<CG>(sB + g * 8192, &tmB, brow + g * 64, k, bar, pol);
-              } else {
-                tma_load<CG>(sB, &tmB, k, brow, bar, pol);
-              }
+              for (int i = 0; i < KS; ++i) tma_load<CG>(sA + i * a_stage, &tmA, k + i * BK, arow, bar, pol);
+            }
+            if (kBMN) {
+              for (int g = 0; g < bn_cta / 64; ++g) tma_load<CG>(sB + g * KS * 8192, &tmB, brow + g * 64, k, bar, pol);
+            } else {
+#pragma unroll
+              for (int i = 0; i < KS; ++i) tma_load<CG>(sB + i * b_bytes, &tmB, k + i * BK, brow, bar, pol);
             }
             if (++st == stages) {
               st = 0;
@@ -639,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1 && half == 0) {
       // ---------------------------------------------------------- MMA issuer
       const uint32_t a0 = smem_u32(smem), b0 = a0 + KS * a_stage;
-      const uint32_t ad0 = desc_lo<kAMN>(a0), bd0 = desc_lo<kBMN>(b0);
+      const uint32_t ad0 = desc_lo<kAMN, KS>(a0), bd0 = desc_lo<kBMN, KS>(b0);
       constexpr uint32_t kStepA = (kAMN ? 2048 : 32) >> 4, kStepB = (kBMN ? 2048 : 32) >> 4;  // 16 K elements on
       int acc = 0;
       uint32_t acc_phase = 0;
@@ -663,8 +662,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < KS; ++i)
 #pragma unroll
                 for (int kk = 0; kk < BK / 16; ++kk)
-                  mma<CG>(d, desc(ad0 + at + i * (a_stage >> 4) + kk * kStepA),
-                          desc(bd0 + at + i * (b_bytes >> 4) + kk * kStepB), p.idesc, kb > kc || i > 0 || kk > 0);
+                  mma<CG>(d, desc(ad0 + at + i * (kAMN ? 8192 >> 4 : a_stage >> 4) + kk * kStepA),
+                          desc(bd0 + at + i * (kBMN ? 8192 >> 4 : b_bytes >> 4) + kk * kStepB), p.idesc,
+                          kb > kc || i > 0 || kk > 0);
               commit<CG>(&empty[st], pair_mask);
               if (++st == stages) {
                 st = 0;
@@ -1082,9 +1082,9 @@ moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue&
   if (g.stages > kMaxStages) g.stages = kMaxStages;
   g.idesc = make_idesc(e.fp16 ? 0 : 1, BM * p.cg, p.bn) | (A.mn ? 1u << 15 : 0) | (B.mn ? 1u << 16 : 0);
   CUtensorMap ma, mb;
-  const bool ok = (A.mn ? make_map(&ma, A.base, e.fp16, e.P, C, A.ld, BK)
+  const bool ok = (A.mn ? make_map(&ma, A.base, e.fp16, e.P, C, A.ld, BK * ks)
                         : make_map(&ma, A.base, e.fp16, C, e.P, A.ld, g.a_rows)) &&
-                  (B.mn ? make_map(&mb, B.base, e.fp16, e.Q, C, B.ld, BK)
+                  (B.mn ? make_map(&mb, B.base, e.fp16, e.Q, C, B.ld, BK * ks)
                         : make_map(&mb, B.base, e.fp16, C, e.Q, B.ld, p.bn / p.cg));
   if (!ok) return MOE_ERR_CUDA;
   auto launch = [&](long long first, long long last, int splits) {
