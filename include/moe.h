@@ -475,8 +475,10 @@ moe_status_t moe_linear(const void *x, const void *w, const void *bias, const vo
  * the activation is MOE_LINEAR_NONE, where it is not read).  The tensor cores take dz in
  * dtype: where it has to be computed, or dout is fp32, it is rounded to dtype once (with
  * fp16, the caller's loss scale keeps it in range).  M == 0 sets dw and dbias to zero.
- * ws: moe_linear_backward_workspace_size(M, N, K) bytes.  Sizes, alignment and the order of
- * sums as for moe_linear; outputs overlap nothing. */
+ * ws: moe_linear_backward_workspace_size(M, N, K) bytes (asked with the call's device
+ * current: it depends on the number of SMs); it belongs to one call at a time -- calls, or
+ * replayed graphs, that may run at once need one each.  Sizes, alignment and the order of sums as
+ * for moe_linear; outputs overlap nothing. */
 moe_status_t moe_linear_backward(const void *dout, moe_dtype_t dout_dtype, const void *x, const void *w,
                                  const void *preact, int M, int N, int K, moe_dtype_t dtype,
                                  int activation, void *dx, void *dw, void *dbias, void *ws,
@@ -498,7 +500,8 @@ size_t moe_linear_backward_workspace_size(int M, int N, int K);
  * The choice is the one of exact arithmetic on the given values: scores too close to be
  * ordered in fp32 are compared in fp64.  (MoE routers of the DeepSeek-V3 kind: sigmoid, bias,
  * 4 of 8 groups by their two best, top 8, scale 2.5; plain softmax top-k: n_group 1.)
- * A logit or bias of -inf or NaN masks the expert: s = 0, no share in its group's score (a
+ * A logit or bias of -inf or NaN masks the expert: weight 0 (a softmax's denominator counts every
+ * unmasked logit, whatever its bias), no share in its group's score (a
  * group of masked experts alone ranks last), chosen only when the kept groups have fewer than
  * top_k others, lower index first, with weight 0.  +inf counts as the largest finite number.
  * logits [T, E] in logits_dtype (MOE_DT_FP32, MOE_DT_BF16 or MOE_DT_FP16); topk_ids [T, top_k]
@@ -556,7 +559,7 @@ moe_status_t moe_route_grouped_backward(const float *dweights, const void *logit
  * (needs rms_weight) may each be NULL: not computed; not all.  Sums in fp32, in a fixed order;
  * G stays in fp32 until an output is rounded.  T == 0 sets drms to zero.  H % 8 == 0, H <=
  * 16384, 1 <= top_k <= 32.  ws: moe_finalize_backward_workspace_size(T, H) bytes (needed for
- * drms alone).  dsum may be dout or dresidual_out itself; no other overlap. */
+ * drms alone; as for moe_linear_backward it depends on the device and belongs to one call).  dsum may be dout or dresidual_out itself; no other overlap. */
 moe_status_t moe_finalize_backward(const void *dout, const void *dresidual_out, const void *residual_out,
                                    const void *rms_weight, float eps, const void *fused_expert_output,
                                    const float *topk_weights, int T, int H, int top_k, void *dy,

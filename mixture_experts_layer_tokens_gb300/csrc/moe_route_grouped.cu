@@ -49,6 +49,16 @@ __device__ __forceinline__ float sigmoid32(float l) {
   return __fdividef(l < 0.f ? e : 1.0f, 1.0f + e);  // (the divisor lies in [1, 2])
 }
 
+// exp(l - m) for l <= m, the rounding of the difference made good (it is |l - m| 2^-24 of the result).
+__device__ __forceinline__ float exp_below(float l, float m) {
+  const float d = l - m;
+  if (!(d > -200.f)) return 0.f;
+  const float t = __fsub_rn(d, l);  // the error of d by Knuth's two-sum
+  const float err = __fsub_rn(__fsub_rn(l, __fsub_rn(d, t)), __fadd_rn(m, t));
+  const float e = expf(d);
+  return fmaf(e, err, e);
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
@@ -266,10 +276,12 @@ __device__ __noinline__ int rank_again(const TL* row, const RouteArgs& a, bool* 
       for (int i = 0; i < NV; ++i) c[i] = 0;
     }
   }
+  // top_k rounds, then on until the rest is surely below the last choice (one that is equal to it does
+  // not vouch for what comes after)
   int mine = 0, prev_id = 0;
-  uint64_t prev = 0;
+  uint64_t prev = 0, last = 0;
 #pragma unroll 1
-  for (int r = 0; r <= a.top_k; ++r) {
+  for (int r = 0;; ++r) {
     uint64_t bc = 0;
     uint32_t bl = 0;
     int at = 0;
@@ -289,9 +301,11 @@ __device__ __noinline__ int rank_again(const TL* row, const RouteArgs& a, bool* 
       expert_inputs(row, a.bias, id, ly, by);
       doubt |= !(lx == ly && bx == by);
     }
+    if (r >= a.top_k && (doubt || by_logit || top <= kMasked64 || !S::near(last, top))) break;
     if (lane == w) c[at] = 0;
     if (lane == w) lk[at] = 0;
-    if (lane == r) mine = id;
+    if (lane == r && r < a.top_k) mine = id;
+    if (r == a.top_k - 1) last = top;
     prev = top;
     prev_id = id;
   }
@@ -423,7 +437,7 @@ __device__ __forceinline__ uint32_t group_score(uint32_t top, uint32_t second, u
 // den: the row's softmax.  Called by the whole warp.
 __device__ __forceinline__ float choice_weight(const RouteArgs& a, float lj, float m, float den) {
   const bool live = lj > -INFINITY, softmax = a.score == MOE_SCORE_SOFTMAX;
-  if (!a.renorm) return !live ? 0.f : softmax ? __fdividef(expf(lj - m), den) : sigmoid32(lj);
+  if (!a.renorm) return !live ? 0.f : softmax ? __fdividef(exp_below(lj, m), den) : sigmoid32(lj);
   // s_j / sum s is the same for scores scaled by one factor: softmax numerators relative to the
   // largest chosen, sigmoid scores by e^-m (m = the largest chosen logit when all are negative)
   // so that none underflows
@@ -431,9 +445,9 @@ __device__ __forceinline__ float choice_weight(const RouteArgs& a, float lj, flo
   float s = 0.f;
   if (live) {
     if (softmax)
-      s = expf(lj - top);
+      s = exp_below(lj, top);
     else
-      s = top < 0.f ? __fdividef(expf(lj - top), 1.0f + expf(lj)) : sigmoid32(lj);
+      s = top < 0.f ? __fdividef(exp_below(lj, top), 1.0f + expf(lj)) : sigmoid32(lj);
   }
   const float sum = warp_sum(s);
   return sum > 0.f ? __fdividef(s, sum) : 0.f;  // (the sum lies in [1/2, 32])
@@ -778,8 +792,8 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
         }
         if (!unsure) {
           FF c{0.f, 0.f};
+          float x = 0.f, b = 0.f;
           if (id >= 0) {
-            float x, b;
             expert_inputs(row, a.bias, id, x, b);
             c = softmax ? exp_ff(two_sum(x, -m)) : sigmoid_ff(x);  // (a softmax's numerators order like its scores)
             c = b == INFINITY ? FF{b, 0.f} : add(c, {b, 0.f});
@@ -787,8 +801,11 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
           const FF o = PairScores::shfl(c, 1);
           c = c.h == INFINITY || o.h == INFINITY ? FF{fmaxf(c.h, o.h), 0.f} : add(c, o);
           const uint64_t sa = __shfl_sync(kFull, PairScores::key(c), 0), sb = __shfl_sync(kFull, PairScores::key(c), 2);
-          unsure = PairScores::near(max(sa, sb), min(sa, sb));
-          if (sb > sa) keep = (keep && grp != ga) || (in_use && grp == gb);
+          // (equal logits and biases: equal scores, and the lower group was kept)
+          const float x2 = __shfl_down_sync(kFull, x, 2), b2 = __shfl_down_sync(kFull, b, 2);
+          const bool same = __all_sync(kFull, lane >= 2 || (x == x2 && b == b2));
+          unsure = !same && PairScores::near(max(sa, sb), min(sa, sb));
+          if (!same && sb > sa) keep = (keep && grp != ga) || (in_use && grp == gb);
         }
       }
     }
@@ -829,8 +846,21 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     // doubt between neighbours, unless they are equal in logit and bias
     const uint32_t next = __shfl_down_sync(kFull, mine, 1) & ~kPlace;
     const float ln = __shfl_down_sync(kFull, lj, 1), bn = __shfl_down_sync(kFull, bj, 1);
-    const bool near =
-        __any_sync(kFull, lane < a.top_k && doubt.of(mine & ~kPlace, next, kNone) && !(ln == lj && bn == bj));
+    const bool close = lane < a.top_k && doubt.of(mine & ~kPlace, next, kNone), equal = ln == lj && bn == bj;
+    bool near = __any_sync(kFull, close && !equal);
+    if (!near && __any_sync(kFull, close && lane == a.top_k - 1)) {
+      // the first left out equals the last choice: it does not vouch for what comes after
+      const uint32_t last = __shfl_sync(kFull, mine, a.top_k - 1);
+      const float ll = __shfl_sync(kFull, lj, a.top_k - 1), bl = __shfl_sync(kFull, bj, a.top_k - 1);
+      uint32_t low = __shfl_sync(kFull, mine, a.top_k);
+      while (!near) {
+        low = next_below(low);
+        if (!doubt.of(last & ~kPlace, low & ~kPlace, kNone)) break;
+        float x, b;
+        expert_inputs(row, a.bias, expert_of(low), x, b);
+        near = !(x == ll && b == bl);
+      }
+    }
     if (near || unsure) {
       if (!unsure) {
         // the candidates, one a lane: all that are not surely below the last choice
@@ -907,9 +937,9 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     float s = 0.f, f = 1.f;
     if (live) {
       if (a.score == MOE_SCORE_SOFTMAX) {
-        s = expf(lj - top);
+        s = exp_below(lj, top);
       } else {
-        s = top < 0.f ? __fdividef(expf(lj - top), 1.0f + expf(lj)) : sigmoid32(lj);
+        s = top < 0.f ? __fdividef(exp_below(lj, top), 1.0f + expf(lj)) : sigmoid32(lj);
         f = sigmoid32(-lj);  // 1 - s without the cancellation
       }
     }
@@ -933,11 +963,11 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     float den = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      s[i] = s[i] > -INFINITY ? expf(s[i] - m) : 0.f;
+      s[i] = exp_below(s[i], m);  // (0 for a masked logit)
       den += s[i];
     }
     den = warp_sum(den);
-    d = live ? dw * __fdividef(expf(lj - m), den) : 0.f;  // g_j s_j
+    d = live ? dw * __fdividef(exp_below(lj, m), den) : 0.f;  // g_j s_j
     const float dot = warp_sum(d), rden = den > 0.f ? __fdividef(-dot, den) : 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) s[i] *= rden;

@@ -623,6 +623,15 @@ def _launch(stream: Optional[torch.cuda.Stream]):
     return dev, stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream: Optional[torch.cuda.Stream]):
+    """A buffer that the call makes itself: from the pool of the stream that it runs on, so that a workspace
+    freed on return is not handed to work on another stream while the kernels still use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _linear_args(x: torch.Tensor, w: torch.Tensor, activation: str):
     if activation not in LINEAR_ACTIVATIONS:
         raise ValueError(f"unknown activation {activation!r}")
@@ -643,7 +652,7 @@ def moe_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = 
     ``activation``: see ``LINEAR_ACTIVATIONS``."""
     M, N, K, dt, code, act = _linear_args(x, w, activation)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or dt, device=x.device)
+        out = _empty((M, N), out_dtype or dt, x.device, stream)
     odt = out.dtype
     if odt is not dt and odt is not torch.float32 or out_dtype not in (None, odt):
         raise TypeError(f"out: expected {dt} or float32 as out_dtype says, got {odt}")
@@ -671,13 +680,13 @@ def moe_linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pr
     if dout.dtype is not dt and dout.dtype is not torch.float32:
         raise TypeError(f"dout: expected {dt} or float32, got {dout.dtype}")
     if dx is None and need_dx:
-        dx = torch.empty_like(x)
+        dx = _empty((M, K), dt, x.device, stream)
     if dw is None and need_dw:
-        dw = torch.empty_like(w)
+        dw = _empty((N, K), dt, x.device, stream)
     if dbias is None and need_dbias:
-        dbias = torch.empty((N,), dtype=dt, device=x.device)
+        dbias = _empty((N,), dt, x.device, stream)
     if ws is None:
-        ws = torch.empty(max(linear_backward_workspace_size(M, N, K), 16), dtype=torch.uint8, device=x.device)
+        ws = _empty((max(linear_backward_workspace_size(M, N, K), 16),), torch.uint8, x.device, stream)
     dev, s = _launch(stream)
     _check("moe_linear_backward", lib().moe_linear_backward(
         _tensor(dout, dout.dtype, (M, N), "dout", dev), _DT[dout.dtype], _tensor(x, dt, (M, K), "x", dev),
@@ -713,9 +722,9 @@ def moe_route_grouped(logits: torch.Tensor, top_k: int, bias: Optional[torch.Ten
     T, E = logits.shape
     cfg = _route_config(score, n_group, topk_group, group_top, bool(renormalize), scale)
     if topk_ids is None:
-        topk_ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+        topk_ids = _empty((T, top_k), torch.int32, logits.device, stream)
     if topk_weights is None:
-        topk_weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+        topk_weights = _empty((T, top_k), torch.float32, logits.device, stream)
     dev, s = _launch(stream)
     _check("moe_route_grouped", lib().moe_route_grouped(
         _tensor(logits, logits.dtype, (T, E), "logits", dev), _DT[logits.dtype],
@@ -735,7 +744,7 @@ def moe_route_grouped_backward(dweights: torch.Tensor, logits: torch.Tensor, top
     (T, E), top_k = logits.shape, topk_ids.shape[1]
     cfg = _route_config(score, 1, 1, 1, bool(renormalize), scale)
     if dlogits is None:
-        dlogits = torch.empty_like(logits)
+        dlogits = _empty((T, E), logits.dtype, logits.device, stream)
     dev, s = _launch(stream)
     _check("moe_route_grouped_backward", lib().moe_route_grouped_backward(
         _tensor(dweights, torch.float32, (T, top_k), "dweights", dev),
@@ -766,15 +775,15 @@ def moe_finalize_backward(dout: torch.Tensor, fused_expert_output: Optional[torc
     T, H = dout.shape
     bf, d = torch.bfloat16, dout.device
     if dy is None and need_dy:
-        dy = torch.empty((T * top_k, H), dtype=bf, device=d)
+        dy = _empty((T * top_k, H), bf, d, stream)
     if dweights is None and need_dweights and topk_weights is not None:
-        dweights = torch.empty((T, top_k), dtype=torch.float32, device=d)
+        dweights = _empty((T, top_k), torch.float32, d, stream)
     if dsum is None and need_dsum:
-        dsum = torch.empty((T, H), dtype=bf, device=d)
+        dsum = _empty((T, H), bf, d, stream)
     if drms is None and need_drms and rms_weight is not None:
-        drms = torch.empty((H,), dtype=torch.float32, device=d)
+        drms = _empty((H,), torch.float32, d, stream)
     if ws is None and drms is not None:
-        ws = torch.empty(max(finalize_backward_workspace_size(T, H), 16), dtype=torch.uint8, device=d)
+        ws = _empty((max(finalize_backward_workspace_size(T, H), 16),), torch.uint8, d, stream)
     dev, s = _launch(stream)
     _check("moe_finalize_backward", lib().moe_finalize_backward(
         _tensor(dout, bf, (T, H), "dout", dev), _tensor(dresidual_out, bf, (T, H), "dresidual_out", dev),

@@ -114,3 +114,22 @@ def test_finalize_backward_graph_and_stream(cuda_dev):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs.values(), want))
+
+
+def test_finalize_backward_offsets_past_32_bits(cuda_dev):
+    """T * top_k * H past 2^31 elements: tokens at both ends."""
+    T, H, k = 40_000, 7168, 8
+    c = _case(8, H, k, False, False)
+    dout = torch.zeros((T, H), dtype=BF, device=cuda_dev)
+    y = torch.ones((T * k, H), dtype=BF, device=cuda_dev)
+    w = torch.ones((T, k), device=cuda_dev)
+    for t, n in ((dout, 4), (w, 4), (y, 4 * k)):
+        src = {id(dout): c["dout"], id(w): c["topk_weights"], id(y): c["fused_expert_output"]}[id(t)].to(cuda_dev)
+        t[:n], t[-n:] = src[:n], src[n:]
+    dy, dw, dsum, _ = moe.moe_finalize_backward(dout, y, w, k)
+    refs, mags = rr.finalize_backward(c["dout"], c["fused_expert_output"], c["topk_weights"], k)
+    for name, v, n in (("dy", dy, 4 * k), ("dweights", dw, 4), ("dsum", dsum, 4)):
+        v = torch.cat([v[:n], v[-n:]]).cpu().double()
+        tol = mags[name] * 2.0 ** -18 + (refs[name].abs() * 2.0 ** -8 if name != "dweights" else 0) + 1e-38
+        assert ((v - refs[name]).abs() <= tol).all(), name
+    assert (dsum[4:-4] == 0).all() and (dw[4:-4] == 0).all()

@@ -211,3 +211,69 @@ def test_linear_on_another_stream(cuda_dev):
     got = moe.moe_linear(x, w, stream=side)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+def test_linear_offsets_past_32_bits(cuda_dev):
+    """M * N past 2^31 elements: rows at both ends against the definition."""
+    M, N, K = 160_000, 14336, 64
+    g, x, w = _make(64, N, K, BF, 4)
+    big = torch.zeros((M, K), dtype=BF, device=cuda_dev)
+    big[:32], big[-32:] = x[:32].to(cuda_dev), x[32:].to(cuda_dev)
+    out = moe.moe_linear(big, w.to(cuda_dev), activation="silu")
+    ref, z, mag = rr.linear(x, w, None, None, "silu")
+    tol = 1.2 * 2.0 ** -22 * (K / 16 + 16) * mag + 2.0 ** -20 * (1 + z.abs()) + _half_step(ref, BF)
+    _within(torch.cat([out[:32], out[-32:]]), ref, tol, "out")
+    # dw and dbias of a gradient that is zero but for those rows; dx of the last
+    d = torch.randn((64, N), generator=g).to(BF)
+    out.zero_()
+    out[:32], out[-32:] = d[:32].to(cuda_dev), d[32:].to(cuda_dev)
+    dx, dw, db = moe.moe_linear_backward(out, big, w.to(cuda_dev), need_dbias=True)
+    refs, mags = rr.linear_backward(d, x, w)
+    # (zeros add nothing: the sums hold 64 terms)
+    for v, r, m, n in ((torch.cat([dx[:32], dx[-32:]]), refs[0], mags[0], N), (dw, refs[1], mags[1], M), (db, refs[2], mags[2], M)):
+        _within(v, r, 2.0 ** -22 * (n / 16 + 16) * m + _half_step(r, BF), "gradient")
+
+
+def test_linear_first_call_under_capture():
+    """The library's first call in a process may be a captured one."""
+    import subprocess
+    import sys
+    code = (
+        "import torch\n"
+        "from mixture_experts_layer_tokens_gb300 import moe\n"
+        "x, w = (torch.randn(s, device='cuda').bfloat16() for s in ((300, 512), (264, 512)))\n"
+        "o = torch.empty((300, 264), device='cuda', dtype=torch.bfloat16)\n"
+        "dx, dw = torch.empty_like(x), torch.empty_like(w)\n"
+        "l, ids, ws = torch.randn((300, 264), device='cuda'), torch.empty((300, 6), device='cuda', dtype=torch.int32), torch.empty((300, 6), device='cuda')\n"
+        "dl, dn = torch.empty_like(l), torch.randn((50, 512), device='cuda').bfloat16()\n"
+        "y, dy = (torch.randn((300, 512), device='cuda').bfloat16() for _ in range(2))\n"
+        "wf = torch.rand((50, 6), device='cuda')\n"
+        "tmp = torch.empty(1 << 24, device='cuda', dtype=torch.uint8)\n"
+        "outs = [torch.empty((50, 6), device='cuda'), torch.empty_like(dn), torch.empty(512, device='cuda')]\n"
+        "def step():\n"
+        "    moe.moe_linear(x, w, out=o)\n"
+        "    moe.moe_linear_backward(o, x, w, preact=o, activation='silu', dx=dx, dw=dw, ws=tmp)\n"
+        "    moe.moe_route_grouped(l, 6, n_group=8, topk_group=3, group_top=2, topk_ids=ids, topk_weights=ws)\n"
+        "    moe.moe_route_grouped_backward(ws, l, ids, dlogits=dl)\n"
+        "    moe.moe_finalize_backward(dn, y, wf, 6, residual_out=y[:50], rms_weight=y[50], dy=dy, dweights=outs[0], dsum=outs[1], drms=outs[2], ws=tmp)\n"
+        "all_of = [o, dx, dw, ids, ws, dl, dy] + outs\n"
+        "torch.cuda.synchronize()\n"
+        "g = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(g):\n"
+        "    step()\n"
+        "g.replay(); torch.cuda.synchronize()\n"
+        "got = [t.clone() for t in all_of]\n"
+        "step(); torch.cuda.synchronize()\n"
+        "assert all(torch.equal(a, b) for a, b in zip(got, all_of)) and moe.moe_device_status() == 0\n"
+        "print('same')\n")
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("M,N,K", [(256, 1024, 1000), (256, 5120, 512), (300, 5120, 4096), (2050, 2560, 4096), (40, 136, 4104)])
+def test_linear_cuts(cuda_dev, M, N, K):
+    """Sizes whose cuts differ: split K in clusters of 2, 4 and 8, pairs, a split last wave."""
+    _forward(cuda_dev, M, N, K, BF, "none", True, False, False, F32)
+    _backward(cuda_dev, M, N, K)
