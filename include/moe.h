@@ -497,8 +497,9 @@ size_t moe_linear_backward_workspace_size(int M, int N, int K);
  *   larger logit and then to the lower index
  *   topk_weights_j = s_j * scale, with renormalize s_j / (sum of the chosen s) * scale (0 when
  *   that sum is 0)
- * The choice is the one of exact arithmetic on the given values: scores too close to be
- * ordered in fp32 are compared in fp64.  (MoE routers of the DeepSeek-V3 kind: sigmoid, bias,
+ * The choice is the one of fp64 arithmetic on the given values: scores too close to be ordered
+ * in fp32 are compared more exactly (without a bias and with group_top 1 the logits themselves
+ * are ranked, which is exact).  (MoE routers of the DeepSeek-V3 kind: sigmoid, bias,
  * 4 of 8 groups by their two best, top 8, scale 2.5; plain softmax top-k: n_group 1.)
  * A logit or bias of -inf or NaN masks the expert: weight 0 (a softmax's denominator counts every
  * unmasked logit, whatever its bias), no share in its group's score (a

@@ -53,12 +53,12 @@ def linear(x, w, bias=None, residual=None, activation="none"):
 
 
 def linear_backward(dout, x, w, preact=None, activation="none"):
-    """(dx, dw, dbias) and the sums of absolute values (of dz w, dz x, dz) that bound their errors."""
+    """(dx, dw, dbias), and the sums of absolute values of dz w, dz x, dz and of dout w, dout x, dout (what an
+    error of act' multiplies) that bound their errors."""
     dout, x, w = _f64(dout), _f64(x), _f64(w)
     dz = dout if activation == "none" else dout * act_grad(_f64(preact), activation)
-    # the same sums of absolute values with |dout| where a small act' hides its own rounding
-    a = dz.abs() if activation == "none" else dz.abs() + dout.abs() * 2.0 ** -12
-    return (dz @ w, dz.T @ x, dz.sum(0)), (a @ w.abs(), a.T @ x.abs(), a.sum(0))
+    sums = lambda a: (a @ w.abs(), a.T @ x.abs(), a.sum(0))  # noqa: E731
+    return (dz @ w, dz.T @ x, dz.sum(0)), sums(dz.abs()), sums(dout.abs())
 
 
 # ------------------------------------------------------------------ grouped route
@@ -86,11 +86,13 @@ def route_grouped(logits, top_k, bias=None, score="sigmoid", n_group=1, topk_gro
     l, s = _clean(logits), scores(logits, score)
     T, E = l.shape
     b = np.zeros(E) if bias is None else bias.detach().cpu().double().numpy()
+    # without a bias the logits' order is the scores', however close these are to 1
+    sw = l if bias is None and group_top == 1 else s
     size = E // n_group
     ids, ws = np.zeros((T, top_k), np.int32), np.zeros((T, top_k))
     for t in range(T):
         masked = np.isneginf(l[t]) | np.isnan(b) | np.isneginf(b)
-        c = np.where(masked, -np.inf, s[t] + np.where(masked, 0.0, b))
+        c = np.where(masked, -np.inf, sw[t] + np.where(masked, 0.0, b))
         group = []
         for g in range(n_group):
             best = sorted((c[e] for e in range(g * size, (g + 1) * size) if not masked[e]), reverse=True)[:group_top]

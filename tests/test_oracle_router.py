@@ -23,7 +23,8 @@ def test_linear_and_gradients_against_autograd(activation):
     out, zr, _ = rr.linear(x, w, b, None, activation)
     assert torch.allclose(out, f(z), rtol=1e-12, atol=1e-12) and torch.allclose(zr, z)
     want = torch.autograd.grad((f(z) * d).sum(), (x, w, b))
-    got, _ = rr.linear_backward(d, x, w, z, activation)
+    got, mags, _ = rr.linear_backward(d, x, w, z, activation)
+    assert all((m >= g.abs() - 1e-12).all() for m, g in zip(mags, got))
     for a, e in zip(got, want):
         assert torch.allclose(a, e, rtol=1e-10, atol=1e-12)
 

@@ -206,6 +206,24 @@ def test_route_peaked_and_repeated_logits(cuda_dev, score, with_bias):
                 _check(cuda_dev, l, 12, bias, score=score, **kw)
 
 
+@pytest.mark.parametrize("k", [5, 8, 12])
+def test_route_masked_choices_behind_near_ones(cuda_dev, k):
+    """Fewer experts than choices are left, some of them too close for fp32: the masked ones still follow by
+    index, whatever their bias."""
+    g = torch.Generator().manual_seed(5)
+    bias = torch.randint(-100, 101, (36,), generator=g).float() * 1e-3
+    l = torch.full((20, 36), float("-inf"))
+    for t in range(20):
+        at = torch.randperm(36, generator=g)[:6]
+        l[t, at] = torch.randn(6, generator=g)
+        s = torch.sigmoid(l[t, at].double())
+        # two of them with the same biased score to 1e-7
+        want = s[0] + bias[at[0]].double() - bias[at[1]].double()
+        l[t, at[1]] = torch.log(want / (1 - want)).float() if 0 < want < 1 else l[t, at[1]]
+    for kw in (dict(), dict(n_group=4, topk_group=2, group_top=2), dict(n_group=3, topk_group=3, group_top=1)):
+        _check(cuda_dev, l, k, bias, **kw)
+
+
 def test_route_offsets_past_32_bits(cuda_dev):
     """T * E past 2^32 bytes: the first and last rows of a large batch."""
     T, E, k = 9_000_000, 256, 8
