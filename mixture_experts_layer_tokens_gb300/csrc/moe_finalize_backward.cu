@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(256) drms_kernel(const float* __restrict__ par
   depend_wait();
   float s = 0.f;
   if (h < H)
+#pragma unroll 8
     for (int p = part; p < P; p += 8) s += partial[(size_t)p * H + h];
   sums[part][threadIdx.x & 31] = s;
   __syncthreads();

@@ -39,18 +39,6 @@ static_assert((2 * kMaxStages + 5) * 8 + 4 <= kCtrlBytes && kSmemBytes <= 232448
 constexpr int kTmemCols = 512;
 constexpr int kAccCols = 256;     // columns between the two accumulators
 
-// exp(x) and 1 / x by the special-function unit: within (2 + 1.2 |x|) 2^-23 (the product with
-// log2 e rounds) and 1 ulp; results below 2^-126 are 0.
-__device__ __forceinline__ float fast_exp(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
-  return y;
-}
-__device__ __forceinline__ float fast_rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // 1 / (1 + exp(-x)) within 2^-21 (the exponential's error is weighed by at most 0.65 / (2 + 1.2 |x|)),
 // and 0 or 1 where exp overflows or vanishes.
 __device__ __forceinline__ float fast_sigmoid(float x) { return fast_rcp(1.0f + fast_exp(-x)); }
@@ -904,6 +892,7 @@ __global__ void __launch_bounds__(256) linear_dbias_kernel(const float* __restri
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
   float s = 0.f;
   if (c < N)
+#pragma unroll 8
     for (int p = part; p < P; p += 8) s += partial[(size_t)p * N + c];
   sums[part][threadIdx.x & 31] = s;
   __syncthreads();

@@ -73,7 +73,8 @@ struct RouteArgs {
   int T, E, top_k;
   int score, n_group, topk_group, group_top, renorm;
   float scale;
-  int lpg;  // lanes of a group: the largest power of two that gives every group as many
+  int size;  // experts of a group
+  int lpg;   // lanes of a group: the largest power of two that gives every group as many
 };
 
 // Logit and bias of expert e, the masked state folded into the logit.
@@ -190,7 +191,7 @@ __device__ __forceinline__ uint32_t best_lanes(uint64_t c, uint32_t l) {
 template <class S, int NV, class TL>
 __device__ __noinline__ int rank_again(const TL* row, const RouteArgs& a, bool* unsure) {
   const int lane = threadIdx.x & 31;
-  const int size = a.E / a.n_group, grp = lane / a.lpg, in = (lane % a.lpg) * NV;
+  const int size = a.size, grp = lane / a.lpg, in = (lane % a.lpg) * NV;
   const int base = grp * size + in;
   const int cnt = grp < a.n_group ? max(0, min(NV, size - in)) : 0;
   uint64_t c[NV];
@@ -377,9 +378,9 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[NV]) {
           if (i + j + k < NV && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order2(key[i + j], key[i + j + k]);
 }
 
-// Distances below which two ranking scores may be in the wrong order.  __expf(-x) is within
+// Distances below which two ranking scores may be in the wrong order.  fast_exp(-x) is within
 // (2 + 1.2 x) 2^-23 of its value.  Sigmoid: that moves s by at most 0.65 2^-23, the sum and the
-// division (2 ulp) by 2.5 2^-23: two scores are within 2^-20.3.  Softmax: a score's own exponential
+// division (2 roundings) by 2.5 2^-23: two scores are within 2^-20.3.  Softmax: a score's own exponential
 // and division give 2^-21; the denominator moves all scores of a row by one common factor, within
 // 2^-18.2 (its terms' errors weighed by the terms, whose mean x is at most ln E, and up to 69
 // additions): 2^-17.6 for two.  Adding the bias rounds by 2^-24 |c| and cutting the places off the
@@ -407,8 +408,8 @@ struct Doubt {
 
 // A score for ranking alone, by the fast exponential and division.
 __device__ __forceinline__ float rank_score(float x, bool softmax, float m, float rden) {
-  const float e = __expf(softmax ? x - m : -fabsf(x));
-  return softmax ? e * rden : __fdividef(x < 0.f ? e : 1.0f, 1.0f + e);
+  const float e = fast_exp(softmax ? x - m : -fabsf(x));
+  return softmax ? e * rden : (x < 0.f ? e : 1.0f) * fast_rcp(1.0f + e);
 }
 
 // A group's score as an ordered key, from its two best keys (`none`: a masked one); err: how far the
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
   const int lane = threadIdx.x & 31;
   const TL* row = static_cast<const TL*>(a.logits) + (size_t)t * a.E;
   const bool by_logit = a.bias == nullptr, softmax = a.score == MOE_SCORE_SOFTMAX;
-  const int size = a.E / a.n_group, grp = lane / a.lpg, in = (lane % a.lpg) * NV;
+  const int size = a.size, grp = lane / a.lpg, in = (lane % a.lpg) * NV;
   const int base = grp * size + in;
   const int cnt = grp < a.n_group ? min(NV, size - in) : 0;  // (may be negative: none)
 
@@ -681,7 +682,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
   const int lane = threadIdx.x & 31;
   const TL* row = static_cast<const TL*>(a.logits) + (size_t)t * a.E;
   const bool by_logit = a.bias == nullptr, softmax = a.score == MOE_SCORE_SOFTMAX;
-  const int lpg = a.lpg, size = a.E / a.n_group, lane_shift = __ffs(lpg) - 1;
+  const int lpg = a.lpg, size = a.size, lane_shift = __ffs(lpg) - 1;
   const int grp = lane >> lane_shift, in = (lane & (lpg - 1)) * NV;
   const int base = grp * size + in;
   const int cnt = grp < a.n_group ? min(NV, size - in) : 0;  // (may be negative: none)
@@ -830,8 +831,13 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     return __reduce_max_sync(kFull, v);
   };
   uint32_t mine = 0;
+  {
+    uint32_t h[4];
 #pragma unroll
-  for (int i = 0; i < kFew; ++i) mine = lane == i ? best[i] : mine;
+    for (int i = 0; i < 4; ++i) h[i] = lane & 1 ? best[2 * i + 1] : best[2 * i];
+    const uint32_t x = lane & 2 ? h[1] : h[0], y = lane & 2 ? h[3] : h[2];
+    mine = lane >= kFew ? 0u : lane & 4 ? y : x;
+  }
   if (a.top_k == kFew) {
     const uint32_t v = next_below(best[kFew - 1]);
     if (lane == kFew) mine = v;
@@ -1046,7 +1052,7 @@ extern "C" moe_status_t moe_route_grouped(const void* logits, moe_dtype_t logits
   MOE_CHECK_ARG(logits && topk_ids && topk_weights);
   MOE_CHECK_ARG(aligned16(logits) && aligned16(bias) && aligned16(topk_ids) && aligned16(topk_weights));
   RouteArgs a{logits,          bias,           T,              E,               top_k,     cfg->score,
-                    cfg->n_group, cfg->topk_group, cfg->group_top, cfg->renormalize, cfg->scale, 32};
+                    cfg->n_group, cfg->topk_group, cfg->group_top, cfg->renormalize, cfg->scale, E / cfg->n_group, 32};
   const dim3 grid((unsigned)((T + kWarpsPerBlock - 1) / kWarpsPerBlock)), block(kWarpsPerBlock * 32);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   a.lpg = lanes_per_group(cfg->n_group);
@@ -1082,7 +1088,7 @@ extern "C" moe_status_t moe_route_grouped_backward(const float* dweights, const 
   MOE_CHECK_ARG(dweights && logits && topk_ids && dlogits);
   MOE_CHECK_ARG(aligned16(dweights) && aligned16(logits) && aligned16(topk_ids) && aligned16(dlogits));
   const RouteArgs a{logits,          nullptr,        T,              E,               top_k,     cfg->score,
-                    cfg->n_group, cfg->topk_group, cfg->group_top, cfg->renormalize, cfg->scale, 32};
+                    cfg->n_group, cfg->topk_group, cfg->group_top, cfg->renormalize, cfg->scale, E / cfg->n_group, 32};
   const dim3 grid((unsigned)((T + kWarpsPerBlock - 1) / kWarpsPerBlock)), block(kWarpsPerBlock * 32);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   for_nv((E + 31) / 32, [&](auto nv) {

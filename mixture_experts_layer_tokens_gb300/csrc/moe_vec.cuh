@@ -40,6 +40,18 @@ cudaError_t launch_overlapped(void (*kern)(P...), int grid, int block, cudaStrea
   return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
 }
 
+// exp(x) and 1 / x by the special-function unit: within (2 + 1.2 |x|) 2^-23 (the product with
+// log2 e rounds) and 1 ulp; results below 2^-126 are 0.
+__device__ __forceinline__ float fast_exp(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+  return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
 __device__ __forceinline__ float load1(const __half* p) { return __half2float(__ldg(p)); }
