@@ -5,7 +5,7 @@
 //   dy_j = w_j G,  dw_j = <G, y_j>,  dsum = G,  drms = sum_t dn o r
 //
 // Bound by HBM: a token moves 2 H (4 + 2 top_k) bytes and computes a few operations per
-// element.  One CTA per SM takes whole tokens; a producer thread streams the token's rows (dn, o,
+// element.  A CTA takes whole tokens (one CTA per SM for long rows); a producer thread streams the token's rows (dn, o,
 // dres, then the top_k expert rows) by bulk copies into a ring of row slots, so that the next
 // rows are on their way through the two block-wide sums of a token, and G stays in registers
 // between them.  (Rows loaded by the threads themselves, two CTAs a SM: 28 KB in flight a SM and
@@ -20,7 +20,7 @@ namespace {
 constexpr int kMaxConsumers = 512;
 constexpr int kMaxK = 32;
 constexpr int kMaxSlots = 16;
-constexpr int kSmemMost = 220 * 1024;
+constexpr int kSmemMost = 225 * 1024;
 
 struct FinBwd {
   const __nv_bfloat16 *dout, *dres, *o, *gamma, *y;
@@ -275,7 +275,18 @@ void shape(int H, int* consumers, int* nv) {
   *consumers = ((nvec + *nv - 1) / *nv + 31) / 32 * 32;
 }
 
-int grid_ctas(int T) { return T < num_sms() ? T : num_sms(); }
+// CTAs of an SM: short rows leave most of it idle between a token's sums, so several CTAs share it
+// (within its registers: 95 a thread at most).  [2094, 416] top 4: one CTA an SM 40 us, eight under 10.
+int ctas_per_sm(int H) {
+  int consumers, nv;
+  shape(H, &consumers, &nv);
+  const int n = 65536 / (96 * (consumers + 32));
+  return n < 1 ? 1 : n > 8 ? 8 : n;
+}
+int grid_ctas(int T, int H) {
+  const int most = num_sms() * ctas_per_sm(H);
+  return T < most ? T : most;
+}
 
 }  // namespace
 
@@ -287,7 +298,7 @@ using namespace moe;
 
 extern "C" size_t moe_finalize_backward_workspace_size(int T, int H) {
   if (T <= 0 || H <= 0) return 0;
-  return (size_t)grid_ctas(T) * (size_t)H * sizeof(float);
+  return (size_t)grid_ctas(T, H) * (size_t)H * sizeof(float);
 }
 
 extern "C" moe_status_t moe_finalize_backward(const void* dout, const void* dresidual_out, const void* residual_out,
@@ -327,13 +338,13 @@ extern "C" moe_status_t moe_finalize_backward(const void* dout, const void* dres
   a.partial = drms ? static_cast<float*>(ws) : nullptr;
   int consumers, nv;
   shape(H, &consumers, &nv);
-  const int grid = grid_ctas(T);
+  const int grid = grid_ctas(T, H);
   const size_t sums = drms ? (size_t)H * sizeof(float) : 0;
-  a.slots = (int)((kSmemMost - sums) / ((size_t)H * 2));
+  a.slots = (int)(((size_t)kSmemMost / ctas_per_sm(H) - 5120 - sums) / ((size_t)H * 2));  // (5 KB: static)
   if (a.slots > kMaxSlots) a.slots = kMaxSlots;
   const size_t smem = sums + (size_t)a.slots * H * 2;
   auto run = [&](auto kern) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) != cudaSuccess) return false;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost - 5120) != cudaSuccess) return false;
     kern<<<grid, consumers + 32, smem, s>>>(a);
     return true;
   };

@@ -88,9 +88,6 @@ struct Epilogue {
   }
 };
 
-__device__ __forceinline__ float load16(const void* p, size_t i, int fp16) {
-  return fp16 ? load1(static_cast<const __half*>(p) + i) : load1(static_cast<const __nv_bfloat16*>(p) + i);
-}
 __device__ __forceinline__ void store16(void* p, size_t i, float v, int fp16) {
   if (fp16)
     store1(static_cast<__half*>(p) + i, v);
@@ -98,41 +95,93 @@ __device__ __forceinline__ void store16(void* p, size_t i, float v, int fp16) {
     store1(static_cast<__nv_bfloat16*>(p) + i, v);
 }
 
-// R consecutive rows of a column; the loads and stores of the rows are independent.
-template <int R>
-__device__ __forceinline__ void finish_column(const Epilogue& e, int row, int col, float (&z)[R]) {
-  const size_t at = (size_t)row * e.Q + col;
-  const int rows = min(R, e.P - row);
-  const float b = e.bias ? load16(e.bias, col, e.fp16) : 0.f;
-  float res[R];
-  // (residual may be out: plain loads, not the read-only path)
+// W (1 or 2) adjacent columns of a row, as 16-bit or fp32 values.
+template <int W>
+__device__ __forceinline__ void load_few(const void* p, size_t at, int fp16, int wide, float (&v)[W]) {
+  // (plain loads: residual may be out)
+  if (wide) {
+    if constexpr (W == 2) {
+      const float2 f = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + at);
+      v[0] = f.x;
+      v[1] = f.y;
+    } else {
+      v[0] = static_cast<const float*>(p)[at];
+    }
+  } else if constexpr (W == 2) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + at);
+    if (fp16)
+      Word<__half>::get(w, v);
+    else
+      Word<__nv_bfloat16>::get(w, v);
+  } else {
+    v[0] = fp16 ? __half2float(static_cast<const __half*>(p)[at])
+                : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
+  }
+}
+template <int W>
+__device__ __forceinline__ void store_few(void* p, size_t at, int fp16, int wide, const float (&v)[W]) {
+  if (wide) {
+    if constexpr (W == 2)
+      *reinterpret_cast<float2*>(static_cast<float*>(p) + at) = make_float2(v[0], v[1]);
+    else
+      static_cast<float*>(p)[at] = v[0];
+  } else if constexpr (W == 2) {
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + at) =
+        fp16 ? Word<__half>::put(v) : Word<__nv_bfloat16>::put(v);
+  } else {
+    store16(p, at, v[0], fp16);
+  }
+}
+
+// R rows, `step` apart from row `row`, of W adjacent columns (where Q is no multiple of 8); the loads
+// and stores of the rows are independent.
+template <int R, int W>
+__device__ __forceinline__ void finish_columns(const Epilogue& e, int row, int step, int col, float (&z)[R][W]) {
+  size_t at[R];
+  bool valid[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    at[r] = (size_t)(row + r * step) * e.Q + col;
+    valid[r] = row + r * step < e.P;
+  }
+  if (e.bias) {
+    float b[W];
+    load_few<W>(e.bias, col, e.fp16, 0, b);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < W; ++i) z[r][i] += b[i];
+  }
+  float res[R][W];
   if (e.residual) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (r < rows) {
-        const size_t i = at + (size_t)r * e.Q;
-        res[r] = e.out32  ? static_cast<const float*>(e.residual)[i]
-                 : e.fp16 ? __half2float(static_cast<const __half*>(e.residual)[i])
-                          : __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[i]);
-      }
+      if (valid[r]) load_few<W>(e.residual, at[r], e.fp16, e.out32, res[r]);
+  }
+  if (e.preact) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (valid[r]) store_few<W>(e.preact, at[r], e.fp16, 0, z[r]);
+  }
+  if (e.act != MOE_LINEAR_NONE) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < W; ++i) z[r][i] = act_fwd(z[r][i], e.act);
   }
 #pragma unroll
   for (int r = 0; r < R; ++r)
-    if (r < rows) {
-      const size_t i = at + (size_t)r * e.Q;
-      float v = z[r] + b;
-      if (e.preact) store16(e.preact, i, v, e.fp16);
-      v = act_fwd(v, e.act);
-      if (e.residual) v += res[r];
-      if (e.out32)
-        static_cast<float*>(e.out)[i] = v;
-      else
-        store16(e.out, i, v, e.fp16);
+    if (valid[r]) {
+      if (e.residual) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) z[r][i] += res[r][i];
+      }
+      store_few<W>(e.out, at[r], e.fp16, e.out32, z[r]);
     }
 }
 __device__ __forceinline__ void finish1(const Epilogue& e, int row, int col, float z) {
-  float v[1] = {z};
-  finish_column<1>(e, row, col, v);
+  float v[1][1] = {{z}};
+  finish_columns<1, 1>(e, row, 1, col, v);
 }
 
 // 8 consecutive columns (Q % 8 == 0) of R rows, R independent chains of loads and stores;
@@ -274,6 +323,11 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(addr)
                : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_cluster1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
@@ -423,14 +477,30 @@ __device__ __forceinline__ void finish_chunk(const Epilogue& e, float* buf, cons
         }
       }
     } else {
-      // a lane takes a column: 64-byte pieces of rows that start anywhere
-      if (col0 + lane < e.Q)
-        for (int h = 0; h < 32 && row0 + h < e.P; h += 8) {
-          float z[8];
+      // rows start anywhere: a lane takes two columns of every other row, or one column when Q is odd
+      if (e.Q % 2 == 0) {
+        const int c = (lane & 15) * 2, odd = lane >> 4;
+        if (col0 + c < e.Q)
+#pragma unroll 1
+          for (int h = 0; h < 32 && row0 + h < e.P; h += 8) {
+            float z[4][2];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = buf_at(buf, h + i, lane >> 2)[lane & 3];
-          finish_column<8>(e, row0 + h, col0 + lane, z);
+            for (int i = 0; i < 4; ++i) {
+              const float2 f = *reinterpret_cast<const float2*>(buf_at(buf, h + 2 * i + odd, c >> 2) + (c & 3));
+              z[i][0] = f.x;
+              z[i][1] = f.y;
+            }
+            finish_columns<4, 2>(e, row0 + h + odd, 2, col0 + c, z);
+          }
+      } else if (col0 + lane < e.Q) {
+#pragma unroll 1
+        for (int h = 0; h < 32 && row0 + h < e.P; h += 8) {
+          float z[8][1];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i][0] = buf_at(buf, h + i, lane >> 2)[lane & 3];
+          finish_columns<8, 1>(e, row0 + h, 1, col0 + lane, z);
         }
+      }
     }
     __syncwarp();
   }
@@ -448,6 +518,35 @@ __device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int un
   const uint32_t base = smem_u32(smem);
   const int i1 = (int)((long long)items * (split + 1) / S);
   if (status_failed()) return;
+  if (!kPlain && p.e.Q % 8 != 0) {
+    // a warp takes 32 columns of four rows at a time
+    const int warp = (threadIdx.x >> 5) - kFirstEpi, lane = threadIdx.x & 31, pieces = (cols + 31) / 32;
+    const int r0 = rows * split / S, r1 = rows * (split + 1) / S, n = pieces * ((r1 - r0 + 3) / 4);
+#pragma unroll 1
+    for (int i = warp; i < n; i += kEpiWarps) {
+      const int c = i % pieces * 32 + lane, r = r0 + i / pieces * 4;
+      float v[4][S];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+          v[j][s] = ld_cluster1(map_to_rank(base + (uint32_t)((min(r + j, r1 - 1) * (p.BN + 4) + c) * 4), s * CG + half));
+      float z[4][1] = {};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int s = 0; s < S; ++s) z[j][0] += v[j][s];
+      // (rows past r1 are another CTA's)
+      if (c < cols) {
+        if (r + 4 <= r1)
+          finish_columns<4, 1>(p.e, row0 + r, 1, tn * p.BN + c, z);
+        else
+          for (int j = 0; j < 4; ++j)
+            if (r + j < r1) finish1(p.e, row0 + r + j, tn * p.BN + c, j == 0 ? z[0][0] : j == 1 ? z[1][0] : z[2][0]);
+      }
+    }
+    return;
+  }
   constexpr int U = S >= 8 ? 1 : 8 / S;  // items whose loads are in flight together
   constexpr int kStep = kEpiWarps * 32;
   for (int i0 = (int)((long long)items * split / S) + threadIdx.x - kFirstEpi * 32; i0 < i1; i0 += U * kStep) {
@@ -481,12 +580,8 @@ __device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int un
           store8(reinterpret_cast<__half*>(out), z[0]);
         else
           store8(reinterpret_cast<__nv_bfloat16*>(out), z[0]);
-      } else if (p.e.Q % 8 == 0) {
-        finish_rows<1>(p.e, row, col, valid, z);
       } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (col + j < p.e.Q) finish1(p.e, row[0], col + j, z[0][j]);
+        finish_rows<1>(p.e, row, col, valid, z);
       }
     }
   }

@@ -313,6 +313,18 @@ __device__ __noinline__ int rank_again(const TL* row, const RouteArgs& a, bool* 
   return mine;
 }
 
+// The softmax's denominator over the warp's logits (cnt of them at p in this lane): its terms are
+// within 1 ulp, and their sum adds nothing.
+template <class TL>
+__device__ __noinline__ FF sum_ff(const TL* p, int cnt, float m) {
+  FF sum{0.f, 0.f};
+  for (int i = 0; i < cnt; ++i) {
+    const float x = clean_logit(load1(p + i));
+    if (x > -INFINITY) sum = add(sum, {expf(x - m), 0.f});
+  }
+  for (int off = 16; off > 0; off >>= 1) sum = add(sum, PairScores::shfl(sum, off));
+  return sum;
+}
 __device__ __forceinline__ FF sigmoid_ff(float l) {
   const FF e = exp_ff({-fabsf(l), 0.f});
   return div(l < 0.f ? e : FF{1.f, 0.f}, add({1.f, 0.f}, e));
@@ -600,10 +612,10 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     if (r == a.top_k - 1) last_key = top;
     if (lane == r) my_id = id;
   }
-  if (near && softmax && !by_logit) unsure = true;
   if (near && !unsure) {
     // the r candidates, one a lane, ranked by their exact scores
-    my_id = rank_candidates(row, a, my_id, r, m, FF{1.f, 0.f}, &unsure);
+    my_id = rank_candidates(row, a, my_id, r, m, softmax && !by_logit ? sum_ff(row + base, cnt, m) : FF{1.f, 0.f},
+                            &unsure);
   }
   if (unsure) {
     my_id = rank_again<PairScores, NV, TL>(row, a, &unsure);
@@ -629,9 +641,9 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
   }
 }
 
-// Up to 8 choices among up to 8 experts a lane, one token by one warp, without rounds: every lane
-// sorts its keys, and five butterfly steps merge the lists of two lanes into the best 8 of both,
-// so that all lanes end with the chosen 8 in order.  A merge of two sorted lists of 8 takes 8
+// Up to 16 choices among up to 8 experts a lane, one token by one warp, without rounds: every lane
+// sorts its keys, and five butterfly steps merge the lists of two lanes into the best 8 (or 16) of
+// both, so that all lanes end with the chosen ones in order.  A merge of two sorted lists of 8 takes 8
 // shuffles, 8 maxima (of one list against the other reversed, which leaves the best 8 as a
 // bitonic sequence) and 12 comparators.  The keys carry the expert's place in the warp in their low
 // bits (8 of them for 256 experts), so a key names its expert; the cut makes a few tokens in a
@@ -640,8 +652,6 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
 // 23.5 us (0.8 TB/s).  It is bound by the integer pipe that does the minima and maxima: two tokens
 // a warp, 16 lanes each, took a quarter fewer instructions and the same time, and four tokens of
 // 32 experts a lane twice the time.
-constexpr int kFew = 8;
-
 // a[0..N) is bitonic: sorted descending
 template <int N, int M>
 __device__ __forceinline__ void bitonic_sort(uint32_t (&a)[M]) {
@@ -651,28 +661,29 @@ __device__ __forceinline__ void bitonic_sort(uint32_t (&a)[M]) {
     for (int i = 0; i < N; ++i)
       if ((i & k) == 0) order2(a[i], a[i + k]);
 }
-// The best kFew of the warp's lists of LEN sorted keys; OFF: lanes merged so far.
-template <int LEN, int OFF>
-__device__ __forceinline__ void merge_lists(uint32_t (&a)[kFew]) {
+// The best KL of the warp's lists of LEN sorted keys; OFF: lanes merged so far.
+template <int LEN, int OFF, int KL>
+__device__ __forceinline__ void merge_lists(uint32_t (&a)[KL]) {
   if constexpr (OFF < 32) {
     uint32_t o[LEN];
 #pragma unroll
     for (int i = 0; i < LEN; ++i) o[i] = __shfl_xor_sync(kFull, a[i], OFF);
-    if constexpr (LEN < kFew) {
+    if constexpr (LEN < KL) {
 #pragma unroll
       for (int i = 0; i < LEN; ++i) a[LEN + i] = o[LEN - 1 - i];
       bitonic_sort<2 * LEN>(a);
       merge_lists<2 * LEN, 2 * OFF>(a);
     } else {
 #pragma unroll
-      for (int i = 0; i < kFew; ++i) a[i] = max(a[i], o[kFew - 1 - i]);
-      bitonic_sort<kFew>(a);
-      merge_lists<kFew, 2 * OFF>(a);
+      for (int i = 0; i < KL; ++i) a[i] = max(a[i], o[KL - 1 - i]);
+      bitonic_sort<KL>(a);
+      merge_lists<KL, 2 * OFF>(a);
     }
   }
 }
 
-template <int NV, class TL>
+// KL: 8 or 16, at least top_k.
+template <int NV, int KL, class TL>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     route_grouped_merge_kernel(const RouteArgs a, int32_t* __restrict__ topk_ids, float* __restrict__ topk_weights) {
   constexpr uint32_t kPlace = 32 * NV - 1;  // the key bits that hold kPlace - (place in the warp)
@@ -762,7 +773,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
         // of the first left out.
         const uint32_t above = __reduce_min_sync(kFull, in_use && rank < a.topk_group - 1 ? score : kFull);
         const uint32_t below = __reduce_max_sync(kFull, in_use && rank > a.topk_group ? score : 0u);
-        unsure = (softmax && !by_logit) || (above != kFull && doubt.groups(above, left, err)) ||
+        unsure = (above != kFull && doubt.groups(above, left, err)) ||
                  (below > kMaskedKey && doubt.groups(last, below, err));
         const int ga = __shfl_sync(kFull, grp, __ffs(__ballot_sync(kFull, in_use && rank == a.topk_group - 1)) - 1);
         const int gb = __shfl_sync(kFull, grp, __ffs(__ballot_sync(kFull, in_use && rank == a.topk_group)) - 1);
@@ -793,20 +804,26 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
           }
         }
         if (!unsure) {
+          const bool divide = softmax && !by_logit;  // (else a softmax's numerators order like its scores)
+          const FF sum = divide ? sum_ff(row + base, cnt, m) : FF{1.f, 0.f};
           FF c{0.f, 0.f};
-          float x = 0.f, b = 0.f;
+          float x = 0.f, b = 0.f, part = 0.f;  // part: the scores without the biases
           if (id >= 0) {
             expert_inputs(row, a.bias, id, x, b);
-            c = softmax ? exp_ff(two_sum(x, -m)) : sigmoid_ff(x);  // (a softmax's numerators order like its scores)
+            c = softmax ? exp_ff(two_sum(x, -m)) : sigmoid_ff(x);
+            if (divide) c = div(c, sum);
+            part = c.h;
             c = b == INFINITY ? FF{b, 0.f} : add(c, {b, 0.f});
           }
+          part += __shfl_xor_sync(kFull, part, 1);
+          const float apart = divide ? 0x1p-22f * fabsf(__shfl_sync(kFull, part, 0) - __shfl_sync(kFull, part, 2)) : 0.f;
           const FF o = PairScores::shfl(c, 1);
           c = c.h == INFINITY || o.h == INFINITY ? FF{fmaxf(c.h, o.h), 0.f} : add(c, o);
           const uint64_t sa = __shfl_sync(kFull, PairScores::key(c), 0), sb = __shfl_sync(kFull, PairScores::key(c), 2);
           // (equal logits and biases: equal scores, and the lower group was kept)
           const float x2 = __shfl_down_sync(kFull, x, 2), b2 = __shfl_down_sync(kFull, b, 2);
           const bool same = __all_sync(kFull, lane >= 2 || (x == x2 && b == b2));
-          unsure = !same && PairScores::near(max(sa, sb), min(sa, sb));
+          unsure = !same && PairScores::near(max(sa, sb), min(sa, sb), apart);
           if (!same && sb > sa) keep = (keep && grp != ga) || (in_use && grp == gb);
         }
       }
@@ -818,9 +835,9 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
   doubt.cut = (32 * NV + 2) * 0x1p-23f;
   sort_keys(key);
 
-  uint32_t best[kFew];
+  uint32_t best[KL];
 #pragma unroll
-  for (int i = 0; i < kFew; ++i) best[i] = i < NV ? key[i < NV ? i : 0] : 0u;
+  for (int i = 0; i < KL; ++i) best[i] = i < NV ? key[i < NV ? i : 0] : 0u;
   merge_lists<NV, 1>(best);
 
   // lane r holds the r-th best; the first left out (none: 0) after them
@@ -832,15 +849,18 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
   };
   uint32_t mine = 0;
   {
-    uint32_t h[4];
+    uint32_t h[KL];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = lane & 1 ? best[2 * i + 1] : best[2 * i];
-    const uint32_t x = lane & 2 ? h[1] : h[0], y = lane & 2 ? h[3] : h[2];
-    mine = lane >= kFew ? 0u : lane & 4 ? y : x;
+    for (int i = 0; i < KL; ++i) h[i] = best[i];
+#pragma unroll
+    for (int n = KL / 2, bit = 1; n >= 1; n /= 2, bit *= 2)
+#pragma unroll
+      for (int i = 0; i < n; ++i) h[i] = lane & bit ? h[2 * i + 1] : h[2 * i];
+    if (lane < KL) mine = h[0];
   }
-  if (a.top_k == kFew) {
-    const uint32_t v = next_below(best[kFew - 1]);
-    if (lane == kFew) mine = v;
+  if (a.top_k == KL) {
+    const uint32_t v = next_below(best[KL - 1]);
+    if (lane == KL) mine = v;
   }
   auto expert_of = [&](uint32_t k) {
     const int pos = (int)(kPlace - (k & kPlace)), ln = pos / NV;
@@ -884,17 +904,9 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
           if (lane == n) my_id = expert_of(low);
           ++n;
         }
-        FF sum{0.f, 0.f};  // the softmax's denominator: its terms are within 1 ulp, their sum adds nothing
-        if (softmax && !by_logit) {
-#pragma unroll 1
-          for (int i = 0; i < cnt; ++i) {
-            const float x = clean_logit(load1(row + base + i));
-            if (x > -INFINITY) sum = add(sum, {expf(x - m), 0.f});
-          }
-#pragma unroll 1
-          for (int off = 16; off > 0; off >>= 1) sum = add(sum, PairScores::shfl(sum, off));
-        }
-        if (!unsure) my_id = rank_candidates(row, a, my_id, n, m, sum, &unsure);
+        if (!unsure)
+          my_id = rank_candidates(row, a, my_id, n, m,
+                                  softmax && !by_logit ? sum_ff(row + base, cnt, m) : FF{1.f, 0.f}, &unsure);
       }
       if (unsure) my_id = rank_again<PairScores, NV, TL>(row, a, &unsure);
       if (unsure) my_id = rank_again<DoubleScores, NV, TL>(row, a, &unsure);
@@ -1068,11 +1080,16 @@ extern "C" moe_status_t moe_route_grouped(const void* logits, moe_dtype_t logits
   for_nv((size + a.lpg - 1) / a.lpg, [&](auto n) {
     constexpr int NV = decltype(n)::value;
     with_type([&](auto tl) {
-      if constexpr (NV <= 8)
-        if (top_k <= kFew) {
-          route_grouped_merge_kernel<NV, decltype(tl)><<<grid, block, 0, s>>>(a, topk_ids, topk_weights);
+      if constexpr (NV <= 8) {
+        if (top_k <= 8) {
+          route_grouped_merge_kernel<NV, 8, decltype(tl)><<<grid, block, 0, s>>>(a, topk_ids, topk_weights);
           return;
         }
+        if (top_k <= 16) {
+          route_grouped_merge_kernel<NV, 16, decltype(tl)><<<grid, block, 0, s>>>(a, topk_ids, topk_weights);
+          return;
+        }
+      }
       route_grouped_kernel<NV, decltype(tl)><<<grid, block, 0, s>>>(a, topk_ids, topk_weights);
     });
   });
