@@ -525,7 +525,7 @@ moe_status_t moe_route_grouped(const void *logits, moe_dtype_t logits_dtype, con
                                float *topk_weights, moe_stream_t stream);
 
 /* Gradient of moe_route_grouped's weights with respect to the logits, the choice held fixed
- * (the bias has none): given dweights [T, top_k] fp32, the logits and the topk_ids of the
+ * (the bias has none): given dweights [T, top_k] fp32, the logits, bias and topk_ids of the
  * forward call, dlogits [T, E] in logits_dtype, every element written:
  *   renormalize, with p = s / (sum of the chosen s):
  *     dl_j = scale p_j f_j (dw_j - sum_i p_i dw_i),   f = 1 - s (sigmoid) or 1 (softmax)
@@ -534,10 +534,12 @@ moe_status_t moe_route_grouped(const void *logits, moe_dtype_t logits_dtype, con
  *   softmax otherwise:  dl_e = s_e (g_e - sum_i g_i s_i), g = scale dw on the chosen, else 0
  * Only score, renormalize and scale of cfg are used (the others are checked as above).  An id
  * chosen twice in a row adds up; an id outside [0, E) is left out and recorded as
- * MOE_ERR_INVALID_ARG in the device status word.  A masked (-inf or NaN) logit gets 0. */
+ * MOE_ERR_INVALID_ARG in the device status word.  A masked (-inf or NaN) logit gets 0, and the
+ * constant weight of a masked expert has no gradient; bias is read for its masks alone (NULL: it
+ * masks none). */
 moe_status_t moe_route_grouped_backward(const float *dweights, const void *logits,
-                                        moe_dtype_t logits_dtype, const int32_t *topk_ids, int T, int E,
-                                        int top_k, const moe_route_config *cfg, void *dlogits,
+                                        moe_dtype_t logits_dtype, const float *bias, const int32_t *topk_ids,
+                                        int T, int E, int top_k, const moe_route_config *cfg, void *dlogits,
                                         moe_stream_t stream);
 
 /* ------------------------------------------------------------------ finalize, gradient

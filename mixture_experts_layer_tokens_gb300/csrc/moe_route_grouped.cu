@@ -945,7 +945,8 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
       record_status((int)MOE_ERR_INVALID_ARG);
       id = -1;
     } else {
-      lj = clean_logit(load1(row + id));
+      float b;
+      expert_inputs(row, a.bias, id, lj, b);  // (the bias only masks here)
     }
   }
   const bool live = lj > -INFINITY;
@@ -1097,14 +1098,14 @@ extern "C" moe_status_t moe_route_grouped(const void* logits, moe_dtype_t logits
 }
 
 extern "C" moe_status_t moe_route_grouped_backward(const float* dweights, const void* logits, moe_dtype_t logits_dtype,
-                                                   const int32_t* topk_ids, int T, int E, int top_k,
+                                                   const float* bias, const int32_t* topk_ids, int T, int E, int top_k,
                                                    const moe_route_config* cfg, void* dlogits, moe_stream_t stream) {
   const moe_status_t st = check_route(logits_dtype, T, E, top_k, cfg);
   if (st != MOE_OK) return st;
   if (T == 0) return MOE_OK;
   MOE_CHECK_ARG(dweights && logits && topk_ids && dlogits);
-  MOE_CHECK_ARG(aligned16(dweights) && aligned16(logits) && aligned16(topk_ids) && aligned16(dlogits));
-  const RouteArgs a{logits,          nullptr,        T,              E,               top_k,     cfg->score,
+  MOE_CHECK_ARG(aligned16(dweights) && aligned16(logits) && aligned16(bias) && aligned16(topk_ids) && aligned16(dlogits));
+  const RouteArgs a{logits,          bias,           T,              E,               top_k,     cfg->score,
                     cfg->n_group, cfg->topk_group, cfg->group_top, cfg->renormalize, cfg->scale, E / cfg->n_group, 32};
   const dim3 grid((unsigned)((T + kWarpsPerBlock - 1) / kWarpsPerBlock)), block(kWarpsPerBlock * 32);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

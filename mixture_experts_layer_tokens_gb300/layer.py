@@ -72,7 +72,8 @@ class MoERouter:
                                device=dev))
             self._dlogits = torch.empty_like(self.logits)
         ids = self.topk_ids if topk_ids is None else topk_ids
-        moe.moe_route_grouped_backward(dweights, self.logits, ids, dlogits=self._dlogits, stream=stream, **self.weigh)
+        moe.moe_route_grouped_backward(dweights, self.logits, ids, bias=self.balance_bias, dlogits=self._dlogits,
+                                       stream=stream, **self.weigh)
         da1, dgate_w, dgate_bias = moe.moe_linear_backward(self._dlogits, a1, self.gate_w, stream=stream, **self._grads)
         return dgate_w, dgate_bias, da1, self._dlogits
 

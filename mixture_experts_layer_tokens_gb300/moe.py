@@ -112,7 +112,7 @@ SIGNATURES = {
     "moe_linear_backward": ([_P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _Z, _P], _I),
     "moe_linear_backward_workspace_size": ([_I, _I, _I], _Z),
     "moe_route_grouped": ([_P, _I, _P, _I, _I, _I, _RCP, _P, _P, _P], _I),
-    "moe_route_grouped_backward": ([_P, _P, _I, _P, _I, _I, _I, _RCP, _P, _P], _I),
+    "moe_route_grouped_backward": ([_P, _P, _I, _P, _P, _I, _I, _I, _RCP, _P, _P], _I),
     "moe_finalize_backward": ([_P, _P, _P, _P, _F, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _Z, _P], _I),
     "moe_finalize_backward_workspace_size": ([_I, _I], _Z),
     "moe_device_status": ([_I], _I),
@@ -736,9 +736,11 @@ def moe_route_grouped(logits: torch.Tensor, top_k: int, bias: Optional[torch.Ten
 
 def moe_route_grouped_backward(dweights: torch.Tensor, logits: torch.Tensor, topk_ids: torch.Tensor,
                                score: str = "sigmoid", renormalize: bool = True, scale: float = 1.0,
-                               dlogits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                               bias: Optional[torch.Tensor] = None, dlogits: Optional[torch.Tensor] = None,
+                               stream=None) -> torch.Tensor:
     """Gradient of moe_route_grouped's weights with respect to its logits (``moe_route_grouped_backward``), the
-    choice topk_ids held fixed: dweights [T, top_k] fp32 -> dlogits [T, E] in the logits' type."""
+    choice topk_ids held fixed: dweights [T, top_k] fp32 -> dlogits [T, E] in the logits' type.  bias: the forward
+    call's, needed where it masks experts."""
     if logits.dtype not in _DT:
         raise TypeError(f"logits: expected float32, bfloat16 or float16, got {logits.dtype}")
     (T, E), top_k = logits.shape, topk_ids.shape[1]
@@ -749,7 +751,8 @@ def moe_route_grouped_backward(dweights: torch.Tensor, logits: torch.Tensor, top
     _check("moe_route_grouped_backward", lib().moe_route_grouped_backward(
         _tensor(dweights, torch.float32, (T, top_k), "dweights", dev),
         _tensor(logits, logits.dtype, (T, E), "logits", dev), _DT[logits.dtype],
-        _tensor(topk_ids, torch.int32, (T, top_k), "topk_ids", dev), T, E, top_k, cfg,
+        _tensor(bias, torch.float32, (E,), "bias", dev), _tensor(topk_ids, torch.int32, (T, top_k), "topk_ids", dev),
+        T, E, top_k, cfg,
         _tensor(dlogits, logits.dtype, (T, E), "dlogits", dev), s))
     return dlogits
 

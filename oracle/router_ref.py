@@ -117,15 +117,18 @@ def route_grouped(logits, top_k, bias=None, score="sigmoid", n_group=1, topk_gro
     return ids, ws
 
 
-def route_grouped_backward(dweights, logits, topk_ids, score="sigmoid", renormalize=True, scale=1.0):
-    """dlogits [T, E] and a bound on the terms that it is the sum of (numpy)."""
+def route_grouped_backward(dweights, logits, topk_ids, score="sigmoid", renormalize=True, scale=1.0, bias=None):
+    """dlogits [T, E] and a bound on the terms that it is the sum of (numpy); the weight of an expert that the
+    bias masks is the constant 0."""
     l, s = _clean(logits), scores(logits, score)
     T, E = l.shape
     dw = dweights.detach().cpu().double().numpy() * scale
     ids = topk_ids.detach().cpu().numpy()
+    b = np.zeros(E) if bias is None else bias.detach().cpu().double().numpy()
+    gone = np.isnan(b) | np.isneginf(b)
     out, mag = np.zeros((T, E)), np.zeros((T, E))
     for t in range(T):
-        ok = [j for j in range(ids.shape[1]) if 0 <= ids[t, j] < E and not np.isneginf(l[t, ids[t, j]])]
+        ok = [j for j in range(ids.shape[1]) if 0 <= ids[t, j] < E and not (np.isneginf(l[t, ids[t, j]]) or gone[ids[t, j]])]
         if not ok:
             continue
         e = [ids[t, j] for j in ok]

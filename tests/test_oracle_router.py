@@ -101,6 +101,31 @@ def test_route_gradient_against_differences(score, renorm):
     assert (mag >= np.abs(got) - 1e-15).all()
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_gradient_of_masked_choices_against_differences(score, renorm):
+    """More choices than experts: what the bias masks is chosen with the constant weight 0."""
+    g = torch.Generator().manual_seed(10)
+    l = torch.randn((2, 6), generator=g, dtype=torch.float64)
+    bias = torch.tensor([0.1, float("-inf"), 0.0, float("nan"), float("-inf"), -0.2])
+    dw = torch.randn((2, 5), generator=g, dtype=torch.float64)
+    ids, _ = rr.route_grouped(l, 5, bias, score=score, renormalize=renorm)
+    assert sorted(ids[0, :3]) == [0, 2, 5] and ids[0, 3:].tolist() == [1, 3]
+
+    def f(l):
+        got, w = rr.route_grouped(l, 5, bias, score=score, renormalize=renorm, scale=2.5)
+        assert (got == ids).all()
+        return (w * dw.numpy()).sum()
+
+    got, mag = rr.route_grouped_backward(dw, l, torch.from_numpy(ids), score, renorm, 2.5, bias)
+    for t, e in itertools.product(range(2), range(6)):
+        a, b = l.clone(), l.clone()
+        a[t, e] += 1e-5
+        b[t, e] -= 1e-5
+        assert abs((f(a) - f(b)) / 2e-5 - got[t, e]) < 1e-8
+    assert (mag >= np.abs(got) - 1e-15).all()
+
+
 @pytest.mark.parametrize("rms", [True, False])
 def test_finalize_gradient_against_autograd(rms):
     g = torch.Generator().manual_seed(4)

@@ -160,6 +160,24 @@ def test_route_backward_masks_and_repeated_ids(cuda_dev, score, renorm):
     _check_backward(cuda_dev, l, ids, torch.randn((8, 4), generator=g), score=score, renormalize=renorm)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_backward_of_experts_that_the_bias_masks(cuda_dev, score, renorm):
+    """Fewer experts than choices are left: the masked ones are chosen with the constant weight 0."""
+    g = torch.Generator().manual_seed(8)
+    l = torch.randn((20, 12), generator=g)
+    bias = torch.full((12,), float("-inf"))
+    bias[1], bias[4], bias[7], bias[9] = 0.1, float("nan"), -0.2, float("inf")
+    ids, w = moe.moe_route_grouped(l.to(cuda_dev), 6, bias.to(cuda_dev), score=score, renormalize=renorm)
+    assert int((w == 0).sum()) == 20 * 3
+    dw = torch.randn((20, 6), generator=g)
+    dl = moe.moe_route_grouped_backward(dw.to(cuda_dev), l.to(cuda_dev), ids, score=score, renormalize=renorm,
+                                        bias=bias.to(cuda_dev))
+    ref, mag = rr.route_grouped_backward(dw, l, ids, score, renorm, bias=bias)
+    err = np.abs(dl.cpu().double().numpy() - ref)
+    assert (err <= mag * 2.0 ** -19 + np.abs(ref) * 2.0 ** -24).all()
+
+
 def test_route_backward_out_of_range_ids_are_recorded(cuda_dev):
     l = torch.randn((4, 8), device=cuda_dev)
     ids = torch.tensor([[0, 1], [8, 2], [-1, 3], [2 ** 31 - 1, -2 ** 31]], dtype=torch.int32, device=cuda_dev)

@@ -67,11 +67,11 @@ def test_route_grouped_refusals(moelib):
 
 
 def test_route_grouped_backward_refusals(moelib):
-    def call(dw=FAKE, l=FAKE, dt=FP32, ids=FAKE, T=4, E=16, k=2, cfg=None, dl=FAKE):
-        return moelib.moe_route_grouped_backward(dw, l, dt, ids, T, E, k, cfg or _cfg(), dl, None)
+    def call(dw=FAKE, l=FAKE, dt=FP32, b=None, ids=FAKE, T=4, E=16, k=2, cfg=None, dl=FAKE):
+        return moelib.moe_route_grouped_backward(dw, l, dt, b, ids, T, E, k, cfg or _cfg(), dl, None)
 
     for kw in (dict(T=-1), dict(E=0), dict(k=17), dict(dw=None), dict(l=None), dict(ids=None), dict(dl=None),
-               dict(dl=P(4)), dict(cfg=_cfg(score=5))):
+               dict(dl=P(4)), dict(b=P(4)), dict(cfg=_cfg(score=5))):
         assert call(**kw) == BAD, kw
     assert call(dt=FP8) == UNSUP
     assert call(T=0, dw=None) == moe.MOE_OK
