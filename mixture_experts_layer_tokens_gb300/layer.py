@@ -64,13 +64,13 @@ class MoERouter:
         (topk_ids, when forward wrote another buffer than its own) held fixed.  Buffers of the router, written
         again by the next call."""
         if self._grads is None:
-            E, dev = self.E, self.gate_w.device
+            (E, H), dt, dev = self.gate_w.shape, self.gate_w.dtype, self.gate_w.device
+            # (made by the first call, so from the pool of the stream that it runs on)
+            self._dlogits = moe._empty((self.T, E), torch.float32, dev, stream)
             self._grads = dict(
-                dx=torch.empty_like(a1), dw=torch.empty_like(self.gate_w),
-                dbias=None if self.gate_bias is None else torch.empty_like(self.gate_bias),
-                ws=torch.empty(max(moe.linear_backward_workspace_size(self.T, E, a1.shape[1]), 16), dtype=torch.uint8,
-                               device=dev))
-            self._dlogits = torch.empty_like(self.logits)
+                dx=moe._empty((self.T, H), dt, dev, stream), dw=moe._empty((E, H), dt, dev, stream),
+                dbias=None if self.gate_bias is None else moe._empty((E,), dt, dev, stream),
+                ws=moe._empty((max(moe.linear_backward_workspace_size(self.T, E, H), 16),), torch.uint8, dev, stream))
         ids = self.topk_ids if topk_ids is None else topk_ids
         moe.moe_route_grouped_backward(dweights, self.logits, ids, bias=self.balance_bias, dlogits=self._dlogits,
                                        stream=stream, **self.weigh)

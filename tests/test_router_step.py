@@ -116,6 +116,34 @@ def test_router_step_captured_beside_eager_ones_and_on_two_streams(cuda_dev):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_router_gradients_on_another_stream_and_after_a_refused_call(cuda_dev):
+    """The router's gradient buffers are made by its first call: one that is refused leaves them fit for the
+    next, and one on another stream takes none that the current stream still works on."""
+    (cfg, _, layer, *_, g), (_, _, ref, *_) = _layer(cuda_dev), _layer(cuda_dev)
+    dw = torch.randn((cfg.T, cfg.top_k), generator=g).to(cuda_dev)
+    layer.forward(None, layer.inp.a1)
+    ref.forward(None, ref.inp.a1)
+    want = [t.clone() for t in ref.router.backward(dw, ref.inp.a1, ref.topk_ids)]
+    with pytest.raises(ValueError):
+        layer.router.backward(dw, layer.inp.a1[:, :64].contiguous(), layer.topk_ids)
+    got = layer.router.backward(dw, layer.inp.a1, layer.topk_ids)
+    assert all(torch.equal(a, w) for a, w in zip(got, want))
+    torch.cuda.synchronize()
+    layer.router._grads = None
+    side = torch.cuda.Stream()
+    n = layer.router.gate_w.numel()
+    junk = torch.empty(n, dtype=BF, device=cuda_dev)
+    torch.cuda._sleep(20_000_000)
+    junk.fill_(7.0)
+    del junk  # (the current stream still has it to write)
+    got = layer.router.backward(dw, layer.inp.a1, layer.topk_ids, stream=side)
+    side.synchronize()
+    early = [t.cpu() for t in got]
+    torch.cuda.synchronize()
+    for a, b, w in zip(got, early, want):
+        assert torch.equal(a, w) and torch.equal(b, w.cpu())
+
+
 def test_layer_and_router_refusals(cuda_dev):
     cfg, inp, layer, *_ = _layer(cuda_dev)
     other = MoERouter(cfg.T + 1, layer.router.gate_w, cfg.top_k)
