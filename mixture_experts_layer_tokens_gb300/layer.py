@@ -80,19 +80,23 @@ class MoERouter:
 
 class MoELayer:
     """router: a MoERouter of the same tokens, experts and top_k that takes the place of moe_route (the
-    forward call's logits are then not read and may be None)."""
+    forward call's logits are then not read and may be None).  keep_residual: forward also writes the sum before
+    the RMSNorm to residual_out, which router_backward needs."""
 
     def __init__(self, inp: LayerInputs, stream: Optional[torch.cuda.Stream] = None,
-                 router: Optional[MoERouter] = None):
+                 router: Optional[MoERouter] = None, keep_residual: bool = False):
         cfg = self.cfg = inp.cfg
         assert not cfg.finalize_only
         self.router = router
         if router is not None and ((router.T, router.E, router.top_k) != (cfg.T, cfg.E, cfg.top_k) or
                                    cfg.single_launch):
             raise ValueError("router: expected one of the layer's tokens, experts and top_k, and separate launches")
+        if keep_residual and cfg.single_launch:
+            raise ValueError("keep_residual: expected separate launches")
         self.inp = inp
         dev = inp.logits.device
         T, H, I, E, k = cfg.T, cfg.H, cfg.I, cfg.E, cfg.top_k
+        self.residual_out = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if keep_residual else None
         self.scoring = moe.MOE_SCORING_SIGMOID if cfg.scoring == "sigmoid" else moe.MOE_SCORING_SOFTMAX_RENORM
         self.topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
         self.topk_weights = torch.empty((T, k), dtype=torch.float32, device=dev)
@@ -182,18 +186,23 @@ class MoELayer:
         if self.shared_side:
             main.wait_event(self.ev_join)
         moe.moe_finalize(self.y, self.topk_weights, cfg.top_k, cfg.weight_on_input, shared=shared,
-                         residual=inp.residual, rms_weight=inp.rms_weight, output=self.out, stream=stream)
+                         residual=inp.residual, rms_weight=inp.rms_weight, output=self.out,
+                         residual_out=self.residual_out, stream=stream)
         return self.out
 
     def router_backward(self, dout: torch.Tensor, a1: torch.Tensor, residual_out: Optional[torch.Tensor] = None,
                         stream=None):
         """Gradients that train the router of a layer whose experts are held fixed: dout [T, H] bf16, the
         gradient of the last forward call's output -> (finalize gradients, router gradients), as
-        moe_finalize_backward and MoERouter.backward return them.  residual_out: the sum before the RMSNorm
-        (layers with one).  The router weights of a layer that applies them on the input have no gradient
-        here."""
+        moe_finalize_backward and MoERouter.backward return them.  residual_out: the sum before the RMSNorm (layers
+        with one; None: what a keep_residual layer's forward call wrote).  The router weights of a layer that
+        applies them on the input have no gradient here."""
         if self.router is None or self.cfg.weight_on_input:
             raise ValueError("router_backward needs a MoERouter whose weights are applied in the finalize")
+        if residual_out is None:
+            residual_out = self.residual_out
+        if residual_out is None and self.inp.rms_weight is not None:
+            raise ValueError("router_backward under an RMSNorm needs residual_out, or a layer with keep_residual")
         fin = moe.moe_finalize_backward(dout, self.y, self.topk_weights, self.cfg.top_k, residual_out=residual_out,
                                         rms_weight=self.inp.rms_weight, need_dy=False, stream=stream)
         return fin, self.router.backward(fin[1], a1, self.topk_ids, stream=stream)

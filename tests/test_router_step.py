@@ -85,6 +85,24 @@ def test_router_gradients_through_the_layer(cuda_dev, score, renorm, rms):
     assert near(dgb, want.sum(0), 2.0 ** -8 + 2.0 ** -14)
 
 
+def test_layer_keeps_its_residual_for_the_gradients(cuda_dev):
+    """keep_residual: the same output, the residual stream that moe_finalize writes, and the gradients that
+    this stream gives when handed in."""
+    cfg, _, layer, *_, g = _layer(cuda_dev)
+    keep = MoELayer(layer.inp, router=layer.router, keep_residual=True)
+    out = layer.forward(None, layer.inp.a1).clone()
+    assert torch.equal(keep.forward(None, layer.inp.a1), out)
+    o = torch.empty_like(out)
+    moe.moe_finalize(layer.y, layer.topk_weights, cfg.top_k, False, residual=layer.inp.residual,
+                     rms_weight=layer.inp.rms_weight, residual_out=o)
+    assert torch.equal(keep.residual_out, o)
+    dout = torch.randn((cfg.T, cfg.H), generator=g).to(BF).to(cuda_dev)
+    want = [t.clone() for t in layer.router_backward(dout, layer.inp.a1, o)[1]]
+    assert all(torch.equal(a, b) for a, b in zip(keep.router_backward(dout, layer.inp.a1)[1], want))
+    with pytest.raises(ValueError):
+        layer.router_backward(dout, layer.inp.a1)
+
+
 def test_router_step_captured_beside_eager_ones_and_on_two_streams(cuda_dev):
     """Two layers' steps with their own buffers, one captured and replayed, one eager on another stream at the
     same time, give what they give alone."""
