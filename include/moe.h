@@ -449,8 +449,9 @@ moe_status_t moe_finalize(void *output, const void *fused_expert_output, const f
  * MOE_DT_FP16); out [M, N] and residual [M, N] (NULL = none) in out_dtype (dtype itself or
  * MOE_DT_FP32); preact [M, N] in dtype, NULL = not written.  residual may be out itself (the
  * projection is then added in place); any other overlap of an output with another buffer is
- * not allowed.  activation: a moe_linear_activation_t.  M >= 0 (0: nothing is done), N >= 1,
- * K >= 8 and K % 8 == 0; any N (a multiple of 8 is stored by 16-byte vectors).  Every pointer
+ * not allowed.  activation: a moe_linear_activation_t.  0 <= M <= 2^30 (0: nothing is done),
+ * 1 <= N <= 2^21, 8 <= K <= 2^30 and K % 8 == 0 (an N that is a multiple of 8 is stored by
+ * 16-byte vectors); a product of over 2^27 tiles of 128 x 64 may be MOE_ERR_UNSUPPORTED.  Every pointer
  * 16-byte aligned.  A row of x that holds a NaN or an infinity affects that row of out alone.
  * The sums of a call have a fixed order: the same inputs give the same bits. */
 typedef enum {
@@ -506,7 +507,7 @@ size_t moe_linear_backward_workspace_size(int M, int N, int K);
  * group of masked experts alone ranks last), chosen only when the kept groups have fewer than
  * top_k others, lower index first, with weight 0.  +inf counts as the largest finite number.
  * logits [T, E] in logits_dtype (MOE_DT_FP32, MOE_DT_BF16 or MOE_DT_FP16); topk_ids [T, top_k]
- * int32; topk_weights [T, top_k] fp32.  1 <= E <= 1024, 1 <= top_k <= 32, n_group <= 32
+ * int32; topk_weights [T, top_k] fp32.  T <= 2^30, 1 <= E <= 1024, 1 <= top_k <= 32, n_group <= 32
  * divides E, 1 <= topk_group <= n_group, group_top 1 or 2 (at most the group's size), top_k <=
  * topk_group * E / n_group, scale finite. */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
@@ -560,9 +561,10 @@ moe_status_t moe_route_grouped_backward(const float *dweights, const void *logit
  * rms_weight, then required); fused_expert_output (y) [T * top_k, H] bf16 is read for
  * dweights alone (may be NULL without it).  dy, dweights (needs topk_weights), dsum and drms
  * (needs rms_weight) may each be NULL: not computed; not all.  Sums in fp32, in a fixed order;
- * G stays in fp32 until an output is rounded.  T == 0 sets drms to zero.  H % 8 == 0, H <=
+ * G stays in fp32 until an output is rounded.  T <= 2^30 (0 sets drms to zero), H % 8 == 0, H <=
  * 16384, 1 <= top_k <= 32.  ws: moe_finalize_backward_workspace_size(T, H) bytes (needed for
- * drms alone; as for moe_linear_backward it depends on the device and belongs to one call).  dsum may be dout or dresidual_out itself; no other overlap. */
+ * drms alone; as for moe_linear_backward it depends on the device and belongs to one call).  dsum
+ * may be dout or dresidual_out itself; no other overlap. */
 moe_status_t moe_finalize_backward(const void *dout, const void *dresidual_out, const void *residual_out,
                                    const void *rms_weight, float eps, const void *fused_expert_output,
                                    const float *topk_weights, int T, int H, int top_k, void *dy,

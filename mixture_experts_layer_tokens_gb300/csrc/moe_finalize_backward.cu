@@ -306,7 +306,7 @@ extern "C" moe_status_t moe_finalize_backward(const void* dout, const void* dres
                                               const float* topk_weights, int T, int H, int top_k, void* dy,
                                               float* dweights, void* dsum, float* drms, void* ws, size_t ws_bytes,
                                               moe_stream_t stream) {
-  MOE_CHECK_ARG(T >= 0 && H > 0 && H % 8 == 0 && top_k >= 1 && top_k <= kMaxK && eps >= 0.f);
+  MOE_CHECK_ARG(T >= 0 && T <= (1 << 30) && H > 0 && H % 8 == 0 && top_k >= 1 && top_k <= kMaxK && eps >= 0.f);
   MOE_CHECK_ARG(dy || dweights || dsum || drms);
   MOE_CHECK_ARG(!drms || rms_weight);
   if (H > kMaxH) return MOE_ERR_UNSUPPORTED;

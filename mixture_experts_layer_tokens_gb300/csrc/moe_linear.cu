@@ -19,6 +19,8 @@
 
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 namespace moe {
 namespace {
 
@@ -1066,11 +1068,12 @@ cudaError_t launch_gemm(int cg, int ks, const CUtensorMap& ma, const CUtensorMap
 // Clusters of `size` GEMM CTAs that fit the device at once (a cluster lies within one group of
 // SMs, so eight-CTA clusters leave SMs idle); asked once per device and size.
 int cluster_slots(int size) {
-  static int cached[64][4] = {};
+  static std::atomic<int> cached[64][4];  // (host threads may come at once)
   int dev = 0, log2 = 0;
   while ((1 << log2) < size) ++log2;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms() / size;
-  if (cached[dev][log2] == 0) {
+  int n = cached[dev][log2].load(std::memory_order_relaxed);
+  if (n == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)size);
     cfg.blockDim = dim3(kThreads);
@@ -1082,16 +1085,15 @@ int cluster_slots(int size) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int n = 0;
     auto kern = linear_gemm_kernel<false, false, 1, false, 1>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
       (void)cudaGetLastError();
       n = num_sms() / size;
     }
-    cached[dev][log2] = n;
+    cached[dev][log2].store(n, std::memory_order_relaxed);
   }
-  return cached[dev][log2];
+  return n;
 }
 
 // How a product is cut: CTAs per MMA, tile columns, CTAs (pairs) that share a tile's K.

@@ -1037,13 +1037,12 @@ void for_nv(int nv, F f) {
 }
 
 moe_status_t check_route(moe_dtype_t dt, int T, int E, int top_k, const moe_route_config* c) {
-  MOE_CHECK_ARG(c && T >= 0 && E >= 1 && E <= 1024 && top_k >= 1 && top_k <= 32);
+  MOE_CHECK_ARG(c && T >= 0 && T <= (1 << 30) && E >= 1 && E <= 1024 && top_k >= 1 && top_k <= 32);
   MOE_CHECK_ARG(c->n_group >= 1 && c->n_group <= 32 && E % c->n_group == 0);
   MOE_CHECK_ARG(c->topk_group >= 1 && c->topk_group <= c->n_group && top_k <= c->topk_group * (E / c->n_group));
   MOE_CHECK_ARG((c->group_top == 1 || c->group_top == 2) && c->group_top <= E / c->n_group);
   MOE_CHECK_ARG(c->score == MOE_SCORE_SOFTMAX || c->score == MOE_SCORE_SIGMOID);
   MOE_CHECK_ARG(c->scale - c->scale == 0.f);  // finite
-  MOE_CHECK_ARG(T <= 2147483647 - kWarpsPerBlock);
   if (dt != MOE_DT_FP32 && dt != MOE_DT_BF16 && dt != MOE_DT_FP16) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

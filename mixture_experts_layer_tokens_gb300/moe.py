@@ -612,6 +612,9 @@ def _tensor(t: Optional[torch.Tensor], dtype, shape, name: str, device: int):
     raise ValueError(f"{name}: expected a contiguous tensor")
 
 
+_INT_MAX = 2 ** 31 - 1  # (ctypes cuts a longer size without a word)
+
+
 def _launch(stream: Optional[torch.cuda.Stream]):
     """(current device index, raw stream) of a call.  (A call without outputs to allocate costs the host a few
     microseconds, so the raw stream is asked for rather than a torch.cuda.Stream built around it.)"""
@@ -640,6 +643,8 @@ def _linear_args(x: torch.Tensor, w: torch.Tensor, activation: str):
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w: expected [M, K] and [N, K]")
     (M, K), N = x.shape, w.shape[0]
+    if M > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
+        raise ValueError("x and w: expected sizes up to 2^31 - 1")
     return M, N, K, x.dtype, _DT[x.dtype], LINEAR_ACTIVATIONS[activation]
 
 
@@ -697,7 +702,7 @@ def moe_linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pr
 
 
 # ------------------------------------------------------------------ grouped route
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=1024)
 def _route_config(score, n_group, topk_group, group_top, renormalize, scale):
     return ctypes.byref(route_config(score, n_group, topk_group, group_top, renormalize, scale))
 
@@ -720,6 +725,8 @@ def moe_route_grouped(logits: torch.Tensor, top_k: int, bias: Optional[torch.Ten
     if logits.dtype not in _DT:
         raise TypeError(f"logits: expected float32, bfloat16 or float16, got {logits.dtype}")
     T, E = logits.shape
+    if T > _INT_MAX or E > _INT_MAX or not 1 <= top_k <= _INT_MAX:
+        raise ValueError("logits and top_k: expected sizes up to 2^31 - 1")
     cfg = _route_config(score, n_group, topk_group, group_top, bool(renormalize), scale)
     if topk_ids is None:
         topk_ids = _empty((T, top_k), torch.int32, logits.device, stream)
@@ -743,7 +750,9 @@ def moe_route_grouped_backward(dweights: torch.Tensor, logits: torch.Tensor, top
     call's, needed where it masks experts."""
     if logits.dtype not in _DT:
         raise TypeError(f"logits: expected float32, bfloat16 or float16, got {logits.dtype}")
-    (T, E), top_k = logits.shape, topk_ids.shape[1]
+    (T, E), (_, top_k) = logits.shape, topk_ids.shape
+    if T > _INT_MAX or E > _INT_MAX or top_k > _INT_MAX:
+        raise ValueError("logits and topk_ids: expected sizes up to 2^31 - 1")
     cfg = _route_config(score, 1, 1, 1, bool(renormalize), scale)
     if dlogits is None:
         dlogits = _empty((T, E), logits.dtype, logits.device, stream)
@@ -776,6 +785,8 @@ def moe_finalize_backward(dout: torch.Tensor, fused_expert_output: Optional[torc
     bf16 -- the gradient of the shared row and of the residual --, drms [H] fp32), None where not needed.
     topk_weights None: the weights were applied on the input (no dweights)."""
     T, H = dout.shape
+    if T > _INT_MAX or H > _INT_MAX or not 1 <= top_k <= _INT_MAX:
+        raise ValueError("dout and top_k: expected sizes up to 2^31 - 1")
     bf, d = torch.bfloat16, dout.device
     if dy is None and need_dy:
         dy = _empty((T * top_k, H), bf, d, stream)

@@ -18,7 +18,7 @@ def test_linear_refusals(moelib):
 
     for kw in (dict(M=-1), dict(N=0), dict(K=0), dict(K=4), dict(K=68), dict(x=None), dict(w=None), dict(out=None),
                dict(x=P(264)), dict(w=P(258)), dict(b=P(260)), dict(r=P(264)), dict(out=P(2)), dict(pre=P(8)),
-               dict(N=(1 << 21) + 1)):
+               dict(N=(1 << 21) + 1), dict(M=(1 << 30) + 1), dict(K=(1 << 30) + 8)):
         assert call(**kw) == BAD, kw
     for kw in (dict(dt=FP32), dict(dt=FP8), dict(dt=9), dict(odt=FP16), dict(dt=FP16, odt=BF16), dict(odt=FP8),
                dict(act=4), dict(act=-1)):
@@ -53,7 +53,7 @@ def test_route_grouped_refusals(moelib):
     def call(l=FAKE, dt=FP32, b=None, T=4, E=16, k=2, cfg=None, ids=FAKE, w=FAKE):
         return moelib.moe_route_grouped(l, dt, b, T, E, k, cfg or _cfg(), ids, w, None)
 
-    for kw in (dict(T=-1), dict(E=0), dict(E=1025), dict(k=0), dict(k=17), dict(k=33, E=64), dict(l=None), dict(ids=None),
+    for kw in (dict(T=-1), dict(T=(1 << 30) + 1), dict(E=0), dict(E=1025), dict(k=0), dict(k=17), dict(k=33, E=64), dict(l=None), dict(ids=None),
                dict(w=None), dict(l=P(4)), dict(b=P(4)), dict(ids=P(4)), dict(w=P(4)), dict(cfg=_cfg(score=2)),
                dict(cfg=_cfg(n_group=0)), dict(cfg=_cfg(n_group=3)), dict(cfg=_cfg(n_group=33), E=66),
                dict(cfg=_cfg(n_group=4, topk_group=0)), dict(cfg=_cfg(n_group=4, topk_group=5)),
@@ -82,7 +82,7 @@ def test_finalize_backward_refusals(moelib):
              drms=FAKE, ws=FAKE, n=1 << 20):
         return moelib.moe_finalize_backward(d, dr, o, g, eps, y, w, T, H, k, dy, dw, ds, drms, ws, n, None)
 
-    for kw in (dict(T=-1), dict(H=0), dict(H=60), dict(k=0), dict(k=33), dict(eps=-1.0), dict(d=None), dict(o=None),
+    for kw in (dict(T=-1), dict(T=(1 << 30) + 1), dict(H=0), dict(H=60), dict(k=0), dict(k=33), dict(eps=-1.0), dict(d=None), dict(o=None),
                dict(g=None), dict(y=None), dict(w=None), dict(dy=None, dw=None, ds=None, drms=None), dict(d=P(8)),
                dict(dy=P(8)), dict(drms=P(8)), dict(ws=P(8)), dict(eps=float("nan"))):
         assert call(**kw) == BAD, kw
@@ -105,6 +105,20 @@ def test_binding_refusals_without_a_gpu():
         moe.moe_route_grouped(torch.zeros((4, 8)), 2, score="tanh")
     with pytest.raises(TypeError):
         moe.moe_route_grouped(torch.zeros((4, 8), dtype=torch.float64), 2)
+    # sizes past 32 bits are refused, not cut off
+    meta = lambda *shape, t=torch.bfloat16: torch.empty(shape, dtype=t, device="meta")  # noqa: E731
+    for call in (lambda: moe.moe_linear(meta(2 ** 32 + 4, 64), meta(8, 64)),
+                 lambda: moe.moe_linear(meta(4, 64), meta(2 ** 32 + 8, 64)),
+                 lambda: moe.moe_linear_backward(meta(4, 8), meta(4, 2 ** 32 + 8), meta(8, 2 ** 32 + 8)),
+                 lambda: moe.moe_route_grouped(meta(2 ** 32 + 4, 16), 2),
+                 lambda: moe.moe_route_grouped(meta(4, 2 ** 32 + 16), 2),
+                 lambda: moe.moe_route_grouped(meta(4, 16), 2 ** 32 + 2),
+                 lambda: moe.moe_route_grouped(meta(4, 16), -1),
+                 lambda: moe.moe_route_grouped_backward(meta(4, 2), meta(2 ** 32 + 4, 16), meta(4, 2)),
+                 lambda: moe.moe_finalize_backward(meta(2 ** 32 + 4, 64), None, None, 2),
+                 lambda: moe.moe_finalize_backward(meta(4, 64), None, None, 0)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
     # the per-argument check: type, shape, contiguity, device
     ok = torch.zeros((4, 8))
     for t, err in ((ok.double(), TypeError), (ok[:3], ValueError), (torch.zeros((8, 4)).T, ValueError), (ok, ValueError)):
