@@ -97,93 +97,177 @@ __device__ __forceinline__ void store16(void* p, size_t i, float v, int fp16) {
     store1(static_cast<__nv_bfloat16*>(p) + i, v);
 }
 
-// W (1 or 2) adjacent columns of a row, as 16-bit or fp32 values.
-template <int W>
-__device__ __forceinline__ void load_few(const void* p, size_t at, int fp16, int wide, float (&v)[W]) {
-  // (plain loads: residual may be out)
+// One value, or an aligned pair of adjacent ones, of a 16-bit or fp32 (wide) tensor.
+// (plain loads: residual may be out)
+__device__ __forceinline__ float load_one(const void* p, size_t at, int fp16, int wide) {
+  if (wide) return static_cast<const float*>(p)[at];
+  return fp16 ? __half2float(static_cast<const __half*>(p)[at])
+              : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
+}
+__device__ __forceinline__ void store_one(void* p, size_t at, int fp16, int wide, float v) {
+  if (wide)
+    static_cast<float*>(p)[at] = v;
+  else
+    store16(p, at, v, fp16);
+}
+__device__ __forceinline__ void load_pair(const void* p, int fp16, int wide, float (&v)[2]) {
   if (wide) {
-    if constexpr (W == 2) {
-      const float2 f = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + at);
-      v[0] = f.x;
-      v[1] = f.y;
-    } else {
-      v[0] = static_cast<const float*>(p)[at];
-    }
-  } else if constexpr (W == 2) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + at);
+    const float2 f = *static_cast<const float2*>(p);
+    v[0] = f.x;
+    v[1] = f.y;
+  } else {
+    const uint32_t w = *static_cast<const uint32_t*>(p);
     if (fp16)
       Word<__half>::get(w, v);
     else
       Word<__nv_bfloat16>::get(w, v);
-  } else {
-    v[0] = fp16 ? __half2float(static_cast<const __half*>(p)[at])
-                : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
-  }
-}
-template <int W>
-__device__ __forceinline__ void store_few(void* p, size_t at, int fp16, int wide, const float (&v)[W]) {
-  if (wide) {
-    if constexpr (W == 2)
-      *reinterpret_cast<float2*>(static_cast<float*>(p) + at) = make_float2(v[0], v[1]);
-    else
-      static_cast<float*>(p)[at] = v[0];
-  } else if constexpr (W == 2) {
-    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + at) =
-        fp16 ? Word<__half>::put(v) : Word<__nv_bfloat16>::put(v);
-  } else {
-    store16(p, at, v[0], fp16);
   }
 }
 
-// R rows, `step` apart from row `row`, of W adjacent columns (where Q is no multiple of 8); the loads
-// and stores of the rows are independent.
-template <int R, int W>
-__device__ __forceinline__ void finish_columns(const Epilogue& e, int row, int step, int col, float (&z)[R][W]) {
+// One column of R rows; the loads and stores of the rows are independent.
+template <int R>
+__device__ __forceinline__ void finish_column(const Epilogue& e, int row, int col, float (&z)[R]) {
   size_t at[R];
   bool valid[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    at[r] = (size_t)(row + r * step) * e.Q + col;
-    valid[r] = row + r * step < e.P;
+    at[r] = (size_t)(row + r) * e.Q + col;
+    valid[r] = row + r < e.P;
   }
   if (e.bias) {
-    float b[W];
-    load_few<W>(e.bias, col, e.fp16, 0, b);
+    const float b = load_one(e.bias, col, e.fp16, 0);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int i = 0; i < W; ++i) z[r][i] += b[i];
+    for (int r = 0; r < R; ++r) z[r] += b;
   }
-  float res[R][W];
+  float res[R];
   if (e.residual) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (valid[r]) load_few<W>(e.residual, at[r], e.fp16, e.out32, res[r]);
+      if (valid[r]) res[r] = load_one(e.residual, at[r], e.fp16, e.out32);
   }
   if (e.preact) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (valid[r]) store_few<W>(e.preact, at[r], e.fp16, 0, z[r]);
+      if (valid[r]) store16(e.preact, at[r], z[r], e.fp16);
   }
   if (e.act != MOE_LINEAR_NONE) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int i = 0; i < W; ++i) z[r][i] = act_fwd(z[r][i], e.act);
+    for (int r = 0; r < R; ++r) z[r] = act_fwd(z[r], e.act);
   }
 #pragma unroll
   for (int r = 0; r < R; ++r)
-    if (valid[r]) {
-      if (e.residual) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) z[r][i] += res[r][i];
-      }
-      store_few<W>(e.out, at[r], e.fp16, e.out32, z[r]);
-    }
+    if (valid[r]) store_one(e.out, at[r], e.fp16, e.out32, e.residual ? z[r] + res[r] : z[r]);
 }
 __device__ __forceinline__ void finish1(const Epilogue& e, int row, int col, float z) {
-  float v[1][1] = {{z}};
-  finish_columns<1, 1>(e, row, 1, col, v);
+  float v[1] = {z};
+  finish_column(e, row, col, v);
+}
+
+// 32 columns x 32 rows of fp32 sums in a warp's shared buffer; 16-byte pieces are placed by
+// their index xor the row's low bits, which keeps both the row-per-lane writes and the
+// 4-lanes-per-row reads free of bank conflicts.
+__device__ __forceinline__ float* buf_at(float* buf, int row, int piece) { return buf + row * 32 + ((piece ^ (row & 7)) << 2); }
+
+template <int act, int R>
+__device__ __forceinline__ void act_pairs(float (&z)[R][2]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    z[r][0] = act_fwd(z[r][0], act);
+    z[r][1] = act_fwd(z[r][1], act);
+  }
+}
+// The epilogue of one chunk in the warp's buffer where Q is no multiple of 8, so that a row starts
+// anywhere: half a warp takes a row, a lane two columns of every other row that lie in one aligned pair
+// of memory.  With an odd Q the pairs of the odd rows (all of the upper half: row0 and col0 are multiples
+// of 32) start at odd columns, and 32 elements in all stay single, one a lane.  The loads and stores of 8
+// rows are independent, and loaded values are converted after the last load (in the branch of each load
+// they cost its latency 8 times: 49 us instead of 32).  [2154, 4070] over 568, the sums alone / with a
+// residual / with everything: 26.7 / 31.8 / 44.7 us, by vectors (4072 columns) 18.2 / 23.7 / 33.9.
+__device__ __forceinline__ void finish_narrow(const Epilogue& e, float* buf, int row0, int col0, int lane) {
+  constexpr int R = 8;
+  const int half = lane >> 4, i = lane & 15, n = min(32, e.Q - col0);
+  const bool odd = e.Q & 1;
+  const int c = 2 * i - (odd && half);  // the lane's columns: c and c + 1
+  const bool pair = c >= 0 && c + 1 < n;
+  const size_t base = (size_t)(row0 + half) * e.Q + col0 + c;
+  auto valid = [&](int h, int r) { return pair && row0 + half + h + 2 * r < e.P; };
+  if (odd) {
+    // first and last column of the odd rows, or (n odd) the last of the even and the first of the odd ones
+    const int row = n & 1 ? lane : 2 * i + 1, col = (n & 1 ? lane & 1 : lane < 16) ? 0 : n - 1;
+    finish1(e, row0 + row, col0 + col, buf_at(buf, row, col >> 2)[col & 3]);
+  }
+  float ba = 0.f, bb = 0.f;
+  if (e.bias && pair) {
+    ba = load_one(e.bias, col0 + c, e.fp16, 0);
+    bb = load_one(e.bias, col0 + c + 1, e.fp16, 0);
+  }
+  auto put16 = [&](void* p, int h, const float (&z)[R][2]) {
+    uint16_t* q = static_cast<uint16_t*>(p) + base;
+    uint32_t w[R];
+    if (e.fp16) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) w[r] = Word<__half>::put(z[r]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r) w[r] = Word<__nv_bfloat16>::put(z[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (valid(h, r)) *reinterpret_cast<uint32_t*>(q + (h + 2 * r) * e.Q) = w[r];
+  };
+#pragma unroll 1
+  for (int h = 0; h < 32 && row0 + h < e.P; h += 2 * R) {
+    float2 res[R] = {};  // (16-bit types: as loaded, in x; what becomes of it waits for none of the loads)
+    if (e.residual) {
+      if (e.out32) {
+        const float* q = static_cast<const float*>(e.residual) + base;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (valid(h, r)) res[r] = *reinterpret_cast<const float2*>(q + (h + 2 * r) * e.Q);
+      } else {
+        const uint16_t* q = static_cast<const uint16_t*>(e.residual) + base;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (valid(h, r)) res[r].x = *reinterpret_cast<const float*>(q + (h + 2 * r) * e.Q);
+      }
+    }
+    float z[R][2];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int row = h + 2 * r + half, k = max(c, 0);
+      z[r][0] = buf_at(buf, row, k >> 2)[k & 3] + ba;
+      z[r][1] = buf_at(buf, row, (c + 1) >> 2)[(c + 1) & 3] + bb;
+    }
+    if (e.preact) put16(e.preact, h, z);
+    if (e.act == MOE_LINEAR_SILU)
+      act_pairs<MOE_LINEAR_SILU>(z);
+    else if (e.act == MOE_LINEAR_GELU)
+      act_pairs<MOE_LINEAR_GELU>(z);
+    else if (e.act == MOE_LINEAR_GELU_TANH)
+      act_pairs<MOE_LINEAR_GELU_TANH>(z);
+    if (e.residual) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float v[2] = {res[r].x, res[r].y};
+        if (!e.out32) {
+          if (e.fp16)
+            Word<__half>::get(__float_as_uint(res[r].x), v);
+          else
+            Word<__nv_bfloat16>::get(__float_as_uint(res[r].x), v);
+        }
+        z[r][0] += v[0];
+        z[r][1] += v[1];
+      }
+    }
+    if (e.out32) {
+      float* q = static_cast<float*>(e.out) + base;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (valid(h, r)) *reinterpret_cast<float2*>(q + (h + 2 * r) * e.Q) = make_float2(z[r][0], z[r][1]);
+    } else {
+      put16(e.out, h, z);
+    }
+  }
 }
 
 // 8 consecutive columns (Q % 8 == 0) of R rows, R independent chains of loads and stores;
@@ -418,11 +502,6 @@ __device__ __forceinline__ void tile_of(const Gemm& p, int u, int& m, int& n) {
   n = in / rows;
 }
 
-// 32 columns x 32 rows of fp32 sums in a warp's shared buffer; 16-byte pieces are placed by
-// their index xor the row's low bits, which keeps both the row-per-lane writes and the
-// 4-lanes-per-row reads free of bank conflicts.
-__device__ __forceinline__ float* buf_at(float* buf, int row, int piece) { return buf + row * 32 + ((piece ^ (row & 7)) << 2); }
-
 // The epilogue of one 32-column chunk whose sums lane r holds for row row0 + r.  kPlain: nothing but
 // the plain form can come (the gradients).
 template <bool kPlain>
@@ -479,30 +558,7 @@ __device__ __forceinline__ void finish_chunk(const Epilogue& e, float* buf, cons
         }
       }
     } else {
-      // rows start anywhere: a lane takes two columns of every other row, or one column when Q is odd
-      if (e.Q % 2 == 0) {
-        const int c = (lane & 15) * 2, odd = lane >> 4;
-        if (col0 + c < e.Q)
-#pragma unroll 1
-          for (int h = 0; h < 32 && row0 + h < e.P; h += 8) {
-            float z[4][2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 f = *reinterpret_cast<const float2*>(buf_at(buf, h + 2 * i + odd, c >> 2) + (c & 3));
-              z[i][0] = f.x;
-              z[i][1] = f.y;
-            }
-            finish_columns<4, 2>(e, row0 + h + odd, 2, col0 + c, z);
-          }
-      } else if (col0 + lane < e.Q) {
-#pragma unroll 1
-        for (int h = 0; h < 32 && row0 + h < e.P; h += 8) {
-          float z[8][1];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[i][0] = buf_at(buf, h + i, lane >> 2)[lane & 3];
-          finish_columns<8, 1>(e, row0 + h, 1, col0 + lane, z);
-        }
-      }
+      finish_narrow(e, buf, row0, col0, lane);
     }
     __syncwarp();
   }
@@ -533,18 +589,18 @@ __device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int un
 #pragma unroll
         for (int s = 0; s < S; ++s)
           v[j][s] = ld_cluster1(map_to_rank(base + (uint32_t)((min(r + j, r1 - 1) * (p.BN + 4) + c) * 4), s * CG + half));
-      float z[4][1] = {};
+      float z[4] = {};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int s = 0; s < S; ++s) z[j][0] += v[j][s];
+        for (int s = 0; s < S; ++s) z[j] += v[j][s];
       // (rows past r1 are another CTA's)
       if (c < cols) {
         if (r + 4 <= r1)
-          finish_columns<4, 1>(p.e, row0 + r, 1, tn * p.BN + c, z);
+          finish_column(p.e, row0 + r, tn * p.BN + c, z);
         else
           for (int j = 0; j < 4; ++j)
-            if (r + j < r1) finish1(p.e, row0 + r + j, tn * p.BN + c, j == 0 ? z[0][0] : j == 1 ? z[1][0] : z[2][0]);
+            if (r + j < r1) finish1(p.e, row0 + r + j, tn * p.BN + c, j == 0 ? z[0] : j == 1 ? z[1] : z[2]);
       }
     }
     return;
@@ -916,16 +972,26 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------ dz and its column sums
 // dz = dout * act'(preact), in the operand type (row stride ld), and one row of column sums per
-// chunk of rows.  A thread takes 8 columns (or 1 where N % 8) of every 8th row of its chunk.
+// chunk of rows.  A thread takes V columns (8, or 2 or 1 where N is no multiple of 8) of every 8th row of its
+// chunk.
 constexpr int kDzRows = 64;       // rows of a chunk, fewer where that leaves SMs idle, more where it
 constexpr int kDzChunks = 1024;   // would give over this many chunks
 
-template <class TO, class T, bool kVec, int act>
+template <int V, class T>
+__device__ __forceinline__ void load_cols(const T* p, float (&v)[V]) {
+  if constexpr (V == 8)
+    load8(p, v);
+  else if constexpr (V == 2)
+    load_pair(p, std::is_same<T, __half>::value, std::is_same<T, float>::value, v);
+  else
+    v[0] = load1(p);
+}
+
+template <class TO, class T, int V, int act>
 __global__ void __launch_bounds__(256, 4)
     linear_dz_kernel(const TO* __restrict__ dout, const T* __restrict__ preact, int M, int N, T* __restrict__ dz,
                      int ld, int rows, float* __restrict__ partial) {
-  constexpr int V = kVec ? 8 : 1;
-  constexpr int R = 2;  // rows whose loads are in flight together
+  constexpr int R = V == 2 ? 4 : 2;  // rows whose loads are in flight together
   depend_launch();
   __shared__ float sums[8][32 * V];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
@@ -940,16 +1006,8 @@ __global__ void __launch_bounds__(256, 4)
         const int r = rb + 8 * j;
         if (r >= r1) break;
         const size_t at = (size_t)r * N + col;
-        if constexpr (kVec)
-          load8(dout + at, d[j]);
-        else
-          d[j][0] = load1(dout + at);
-        if (act != MOE_LINEAR_NONE) {
-          if constexpr (kVec)
-            load8(preact + at, z[j]);
-          else
-            z[j][0] = load1(preact + at);
-        }
+        load_cols(dout + at, d[j]);
+        if (act != MOE_LINEAR_NONE) load_cols(preact + at, z[j]);
       }
 #pragma unroll
       for (int j = 0; j < R; ++j) {
@@ -960,10 +1018,13 @@ __global__ void __launch_bounds__(256, 4)
           for (int i = 0; i < V; ++i) d[j][i] *= act_grad(z[j][i], act);
         }
         if (dz) {
-          if constexpr (kVec)
-            store8(dz + (size_t)r * ld + col, d[j]);
+          T* p = dz + (size_t)r * ld + col;
+          if constexpr (V == 8)
+            store8(p, d[j]);
+          else if constexpr (V == 2)
+            *reinterpret_cast<uint32_t*>(p) = Word<T>::put(d[j]);
           else
-            store1(dz + (size_t)r * ld + col, d[j][0]);
+            store1(p, d[j][0]);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) sum[i] += d[j][i];
@@ -1103,12 +1164,14 @@ struct Plan {
 
 // The cheapest cut by a model fitted to measurements (ns, at 1.9 GHz): a K block takes 200 (the
 // turn of the copy and MMA loops) or 1.06 a column (the MMA rate) or 6.5 a KB copied (all SMs
-// reading L2); a tile's epilogue 1200 (1800 with pairs) + 12 a column, overlapped with the next tile's K loop; joining
+// reading L2; 16 where the operand's rows do not start on 128 bytes: every row of a box then lies in
+// two lines); a tile's epilogue 1200 (1800 with pairs) + 12 a column, overlapped with the next tile's K loop; joining
 // split tiles 1500 and its bytes at 10 a ns.  Measured either side of it: [64, 256] over K 7168 in
 // 64-column tiles, 1 / 2 / 4 / 8 splits 26 / 16 / 11 / 8.9 us; [4096, 256] over 7168, (128 columns,
 // 2 splits) 20 us, (256, 4) 23; [8192, 4096] over 4096, one CTA or a pair per MMA 174 / 152 us;
-// [4096, 7168] over 256, 26 / 29.
-Plan plan_gemm(long long P, long long Q, int KB) {
+// [4096, 7168] over 256, 26 / 29; and by the rows' pitch: [2154, 4064] over 568, (one CTA an MMA, 128
+// columns) / (256) / (pairs, 256) 27.9 / 20.7 / 18.0, over 576 15 to 17; [4683, 2456] over 720 31 / 28 / 23.
+Plan plan_gemm(long long P, long long Q, int KB, double a_kb, double b_kb) {
   Plan best{1, 64, 1};
   double best_cost = 1e30;
   const double rows = P < BM ? (double)P : (double)BM;
@@ -1120,7 +1183,7 @@ Plan plan_gemm(long long P, long long Q, int KB) {
         const int slots = cluster_slots(s * cg);
         if (s > 1 && (KB < 4 * s || tiles > slots)) break;
         const double busy = (double)(tiles < slots ? tiles : slots) * s * cg / num_sms();
-        const double copy = (rows + bn / cg) * 0.125 * 6.5 * (busy > 0.5 ? busy : 0.5);
+        const double copy = (rows * a_kb + bn / cg * b_kb) * 0.125 * (busy > 0.5 ? busy : 0.5);
         double kb = 1.06 * bn > copy ? 1.06 * bn : copy;
         if (kb < 200) kb = 200;
         const double loop = cdiv(KB, s) * kb, epi = 600 * (1 + cg) + 12.0 * bn;
@@ -1153,7 +1216,8 @@ moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue&
   g.e = e;
   g.KB = cdiv(C, BK);
   const bool promote = e.out32 && g.KB > kPromoteKB;  // (the gradients' outputs have 16 bits)
-  const Plan p = plan_gemm(e.P, e.Q, g.KB);
+  auto kb_ns = [](const Operand& o) { return o.ld % 64 || reinterpret_cast<uintptr_t>(o.base) % 128 ? 16.0 : 6.5; };
+  const Plan p = plan_gemm(e.P, e.Q, g.KB, kb_ns(A), kb_ns(B));
   g.tiles_m = cdiv(e.P, BM * p.cg);
   g.tiles_n = cdiv(e.Q, p.bn);
   g.raster = cdiv(g.tiles_m, cdiv(g.tiles_m, kRaster));
@@ -1213,11 +1277,13 @@ struct BwdLayout {
   int rows, chunks;  // of linear_dz_kernel
   size_t partial, total;
 };
+int dz_cols(int N) { return N % 8 == 0 ? 8 : N % 2 == 0 ? 2 : 1; }  // columns a thread of linear_dz_kernel
 BwdLayout bwd_layout(int M, int N) {
   BwdLayout l;
-  l.ld = ((long long)N + 7) / 8 * 8;
+  const int pitch = N > 256 ? 64 : 8;  // (rows on 128 bytes copy at more than twice the rate of others; TMA
+  l.ld = ((long long)N + pitch - 1) / pitch * pitch;  // wants 16)
   l.rows = kDzRows;
-  const int blocks = cdiv(N, N % 8 == 0 ? 256 : 32);
+  const int blocks = cdiv(N, 32 * dz_cols(N));
   while (l.rows > 8 && (long long)blocks * cdiv(M, l.rows) < 4LL * num_sms()) l.rows /= 2;
   while (cdiv(M, l.rows) > kDzChunks) l.rows *= 2;
   l.chunks = cdiv(M, l.rows);
@@ -1228,12 +1294,18 @@ BwdLayout bwd_layout(int M, int N) {
 
 template <class TO, class T, int act>
 void launch_dz_act(const TO* d, const T* z, int M, int N, T* dz, const BwdLayout& l, float* partial, cudaStream_t s) {
-  if (N % 8 == 0)
-    linear_dz_kernel<TO, T, true, act>
-        <<<dim3(cdiv(N, 256), l.chunks), 256, 0, s>>>(d, z, M, N, dz, (int)l.ld, l.rows, partial);
+  auto go = [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    linear_dz_kernel<TO, T, V, act>
+        <<<dim3(cdiv(N, 32 * V), l.chunks), 256, 0, s>>>(d, z, M, N, dz, (int)l.ld, l.rows, partial);
+  };
+  const int cols = dz_cols(N);
+  if (cols == 8)
+    go(std::integral_constant<int, 8>());
+  else if (cols == 2)
+    go(std::integral_constant<int, 2>());
   else
-    linear_dz_kernel<TO, T, false, act>
-        <<<dim3(cdiv(N, 32), l.chunks), 256, 0, s>>>(d, z, M, N, dz, (int)l.ld, l.rows, partial);
+    go(std::integral_constant<int, 1>());
 }
 template <class TO, class T>
 void launch_dz(const void* dout, const void* preact, int M, int N, int act, void* dz, const BwdLayout& l, float* partial,

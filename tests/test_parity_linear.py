@@ -279,3 +279,12 @@ def test_linear_cuts(cuda_dev, M, N, K):
     """Sizes whose cuts differ: split K in clusters of 2, 4 and 8, pairs, a split last wave."""
     _forward(cuda_dev, M, N, K, BF, "none", True, False, False, F32)
     _backward(cuda_dev, M, N, K)
+
+
+@pytest.mark.parametrize("N", [9, 31, 33, 34, 35, 62, 63, 65, 97, 126, 130, 257, 290, 319])
+def test_linear_widths_beside_the_vectors(cuda_dev, N):
+    """Rows that start anywhere: every parity of row and width, tiles whose last columns are few, in place."""
+    for M, out_dtype in ((37, None), (133, F32), (300, None)):
+        _forward(cuda_dev, M, N, 136, BF, "gelu", True, True, True, out_dtype, inplace=True)
+        _forward(cuda_dev, M, N, 136, HF, "silu", False, False, True, out_dtype)
+        _forward(cuda_dev, M, N, 136, BF, "none", False, True, False, out_dtype)
