@@ -398,6 +398,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same without its memory order: a release waits for the thread's global stores too (over a
+// microsecond).
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t smem_addr, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr), "r"(rank));
@@ -565,7 +570,8 @@ __device__ __forceinline__ void finish_chunk(const Epilogue& e, float* buf, cons
 }
 
 // The share of CTA (pair) `split` of a split tile: its elements summed over the S partial tiles,
-// in rank order, through the epilogue.  Called by the epilogue warps.
+// in rank order, through the epilogue.  Called by the epilogue warps.  (Every value that is loaded from
+// another CTA is used, so that it has arrived when this one's threads come to the last barrier.)
 template <int S, int CG, bool kPlain>
 __device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int unit, int split, int half) {
   int tm, tn;
@@ -583,12 +589,14 @@ __device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int un
 #pragma unroll 1
     for (int i = warp; i < n; i += kEpiWarps) {
       const int c = i % pieces * 32 + lane, r = r0 + i / pieces * 4;
-      float v[4][S];
+      float v[4][S] = {};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
+        if (c < cols && r + j < r1) {
 #pragma unroll
-        for (int s = 0; s < S; ++s)
-          v[j][s] = ld_cluster1(map_to_rank(base + (uint32_t)((min(r + j, r1 - 1) * (p.BN + 4) + c) * 4), s * CG + half));
+          for (int s = 0; s < S; ++s)
+            v[j][s] = ld_cluster1(map_to_rank(base + (uint32_t)(((r + j) * (p.BN + 4) + c) * 4), s * CG + half));
+        }
       float z[4] = {};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -607,11 +615,12 @@ __device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int un
   }
   constexpr int U = S >= 8 ? 1 : 8 / S;  // items whose loads are in flight together
   constexpr int kStep = kEpiWarps * 32;
-  for (int i0 = (int)((long long)items * split / S) + threadIdx.x - kFirstEpi * 32; i0 < i1; i0 += U * kStep) {
-    float4 lo[U][S], hi[U][S];
+  auto some = [&](auto count, int i0) {
+    constexpr int C = decltype(count)::value;
+    float4 lo[C][S], hi[C][S];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = min(i0 + u * kStep, i1 - 1), r = i / groups, c = (i - r * groups) * 8;
+    for (int u = 0; u < C; ++u) {
+      const int i = i0 + u * kStep, r = i / groups, c = (i - r * groups) * 8;
       const uint32_t at = base + (uint32_t)((r * (p.BN + 4) + c) * 4);
 #pragma unroll
       for (int s = 0; s < S; ++s) {
@@ -621,9 +630,8 @@ __device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int un
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < C; ++u) {
       const int i = i0 + u * kStep, r = i / groups, c = (i - r * groups) * 8;
-      if (i >= i1) break;
       float z[1][8] = {};
 #pragma unroll
       for (int s = 0; s < S; ++s) {
@@ -642,7 +650,11 @@ __device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int un
         finish_rows<1>(p.e, row, col, valid, z);
       }
     }
-  }
+  };
+  int i = (int)((long long)items * split / S) + threadIdx.x - kFirstEpi * 32;
+  if (U > 1)
+    for (; i + (U - 1) * kStep < i1; i += U * kStep) some(std::integral_constant<int, U>(), i);
+  for (; i < i1; i += kStep) some(std::integral_constant<int, 1>(), i);
 }
 
 // kAMN / kBMN: the operand is MN-major (its contraction dimension is the row of its tensor).
@@ -685,6 +697,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint16_t pair_mask = (uint16_t)(3u << leader);
 
   depend_launch();
+  if (warp == 2 && elect_one()) {
+    prefetch_tensormap(&tmA);
+    prefetch_tensormap(&tmB);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
@@ -696,8 +712,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(drain, 1);
     fence_mbar_init();
-    prefetch_tensormap(&tmA);
-    prefetch_tensormap(&tmB);
   }
   if (warp == 1) tmem_take<CG>(tmem_slot);
   tc_fence_before();
@@ -921,7 +935,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (CG > 1 || splits > 1) cluster_sync();  // no CTA leaves while another uses its memory or barriers
+  // No CTA leaves while another uses its memory or barriers.  (With splits all that is left to come after
+  // the barrier above are the loads of the partial tiles.)
+  if (splits > 1)
+    cluster_sync_relaxed();
+  else if (CG > 1)
+    cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_release<CG>(tmem);
 }
@@ -1349,13 +1368,18 @@ extern "C" moe_status_t moe_linear(const void* x, const void* w, const void* bia
                 aligned16(preact));
   const Epilogue e{bias, residual, out, preact, M, N, activation, dtype == MOE_DT_FP16, out_dtype == MOE_DT_FP32};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (M <= 4) {
+  // Few rows: dot products start 3 us sooner than the tensor cores, which win once there is work.  In a
+  // graph, rows / GEMM: [8, 256] over 1024 4.0 / 6.1 us, [8, 256] over 7168 8.1 / 8.0, [4, 1024] over
+  // 4096 5.4 / 7.0 and [8, 1024] 8.9 / 7.2, [4, 4096] over 4096 12.7 / 9.4; [1, 4096] 6.2 / 9.4.
+  if (M <= 2 || (M <= 8 && (long long)M * N * K <= 24000000)) {
     if (M == 1)
       launch_rows<1>(x, w, M, N, K, e, s);
     else if (M == 2)
       launch_rows<2>(x, w, M, N, K, e, s);
-    else
+    else if (M <= 4)
       launch_rows<4>(x, w, M, N, K, e, s);
+    else
+      launch_rows<8>(x, w, M, N, K, e, s);
     return launch_status();
   }
   return run_gemm({x, false, K}, {w, false, K}, K, e, false, s);
