@@ -1181,15 +1181,16 @@ struct Plan {
   int cg, bn, splits;
 };
 
-// The cheapest cut by a model fitted to measurements (ns, at 1.9 GHz): a K block takes 200 (the
-// turn of the copy and MMA loops) or 1.06 a column (the MMA rate) or 6.5 a KB copied (all SMs
-// reading L2; 16 where the operand's rows do not start on 128 bytes: every row of a box then lies in
-// two lines); a tile's epilogue 1200 (1800 with pairs) + 12 a column, overlapped with the next tile's K loop; joining
-// split tiles 1500 and its bytes at 10 a ns.  Measured either side of it: [64, 256] over K 7168 in
-// 64-column tiles, 1 / 2 / 4 / 8 splits 26 / 16 / 11 / 8.9 us; [4096, 256] over 7168, (128 columns,
-// 2 splits) 20 us, (256, 4) 23; [8192, 4096] over 4096, one CTA or a pair per MMA 174 / 152 us;
-// [4096, 7168] over 256, 26 / 29; and by the rows' pitch: [2154, 4064] over 568, (one CTA an MMA, 128
-// columns) / (256) / (pairs, 256) 27.9 / 20.7 / 18.0, over 576 15 to 17; [4683, 2456] over 720 31 / 28 / 23.
+// The cheapest cut by a model fitted to measurements (ns, at 1.9 GHz): a K block takes 140 (the MMAs
+// read 128 rows of A from shared memory whatever the columns) or 1.06 a column (the MMA rate) or 8 a KB
+// copied (the SM's port to L2; 16 where the operand's rows do not start on 128 bytes: every row of a
+// box then lies in two lines), 15 % less when fewer SMs copy; a tile's epilogue 1200 (1800 with pairs)
+// + 12 a column, overlapped with the next tile's K loop; joining split tiles 1500 and its bytes at 10 a
+// ns.  Measured either side of it: [64, 256] over K 7168 in 64-column tiles, 1 / 2 / 4 / 8 splits 26 /
+// 16 / 11 / 8.9 us; [4096, 256] over 7168 to fp32, (one CTA an MMA, 128 columns, 2 splits) 23.3, (one,
+// 256, 4) 25.2, (pairs, 128, 2) 21.5; [8192, 4096] over 4096, one CTA or a pair per MMA 174 / 152;
+// [512, 4096] over 4096 in 128 columns, one CTA / a pair 20.5 / 18.0; and by the rows' pitch:
+// [2154, 4064] over 568, (one, 128) / (one, 256) / (pairs, 256) 27.9 / 20.7 / 18.0, over 576 13.
 Plan plan_gemm(long long P, long long Q, int KB, double a_kb, double b_kb) {
   Plan best{1, 64, 1};
   double best_cost = 1e30;
@@ -1202,9 +1203,9 @@ Plan plan_gemm(long long P, long long Q, int KB, double a_kb, double b_kb) {
         const int slots = cluster_slots(s * cg);
         if (s > 1 && (KB < 4 * s || tiles > slots)) break;
         const double busy = (double)(tiles < slots ? tiles : slots) * s * cg / num_sms();
-        const double copy = (rows * a_kb + bn / cg * b_kb) * 0.125 * (busy > 0.5 ? busy : 0.5);
+        const double copy = (rows * a_kb + bn / cg * b_kb) * 0.125 * (busy > 0.85 ? busy : 0.85);
         double kb = 1.06 * bn > copy ? 1.06 * bn : copy;
-        if (kb < 200) kb = 200;
+        if (kb < 140) kb = 140;
         const double loop = cdiv(KB, s) * kb, epi = 600 * (1 + cg) + 12.0 * bn;
         const double waves = cdiv(tiles, slots);
         const double join = s > 1 ? 1500 + rows * bn * 4 * (s - 1) / s / 10 : 0;
@@ -1235,7 +1236,7 @@ moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue&
   g.e = e;
   g.KB = cdiv(C, BK);
   const bool promote = e.out32 && g.KB > kPromoteKB;  // (the gradients' outputs have 16 bits)
-  auto kb_ns = [](const Operand& o) { return o.ld % 64 || reinterpret_cast<uintptr_t>(o.base) % 128 ? 16.0 : 6.5; };
+  auto kb_ns = [](const Operand& o) { return o.ld % 64 || reinterpret_cast<uintptr_t>(o.base) % 128 ? 16.0 : 8.0; };
   const Plan p = plan_gemm(e.P, e.Q, g.KB, kb_ns(A), kb_ns(B));
   g.tiles_m = cdiv(e.P, BM * p.cg);
   g.tiles_n = cdiv(e.Q, p.bn);

@@ -288,3 +288,10 @@ def test_linear_widths_beside_the_vectors(cuda_dev, N):
         _forward(cuda_dev, M, N, 136, BF, "gelu", True, True, True, out_dtype, inplace=True)
         _forward(cuda_dev, M, N, 136, HF, "silu", False, False, True, out_dtype)
         _forward(cuda_dev, M, N, 136, BF, "none", False, True, False, out_dtype)
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 4100, 2056), (4, 4096, 2048), (5, 24, 512), (8, 1000, 2992), (8, 1000, 3008), (6, 33, 5000)])
+def test_linear_few_rows(cuda_dev, M, N, K):
+    """Both kernels for a few rows, either side of the choice."""
+    _forward(cuda_dev, M, N, K, BF, "silu", True, True, True, F32)
+    _forward(cuda_dev, M, N, K, HF, "none", True, False, False)
