@@ -946,30 +946,41 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ a few rows
-// out [M, N] for M <= kM: each warp takes one weight row (or 1/KS of it) and all M rows of x.
-// Bound by the weights' bytes; a lane's loads are independent, so a CTA has the whole of its
-// weight slice in flight.
+// out [kM, N]: each warp takes one weight row (or 1/ks of it) and all rows of x.
+// Bound by the weights' bytes; a lane's loads are independent (four vectors of the weights, and of
+// each the rows of x: no branch between them, so that they are in flight together), and a CTA has the
+// whole of its weight slice on its way.
 template <int kM, class T>
 __global__ void __launch_bounds__(256)
-    linear_rows_kernel(const T* __restrict__ x, const T* __restrict__ w, int M, int N, int K, int ks, const Epilogue e) {
+    linear_rows_kernel(const T* __restrict__ x, const T* __restrict__ w, int N, int K, int ks, const Epilogue e) {
   __shared__ float sums[8][kM];
+  constexpr int U = 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = 8 / ks;  // weight rows of the CTA
   const int n = blockIdx.x * per + warp / ks, part = warp % ks;
   float acc[kM] = {};
   if (n < N) {
     const T* wr = w + (size_t)n * K;
-#pragma unroll 4
-    for (int k = (part * 32 + lane) * 8; k < K; k += ks * 256) {
-      float wv[8];
-      load8(wr + k, wv);
+    const int step = ks * 256;
+    for (int k0 = part * 256; k0 < K; k0 += U * step) {
+      float wv[U][8];
 #pragma unroll
-      for (int m = 0; m < kM; ++m) {
-        if (m >= M) break;
-        float xv[8];
-        load8(x + (size_t)m * K + k, xv);
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * step + lane * 8;
+        if (k < K) load8(wr + k, wv[u]);
+      }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[m] = fmaf(wv[i], xv[i], acc[m]);
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * step + lane * 8;
+        if (k < K) {
+          float xv[kM][8];
+#pragma unroll
+          for (int m = 0; m < kM; ++m) load8(x + (size_t)m * K + k, xv[m]);
+#pragma unroll
+          for (int m = 0; m < kM; ++m)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[m] = fmaf(wv[u][i], xv[m][i], acc[m]);
+        }
       }
     }
   }
@@ -980,7 +991,7 @@ __global__ void __launch_bounds__(256)
     if (lane == 0) sums[warp][m] = acc[m];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < per * M; i += blockDim.x) {
+  for (int i = threadIdx.x; i < per * kM; i += blockDim.x) {
     const int r = i % per, m = i / per, col = blockIdx.x * per + r;
     if (col >= N) continue;
     float z = 0.f;
@@ -1280,16 +1291,16 @@ moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue&
 }
 
 template <int kM>
-void launch_rows(const void* x, const void* w, int M, int N, int K, const Epilogue& e, cudaStream_t s) {
+void launch_rows(const void* x, const void* w, int N, int K, const Epilogue& e, cudaStream_t s) {
   int ks = 1;
   while (ks < 8 && (long long)N * ks < 16LL * num_sms() && ks * 512 <= K) ks *= 2;
   const int grid = cdiv(N, 8 / ks);
   if (e.fp16)
     linear_rows_kernel<kM, __half>
-        <<<grid, 256, 0, s>>>(static_cast<const __half*>(x), static_cast<const __half*>(w), M, N, K, ks, e);
+        <<<grid, 256, 0, s>>>(static_cast<const __half*>(x), static_cast<const __half*>(w), N, K, ks, e);
   else
     linear_rows_kernel<kM, __nv_bfloat16>
-        <<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(w), M, N, K, ks, e);
+        <<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(w), N, K, ks, e);
 }
 
 struct BwdLayout {
@@ -1370,17 +1381,20 @@ extern "C" moe_status_t moe_linear(const void* x, const void* w, const void* bia
   const Epilogue e{bias, residual, out, preact, M, N, activation, dtype == MOE_DT_FP16, out_dtype == MOE_DT_FP32};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // Few rows: dot products start 3 us sooner than the tensor cores, which win once there is work.  In a
-  // graph, rows / GEMM: [8, 256] over 1024 4.0 / 6.1 us, [8, 256] over 7168 8.1 / 8.0, [4, 1024] over
-  // 4096 5.4 / 7.0 and [8, 1024] 8.9 / 7.2, [4, 4096] over 4096 12.7 / 9.4; [1, 4096] 6.2 / 9.4.
-  if (M <= 2 || (M <= 8 && (long long)M * N * K <= 24000000)) {
-    if (M == 1)
-      launch_rows<1>(x, w, M, N, K, e, s);
-    else if (M == 2)
-      launch_rows<2>(x, w, M, N, K, e, s);
-    else if (M <= 4)
-      launch_rows<4>(x, w, M, N, K, e, s);
-    else
-      launch_rows<8>(x, w, M, N, K, e, s);
+  // graph, rows / GEMM in us: [4, 256] over 7168 4.4 / 7.9, [8, 256] 6.7 / 8.0, [8, 256] over 12288 9.1 /
+  // 9.9; [4, 1024] over 4096 7.2 / 6.9, [5, 4096] over 1024 7.6 / 7.8, [3, 1024] over 7168 8.6 / 8.4;
+  // [1, 4096] over 4096 6.4 / 9.0, [2, 4096] 8.8 / 9.1, [1, 14336] 30.4 / 24.7.
+  if (M <= 8 && (long long)M * N * K <= (M <= 2 ? 34000000 : 20000000)) {
+    switch (M) {
+      case 1: launch_rows<1>(x, w, N, K, e, s); break;
+      case 2: launch_rows<2>(x, w, N, K, e, s); break;
+      case 3: launch_rows<3>(x, w, N, K, e, s); break;
+      case 4: launch_rows<4>(x, w, N, K, e, s); break;
+      case 5: launch_rows<5>(x, w, N, K, e, s); break;
+      case 6: launch_rows<6>(x, w, N, K, e, s); break;
+      case 7: launch_rows<7>(x, w, N, K, e, s); break;
+      default: launch_rows<8>(x, w, N, K, e, s); break;
+    }
     return launch_status();
   }
   return run_gemm({x, false, K}, {w, false, K}, K, e, false, s);

@@ -290,7 +290,8 @@ def test_linear_widths_beside_the_vectors(cuda_dev, N):
         _forward(cuda_dev, M, N, 136, BF, "none", False, True, False, out_dtype)
 
 
-@pytest.mark.parametrize("M,N,K", [(3, 4100, 2056), (4, 4096, 2048), (5, 24, 512), (8, 1000, 2992), (8, 1000, 3008), (6, 33, 5000)])
+@pytest.mark.parametrize("M,N,K", [(3, 4100, 2056), (4, 4096, 2048), (5, 24, 512), (8, 1000, 2496), (8, 1000, 2504), (6, 33, 5000),
+                                   (7, 129, 6448), (1, 4100, 8192), (2, 4100, 4160)])
 def test_linear_few_rows(cuda_dev, M, N, K):
     """Both kernels for a few rows, either side of the choice."""
     _forward(cuda_dev, M, N, K, BF, "silu", True, True, True, F32)
