@@ -807,7 +807,9 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
           const bool divide = softmax && !by_logit;  // (else a softmax's numerators order like its scores)
           const FF sum = divide ? sum_ff(row + base, cnt, m) : FF{1.f, 0.f};
           FF c{0.f, 0.f};
-          float x = 0.f, b = 0.f, part = 0.f;  // part: the scores without the biases
+          // (a lane without an expert, of a group with fewer usable ones than group_top, has a logit that no
+          // expert here has: it equals only another of its kind); part: the scores without the biases
+          float x = -INFINITY, b = 0.f, part = 0.f;
           if (id >= 0) {
             expert_inputs(row, a.bias, id, x, b);
             c = softmax ? exp_ff(two_sum(x, -m)) : sigmoid_ff(x);
