@@ -412,8 +412,10 @@ struct Doubt {
     const float x = key_value(kx), y = key_value(ky);
     float tol = 2.f * (tol0 + err) + 0x1p-22f * (fabsf(x) + fabsf(y));
     // without a bias the errors are relative too (the exponential's at most (2 + 1.2 88) 2^-23, the
-    // cut logits' err): sums of small scores are told apart by their own size
-    if (by_logit) tol = fminf(tol, (0x1p-15f + 8.f * cut) * (x + y) + 2.f * err * (x + y));
+    // cut logits' err): sums of small scores are told apart by their own size.  An exponential below
+    // 2^-126 counts as 0, which takes up to 2^-125 from a sum of two, and one last place of a subnormal
+    // product with 1 / den is 2^-149: within 2^-124 for two sums.
+    if (by_logit) tol = fminf(tol, (0x1p-15f + 8.f * cut) * (x + y) + 2.f * err * (x + y) + 0x1p-124f);
     return !(x - y > tol);
   }
 };

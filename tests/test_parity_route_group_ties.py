@@ -1,5 +1,5 @@
 """moe_route_grouped where the kept groups hang on what fp32 cannot tell: groups with fewer usable
-experts than group_top.  The choice is the one of
+experts than group_top, and group scores near the smallest fp32 numbers.  The choice is the one of
 fp64 arithmetic (no case below holds two scores that fp64 cannot order but for equal ones, which go
 to the lower group), so ids are compared for equality."""
 import numpy as np
@@ -52,3 +52,18 @@ def test_group_with_one_usable_expert(cuda_dev, score, with_bias, size, k):
     if with_bias:  # a zero of score and bias together, and biases that are equal
         _same_choice(cuda_dev, l, k, torch.full((4 * size,), 0.25), score=score, n_group=4, topk_group=1, group_top=2)
         _same_choice(cuda_dev, l, k, torch.full((4 * size,), -1e-3), score=score, n_group=4, topk_group=2, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("size,k", [(4, 3), (60, 20)])
+def test_group_scores_near_the_smallest_numbers(cuda_dev, score, size, k):
+    """Sums of scores about 2^-126, some terms below it: e^-86.64 is 2^-125, e^-87.34 is below 2^-126."""
+    g = torch.Generator().manual_seed(4)
+    l = torch.full((64, 4 * size), -300.0)
+    l[:, 0] = 0.0 if score == "softmax" else -60.0  # a group that is kept in any case
+    for t in range(64):
+        for grp in (1, 2, 3):
+            l[t, grp * size:grp * size + 2] = -86.6 - torch.rand(2, generator=g) * 1.2
+    l[0, size:size + 2] = torch.tensor([-86.64, -87.35])
+    l[0, 2 * size:2 * size + 2] = -87.14
+    _same_choice(cuda_dev, l, k, score=score, n_group=4, topk_group=2, group_top=2)
