@@ -33,7 +33,9 @@ constexpr int kMaxStages = 16;
 constexpr int kStageBudget = 192 * 1024;
 constexpr int kCtrlBytes = 512;
 constexpr int kSmemBytes = 1024 + kStageBudget + kCtrlBytes + kEpiWarps * 32 * 32 * 4;
-constexpr int kPromoteKB = 8;     // K blocks between two roundings of an fp32 output's sums
+constexpr int kPromoteKB = 8;     // K blocks between two roundings of an fp32 output's sums,
+constexpr int kPromoteKB16 = 64;  // and of a 16-bit output's, which is promoted
+constexpr int kPlainKB16 = 256;   // over more than this many in one sum
 // kPromote: the epilogue holds up to 128 sums a thread, so the first warpgroup hands it registers
 constexpr int kLaunchRegs = 168, kLowRegs = 40, kHighRegs = 232;
 static_assert(128 * kLowRegs + 256 * kHighRegs == kThreads * kLaunchRegs, "register split must balance");
@@ -342,6 +344,7 @@ struct Gemm {
   int KB;               // stages of K
   int splits;           // CTAs (CTA pairs) of a cluster that share a tile's K blocks
   int BN;               // tile columns
+  int chunk;            // kPromote: stages added up in the tensor memory
   int stages;
   int a_rows;           // rows of the A box (K-major A): with fewer than 128 a stage is smaller and more of
                         // them fit; the MMA reads what lies behind for the other rows, whose
@@ -660,10 +663,12 @@ __device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int un
 // kAMN / kBMN: the operand is MN-major (its contraction dimension is the row of its tensor).
 // CG: CTAs that share an MMA.  2: a tile has 256 rows, each CTA of the pair copies its 128 rows
 //   of A and half of the B rows and holds its rows' accumulators; the even CTA issues the MMAs.
-// kPromote: fp32 outputs.  The tensor core adds to its fp32 accumulator by truncation, which
-//   over K = 7168 left outputs 8e-6 off (2-norm); so every kPromoteKB K blocks the accumulator
-//   is added, with rounding, to fp32 sums in the epilogue's registers, and the next block starts
-//   from zero in the other accumulator.
+// kPromote: the tensor core adds to its fp32 accumulator by truncation, which over K = 7168 left
+//   outputs 8e-6 off (2-norm), and sums of one sign 2^-24.5 a step of 16 elements (2.2e-3 at a million, the
+//   rounding of fp16 output is 4.9e-4); so every `chunk` stages the accumulator is added, with rounding,
+//   to fp32 sums in the epilogue's registers, and the next block starts from zero in the other
+//   accumulator.  fp32 outputs: every 512 elements; 16-bit ones: over more than 16384 in one sum (up to
+//   there 2^-14 of the sum at most, an eighth of fp16's rounding), every 4096, which the K loop hides.
 // KS: K blocks of a stage, copied, awaited and multiplied together.  2 where a stage stays at most
 //   64 KB: fewer turns of the two loops, which bound narrow tiles ([16, 4096] over K 4096 in
 //   64-column tiles 16.5 -> 12.6 us; wider stages lose at 256 columns, 129 -> 150 us for
@@ -725,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int units = p.units;
   const int first = p.unit0 + blockIdx.x / (splits * CG);
   const int step = splits > 1 ? units : gridDim.x / CG;  // a split tile is its cluster's only work
-  const int chunk = kPromote ? kPromoteKB / KS : kb1 - kb0;  // stages added up in the tensor memory
+  const int chunk = kPromote ? p.chunk : kb1 - kb0;  // stages added up in the tensor memory
 
   if (warp < kFirstEpi) {
     if (kPromote) setmaxnreg_dec<kLowRegs>();
@@ -1156,6 +1161,13 @@ cudaError_t launch_gemm(int cg, int ks, const CUtensorMap& ma, const CUtensorMap
                  : launch_gemm<kAMN, kBMN, 1, kPromote, 1>(ma, mb, g, grid, overlap, s);
 }
 
+template <bool kAMN, bool kBMN>
+cudaError_t launch_gemm(bool promote, int cg, int ks, const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g,
+                        int grid, bool overlap, cudaStream_t s) {
+  return promote ? launch_gemm<kAMN, kBMN, true>(cg, ks, ma, mb, g, grid, overlap, s)
+                 : launch_gemm<kAMN, kBMN, false>(cg, ks, ma, mb, g, grid, overlap, s);
+}
+
 // Clusters of `size` GEMM CTAs that fit the device at once (a cluster lies within one group of
 // SMs, so eight-CTA clusters leave SMs idle); asked once per device and size.
 int cluster_slots(int size) {
@@ -1246,7 +1258,6 @@ moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue&
   Gemm g;
   g.e = e;
   g.KB = cdiv(C, BK);
-  const bool promote = e.out32 && g.KB > kPromoteKB;  // (the gradients' outputs have 16 bits)
   auto kb_ns = [](const Operand& o) { return o.ld % 64 || reinterpret_cast<uintptr_t>(o.base) % 128 ? 16.0 : 8.0; };
   const Plan p = plan_gemm(e.P, e.Q, g.KB, kb_ns(A), kb_ns(B));
   g.tiles_m = cdiv(e.P, BM * p.cg);
@@ -1261,6 +1272,9 @@ moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue&
   g.KB = cdiv(blocks, ks);
   g.stages = kStageBudget / (ks * (g.a_rows + p.bn / p.cg) * 128);
   if (g.stages > kMaxStages) g.stages = kMaxStages;
+  // a tile of the launch that does not split K, or splits it least, has the longest sums
+  const bool promote = e.out32 ? blocks > kPromoteKB : cdiv(blocks, p.splits) > kPlainKB16;
+  g.chunk = (e.out32 ? kPromoteKB : kPromoteKB16) / ks;
   g.idesc = make_idesc(e.fp16 ? 0 : 1, BM * p.cg, p.bn) | (A.mn ? 1u << 15 : 0) | (B.mn ? 1u << 16 : 0);
   CUtensorMap ma, mb;
   const bool ok = (A.mn ? make_map(&ma, A.base, e.fp16, e.P, C, A.ld, BK * ks)
@@ -1275,10 +1289,9 @@ moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue&
     const long long ctas = (last - first) * splits * p.cg;
     const int most = cluster_slots(p.cg) * p.cg;
     const int grid = (int)(splits > 1 || ctas < most ? ctas : most);
-    const cudaError_t err = A.mn      ? launch_gemm<true, true, false>(p.cg, ks, ma, mb, g, grid, overlap, s)
-                            : B.mn    ? launch_gemm<false, true, false>(p.cg, ks, ma, mb, g, grid, overlap, s)
-                            : promote ? launch_gemm<false, false, true>(p.cg, ks, ma, mb, g, grid, overlap, s)
-                                      : launch_gemm<false, false, false>(p.cg, ks, ma, mb, g, grid, overlap, s);
+    const cudaError_t err = A.mn   ? launch_gemm<true, true>(promote, p.cg, ks, ma, mb, g, grid, overlap, s)
+                            : B.mn ? launch_gemm<false, true>(promote, p.cg, ks, ma, mb, g, grid, overlap, s)
+                                   : launch_gemm<false, false>(promote, p.cg, ks, ma, mb, g, grid, overlap, s);
     overlap = true;
     return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   };
