@@ -191,7 +191,7 @@ class MoELayer:
         return self.out
 
     def router_backward(self, dout: torch.Tensor, a1: torch.Tensor, residual_out: Optional[torch.Tensor] = None,
-                        stream=None):
+                        stream=None, dresidual_out: Optional[torch.Tensor] = None):
         """Gradients that train the router of a layer whose experts are held fixed: dout [T, H] bf16, the
         gradient of the last forward call's output -> (finalize gradients, router gradients), as
         moe_finalize_backward and MoERouter.backward return them.  residual_out: the sum before the RMSNorm (layers
@@ -204,7 +204,8 @@ class MoELayer:
         if residual_out is None and self.inp.rms_weight is not None:
             raise ValueError("router_backward under an RMSNorm needs residual_out, or a layer with keep_residual")
         fin = moe.moe_finalize_backward(dout, self.y, self.topk_weights, self.cfg.top_k, residual_out=residual_out,
-                                        rms_weight=self.inp.rms_weight, need_dy=False, stream=stream)
+                                        rms_weight=self.inp.rms_weight, dresidual_out=dresidual_out, need_dy=False,
+                                        stream=stream)
         return fin, self.router.backward(fin[1], a1, self.topk_ids, stream=stream)
 
     def experts(self, a1q, a1q_scale, a1, stream=None, shared_launched=False):
