@@ -670,6 +670,8 @@ def moe_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = 
 
 
 def linear_backward_workspace_size(M: int, N: int, K: int) -> int:
+    if max(M, N, K) > _INT_MAX:
+        raise ValueError("M, N and K: expected sizes up to 2^31 - 1")
     return int(lib().moe_linear_backward_workspace_size(M, N, K))
 
 
@@ -711,6 +713,8 @@ def route_config(score: str = "sigmoid", n_group: int = 1, topk_group: int = 1, 
                  renormalize: bool = True, scale: float = 1.0) -> RouteConfig:
     if score not in SCORES:
         raise ValueError(f"unknown score {score!r}")
+    if not all(-_INT_MAX <= v <= _INT_MAX for v in (n_group, topk_group, group_top)):
+        raise ValueError("n_group, topk_group and group_top: expected sizes up to 2^31 - 1")
     return RouteConfig(SCORES[score], n_group, topk_group, group_top, int(bool(renormalize)), scale)
 
 
@@ -768,6 +772,8 @@ def moe_route_grouped_backward(dweights: torch.Tensor, logits: torch.Tensor, top
 
 # ------------------------------------------------------------------ finalize, gradient
 def finalize_backward_workspace_size(T: int, H: int) -> int:
+    if max(T, H) > _INT_MAX:
+        raise ValueError("T and H: expected sizes up to 2^31 - 1")
     return int(lib().moe_finalize_backward_workspace_size(T, H))
 
 

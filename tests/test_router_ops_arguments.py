@@ -1,5 +1,4 @@
-"""Arguments that ctypes would cut to 32 bits without a word, and configurations that a cache may not keep: no
-GPU needed."""
+"""Arguments that ctypes would cut to 32 bits without a word: no GPU needed."""
 import pytest
 import torch
 
@@ -23,27 +22,3 @@ def test_workspace_sizes_refuse_what_does_not_fit(moelib):
     for T, H in ((2 ** 32 + 4, 64), (4, 2 ** 31)):
         with pytest.raises(ValueError, match="2\\^31"):
             moe.finalize_backward_workspace_size(T, H)
-
-
-def test_scale_is_read_at_each_call(moelib, monkeypatch):
-    """A scale that the caller holds in a tensor and changes is the one of the call, not of the first call."""
-    seen = []
-
-    class Lib:
-        def moe_route_grouped(self, *a):
-            seen.append(a[6]._obj.scale)
-            return 0
-
-        def moe_route_grouped_backward(self, *a):
-            seen.append(a[8]._obj.scale)
-            return 0
-
-    monkeypatch.setattr(moe, "lib", Lib)
-    monkeypatch.setattr(moe, "_launch", lambda stream: (-1, None))  # (the tensors below are the host's)
-    logits, w, ids = torch.zeros((4, 16)), torch.zeros((4, 2)), torch.zeros((4, 2), dtype=torch.int32)
-    scale = torch.tensor(1.5)
-    for want in (1.5, 3.0):
-        moe.moe_route_grouped(logits, 2, scale=scale)
-        moe.moe_route_grouped_backward(w, logits, ids, scale=scale)
-        assert seen[-2:] == [want, want]
-        scale.mul_(2)
