@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+from operator import index
 from typing import Optional, Tuple
 
 import torch
@@ -704,6 +705,7 @@ def moe_linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pr
 
 
 # ------------------------------------------------------------------ grouped route
+# (plain values alone: an object that hashes by its identity, a tensor say, may change under its entry)
 @functools.lru_cache(maxsize=1024)
 def _route_config(score, n_group, topk_group, group_top, renormalize, scale):
     return ctypes.byref(route_config(score, n_group, topk_group, group_top, renormalize, scale))
@@ -731,7 +733,7 @@ def moe_route_grouped(logits: torch.Tensor, top_k: int, bias: Optional[torch.Ten
     T, E = logits.shape
     if T > _INT_MAX or E > _INT_MAX or not 1 <= top_k <= _INT_MAX:
         raise ValueError("logits and top_k: expected sizes up to 2^31 - 1")
-    cfg = _route_config(score, n_group, topk_group, group_top, bool(renormalize), scale)
+    cfg = _route_config(score, index(n_group), index(topk_group), index(group_top), bool(renormalize), float(scale))
     if topk_ids is None:
         topk_ids = _empty((T, top_k), torch.int32, logits.device, stream)
     if topk_weights is None:
@@ -757,7 +759,7 @@ def moe_route_grouped_backward(dweights: torch.Tensor, logits: torch.Tensor, top
     (T, E), (_, top_k) = logits.shape, topk_ids.shape
     if T > _INT_MAX or E > _INT_MAX or top_k > _INT_MAX:
         raise ValueError("logits and topk_ids: expected sizes up to 2^31 - 1")
-    cfg = _route_config(score, 1, 1, 1, bool(renormalize), scale)
+    cfg = _route_config(score, 1, 1, 1, bool(renormalize), float(scale))
     if dlogits is None:
         dlogits = _empty((T, E), logits.dtype, logits.device, stream)
     dev, s = _launch(stream)
