@@ -59,18 +59,22 @@ __device__ __forceinline__ float act_fwd(float z, int act) {
   return z;
 }
 
+// The slopes are 1 or 0 to fp32 beyond |z| = 128 (silu) and 16; c, z kept to that range, goes into the factors
+// that grow, so that they stay finite where the one that vanishes is 0 (z = 1e20, or the infinity that a
+// sum became in 16 bits).  A NaN comes through the sigmoid or erff of z itself.
 __device__ __forceinline__ float act_grad(float z, int act) {
+  const float c = fminf(fmaxf(z, act == MOE_LINEAR_SILU ? -128.f : -16.f), act == MOE_LINEAR_SILU ? 128.f : 16.f);
   switch (act) {
     case MOE_LINEAR_SILU: {
       const float q = fast_sigmoid(z);
-      return q * fmaf(z, 1.0f - q, 1.0f);
+      return q * fmaf(c, 1.0f - q, 1.0f);
     }
     case MOE_LINEAR_GELU:
-      return fmaf(z * 0.39894228f, fast_exp(-0.5f * z * z), 0.5f * (1.0f + erff(z * 0.70710678f)));
+      return fmaf(c * 0.39894228f, fast_exp(-0.5f * c * c), 0.5f * (1.0f + erff(z * 0.70710678f)));
     case MOE_LINEAR_GELU_TANH: {
       const float q = fast_sigmoid(2.0f * gelu_u(z));
       // z q (1 - q) 2 u'
-      return fmaf(z * q * (1.0f - q), 1.59576912f * fmaf(0.134145f * z, z, 1.0f), q);
+      return fmaf(c * q * (1.0f - q), 1.59576912f * fmaf(0.134145f * c, c, 1.0f), q);
     }
   }
   return 1.0f;
