@@ -396,11 +396,12 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo) { return (uint64_t)kDescHi
 
 // mbar_wait that looks at the clock only after a while: reading the global timer costs several
 // hundred clocks, and in short K loops most waits miss their first test.  For one thread.
+template <bool kBail = true>
 __device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
   for (int i = 0; i < 64; ++i)
     if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity);
+  return mbar_wait(bar, parity, kBail);
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
@@ -820,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_wait(&full[i], i < st ? ph : ph ^ 1, false, 100000000ull);
         }
         __syncwarp();
-        if (__any_sync(0xffffffffu, failed)) break;
+        if ((failed = __any_sync(0xffffffffu, failed))) break;
         advance(kb1 - kb0);
       }
     } else if (warp == 1 && half == 0) {
@@ -877,6 +878,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     if (splits > 1) cluster_sync();  // (the partial tiles are in shared memory)
+    // Every stage comes back before this CTA leaves: the commits of its MMAs arrive on the barriers here, with a
+    // pair on those of both CTAs, and the accumulator's barrier, which the epilogue awaited, says nothing about
+    // the arrivals of earlier commits.  (It also ends the MMAs that an epilogue which gave up did not await.)
+    if (warp == 0 && elect_one() && !failed)
+      for (int i = 0; i < stages && lane_wait<false>(&empty[stage], phase ^ 1); ++i)
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1;
+        }
   } else {
     // ------------------------------------------------------------ epilogue
     if (kPromote) setmaxnreg_inc<kHighRegs>();
