@@ -1171,6 +1171,19 @@ int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
 template <bool kAMN, bool kBMN, int CG, bool kPromote, int KS>
 cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g, int grid, bool overlap, cudaStream_t s) {
   auto kern = linear_gemm_kernel<kAMN, kBMN, CG, kPromote, KS>;
+  if (kPromote) {
+    // The epilogue's warps take more registers than a thread is launched with (setmaxnreg), from those that the
+    // first warpgroup gives back: a build with fewer than kLaunchRegs would wait for them without an end, so
+    // it never launches.
+    static std::atomic<bool> checked;
+    if (!checked.load(std::memory_order_relaxed)) {
+      cudaFuncAttributes fa;
+      const cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+      if (e != cudaSuccess) return e;
+      if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+      checked.store(true, std::memory_order_relaxed);
+    }
+  }
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
