@@ -68,8 +68,10 @@ __global__ void __launch_bounds__(kMaxConsumers + 32, 1)
       int slot = 0;
       uint32_t phase = 0;
       bool ok = true;
+      // A consumer whose wait gave up hands slots back whose copies may still be on their way: none is filled,
+      // and its barrier armed, again before the copy has landed (else it has long landed by then).
       auto push = [&](const __nv_bfloat16* row) {
-        if (!ok || !(ok = mbar_wait(&empty[slot], phase ^ 1))) return;
+        if (!ok || !(ok = mbar_wait(&empty[slot], phase ^ 1) && mbar_wait(&full[slot], phase ^ 1, false))) return;
         mbar_arrive_expect_tx(&full[slot], row_bytes);
         bulk_load(smem + (size_t)slot * row_bytes, row, row_bytes, &full[slot]);
         if (++slot == a.slots) {
@@ -84,8 +86,10 @@ __global__ void __launch_bounds__(kMaxConsumers + 32, 1)
         if (a.dw)
           for (int j = 0; j < a.k; ++j) push(a.y + ((size_t)t * a.k + j) * a.H);
       }
-      if (!ok)  // wait (bounded) for the copies still in flight before the shared memory goes
-        for (int i = 0; i < a.slots; ++i) mbar_wait(&full[i], i < slot ? phase : phase ^ 1, false, 100000000ull);
+      // wait (bounded) for the copies still in flight before the shared memory goes: consumers that gave up
+      // have not
+      for (int i = 0; i < a.slots; ++i)
+        mbar_wait(&full[i], i < slot ? phase : phase ^ 1, false, ok ? kWaitLimitNs : 100000000ull);
     }
   } else {
     // ------------------------------------------------------------ consumers
