@@ -1294,9 +1294,9 @@ Plan plan_gemm(long long P, long long Q, int KB, double a_kb, double b_kb) {
 }
 
 // Splits of the last, partly filled wave of tiles: `rem` tiles that would leave the other slots idle
-// for a whole K loop take a launch of their own, several CTAs (pairs) to a tile, when that saves
-// more than its launch and join cost (about 6 us; the dense dx of 2050 x 5120 over 8192, 152
-// tiles and 28 more on 76 pairs, 122 -> 117 us).
+// for a whole K loop take a launch of their own, several CTAs (pairs) to a tile, when at the MMA rate
+// that saves 8 us: its launch and join cost about 6 of them.  (The dense dx of
+// 2050 x 5120 over 8192, 152 tiles and 28 more on 76 pairs, 122 -> 117 us.)
 int tail_splits(const Plan& p, long long rem, int KB) {
   int s = 1;
   while (2 * s * p.cg <= 8 && rem <= cluster_slots(2 * s * p.cg) && KB >= 16 * s) s *= 2;
@@ -1375,8 +1375,11 @@ struct BwdLayout {
 int dz_cols(int N) { return N % 8 == 0 ? 8 : N % 2 == 0 ? 2 : 1; }  // columns a thread of linear_dz_kernel
 BwdLayout bwd_layout(int M, int N) {
   BwdLayout l;
-  const int pitch = N > 256 ? 64 : 8;  // (rows on 128 bytes copy at more than twice the rate of others; TMA
-  l.ld = ((long long)N + pitch - 1) / pitch * pitch;  // wants 16)
+  // Rows of dz on 128 bytes copy at more than twice the rate of others (TMA wants 16), but narrow ones grow the
+  // workspace by a factor for little: [4096, N] to 7168 in a graph, us at 16 / 128 bytes: N 16 36.8 / 36.1,
+  // 24 41.2 / 39.0, 56 47.8 / 38.8, 72 53.9 / 47.7, 200 54.2 / 47.8; [16384, 8] to 2048 75.7 / 81.5.
+  const int pitch = N > 32 ? 64 : 8;
+  l.ld = ((long long)N + pitch - 1) / pitch * pitch;
   l.rows = kDzRows;
   const int blocks = cdiv(N, 32 * dz_cols(N));
   while (l.rows > 8 && (long long)blocks * cdiv(M, l.rows) < 4LL * num_sms()) l.rows /= 2;
