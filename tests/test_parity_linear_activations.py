@@ -43,3 +43,18 @@ def test_gelu_keeps_its_digits_below_zero(cuda_dev, M, dtype):
     got = moe.moe_linear(x.to(cuda_dev), w.to(cuda_dev), activation="gelu", out_dtype=F32,
                          residual=torch.zeros((M, N), device=cuda_dev)).cpu().double()
     assert ((got - ref[:N]).abs() <= ((z[:N] ** 2 + 1) * 2.0 ** -23 + 2.0 ** -20) * ref[:N].abs()).all()
+
+
+def test_gelu_slope_keeps_its_digits_below_zero(cuda_dev):
+    """The slope is the part below z plus z times the density, of opposite signs there: together at most 1.6 of the
+    slope for z <= -2, each within (z^2 + 8) 2^-23; then half a bf16 step."""
+    z = torch.arange(-8.0, -2.0, 1 / 32).to(BF).double()
+    N = z.numel()
+    pre = z.to(BF).repeat(3, 1)
+    dx, _, _ = moe.moe_linear_backward(torch.ones((3, N), dtype=BF, device=cuda_dev),
+                                       torch.zeros((3, N), dtype=BF, device=cuda_dev),
+                                       torch.eye(N, dtype=BF, device=cuda_dev), pre.to(cuda_dev), "gelu", need_dw=False)
+    ref = rr.act_grad(z, "gelu")
+    assert moe.moe_device_status() == moe.MOE_OK
+    tol = (2.0 ** -8 + 1.6 * (z * z + 8) * 2.0 ** -23) * ref.abs()
+    assert ((dx.cpu().double() - ref).abs() <= tol).all()

@@ -100,3 +100,33 @@ def test_host_threads_at_once(moelib):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+def test_first_promoted_products_under_capture(moelib):
+    """The first product that promotes its sums may be a captured one."""
+    import os
+    import subprocess
+    import sys
+    code = (
+        "import torch\n"
+        "from mixture_experts_layer_tokens_gb300 import moe\n"
+        "x, w = torch.randn((300, 4096), device='cuda').bfloat16(), torch.randn((264, 4096), device='cuda').bfloat16()\n"
+        "a, b = torch.rand((300000, 64), device='cuda').bfloat16(), torch.rand((300000, 72), device='cuda').bfloat16()\n"
+        "o, dw, v = torch.empty((300, 264), device='cuda'), torch.empty_like(b[:64]), torch.zeros_like(b[:64])\n"
+        "ws = torch.empty(1 << 26, device='cuda', dtype=torch.uint8)\n"
+        "def step():\n"
+        "    moe.moe_linear(x, w, out=o)\n"
+        "    moe.moe_linear_backward(a, b, v, dw=dw, ws=ws, need_dx=False)\n"
+        "torch.cuda.synchronize()\n"
+        "g = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(g):\n"
+        "    step()\n"
+        "g.replay(); torch.cuda.synchronize()\n"
+        "got = [o.clone(), dw.clone()]\n"
+        "step(); torch.cuda.synchronize()\n"
+        "assert torch.equal(got[0], o) and torch.equal(got[1], dw) and moe.moe_device_status() == 0\n"
+        "assert (o.double() - x.double() @ w.double().T).norm() <= 2e-6 * o.double().norm()\n"
+        "print('same')\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
