@@ -452,7 +452,13 @@ moe_status_t moe_finalize(void *output, const void *fused_expert_output, const f
  * not allowed.  activation: a moe_linear_activation_t.  0 <= M <= 2^30 (0: nothing is done),
  * 1 <= N <= 2^21, 8 <= K <= 2^30 and K % 8 == 0 (an N that is a multiple of 8 is stored by
  * 16-byte vectors); a product of over 2^27 tiles of 128 x 64 may be MOE_ERR_UNSUPPORTED.  Every pointer
- * 16-byte aligned.  A row of x that holds a NaN or an infinity affects that row of out alone.
+ * 16-byte aligned.  A K that is no multiple of 64 (rows that do not start on 128 bytes) is
+ * copied at about half the rate, which large products feel: a caller who can pad K should.
+ * A row of x that holds a NaN or an infinity affects that row of out alone.  The tensor core's
+ * own fp32 sums truncate; they are added with rounding to fp32 sums every 512 elements (fp32
+ * outputs), 8192 (fp16 outputs and gradients) or 16384 (bf16), so that terms of one sign lose at
+ * most about 5e-5 (fp16) and 1e-4 (bf16) of a sum however long: a tenth and a fortieth of the
+ * rounding of the output.
  * The sums of a call have a fixed order: the same inputs give the same bits. */
 typedef enum {
   MOE_LINEAR_NONE = 0,      /* act(z) = z                                            */
@@ -467,7 +473,8 @@ moe_status_t moe_linear(const void *x, const void *w, const void *bias, const vo
 
 /* Gradients of moe_linear, given dout [M, N], the gradient of out, in dout_dtype (dtype or
  * MOE_DT_FP32):
- *   dz    = dout * act'(preact)
+ *   dz    = dout * act'(preact)             (finite for every dout and preact but NaN: act' is 1 or
+ *                                            0 far from 0 and at the infinities)
  *   dx    = dz . w          [M, K] in dtype
  *   dw    = dz^T . x        [N, K] in dtype
  *   dbias = sum over m of dz  [N] in dtype (summed in fp32 from dz before any rounding)
@@ -500,7 +507,8 @@ size_t moe_linear_backward_workspace_size(int M, int N, int K);
  *   that sum is 0)
  * The choice is the one of fp64 arithmetic on the given values: scores too close to be ordered
  * in fp32 are compared more exactly (without a bias and with group_top 1 the logits themselves
- * are ranked, which is exact).  (MoE routers of the DeepSeek-V3 kind: sigmoid, bias,
+ * are ranked, which is exact; scores below 1e-300, which fp64 itself holds with few digits or not at
+ * all, may count as 0).  (MoE routers of the DeepSeek-V3 kind: sigmoid, bias,
  * 4 of 8 groups by their two best, top 8, scale 2.5; plain softmax top-k: n_group 1.)
  * A logit or bias of -inf or NaN masks the expert: weight 0 (a softmax's denominator counts every
  * unmasked logit, whatever its bias), no share in its group's score (a

@@ -33,9 +33,8 @@ constexpr int kMaxStages = 16;
 constexpr int kStageBudget = 192 * 1024;
 constexpr int kCtrlBytes = 512;
 constexpr int kSmemBytes = 1024 + kStageBudget + kCtrlBytes + kEpiWarps * 32 * 32 * 4;
-constexpr int kPromoteKB = 8;     // K blocks between two roundings of an fp32 output's sums,
-constexpr int kPromoteKB16 = 64;  // and of a 16-bit output's, which is promoted
-constexpr int kPlainKB16 = 256;   // over more than this many in one sum
+// K blocks of a sum in tensor memory, by the output's type: longer ones are promoted (see kPromote)
+constexpr int kRunFP32 = 8, kRunFP16 = 128, kRunBF16 = 256;
 // kPromote: the epilogue holds up to 128 sums a thread, so the first warpgroup hands it registers
 constexpr int kLaunchRegs = 168, kLowRegs = 40, kHighRegs = 232;
 static_assert(128 * kLowRegs + 256 * kHighRegs == kThreads * kLaunchRegs, "register split must balance");
@@ -693,11 +692,11 @@ __device__ __forceinline__ void join_splits(const Gemm& p, uint8_t* smem, int un
 // CG: CTAs that share an MMA.  2: a tile has 256 rows, each CTA of the pair copies its 128 rows
 //   of A and half of the B rows and holds its rows' accumulators; the even CTA issues the MMAs.
 // kPromote: the tensor core adds to its fp32 accumulator by truncation, which over K = 7168 left
-//   outputs 8e-6 off (2-norm), and sums of one sign 2^-24.5 a step of 16 elements (2.2e-3 at a million, the
-//   rounding of fp16 output is 4.9e-4); so every `chunk` stages the accumulator is added, with rounding,
-//   to fp32 sums in the epilogue's registers, and the next block starts from zero in the other
-//   accumulator.  fp32 outputs: every 512 elements; 16-bit ones: over more than 16384 in one sum (up to
-//   there 2^-14 of the sum at most, an eighth of fp16's rounding), every 4096, which the K loop hides.
+//   outputs 8e-6 off (2-norm), and of sums of one sign takes 1.0e-7 a step of 16 elements (measured: 1.0e-4
+//   over 16384, 5.9e-3 over a million; fp16 rounds by up to 4.9e-4); so every `chunk` stages the accumulator is
+//   added, with rounding, to fp32 sums in the epilogue's registers, and the next block starts from zero in
+//   the other accumulator.  fp32 outputs: every 512 elements; fp16 ones every 8192 (5e-5, a tenth of their
+//   rounding), bf16 ones every 16384 (1.0e-4, a fortieth), which the K loop nearly hides.
 // KS: K blocks of a stage, copied, awaited and multiplied together.  2 where a stage stays at most
 //   64 KB: fewer turns of the two loops, which bound narrow tiles ([16, 4096] over K 4096 in
 //   64-column tiles 16.5 -> 12.6 us; wider stages lose at 256 columns, 129 -> 150 us for
@@ -1324,8 +1323,9 @@ moe_status_t run_gemm(const Operand& A, const Operand& B, int C, const Epilogue&
   g.stages = kStageBudget / (ks * (g.a_rows + p.bn / p.cg) * 128);
   if (g.stages > kMaxStages) g.stages = kMaxStages;
   // a tile of the launch that does not split K, or splits it least, has the longest sums
-  const bool promote = e.out32 ? blocks > kPromoteKB : cdiv(blocks, p.splits) > kPlainKB16;
-  g.chunk = (e.out32 ? kPromoteKB : kPromoteKB16) / ks;
+  const int run = e.out32 ? kRunFP32 : e.fp16 ? kRunFP16 : kRunBF16;
+  const bool promote = e.out32 ? blocks > run : cdiv(blocks, p.splits) > run;
+  g.chunk = run / ks;
   g.idesc = make_idesc(e.fp16 ? 0 : 1, BM * p.cg, p.bn) | (A.mn ? 1u << 15 : 0) | (B.mn ? 1u << 16 : 0);
   CUtensorMap ma, mb;
   const bool ok = (A.mn ? make_map(&ma, A.base, e.fp16, e.P, C, A.ld, BK * ks)

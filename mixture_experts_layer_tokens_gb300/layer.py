@@ -1,5 +1,6 @@
 """One fused-MoE layer step composed from the C-ABI calls, with every buffer
-allocated once up front (PyTorch allocates, the library computes).
+allocated once up front (PyTorch allocates, the library computes); the gradients of the
+finalize alone are made by each MoELayer.router_backward call.
 
 Step: moe_route -> moe_align -> moe_prepare -> moe_experts [-> shared expert via
   moe_experts with one expert and the identity permutation] -> moe_finalize, on the
@@ -61,8 +62,9 @@ class MoERouter:
 
     def backward(self, dweights: torch.Tensor, a1: torch.Tensor, topk_ids: Optional[torch.Tensor] = None, stream=None):
         """Gradients of the last forward call's weights: (dgate_w, dgate_bias or None, da1, dlogits), the choice
-        (topk_ids, when forward wrote another buffer than its own) held fixed.  Buffers of the router, written
-        again by the next call."""
+        (topk_ids, when forward wrote another buffer than its own) held fixed.  da1 is what reaches the hidden
+        states through the gate alone: the experts' share, and the residual's, are the caller's to add.  Buffers of
+        the router, written again by the next call."""
         if self._grads is None:
             (E, H), dt, dev = self.gate_w.shape, self.gate_w.dtype, self.gate_w.device
             # (made by the first call, so from the pool of the stream that it runs on)
