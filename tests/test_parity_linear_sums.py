@@ -6,14 +6,14 @@ at each step, always towards zero.  fp32 outputs are promoted every 512 elements
 random signs a run's sums grow like the root of the steps, so a run adds 2^-24.5 (the mean of half
 a last place, relative) of sqrt(16 i / K) over i = 1 .. 32, 1.2e-5 / sqrt(K) of an output of size 1, and the K / 512
 runs' errors, independent in sign, 9e-7 together; without the promotion one run of K / 16 steps
-adds 1.2e-5 at K = 7168.  2e-6 lies between.  
+adds 1.2e-5 at K = 7168.  2e-6 lies between.
 
 16-bit outputs are rounded once, by half a step of the type at most (2^-11 of the value in fp16, 2^-8 in
 bf16).  Terms of one sign lose about half a last place of the growing sum at each step of 16, or two where
-the hardware adds the 16 in groups: 2^-23 of the final sum a step (1.2e-7).  fp16 sums are left in the tensor
+the hardware adds the 16 in groups: 2^-23 of the final sum a step (1.2e-7; measured 1.0e-7).  fp16 sums are left in the tensor
 core for 8192 elements, 512 steps: 2^-14.  bf16 sums for 16384: 2^-13.  Longer ones are sums of such runs
-with one fp32 rounding each, 2^-24 of the sum and 122 of them at a million elements: within the same slack,
-as the first of each run's steps lose next to nothing."""
+with one fp32 rounding each: 122 of them at a million elements in fp16, of 2^-25 of the growing sum each, are
+3.6e-6 at most, within the 8e-6 that the measured loss a step leaves of 2^-14."""
 import pytest
 import torch
 
