@@ -482,7 +482,9 @@ moe_status_t moe_linear(const void *x, const void *w, const void *bias, const vo
  * residual is dout itself.  preact [M, N] in dtype is what moe_linear wrote (required unless
  * the activation is MOE_LINEAR_NONE, where it is not read).  The tensor cores take dz in
  * dtype: where it has to be computed, or dout is fp32, it is rounded to dtype once (with
- * fp16, the caller's loss scale keeps it in range).  M == 0 sets dw and dbias to zero.
+ * fp16, the caller's loss scale keeps it in range).  A caller who wants an fp32 dout kept hands in
+ * its two parts, dout rounded to dtype and what that leaves, rounded too, as 2M rows over x
+ * twice: dw and dbias then sum both, and dx comes in two parts to add.  M == 0 sets dw and dbias to zero.
  * ws: moe_linear_backward_workspace_size(M, N, K) bytes (asked with the call's device
  * current: it depends on the number of SMs); it belongs to one call at a time -- calls, or
  * replayed graphs, that may run at once need one each.  Sizes, alignment and the order of sums as

@@ -85,6 +85,21 @@ def test_long_sums_of_one_sign_in_one_piece(cuda_dev, C, dtype):
         assert float(err.max()) <= torch.finfo(dtype).eps / 2 + SLACK[dtype], f"{float(err.max()):.3e}"
 
 
+def test_fp32_gradients_in_two_parts(cuda_dev):
+    """dout in two 16-bit parts as 2M rows over x twice: dw and dx are then off by their own rounding alone, 1.7e-3
+    in the 2-norm for normally distributed values in bf16; dz rounded to bf16 adds as much again (2.3e-3)."""
+    M, N, K = 1024, 256, 1000
+    g = torch.Generator(device=cuda_dev).manual_seed(9)
+    dout, x, w = (torch.randn(s, generator=g, device=cuda_dev) for s in ((M, N), (M, K), (N, K)))
+    x, w, hi = x.to(BF), w.to(BF), dout.to(BF)
+    both = torch.cat([hi, (dout - hi.float()).to(BF)])
+    dx, dw, _ = moe.moe_linear_backward(both, torch.cat([x, x]), w)
+    dx = dx[:M].float() + dx[M:].float()
+    assert moe.moe_device_status() == moe.MOE_OK
+    for got, ref in ((dw, dout.double().T @ x.double()), (dx, dout.double() @ w.double())):
+        assert (got.double() - ref).norm() <= 2e-3 * ref.norm()
+
+
 def test_host_threads_at_once(moelib):
     """The library's first products may come from several host threads at once, each on its stream."""
     import os
