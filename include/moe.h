@@ -473,8 +473,8 @@ moe_status_t moe_linear(const void *x, const void *w, const void *bias, const vo
 
 /* Gradients of moe_linear, given dout [M, N], the gradient of out, in dout_dtype (dtype or
  * MOE_DT_FP32):
- *   dz    = dout * act'(preact)             (finite for every dout and preact but NaN: act' is 1 or
- *                                            0 far from 0 and at the infinities)
+ *   dz    = dout * act'(preact)             (act' is 1 or 0 far from 0 and at the infinities: of
+ *                                            the preacts only a NaN makes a NaN)
  *   dx    = dz . w          [M, K] in dtype
  *   dw    = dz^T . x        [N, K] in dtype
  *   dbias = sum over m of dz  [N] in dtype (summed in fp32 from dz before any rounding)

@@ -671,7 +671,7 @@ def moe_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = 
 
 
 def linear_backward_workspace_size(M: int, N: int, K: int) -> int:
-    if max(M, N, K) > _INT_MAX:
+    if max(abs(M), abs(N), abs(K)) > _INT_MAX:
         raise ValueError("M, N and K: expected sizes up to 2^31 - 1")
     return int(lib().moe_linear_backward_workspace_size(M, N, K))
 
@@ -774,7 +774,7 @@ def moe_route_grouped_backward(dweights: torch.Tensor, logits: torch.Tensor, top
 
 # ------------------------------------------------------------------ finalize, gradient
 def finalize_backward_workspace_size(T: int, H: int) -> int:
-    if max(T, H) > _INT_MAX:
+    if max(abs(T), abs(H)) > _INT_MAX:
         raise ValueError("T and H: expected sizes up to 2^31 - 1")
     return int(lib().moe_finalize_backward_workspace_size(T, H))
 

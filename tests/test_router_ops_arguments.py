@@ -17,10 +17,10 @@ def test_route_config_refuses_what_does_not_fit(name, value):
 
 
 def test_workspace_sizes_refuse_what_does_not_fit(moelib):
-    for M, N, K in ((2 ** 32 + 5, 8, 64), (5, 2 ** 32 + 8, 64), (5, 8, 2 ** 31)):
+    for M, N, K in ((2 ** 32 + 5, 8, 64), (5, 2 ** 32 + 8, 64), (5, 8, 2 ** 31), (-2 ** 32 + 5, 8, 64)):
         with pytest.raises(ValueError, match="2\\^31"):
             moe.linear_backward_workspace_size(M, N, K)
-    for T, H in ((2 ** 32 + 4, 64), (4, 2 ** 31)):
+    for T, H in ((2 ** 32 + 4, 64), (4, 2 ** 31), (4, -2 ** 32 + 64)):
         with pytest.raises(ValueError, match="2\\^31"):
             moe.finalize_backward_workspace_size(T, H)
 
