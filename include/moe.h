@@ -61,7 +61,7 @@ typedef enum {
   MOE_DT_FP8_E4M3 = 1, /* OCP E4M3 ("e4m3fn"), saturating                    */
   MOE_DT_NVFP4 = 2,    /* E2M1 pairs + one E4M3 scale per 16 elements        */
   MOE_DT_FP32 = 3,
-  MOE_DT_FP16 = 4 /* moe_linear, moe_linear_backward and the logits of moe_route_grouped only */
+  MOE_DT_FP16 = 4 /* the linear and grouped products, moe_activation and the logits of moe_route_grouped only */
 } moe_dtype_t;
 
 typedef enum {
@@ -581,6 +581,86 @@ moe_status_t moe_finalize_backward(const void *dout, const void *dresidual_out, 
                                    float *dweights, void *dsum, float *drms, void *ws, size_t ws_bytes,
                                    moe_stream_t stream);
 size_t moe_finalize_backward_workspace_size(int T, int H);
+
+/* ------------------------------------------------------------------ RMSNorm
+ * The norm in front of the layer, with the residual's addition before it and the 8-bit rows of
+ * the fp8 experts behind it, in one pass over the rows:
+ *   v = x + residual              (fp32; residual NULL: v = x)
+ *   residual_out = bf16(v)        (optional, NULL = not written)
+ *   n = v * weight / sqrt(mean_h(v^2) + eps)
+ *   out = bf16(n)                 (optional)
+ *   q, q_scale                    n quantised as by moe_prepare, from the fp32 n: s =
+ *                                 fp32(max(amax, 1e-10) / 448), q = e4m3_rn_satfinite(n / s)
+ * qc: NULL or act MOE_DT_BF16: no q (q and q_scale NULL).  act MOE_DT_FP8_E4M3: act_group 128
+ * (q_scale [T, ceil(H / 128)]; a last group may be shorter) or MOE_GROUP_TOKEN (q_scale [T]); other
+ * groups are MOE_ERR_UNSUPPORTED.  x, residual, residual_out, out [T, H] and weight [H] bf16, q
+ * [T, H] E4M3 codes.  0 <= T <= 2^30, H % 8 == 0, 8 <= H <= 16384, eps >= 0; out or q is required.
+ * The squares are summed in fp32 in a fixed order (|v| beyond 1e19 / sqrt(H) overflows them); a row with a NaN or
+ * an infinity affects that row alone.  residual_out may be residual or x, and out x or residual, itself (a row
+ * is read before it is written); no other overlap.  The gradients, from residual_out (x without a residual),
+ * are moe_finalize_backward's dsum and drms (topk_weights, dy and dweights NULL, top_k 1). */
+moe_status_t moe_rmsnorm(const void *x, const void *residual, const void *weight, float eps, int T, int H,
+                         const moe_quant_config *qc, void *out, void *residual_out, void *q,
+                         float *q_scale, moe_stream_t stream);
+
+/* ------------------------------------------------------------------ grouped products
+ * The experts' products over ragged groups of rows, as calls of their own: a training step keeps
+ * what lies between them.  The S sorted rows are grouped by expert: those of expert e are p in
+ * [expert_offsets[e], expert_offsets[e + 1]), with slot sorted_slot[p] and token slot / top_k
+ * (moe_align's outputs).
+ *   out_p = x_p . w[e]^T           w [E, N, K] (K-contiguous), fp32 accumulation
+ * A tensor of rows comes in one of these orders:
+ *   MOE_ROWS_SORTED  [S, .], row p               MOE_ROWS_SLOT  [S, .], row sorted_slot[p]
+ *   MOE_ROWS_TOKEN   [S / top_k, .], row sorted_slot[p] / top_k (x and dout only)
+ * x, w and out in dtype (MOE_DT_BF16 or MOE_DT_FP16).  expert_offsets [E + 1] int32 ascend within [0, S];
+ * sorted_slot [S] int32, distinct values in [0, S), is read for the rows of a group alone (NULL where
+ * every order is MOE_ROWS_SORTED); a value out of range is recorded as MOE_ERR_INVALID_ARG
+ * in the device status word, its row read as zeros and not written.  Rows of out that belong to no group (behind
+ * expert_offsets[E]) are left as they were.  0 <= S <= 2^30 (0: nothing is done), 1 <= E <= 1024, N and K
+ * multiples of 8 up to 2^21, S % top_k == 0 where MOE_ROWS_TOKEN is used; more than 2^30 tiles may be
+ * MOE_ERR_UNSUPPORTED.  A row of x that holds a NaN or an infinity affects its row of out alone.
+ * Long sums are treated as moe_linear's are; the order of a sum is fixed by the sizes and
+ * the group, so the same inputs give the same bits.  ws: moe_grouped_linear_workspace_size(...)
+ * bytes (0 for MOE_ROWS_SORTED: ws may be NULL), for one call at a time.  Outputs overlap nothing. */
+typedef enum { MOE_ROWS_SORTED = 0, MOE_ROWS_SLOT = 1, MOE_ROWS_TOKEN = 2 } moe_rows_t;
+
+moe_status_t moe_grouped_linear(const void *x, int x_rows, const void *w, const int32_t *expert_offsets,
+                                const int32_t *sorted_slot, int S, int E, int N, int K, int top_k,
+                                moe_dtype_t dtype, void *out, int out_rows, void *ws, size_t ws_bytes,
+                                moe_stream_t stream);
+size_t moe_grouped_linear_workspace_size(int S, int E, int N, int K, int x_rows);
+
+/* Gradients of moe_grouped_linear, given dout, the gradient of out, in dtype:
+ *   dx_p  = dout_p . w[e]                         (dx_rows: MOE_ROWS_SORTED or MOE_ROWS_SLOT; the gradient
+ *                                                  of a token's row is the sum of its slots', which
+ *                                                  moe_finalize with the weights on the input adds)
+ *   dw[e] = sum over p of dout_p^T x_p            [E, N, K] in dw_dtype (dtype or MOE_DT_FP32); accumulate:
+ *                                                  added to what dw holds (in fp32, rounded once), else
+ *                                                  written, zeros for an expert without rows
+ * dx (needs w) and dw (needs x) may each be NULL, not both.  S == 0 sets dw to zero (accumulate: leaves it).
+ * ws: moe_grouped_linear_backward_workspace_size(...) bytes, for one call at a time.  Everything else as
+ * for moe_grouped_linear. */
+moe_status_t moe_grouped_linear_backward(const void *dout, int dout_rows, const void *x, int x_rows, const void *w,
+                                         const int32_t *expert_offsets, const int32_t *sorted_slot, int S,
+                                         int E, int N, int K, int top_k, moe_dtype_t dtype, void *dx,
+                                         int dx_rows, void *dw, moe_dtype_t dw_dtype, int accumulate,
+                                         void *ws, size_t ws_bytes, moe_stream_t stream);
+size_t moe_grouped_linear_backward_workspace_size(int S, int E, int N, int K, int dout_rows, int x_rows);
+
+/* ------------------------------------------------------------------ activation
+ * The activation between an expert's two products (a moe_activation_t) as a call of its own:
+ * gu [S, 2 I] = [g | u] (the *_NO_MUL activations: [S, I] = g) -> h [S, I], both in dtype (MOE_DT_BF16 or
+ * MOE_DT_FP16), computed in fp32 and rounded once.  0 <= S <= 2^30, I % 8 == 0, 8 <= I <= 2^21.
+ * The gate is 0 far below 0 and at -inf, where u is finite; a NaN affects its own h. */
+moe_status_t moe_activation(const void *gu, int S, int I, moe_dtype_t dtype, int activation, void *h,
+                            moe_stream_t stream);
+
+/* Its gradient: dh [S, I] -> dgu, as gu,
+ *   dg = dh act'(g) u,  du = dh act(g)
+ * with MOE_ACT_SWIGLUOAI 0 where a clamp holds g or u (the border itself passes).  h: the activation's
+ * output made again in the same pass (NULL: not written).  dgu may be gu itself, and h dh itself. */
+moe_status_t moe_activation_backward(const void *dh, const void *gu, int S, int I, moe_dtype_t dtype,
+                                     int activation, void *dgu, void *h, moe_stream_t stream);
 
 /* ------------------------------------------------------------------ status
  * Every device-side wait in the library's kernels gives up after about two

@@ -15,9 +15,8 @@
 // Problems with fewer tiles than SMs split K over the CTAs of a thread-block cluster: each
 // leaves its fp32 partial tile in its own shared memory, and after one cluster barrier every
 // CTA adds its share of the elements over distributed shared memory, in rank order.
-#include "moe_vec.cuh"
-
-#include <cudaTypedefs.h>
+#include "moe_act.cuh"
+#include "moe_mma.cuh"
 
 #include <atomic>
 
@@ -39,69 +38,6 @@ constexpr int kRunFP32 = 8, kRunFP16 = 128, kRunBF16 = 256;
 constexpr int kLaunchRegs = 168, kLowRegs = 40, kHighRegs = 232;
 static_assert(128 * kLowRegs + 256 * kHighRegs == kThreads * kLaunchRegs, "register split must balance");
 static_assert((2 * kMaxStages + 5) * 8 + 4 <= kCtrlBytes && kSmemBytes <= 232448, "shared memory layout");
-constexpr int kTmemCols = 512;
-constexpr int kAccCols = 256;     // columns between the two accumulators
-
-// 1 / (1 + exp(-x)) within 2^-21 (the exponential's error is weighed by at most 0.65 / (2 + 1.2 |x|)),
-// and 0 or 1 where exp overflows or vanishes.
-__device__ __forceinline__ float fast_sigmoid(float x) { return fast_rcp(1.0f + fast_exp(-x)); }
-
-// sqrt(2/pi) (z + 0.044715 z^3): (1 + tanh(u)) / 2 is the sigmoid of 2 u
-__device__ __forceinline__ float gelu_u(float z) { return 0.79788456f * z * fmaf(0.044715f * z, z, 1.0f); }
-
-// The normal distribution below -x, x >= 0, with e = exp(-x^2 / 2): e t P(t), t = 1 / (1 + 0.305 x) (the form of
-// Hastings' approximations of erf), P of degree 7 fitted to erfcx(x / sqrt 2) / (2 t) for the least largest relative
-// error on [0, 14]: 0.8 2^-23, in fp32 with e and 1 / x as above within (0.85 x^2 + 6) 2^-23 of the value
-// where it does not vanish (x < 13.2).  GELU from it keeps its digits below 0, where z/2 (1 + erf)
-// cancels (4 % of the value at -5), and the gradient shares e.  8192 x 4096 over 512 with a full epilogue: 89
-// us, by erfcf 133, by 1 + erff 100.
-__device__ __forceinline__ float normal_below(float x, float e) {
-  const float t = fast_rcp(fmaf(0.305f, x, 1.0f));
-  float p = 0.0367012769f;
-  p = fmaf(p, t, -0.152997345f);
-  p = fmaf(p, t, 0.18573311f);
-  p = fmaf(p, t, -0.0379923917f);
-  p = fmaf(p, t, 0.121030286f);
-  p = fmaf(p, t, 0.103418142f);
-  p = fmaf(p, t, 0.122467272f);
-  p = fmaf(p, t, 0.121639699f);
-  return p * t * e;
-}
-
-__device__ __forceinline__ float act_fwd(float z, int act) {
-  switch (act) {
-    case MOE_LINEAR_SILU: return z * fast_sigmoid(z);
-    case MOE_LINEAR_GELU: {
-      const float x = fminf(fabsf(z), 16.f);  // (the tail is 0 there)
-      return fmaf(-x, normal_below(fabsf(z), fast_exp(-0.5f * x * x)), fmaxf(z, 0.f));
-    }
-    case MOE_LINEAR_GELU_TANH: return z * fast_sigmoid(2.0f * gelu_u(z));
-  }
-  return z;
-}
-
-// The slopes are 1 or 0 to fp32 beyond |z| = 128 (silu) and 16; c, z kept to that range, goes into the factors
-// that grow, so that they stay finite where the one that vanishes is 0 (z = 1e20, or the infinity that a
-// sum became in 16 bits).  A NaN comes through the sigmoid or the tail of z itself.
-__device__ __forceinline__ float act_grad(float z, int act) {
-  const float c = fminf(fmaxf(z, act == MOE_LINEAR_SILU ? -128.f : -16.f), act == MOE_LINEAR_SILU ? 128.f : 16.f);
-  switch (act) {
-    case MOE_LINEAR_SILU: {
-      const float q = fast_sigmoid(z);
-      return q * fmaf(c, 1.0f - q, 1.0f);
-    }
-    case MOE_LINEAR_GELU: {
-      const float e = fast_exp(-0.5f * c * c), below = normal_below(fabsf(z), e);
-      return fmaf(c * 0.39894228f, e, z < 0.f ? below : 1.0f - below);
-    }
-    case MOE_LINEAR_GELU_TANH: {
-      const float q = fast_sigmoid(2.0f * gelu_u(z));
-      // z q (1 - q) 2 u'
-      return fmaf(c * q * (1.0f - q), 1.59576912f * fmaf(0.134145f * c, c, 1.0f), q);
-    }
-  }
-  return 1.0f;
-}
 
 // What is done with a sum z at (row, col) of D [P, Q].
 struct Epilogue {
@@ -380,152 +316,6 @@ struct Gemm {
   int unit0, units;     // the tiles of this launch: [unit0, units)
   uint32_t idesc;
 };
-
-// Shared-memory matrix descriptors of 128-byte-swizzled operands (see sw128_desc): 8-row atoms of
-// 1024 bytes (stride offset) along M/N for a K-major operand, along K for an MN-major one, which
-// lies as TMA boxes of 64 MN elements x KS 64 K elements write it, so that consecutive 64-element MN
-// groups are KS 8 KB apart (leading offset; unused by K-major).  The upper word is a constant and an
-// offset in shared memory stays below 2^18, so steps are added to the lower word alone.
-constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;  // stride offset, version, 128-byte swizzle
-template <bool kMN, int KS>
-__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr) {
-  return (smem_addr & 0x3FFFF) >> 4 | (kMN ? KS * 8192u >> 4 : 1u) << 16;  // (in a cluster the upper bits hold the rank)
-}
-__device__ __forceinline__ uint64_t desc(uint32_t lo) { return (uint64_t)kDescHi << 32 | lo; }
-
-// mbar_wait that looks at the clock only after a while: reading the global timer costs several
-// hundred clocks, and in short K loops most waits miss their first test.  For one thread.
-template <bool kBail = true>
-__device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity) {
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, kBail);
-}
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
-}
-
-// One thread of a converged warp, the same each time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(one));
-  return one != 0;
-}
-template <int N>
-__device__ __forceinline__ void setmaxnreg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void setmaxnreg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The same without its memory order: a release waits for the thread's global stores too (over a
-// microsecond).
-__device__ __forceinline__ void cluster_sync_relaxed() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t smem_addr, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ float ld_cluster1(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
-// The forms for a pair of CTAs that share an MMA (cta_group::2), beside the plain ones.
-template <int CG>
-__device__ __forceinline__ void tma_load(void* smem_dst, const CUtensorMap* map, int x, int y, uint32_t bar,
-                                         uint64_t policy) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
-        : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (CG == 1)
-    mma_bf16(d_tmem, adesc, bdesc, idesc, accumulate);
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Arrive on `bar` (CG 2: at its place in both CTAs of the pair, ranks in mask) when this
-// thread's MMAs so far complete.
-template <int CG>
-__device__ __forceinline__ void commit(uint64_t* bar, uint16_t mask) {
-  if constexpr (CG == 1)
-    tc_commit(bar);
-  else
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"(mask)
-        : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void tmem_take(uint32_t* slot) {
-  if constexpr (CG == 1) {
-    tmem_alloc(slot, kTmemCols);
-    tmem_relinquish();
-  } else {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
-}
-template <int CG>
-__device__ __forceinline__ void tmem_release(uint32_t taddr) {
-  if constexpr (CG == 1)
-    tmem_dealloc(taddr, kTmemCols);
-  else
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(kTmemCols) : "memory");
-}
-
-// 32 lanes x 16 consecutive fp32 columns from tensor memory.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
 
 // The tile of a unit: blocks of `raster` tile rows run through all tile columns, so that the CTAs
 // that work at the same time share A rows and B rows in L2.
@@ -1133,18 +923,6 @@ __global__ void __launch_bounds__(256) linear_dbias_kernel(const float* __restri
 }
 
 // ------------------------------------------------------------------ host side
-PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }();
-  return fn;
-}
-
 // A 16-bit row-major tensor [rows][inner] with row stride ld (elements), read in boxes of 64
 // inner elements x box_rows rows.
 bool make_map(CUtensorMap* m, const void* base, int fp16, long long inner, long long rows, long long ld, int box_rows) {
@@ -1164,8 +942,6 @@ struct Operand {
   bool mn;  // MN-major: the tensor's rows are the contraction
   long long ld;
 };
-
-int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 template <bool kAMN, bool kBMN, int CG, bool kPromote, int KS>
 cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g, int grid, bool overlap, cudaStream_t s) {

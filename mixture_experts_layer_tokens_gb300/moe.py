@@ -30,6 +30,9 @@ ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "swigluoai": 3, "silu_no_mu
 LINEAR_ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
 SCORES = {"softmax": 0, "sigmoid": 1}
 
+# moe_rows_t, by name: the order of a tensor's rows in the grouped products
+ROWS = {"sorted": 0, "slot": 1, "token": 2}
+
 # (name, argtypes, restype) of every exported entry point
 _P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 
@@ -116,6 +119,14 @@ SIGNATURES = {
     "moe_route_grouped_backward": ([_P, _P, _I, _P, _P, _I, _I, _I, _RCP, _P, _P], _I),
     "moe_finalize_backward": ([_P, _P, _P, _P, _F, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _Z, _P], _I),
     "moe_finalize_backward_workspace_size": ([_I, _I], _Z),
+    "moe_rmsnorm": ([_P, _P, _P, _F, _I, _I, _QCP, _P, _P, _P, _P, _P], _I),
+    "moe_grouped_linear": ([_P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _I, _P, _Z, _P], _I),
+    "moe_grouped_linear_workspace_size": ([_I, _I, _I, _I, _I], _Z),
+    "moe_grouped_linear_backward": ([_P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _I, _P, _I, _I, _P, _Z,
+                                     _P], _I),
+    "moe_grouped_linear_backward_workspace_size": ([_I, _I, _I, _I, _I, _I], _Z),
+    "moe_activation": ([_P, _I, _I, _I, _I, _P, _P], _I),
+    "moe_activation_backward": ([_P, _P, _I, _I, _I, _I, _P, _P, _P], _I),
     "moe_device_status": ([_I], _I),
     "moe_selftest_wait_timeout": ([ctypes.c_uint64, _P], _I),
     "moe_selftest_row_division": ([ctypes.c_longlong, ctypes.c_uint32, _P, _P], _I),
@@ -816,3 +827,194 @@ def moe_finalize_backward(dout: torch.Tensor, fused_expert_output: Optional[torc
         _tensor(dsum, bf, (T, H), "dsum", dev), _tensor(drms, torch.float32, (H,), "drms", dev),
         None if ws is None else _tensor(ws, torch.uint8, ws.shape, "ws", dev), 0 if ws is None else ws.numel(), s))
     return dy, dweights, dsum, drms
+
+
+# ------------------------------------------------------------------ RMSNorm
+def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                quant: Optional[str] = None, out: Optional[torch.Tensor] = None,
+                residual_out: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                q_scale: Optional[torch.Tensor] = None, need_out: bool = True, need_residual_out: bool = True,
+                stream=None):
+    """RMSNorm of x + residual (``moe_rmsnorm``): x and residual [T, H], weight [H] bf16 -> (out [T, H] bf16,
+    residual_out [T, H] bf16 -- the sum, made where there is a residual --, q [T, H] E4M3 codes (uint8), q_scale
+    fp32), None where not needed.  quant: None or "bf16" (no q), "fp8" (a scale per 128 columns, [T, ceil(H / 128)]) or
+    "fp8_token" ([T]), as moe_prepare's.  Gradients: ``moe_finalize_backward(dout, None, None, 1,
+    residual_out=..., rms_weight=weight, need_dy=False)`` gives dsum (of x and of the residual) and drms."""
+    if x.dim() != 2:
+        raise ValueError("x: expected [T, H]")
+    T, H = x.shape
+    if T > _INT_MAX or H > _INT_MAX:
+        raise ValueError("x: expected sizes up to 2^31 - 1")
+    quant = "bf16" if quant is None else quant
+    if quant not in ("bf16", "fp8", "fp8_token"):
+        raise ValueError(f"quant: expected None, 'bf16', 'fp8' or 'fp8_token', got {quant!r}")
+    bf, d, fp8 = torch.bfloat16, x.device, quant != "bf16"
+    if out is None and need_out:
+        out = _empty((T, H), bf, d, stream)
+    if residual_out is None and need_residual_out and residual is not None:
+        residual_out = _empty((T, H), bf, d, stream)
+    groups = (T, (H + 127) // 128) if quant == "fp8" else (T,)
+    if fp8 and q is None:
+        q = _empty((T, H), torch.uint8, d, stream)
+    if fp8 and q_scale is None:
+        q_scale = _empty(groups, torch.float32, d, stream)
+    if not fp8 and (q is not None or q_scale is not None):
+        raise ValueError("q and q_scale: expected None without a quant")
+    dev, s = _launch(stream)
+    _check("moe_rmsnorm", lib().moe_rmsnorm(
+        _tensor(x, bf, (T, H), "x", dev), _tensor(residual, bf, (T, H), "residual", dev),
+        _tensor(weight, bf, (H,), "weight", dev), eps, T, H, ctypes.byref(QUANT_CONFIGS[quant]),
+        _tensor(out, bf, (T, H), "out", dev), _tensor(residual_out, bf, (T, H), "residual_out", dev),
+        _tensor(q, torch.uint8, (T, H), "q", dev), _tensor(q_scale, torch.float32, groups, "q_scale", dev), s))
+    return out, residual_out, q, q_scale
+
+
+# ------------------------------------------------------------------ grouped products
+def _rows(name: str, order: str, S: int, top_k: int, token: bool = True) -> int:
+    """Rows of a tensor in the given order; the order checked."""
+    if order not in ROWS or order == "token" and not token:
+        raise ValueError(f"{name}: expected 'sorted'{', ' if token else ' or '}'slot'{' or ' if token else ''}"
+                         f"{repr('token') if token else ''}, got {order!r}")
+    if order != "token":
+        return S
+    if S % top_k:
+        raise ValueError(f"{name}: expected a multiple of top_k rows for the token order")
+    return S // top_k
+
+
+def _grouped_args(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, slots: Optional[torch.Tensor], top_k: int,
+                  orders):
+    """(S, E, N, K, dtype, dtype code) of a grouped product."""
+    if w.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"w: expected bfloat16 or float16, got {w.dtype}")
+    if w.dim() != 3 or x.dim() != 2 or offsets.dim() != 1 or (slots is not None and slots.dim() != 1):
+        raise ValueError("w, the rows, expert_offsets and sorted_slot: expected [E, N, K], [rows, columns], [E + 1] and [S]")
+    if not 1 <= top_k <= _INT_MAX:
+        raise ValueError("top_k: expected 1 .. 2^31 - 1")
+    if slots is None and any(o != "sorted" for o in orders):
+        raise ValueError("sorted_slot: expected for rows in another order than 'sorted'")
+    (E, N, K), S = w.shape, x.shape[0] if slots is None else slots.shape[0]
+    if max(S, E, N, K) > _INT_MAX:
+        raise ValueError("x and w: expected sizes up to 2^31 - 1")
+    return S, E, N, K, w.dtype, _DT[w.dtype]
+
+
+def grouped_linear_workspace_size(S: int, E: int, N: int, K: int, x_rows: str = "sorted") -> int:
+    if max(abs(S), abs(E), abs(N), abs(K)) > _INT_MAX:
+        raise ValueError("S, E, N and K: expected sizes up to 2^31 - 1")
+    return int(lib().moe_grouped_linear_workspace_size(S, E, N, K, ROWS[x_rows]))
+
+
+def grouped_linear_backward_workspace_size(S: int, E: int, N: int, K: int, dout_rows: str = "sorted",
+                                           x_rows: str = "sorted") -> int:
+    if max(abs(S), abs(E), abs(N), abs(K)) > _INT_MAX:
+        raise ValueError("S, E, N and K: expected sizes up to 2^31 - 1")
+    return int(lib().moe_grouped_linear_backward_workspace_size(S, E, N, K, ROWS[dout_rows], ROWS[x_rows]))
+
+
+def moe_grouped_linear(x: torch.Tensor, w: torch.Tensor, expert_offsets: torch.Tensor,
+                       sorted_slot: Optional[torch.Tensor] = None, top_k: int = 1, x_rows: str = "sorted",
+                       out_rows: str = "sorted", out: Optional[torch.Tensor] = None,
+                       ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The experts' product over ragged groups of rows (``moe_grouped_linear``): out_p = x_p w[e]^T for the sorted
+    rows p in [expert_offsets[e], expert_offsets[e + 1]); w [E, N, K] bf16 or fp16, expert_offsets [E + 1] and
+    sorted_slot [S] int32 as moe_align writes them (sorted_slot may be None where every order is "sorted").
+    x_rows, out_rows: the order of a tensor's rows (``ROWS``): "sorted" and "slot" have S rows, "token" (x alone)
+    S / top_k.  out [S, N] in the operands' type; rows behind expert_offsets[E] are left as they were."""
+    S, E, N, K, dt, code = _grouped_args(x, w, expert_offsets, sorted_slot, top_k, (x_rows, out_rows))
+    rx, ro = _rows("x_rows", x_rows, S, top_k), _rows("out_rows", out_rows, S, top_k, False)
+    if out is None:
+        out = _empty((ro, N), dt, x.device, stream)
+    if ws is None and x_rows != "sorted":
+        ws = _empty((max(grouped_linear_workspace_size(S, E, N, K, x_rows), 16),), torch.uint8, x.device, stream)
+    dev, s = _launch(stream)
+    i32 = torch.int32
+    _check("moe_grouped_linear", lib().moe_grouped_linear(
+        _tensor(x, dt, (rx, K), "x", dev), ROWS[x_rows], _tensor(w, dt, (E, N, K), "w", dev),
+        _tensor(expert_offsets, i32, (E + 1,), "expert_offsets", dev), _tensor(sorted_slot, i32, (S,), "sorted_slot", dev),
+        S, E, N, K, top_k, code, _tensor(out, dt, (ro, N), "out", dev), ROWS[out_rows],
+        None if ws is None else _tensor(ws, torch.uint8, ws.shape, "ws", dev), 0 if ws is None else ws.numel(), s))
+    return out
+
+
+def moe_grouped_linear_backward(dout: torch.Tensor, x: Optional[torch.Tensor], w: torch.Tensor,
+                                expert_offsets: torch.Tensor, sorted_slot: Optional[torch.Tensor] = None,
+                                top_k: int = 1, dout_rows: str = "sorted", x_rows: str = "sorted",
+                                dx_rows: str = "sorted", dx: Optional[torch.Tensor] = None,
+                                dw: Optional[torch.Tensor] = None, dw_dtype: Optional[torch.dtype] = None,
+                                accumulate: bool = False, ws: Optional[torch.Tensor] = None, need_dx: bool = True,
+                                need_dw: bool = True, stream=None):
+    """Gradients of moe_grouped_linear (``moe_grouped_linear_backward``) given dout, rows of N columns in
+    dout_rows order, and the forward call's x (None without dw): returns (dx [S, K] in dx_rows order, "sorted" or
+    "slot", in the operands' type; dw [E, N, K] in that type or fp32 (``dw_dtype``)), None where not needed.
+    accumulate: dw (then required) is added to instead of written."""
+    S, E, N, K, dt, code = _grouped_args(dout, w, expert_offsets, sorted_slot, top_k, (dout_rows, x_rows, dx_rows))
+    rd, rx = _rows("dout_rows", dout_rows, S, top_k), _rows("x_rows", x_rows, S, top_k)
+    ro = _rows("dx_rows", dx_rows, S, top_k, False)
+    if accumulate and dw is None:
+        raise ValueError("dw: expected with accumulate")
+    if dx is None and need_dx:
+        dx = _empty((ro, K), dt, dout.device, stream)
+    if dw is None and need_dw:
+        dw = _empty((E, N, K), dw_dtype or dt, dout.device, stream)
+    wdt = dt if dw is None else dw.dtype
+    if wdt is not dt and wdt is not torch.float32 or dw is not None and dw_dtype not in (None, wdt):
+        raise TypeError(f"dw: expected {dt} or float32 as dw_dtype says, got {wdt}")
+    if ws is None and (dout_rows != "sorted" or x_rows != "sorted"):
+        ws = _empty((max(grouped_linear_backward_workspace_size(S, E, N, K, dout_rows, x_rows), 16),), torch.uint8,
+                    dout.device, stream)
+    dev, s = _launch(stream)
+    i32 = torch.int32
+    _check("moe_grouped_linear_backward", lib().moe_grouped_linear_backward(
+        _tensor(dout, dt, (rd, N), "dout", dev), ROWS[dout_rows], _tensor(x, dt, (rx, K), "x", dev), ROWS[x_rows],
+        _tensor(w, dt, (E, N, K), "w", dev), _tensor(expert_offsets, i32, (E + 1,), "expert_offsets", dev),
+        _tensor(sorted_slot, i32, (S,), "sorted_slot", dev), S, E, N, K, top_k, code,
+        _tensor(dx, dt, (ro, K), "dx", dev), ROWS[dx_rows], _tensor(dw, wdt, (E, N, K), "dw", dev), _DT[wdt],
+        int(bool(accumulate)), None if ws is None else _tensor(ws, torch.uint8, ws.shape, "ws", dev),
+        0 if ws is None else ws.numel(), s))
+    return dx, dw
+
+
+# ------------------------------------------------------------------ activation
+def _activation_args(gu: torch.Tensor, activation: str):
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}")
+    if gu.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"gu: expected bfloat16 or float16, got {gu.dtype}")
+    if gu.dim() != 2 or not activation.endswith("_no_mul") and gu.shape[1] % 2:
+        raise ValueError("gu: expected [S, 2 I], or [S, I] for the *_no_mul activations")
+    (S, cols), dt = gu.shape, gu.dtype
+    if S > _INT_MAX or cols > _INT_MAX:
+        raise ValueError("gu: expected sizes up to 2^31 - 1")
+    return S, cols, cols if activation.endswith("_no_mul") else cols // 2, dt
+
+
+def moe_activation(gu: torch.Tensor, activation: str = "silu", h: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """The activation between an expert's two products (``moe_activation``, ``ACTIVATIONS``): gu [S, 2 I] = [g | u]
+    (*_no_mul: [S, I]) bf16 or fp16 -> h [S, I]."""
+    S, cols, I, dt = _activation_args(gu, activation)
+    if h is None:
+        h = _empty((S, I), dt, gu.device, stream)
+    dev, s = _launch(stream)
+    _check("moe_activation", lib().moe_activation(
+        _tensor(gu, dt, (S, cols), "gu", dev), S, I, _DT[dt], ACTIVATIONS[activation], _tensor(h, dt, (S, I), "h", dev),
+        s))
+    return h
+
+
+def moe_activation_backward(dh: torch.Tensor, gu: torch.Tensor, activation: str = "silu",
+                            dgu: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                            need_h: bool = False, stream=None):
+    """Gradient of moe_activation (``moe_activation_backward``): dh [S, I] -> (dgu, as gu; h, the activation's output
+    made again in the same pass, None where not needed)."""
+    S, cols, I, dt = _activation_args(gu, activation)
+    if dgu is None:
+        dgu = _empty((S, cols), dt, gu.device, stream)
+    if h is None and need_h:
+        h = _empty((S, I), dt, gu.device, stream)
+    dev, s = _launch(stream)
+    _check("moe_activation_backward", lib().moe_activation_backward(
+        _tensor(dh, dt, (S, I), "dh", dev), _tensor(gu, dt, (S, cols), "gu", dev), S, I, _DT[dt], ACTIVATIONS[activation],
+        _tensor(dgu, dt, (S, cols), "dgu", dev), _tensor(h, dt, (S, I), "h", dev), s))
+    return dgu, h
