@@ -165,14 +165,14 @@ def test_long_sums(cuda_dev, counts, N, K, dtype, wdt):
 
 
 def test_sums_of_one_sign(cuda_dev):
-    """Terms of one sign, where truncation would add up: an fp32 gradient within 3e-6 (every 512 terms lose at most
-    512 / 16 2^-23 = 3.8e-6 of their part, half of it on the average of a growing sum, and the fp32 sums of the parts
-    round by 2^-24 each)."""
+    """Terms of one sign, where truncation would add up: 32 steps of 16 terms lose at most 2^-23 of the part so far
+    each, 16.5 2^-23 of a part of 512, and 40 parts are added in fp32 with a half step of the sum so far each, 20.5
+    2^-24 in all: within 27 2^-23 < 3.3e-6."""
     p = Problem([20000], 64, 64, 1, BF)
     p.x, p.dout = torch.ones_like(p.x) * 1.0078125, torch.ones_like(p.dout) * 1.0078125
     _, dw = p.backward(cuda_dev, F32, need_dx=True)
     exact = 20000 * 1.0078125 ** 2
-    assert ((dw.double().cpu() - exact).abs() <= 3e-6 * exact).all()
+    assert ((dw.double().cpu() - exact).abs() <= 3.3e-6 * exact).all()
 
 
 def test_not_a_number_stays(cuda_dev):
