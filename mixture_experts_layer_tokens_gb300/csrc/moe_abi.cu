@@ -34,7 +34,8 @@ extern "C" moe_status_t moe_device_status(int clear) {
   const moe_status_t f = linear_status(clear);
   const moe_status_t g = finalize_backward_status(clear);
   const moe_status_t h = grouped_status(clear);
-  for (const moe_status_t st : {a, b, c, d, e, f, g, h})
+  const moe_status_t i = rmsnorm_status(clear);
+  for (const moe_status_t st : {a, b, c, d, e, f, g, h, i})
     if (st != MOE_OK) return st;
   return MOE_OK;
 }

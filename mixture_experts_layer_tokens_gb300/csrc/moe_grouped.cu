@@ -9,12 +9,13 @@
 // weights' bytes below.  Forward and dx put the weights on the MMA's 256 rows (a pair of CTAs, 128 each) and the
 // group's rows on its columns: a tile has as many columns as its group has rows left, in steps of 32, so a
 // ragged group wastes 16 columns on the average where tiles of 128 rows of it waste 64, and a decoded
-// token's experts read their weights once over narrow tiles.  dw has no ragged side but its contraction: 64 rows
-// at a time, and in the group's last block the rows behind its end (the next expert's) are zeroed in
-// shared memory before the MMAs see them.
+// token's experts read their weights once over narrow tiles.  dw has no ragged side but its contraction: a small
+// kernel makes tensor maps that end with each group, so that the copies of a group's last rows bring zeros
+// for what lies behind them.  (Zeroing those rows in shared memory between copy and MMAs stalled the K loop some 2500
+// clocks a tile: 4096 x 14336 over groups of 1024 rows 670 us.)
 //
 // Persistent, warp-specialised, pairs of CTAs: warp 0 copies stages of K blocks by TMA, warp 1 issues the MMAs, warps
-// 2 and 3 zero dw's tails, warps 4-11 run the epilogue from one of two accumulators in tensor memory while the
+// 4-11 run the epilogue from one of two accumulators in tensor memory while the
 // other fills.  Every CTA counts the tiles from the offsets itself; nothing comes back to the host.
 #include "moe_mma.cuh"
 
@@ -30,21 +31,24 @@ constexpr int kFirstEpi = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kMaxStages = 8;
 constexpr int kMaxE = 1024;
-constexpr int kStageBudget = 192 * 1024;
 constexpr int kCtrlBytes = 512;
-constexpr int kBufBytes = 2048;   // of an epilogue warp
 constexpr int kTableBytes = 2 * (kMaxE + 4) * 4;
-constexpr int kSmemBytes = 1024 + kStageBudget + kCtrlBytes + kEpiWarps * kBufBytes + kTableBytes;
+enum Mode { kForward, kDx, kDw };
+// Shared memory: the stages, a buffer for each epilogue warp, barriers, the groups' table.
+constexpr int stage_budget(Mode m) { return (m == kDw ? 160 : 192) * 1024; }
+constexpr int buf_bytes(Mode m) { return m == kDw ? 4096 : 2048; }
+constexpr int smem_bytes(Mode m) {
+  return 1024 + stage_budget(m) + kEpiWarps * buf_bytes(m) + kCtrlBytes + kTableBytes;
+}
 // K blocks of a sum in tensor memory, whose additions truncate, by the output's type; longer ones are added up in
 // fp32 registers with rounding (kPromote), as moe_linear's are
 constexpr int kRunFP32 = 8, kRunFP16 = 128, kRunBF16 = 256;
 constexpr int kLaunchRegs = 168, kLowRegs = 40, kHighRegs = 232;
 static_assert(128 * kLowRegs + 256 * kHighRegs == kThreads * kLaunchRegs, "register split must balance");
-static_assert((4 * kMaxStages + 5) * 8 + 4 <= kCtrlBytes && kSmemBytes <= 232448, "shared memory layout");
-
-enum Mode { kForward, kDx, kDw };
+static_assert((2 * kMaxStages + 5) * 8 + 4 <= kCtrlBytes && smem_bytes(kForward) <= 232448 && smem_bytes(kDw) <= 232448, "shared memory layout");
 
 struct Grouped {
+  const CUtensorMap* ends;         // dw: maps of dout and x that end with each group
   const int32_t *offsets, *slots;  // slots: rows of out are the slots of the sorted rows (NULL: the sorted rows)
   void* out;
   int S, E;
@@ -52,10 +56,15 @@ struct Grouped {
   int KB;                // stages of the contraction (dw: by the group's rows)
   int tiles_p, tiles_q;  // of 256 rows of A; dw: of `width` columns
   int width;             // columns of a tile at most
-  int box;               // rows of a box of B (forward and dx)
   int stages, chunk;     // chunk: stages added up in the tensor memory (kPromote)
   int fp16, out32, accumulate;
   uint32_t idesc;        // but for the columns
+};
+
+// Forward, dx: B's tensor in boxes of 16, 32, .. rows, one for each half tile there can be, so that a K block of B is
+// one copy whatever the tile (in boxes of 32 rows the copies' issue bounded the K loop).
+struct Maps {
+  CUtensorMap b[8];
 };
 
 struct Unit {
@@ -116,18 +125,9 @@ __device__ __forceinline__ void tma_load_pair_3d(void* smem_dst, const CUtensorM
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
       : "memory");
 }
-// lane_wait that also acquires what the other CTA of the pair released.
-__device__ __forceinline__ bool lane_wait_cluster(uint64_t* bar, uint32_t parity) {
-  if (!lane_wait(bar, parity)) return false;
-  uint32_t ok;  // (the phase is over: one test)
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
+// A tensor map in global memory that an earlier kernel wrote.
+__device__ __forceinline__ void acquire_map(const CUtensorMap* map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -136,123 +136,113 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, int fp16) {
   return fp16 ? Word<__half>::put(v) : Word<__nv_bfloat16>::put(v);
 }
 
-// 32 rows of A (lanes, from n0) x 32 sorted rows (v, from row0, `rows` of them valid) into out, 16 bits, transposed
-// through the warp's buffer: lanes pair up so that a word holds two neighbouring columns of out.
-__device__ __forceinline__ void store_rows32(const Grouped& p, char* buf, const float* v, int n0, int row0, int rows,
-                                             int lane) {
+// Without order: the accumulator's values are in registers (tcgen05.wait::ld), and a release would wait for the
+// thread's stores to global memory too (over a microsecond).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// 32 rows of A (lanes, from n0) x 32 sorted rows into out, 16 bits (w: sorted rows 2 i and 2 i + 1 in word i),
+// transposed through the warp's buffer: lanes pair up so that a word holds two neighbouring columns of out.  to: of
+// each sorted row (lane) its row of out, below 0 where it has none.
+__device__ __forceinline__ void store_rows32(const Grouped& p, char* buf, const uint32_t (&w)[16], int n0, int to, int lane) {
   uint32_t* words = reinterpret_cast<uint32_t*>(buf);
   const bool odd = lane & 1;
 #pragma unroll
-  for (int c = 0; c < 32; c += 2) {
-    const uint32_t mine = pack16(v[c], v[c + 1], p.fp16), other = __shfl_xor_sync(0xffffffffu, mine, 1);
-    words[(c + odd) * 16 + (lane >> 1)] = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+  for (int c = 0; c < 16; ++c) {
+    const uint32_t mine = w[c], other = __shfl_xor_sync(0xffffffffu, mine, 1);
+    words[(2 * c + odd) * 16 + (lane >> 1)] = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
   }
   __syncwarp();
   const int piece = lane & 3, col = n0 + piece * 8;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int c = i * 8 + (lane >> 2);
-    if (c < rows && col < p.P) {
-      long long row = row0 + c;
-      if (p.slots) {
-        row = p.slots[row];
-        if (row < 0 || row >= p.S) {
-          record_status((int)MOE_ERR_INVALID_ARG);
-          continue;
-        }
+    const int c = i * 8 + (lane >> 2), row = __shfl_sync(0xffffffffu, to, c);
+    const uint4 v = *reinterpret_cast<const uint4*>(buf + c * 64 + piece * 16);
+    if (row >= 0 && col < p.P) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (size_t)row * p.P + col) = v;
+  }
+  __syncwarp();
+}
+
+// ---- a weight gradient: 32 rows x 128 bytes at a time, by TMA from the warp's buffer (128-byte swizzle; what lies
+// behind the matrix is clipped)
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int x, int y, int z, bool add) {
+  if (add)
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(smem_src))
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(smem_src))
+                 : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// The thread's stores have read their buffers.
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+__device__ __forceinline__ char* grad_at(char* buf, int row, int piece) { return buf + row * 128 + ((piece ^ (row & 7)) << 4); }
+
+// 32 words of a row in each lane.
+__device__ __forceinline__ void store_grad(const CUtensorMap* map, char* buf, const uint32_t* w, int n0, int k0, int e, bool add,
+                                           int lane) {
+  if (lane == 0) tma_store_wait();
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint4*>(grad_at(buf, lane, i)) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  fence_async_smem();
+  __syncwarp();
+  if (lane == 0) tma_store_3d(map, buf, k0, n0, e, add);
+}
+
+// 32 x 32 sums added to 16-bit gradients, in fp32, rounded once.
+__device__ __forceinline__ void add_grad16(const Grouped& p, char* buf, const float* v, int n0, int k0, size_t out, int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<float4*>(grad_at(buf, lane, i)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  __syncwarp();
+  const int piece = lane & 7, col = k0 + piece * 4;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = i * 4 + (lane >> 3);
+    if (n0 + r < p.P && col < p.Q) {
+      const float4 w = *reinterpret_cast<const float4*>(grad_at(buf, r, piece));
+      uint2* d = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + out + (size_t)(n0 + r) * p.Q + col);
+      const uint2 o = *d;
+      float a[2], b[2];
+      if (p.fp16) {
+        Word<__half>::get(o.x, a);
+        Word<__half>::get(o.y, b);
+      } else {
+        Word<__nv_bfloat16>::get(o.x, a);
+        Word<__nv_bfloat16>::get(o.y, b);
       }
-      const uint4 w = *reinterpret_cast<const uint4*>(buf + c * 64 + piece * 16);
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.P + col) = w;
+      *d = make_uint2(pack16(w.x + a[0], w.y + a[1], p.fp16), pack16(w.z + b[0], w.w + b[1], p.fp16));
     }
   }
   __syncwarp();
 }
 
-// 32 rows (lanes, from n0) x 32 columns (v, from k0) of an expert's weight gradient at `out`.
-__device__ __forceinline__ void store_grad32(const Grouped& p, char* buf, const float* v, size_t out, int n0, int k0, int lane) {
-  auto at = [&](int row, int piece) { return buf + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4); };
-  const int piece = lane & 3;
-  if (!p.out32 && !p.accumulate) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = pack16(v[8 * i + 2 * j], v[8 * i + 2 * j + 1], p.fp16);
-      *reinterpret_cast<uint4*>(at(lane, i)) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    __syncwarp();
-    const int col = k0 + piece * 8;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2);
-      if (n0 + r < p.P && col < p.Q)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out + (size_t)(n0 + r) * p.Q + col) =
-            *reinterpret_cast<const uint4*>(at(r, piece));
-    }
-    __syncwarp();
-    return;
-  }
-#pragma unroll
-  for (int h = 0; h < 32; h += 16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<float4*>(at(lane, i)) =
-          make_float4(v[h + 4 * i], v[h + 4 * i + 1], v[h + 4 * i + 2], v[h + 4 * i + 3]);
-    __syncwarp();
-    const int col = k0 + h + piece * 4;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2);
-      if (n0 + r < p.P && col < p.Q) {
-        float4 w = *reinterpret_cast<const float4*>(at(r, piece));
-        const size_t to = out + (size_t)(n0 + r) * p.Q + col;
-        if (p.out32) {
-          float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.out) + to);
-          if (p.accumulate) {
-            const float4 o = *d;
-            w = make_float4(w.x + o.x, w.y + o.y, w.z + o.z, w.w + o.w);
-          }
-          *d = w;
-        } else {
-          uint2* d = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + to);
-          const uint2 o = *d;
-          float a[2], b[2];
-          if (p.fp16) {
-            Word<__half>::get(o.x, a);
-            Word<__half>::get(o.y, b);
-          } else {
-            Word<__nv_bfloat16>::get(o.x, a);
-            Word<__nv_bfloat16>::get(o.y, b);
-          }
-          *d = make_uint2(pack16(w.x + a[0], w.y + a[1], p.fp16), pack16(w.z + b[0], w.w + b[1], p.fp16));
-        }
-      }
-    }
-    __syncwarp();
-  }
-}
-
 // KS: K blocks of a stage.  kPromote: see moe_linear's kernel.
 template <Mode kMode, bool kPromote, int KS>
 __global__ void __launch_bounds__(kThreads, 1)
-    grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                        const __grid_constant__ Grouped p) {
+    grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ Maps maps,
+                        const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ Grouped p) {
   constexpr bool kAMN = kMode != kForward, kBMN = kMode == kDw;
   constexpr int kAStage = kRows * 128;  // bytes of a K block of A
-  static_assert(kMode != kDw || KS == 1, "a tail is one K block");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* ctrl = smem + kStageBudget;
+  char* bufs = reinterpret_cast<char*>(smem + stage_budget(kMode));
+  uint8_t* ctrl = reinterpret_cast<uint8_t*>(bufs + kEpiWarps * buf_bytes(kMode));
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
   uint64_t* empty = full + kMaxStages;
-  uint64_t* tail = empty + kMaxStages;   // dw: this CTA's copies of a group's last block have landed
-  uint64_t* fixed = tail + kMaxStages;   // dw, in the leader: the rows behind the end are zero in both CTAs
-  uint64_t* tfull = fixed + kMaxStages;  // [2] accumulator complete
+  uint64_t* tfull = empty + kMaxStages;  // [2] accumulator complete
   uint64_t* tempty = tfull + 2;          // [2] accumulator read
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  char* bufs = reinterpret_cast<char*>(ctrl + kCtrlBytes);
-  int* start = reinterpret_cast<int*>(bufs + kEpiWarps * kBufBytes);  // [E + 1] first sorted row of each group
+  int* start = reinterpret_cast<int*>(ctrl + kCtrlBytes);  // [E + 1] first sorted row of each group
   int* pre = start + kMaxE + 4;                                       // [E + 1] tiles of the groups before it
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int stages = p.stages, half_width = p.width / 2;
@@ -263,15 +253,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   depend_launch();
   if (warp == 2 && elect_one()) {
-    prefetch_tensormap(&tmA);
-    prefetch_tensormap(&tmB);
+    if (kMode == kDw) {
+      prefetch_tensormap(&tmOut);
+    } else {
+      prefetch_tensormap(&tmA);
+      for (int i = 0; i < p.width / 32; ++i) prefetch_tensormap(&maps.b[i]);
+    }
   }
+  // (offsets out of order or range would be the caller's mistake; no row outside [0, S) is touched)
+  for (int e = threadIdx.x; e <= p.E; e += kThreads) start[e] = min(max(__ldg(p.offsets + e), 0), p.S);
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&tail[s], 1);
-      mbar_init(&fixed[s], 4);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
@@ -281,34 +275,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_take<2>(tmem_slot);
-  if (warp == 3) {
+  tc_fence_before();
+  __syncthreads();
+  if (kMode != kDw && warp == 3) {  // tiles of the groups
     int before = 0;
     for (int b = 0; b < p.E; b += 32) {
       const int e = b + lane;
-      // (offsets out of order or range would be the caller's mistake; no row outside [0, S) is touched)
-      const int first = e < p.E ? min(max(p.offsets[e], 0), p.S) : 0;
-      const int end = e < p.E ? min(max(p.offsets[e + 1], 0), p.S) : 0;
-      int n = (max(0, end - first) + p.width - 1) / p.width;
+      int n = e < p.E ? (max(0, start[e + 1] - start[e]) + p.width - 1) / p.width : 0;
       const int own = n;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, n, off);
         if (lane >= off) n += v;
       }
-      if (e < p.E) {
-        start[e] = first;
-        pre[e] = before + n - own;
-      }
-      if (e == p.E - 1) {
-        start[p.E] = end;
-        pre[p.E] = before + n;
-      }
+      if (e < p.E) pre[e] = before + n - own;
       before += __shfl_sync(0xffffffffu, n, 31);
     }
+    if (lane == 0) pre[p.E] = before;
+    __syncwarp();
   }
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();  // the pair's barriers are set up
+  cluster_sync();  // the pair's barriers are set up, the tiles counted
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   depend_wait();
@@ -330,14 +316,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- TMA producer
       const uint64_t pol = policy_evict_normal();
       const uint32_t full0 = map_to_rank(smem_u32(full), 0);  // (both CTAs' copies complete there)
-      uint32_t tailed = 0, tail_phase = 0;  // a bit a stage: its last use was a tail's; phase of its next tail
+      long long seen = -1;  // dw: the group whose maps were acquired
       for (int u = first; u < units; u += step) {
         const Unit t = unit_of<kMode>(p, start, pre, u);
         const int arow = (t.p * 2 + half) * kRows;
-        const int boxes = kBMN ? half_width / 64 : (t.width / 2 + p.box - 1) / p.box;
+        const int boxes = kBMN ? half_width / 64 : 1;
         const int brow = kBMN ? t.q * p.width + half * half_width : t.row0 + half * (t.width / 2);
-        const uint32_t bytes = KS * (kAStage + (kBMN ? b_stage : boxes * p.box * 128));
+        const uint32_t bytes = KS * (kAStage + (kBMN ? b_stage : t.width / 2 * 128));
+        const CUtensorMap* mA = kMode == kDw ? p.ends + 2 * t.e : &tmA;
+        const CUtensorMap* mB = kMode == kDw ? mA + 1 : &maps.b[t.width / 32 - 1];
         if (elect_one()) {
+          if (kMode == kDw && seen != t.e && t.stages) {
+            acquire_map(mA);
+            acquire_map(mB);
+          }
           int st = stage;
           uint32_t ph = phase;
           for (int kb = 0; kb < t.stages; ++kb) {
@@ -347,43 +339,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             uint8_t* sA = smem + st * stage_bytes;
             uint8_t* sB = sA + KS * kAStage;
-            const bool last = kMode == kDw && kb == t.stages - 1 && t.rows % BK != 0;
-            // a tail's copies complete in each CTA, where warps 2 and 3 wait for them
-            const uint32_t bar = last ? smem_u32(&tail[st]) : full0 + st * 8;
-            if (last) {
-              mbar_arrive_expect_tx(&tail[st], bytes);
-              if (half == 0) mbar_arrive(&full[st]);
-              tailed |= 1u << st;
-              tail_phase ^= 1u << st;
-            } else {
-              if (half == 0) mbar_arrive_expect_tx(&full[st], 2 * bytes);
-              tailed &= ~(1u << st);
-            }
+            const uint32_t bar = full0 + st * 8;
+            if (half == 0) mbar_arrive_expect_tx(&full[st], 2 * bytes);
             const int k = kMode == kDw ? t.row0 + kb * BK : kb * KS * BK;
             if constexpr (kMode == kForward) {
 #pragma unroll
               for (int i = 0; i < KS; ++i)
-                tma_load_pair_3d(sA + i * kAStage, &tmA, k + i * BK, arow, (int)t.e, bar, pol);
+                tma_load_pair_3d(sA + i * kAStage, mA, k + i * BK, arow, (int)t.e, bar, pol);
             } else if constexpr (kMode == kDx) {
 #pragma unroll
-              for (int g = 0; g < 2; ++g) tma_load_pair_3d(sA + g * KS * 8192, &tmA, arow + g * 64, k, (int)t.e, bar, pol);
+              for (int g = 0; g < 2; ++g) tma_load_pair_3d(sA + g * KS * 8192, mA, arow + g * 64, k, (int)t.e, bar, pol);
             } else {
-              auto load = [&](auto cg) {
 #pragma unroll
-                for (int g = 0; g < 2; ++g) tma_load<decltype(cg)::value>(sA + g * 8192, &tmA, arow + g * 64, k, bar, pol);
-                for (int g = 0; g < boxes; ++g)
-                  tma_load<decltype(cg)::value>(sB + g * 8192, &tmB, brow + g * 64, k, bar, pol);
-              };
-              if (last)
-                load(std::integral_constant<int, 1>());
-              else
-                load(std::integral_constant<int, 2>());
+              for (int g = 0; g < 2; ++g) tma_load<2>(sA + g * 8192, mA, arow + g * 64, k, bar, pol);
+              for (int g = 0; g < boxes; ++g) tma_load<2>(sB + g * 8192, mB, brow + g * 64, k, bar, pol);
             }
             if constexpr (!kBMN) {
 #pragma unroll
               for (int i = 0; i < KS; ++i)
-                for (int g = 0; g < boxes; ++g)
-                  tma_load<2>(sB + i * b_stage + g * p.box * 128, &tmB, k + i * BK, brow + g * p.box, bar, pol);
+                tma_load<2>(sB + i * b_stage, mB, k + i * BK, brow, bar, pol);
             }
             if (++st == stages) {
               st = 0;
@@ -392,16 +366,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (failed) {
             // wait (bounded) for the copies still in flight: each stage's phase that the ring was in
-            for (int i = 0; i < stages; ++i)
-              if (tailed >> i & 1)
-                mbar_wait(&tail[i], (tail_phase >> i & 1) ^ 1, false, 100000000ull);
-              else if (half == 0)
-                mbar_wait(&full[i], i < st ? ph : ph ^ 1, false, 100000000ull);
+            if (half == 0)
+              for (int i = 0; i < stages; ++i) mbar_wait(&full[i], i < st ? ph : ph ^ 1, false, 100000000ull);
           }
         }
         __syncwarp();
         if ((failed = __any_sync(0xffffffffu, failed))) break;
         advance(t.stages);
+        seen = t.stages ? t.e : seen;
       }
     } else if (warp == 1 && half == 0) {
       // ---------------------------------------------------------- MMA issuer
@@ -409,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t ad0 = desc_lo<kAMN, KS>(a0), bd0 = desc_lo<kBMN, KS>(b0);
       constexpr uint32_t kStepA = (kAMN ? 2048 : 32) >> 4, kStepB = (kBMN ? 2048 : 32) >> 4;  // 16 K elements on
       int acc = 0;
-      uint32_t acc_phase = 0, fixed_phase = 0;  // fixed_phase: a bit a stage
+      uint32_t acc_phase = 0;
       for (int u = first; u < units && !failed; u += step) {
         const Unit t = unit_of<kMode>(p, start, pre, u);
         const uint32_t idesc = p.idesc | (uint32_t)(t.width >> 3) << 17;
@@ -417,7 +389,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kc = 0; kc < t.stages; kc += chunk) {
           const uint32_t d = tmem + acc * kAccCols;
           const int ke = min(t.stages, kc + chunk);
-          uint32_t flip = 0;
           if (elect_one()) {
             int st = stage;
             uint32_t ph = phase;
@@ -427,13 +398,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!lane_wait(&full[st], ph)) {
                 failed = true;
                 break;
-              }
-              if (kMode == kDw && kb == t.stages - 1 && t.rows % BK != 0) {
-                if (!lane_wait_cluster(&fixed[st], fixed_phase >> st & 1)) {
-                  failed = true;
-                  break;
-                }
-                flip = 1u << st;
               }
               tc_fence_after();
               const uint32_t at = (uint32_t)(st * stage_bytes) >> 4;
@@ -460,34 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           if ((failed = __any_sync(0xffffffffu, failed))) break;
-          fixed_phase ^= __reduce_or_sync(0xffffffffu, flip);
           advance(ke - kc);
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1;
-        }
-      }
-    } else if (kMode == kDw && warp >= 2) {
-      // ---------------------------------------------------------- zeroes of dw's tails
-      // warp 2 A's rows, warp 3 B's: a row of a box is 128 bytes whatever the swizzle, which stays within it
-      const uint32_t fixed0 = map_to_rank(smem_u32(fixed), 0);
-      uint32_t tail_phase = 0;
-      for (int u = first; u < units; u += step) {
-        const Unit t = unit_of<kMode>(p, start, pre, u);
-        if (t.rows % BK != 0) {
-          advance(t.stages - 1);
-          if (!__all_sync(0xffffffffu, lane_wait(&tail[stage], tail_phase >> stage & 1))) break;
-          tail_phase ^= 1u << stage;
-          uint8_t* at = smem + stage * stage_bytes + (warp == 3 ? kAStage : 0);
-          const int boxes = warp == 3 ? half_width / 64 : 2, from = t.rows % BK * 128;
-          for (int b = 0; b < boxes; ++b)
-            for (int i = from + lane * 16; i < 8192; i += 512)
-              *reinterpret_cast<uint4*>(at + b * 8192 + i) = make_uint4(0, 0, 0, 0);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(fixed0 + stage * 8);
-          advance(1);
-        } else {
-          advance(t.stages);
         }
       }
     }
@@ -503,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     if (kPromote) setmaxnreg_inc<kHighRegs>();
     const int quarter = warp & 3;              // TMEM lanes this warp may access
-    const int side = (warp - kFirstEpi) >> 2;  // every other 32 columns
-    char* buf = bufs + (warp - kFirstEpi) * kBufBytes;
+    const int side = (warp - kFirstEpi) >> 2;  // forward, dx: every other 32 columns; dw: half of them
+    char* buf = bufs + (warp - kFirstEpi) * buf_bytes(kMode);
     const uint32_t tb = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t freed = map_to_rank(smem_u32(tempty), 0);
     int acc = 0;
@@ -512,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto release = [&]() {  // this warp is done with the accumulator
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(freed + acc * 8);
+      if (lane == 0) mbar_arrive_cluster_relaxed(freed + acc * 8);
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     };
@@ -520,17 +459,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = first; ok && u < units; u += step) {
       const Unit t = unit_of<kMode>(p, start, pre, u);
       const int n0 = (t.p * 2 + half) * kRows + quarter * 32;
-      const int cols = n0 >= p.P ? 0 : kMode == kDw ? min(t.width, p.Q - t.q * p.width) : t.rows;
-      auto take = [&](const float* v, int c) {
-        if constexpr (kMode == kDw)
-          store_grad32(p, buf, v, (size_t)t.e * p.P * p.Q, n0, t.q * p.width + c, lane);
-        else
-          store_rows32(p, buf, v, n0, t.row0 + c, t.rows - c, lane);
+      // first column of the c-th 32 columns of this warp, in the tile; columns of the tile that are of use
+      auto at = [&](int c) { return kMode == kDw ? side * (p.width / 2) + c * 32 : c * 64 + side * 32; };
+      const int cols = n0 >= p.P ? 0 : kMode == kDw ? min((side + 1) * (p.width / 2), p.Q - t.q * p.width) : t.rows;
+      int to[4];  // rows of out (see store_rows32), on their way before the accumulator is complete
+      if constexpr (kMode != kDw) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int row = at(c) + lane;
+          to[c] = row < cols ? t.row0 + row : -1;
+          if (p.slots && to[c] >= 0) {
+            to[c] = __ldg(p.slots + to[c]);
+            if (to[c] < 0 || to[c] >= p.S) {
+              record_status((int)MOE_ERR_INVALID_ARG);
+              to[c] = -1;
+            }
+          }
+        }
+      }
+      auto finish = [&](const uint32_t (&w)[4][16]) {  // 16-bit words of all columns
+        if constexpr (kMode == kDw) {
+#pragma unroll
+          for (int c = 0; c < 4; c += 2)
+            if (at(c) < cols) store_grad(&tmOut, buf, &w[0][0] + c * 16, n0, t.q * p.width + at(c), (int)t.e, false, lane);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (at(c) < cols) store_rows32(p, buf, w[c], n0, to[c], lane);
+        }
       };
+      uint32_t words[4][16] = {};
       if (kMode == kDw && t.stages == 0) {  // an expert without rows
-        if (!p.accumulate) {
-          const float v[32] = {};
-          for (int c = side * 32; c < cols; c += 64) take(v, c);
+        if (p.accumulate) continue;
+        if (!p.out32) {
+          finish(words);
+        } else {
+          const uint32_t zero[32] = {};
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (at(c) < cols) store_grad(&tmOut, buf, zero, n0, t.q * p.width + at(c), (int)t.e, false, lane);
         }
         continue;
       }
@@ -541,11 +508,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (c * 64 + side * 32 < cols) {
+            if (at(c) < cols) {
 #pragma unroll
               for (int h = 0; h < 32; h += 16) {
                 float v[16];
-                tmem_ld16(tb + acc * kAccCols + c * 64 + side * 32 + h, v);
+                tmem_ld16(tb + acc * kAccCols + at(c) + h, v);
                 tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) sums[c * 32 + h + i] += v[i];
@@ -554,21 +521,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           release();
         }
         if (!ok) break;
+        if (kMode == kDw && (p.out32 || p.accumulate)) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c * 64 + side * 32 < cols) take(sums + c * 32, c * 64 + side * 32);
+          for (int c = 0; c < 4; ++c)
+            if (at(c) < cols) {
+              if (p.out32)
+                store_grad(&tmOut, buf, reinterpret_cast<const uint32_t*>(sums + c * 32), n0, t.q * p.width + at(c),
+                           (int)t.e, p.accumulate, lane);
+              else
+                add_grad16(p, buf, sums + c * 32, n0, t.q * p.width + at(c), (size_t)t.e * p.P * p.Q, lane);
+            }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) words[c][i] = pack16(sums[c * 32 + 2 * i], sums[c * 32 + 2 * i + 1], p.fp16);
+          finish(words);
+        }
       } else {
         if (!(ok = warp_wait(&tfull[acc], acc_phase))) break;
         tc_fence_after();
-        for (int c = side * 32; c < cols; c += 64) {
-          float v[32];
-          tmem_ld32(tb + acc * kAccCols + c, v);
-          tmem_ld_wait();
-          take(v, c);
-        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (at(c) < cols) {
+            float v[32];
+            tmem_ld32(tb + acc * kAccCols + at(c), v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) words[c][i] = pack16(v[2 * i], v[2 * i + 1], p.fp16);
+          }
         release();
+        finish(words);
       }
     }
+    if (kMode == kDw && lane == 0) tma_store_wait();
   }
 
   __syncwarp();
@@ -580,15 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ rows into sorted order
-// to[p] = from[slots[p] / div] for the sorted rows p that belong to a group: a warp a row.
-__global__ void __launch_bounds__(256)
-    gather_rows_kernel(const uint4* __restrict__ from, const int32_t* __restrict__ slots,
-                       const int32_t* __restrict__ offsets, int E, int S, int div, int nvec, uint4* __restrict__ to) {
-  depend_launch();
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= S || row >= __ldg(offsets + E)) return;
-  const int slot = __ldg(slots + row);
-  uint4* d = to + (size_t)row * nvec;
+__device__ __forceinline__ void gather_row(const uint4* __restrict__ from, int slot, int S, int div, int nvec,
+                                           uint4* __restrict__ d, int lane) {
   if (slot < 0 || slot >= S) {
     if (lane == 0) record_status((int)MOE_ERR_INVALID_ARG);
     for (int i = lane; i < nvec; i += 32) d[i] = make_uint4(0, 0, 0, 0);
@@ -605,26 +584,59 @@ __global__ void __launch_bounds__(256)
   }
   for (; i < nvec; i += 32) d[i] = __ldg(s + i);
 }
+// to[p] = from[slots[p] / div] for the sorted rows p that belong to a group: a warp a row.
+__global__ void __launch_bounds__(256)
+    gather_rows_kernel(const uint4* __restrict__ from, const int32_t* __restrict__ slots,
+                       const int32_t* __restrict__ offsets, int E, int S, int div, int nvec, uint4* __restrict__ to) {
+  depend_launch();
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row < S && row < __ldg(offsets + E)) gather_row(from, __ldg(slots + row), S, div, nvec, to + (size_t)row * nvec, lane);
+  depend_wait();  // (not for its own sake: what comes after this kernel comes after the one before it, too)
+}
+
+// ------------------------------------------------------------------ maps that end with a group
+// ends[2 e] and ends[2 e + 1]: the maps of dout and x with their rows cut at the end of group e.  A warp a map.
+__global__ void __launch_bounds__(32)
+    group_maps_kernel(const __grid_constant__ CUtensorMap d, const __grid_constant__ CUtensorMap x,
+                      const int32_t* __restrict__ offsets, int S, CUtensorMap* ends) {
+  __shared__ __align__(128) CUtensorMap map;
+  depend_launch();
+  const int end = min(max(__ldg(offsets + (blockIdx.x >> 1) + 1), 0), S), lane = threadIdx.x;
+  const CUtensorMap& from = blockIdx.x & 1 ? x : d;
+  reinterpret_cast<uint32_t*>(&map)[lane] = reinterpret_cast<const uint32_t*>(&from)[lane];
+  __syncwarp();
+  if (lane == 0)
+    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(smem_u32(&map)), "r"(max(end, 1))
+                 : "memory");
+  __syncwarp();
+  asm volatile(
+      "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
+          reinterpret_cast<uint64_t>(ends + blockIdx.x)),
+      "r"(smem_u32(&map))
+      : "memory");
+}
 
 // ------------------------------------------------------------------ host side
-// A 16-bit tensor [outer][rows][inner] read in boxes of 64 inner elements x box rows of one matrix; outer 0: two
-// dimensions.
-bool make_map(CUtensorMap* m, const void* base, int fp16, long long inner, long long rows, long long outer, int box) {
+// A tensor [outer][rows][inner] in boxes of 128 bytes x box rows of one matrix; outer 0: two dimensions.
+bool make_map(CUtensorMap* m, const void* base, int dtype, long long inner, long long rows, long long outer, int box) {
   auto enc = get_encode();
   if (!enc) return false;
-  const int rank = outer ? 3 : 2;
+  const int rank = outer ? 3 : 2, size = dtype == MOE_DT_FP32 ? 4 : 2;
   cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)outer};
-  cuuint64_t strides[2] = {(cuuint64_t)inner * 2, (cuuint64_t)inner * rows * 2};
-  cuuint32_t boxes[3] = {64, (cuuint32_t)box, 1};
+  cuuint64_t strides[2] = {(cuuint64_t)inner * size, (cuuint64_t)inner * rows * size};
+  cuuint32_t boxes[3] = {(cuuint32_t)(128 / size), (cuuint32_t)box, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base),
-             dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const CUtensorMapDataType type = dtype == MOE_DT_FP32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : dtype == MOE_DT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return enc(m, type, rank, const_cast<void*>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <Mode kMode, bool kPromote, int KS>
-cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const Grouped& g, long long units, bool overlap,
-                   cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& ma, const Maps& mb, const CUtensorMap& mo, const Grouped& g, long long units,
+                   bool overlap, cudaStream_t s) {
   auto kern = grouped_gemm_kernel<kMode, kPromote, KS>;
   if (kPromote) {
     // The epilogue's warps take registers that the first warpgroup gives back (setmaxnreg): a build with another
@@ -638,11 +650,11 @@ cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const Grouped& 
       checked.store(true, std::memory_order_relaxed);
     }
   }
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kMode));
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = smem_bytes(kMode);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -654,21 +666,22 @@ cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const Grouped& 
   const long long pairs = num_sms() / 2;
   cfg.gridDim = dim3((unsigned)(2 * (units < pairs ? units : pairs)));
   cfg.numAttrs = overlap ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, ma, mb, g);
+  return cudaLaunchKernelEx(&cfg, kern, ma, mb, mo, g);
 }
 template <Mode kMode, bool kPromote>
-cudaError_t launch(int ks, const CUtensorMap& ma, const CUtensorMap& mb, const Grouped& g, long long units, bool overlap,
-                   cudaStream_t s) {
+cudaError_t launch(int ks, const CUtensorMap& ma, const Maps& mb, const CUtensorMap& mo, const Grouped& g,
+                   long long units, bool overlap, cudaStream_t s) {
   if constexpr (kMode != kDw)
-    if (ks == 2) return launch<kMode, kPromote, 2>(ma, mb, g, units, overlap, s);
-  return launch<kMode, kPromote, 1>(ma, mb, g, units, overlap, s);
+    if (ks == 2) return launch<kMode, kPromote, 2>(ma, mb, mo, g, units, overlap, s);
+  return launch<kMode, kPromote, 1>(ma, mb, mo, g, units, overlap, s);
 }
 
 // One product.  a: the weights [E, N, K] (dw: dout, sorted), b: sorted rows.
 template <Mode kMode>
 moe_status_t run(const void* a, const void* b, const int32_t* offsets, const int32_t* slots, int S, int E, int N, int K,
-                 int fp16, void* out, int out32, int accumulate, bool overlap, cudaStream_t s) {
+                 int fp16, void* out, int out32, int accumulate, const CUtensorMap* ends, bool overlap, cudaStream_t s) {
   Grouped g = {};
+  g.ends = ends;
   g.offsets = offsets;
   g.slots = slots;
   g.out = out;
@@ -688,44 +701,62 @@ moe_status_t run(const void* a, const void* b, const int32_t* offsets, const int
     g.width = S <= 32 ? 32 : mean <= 24 ? 64 : mean <= 48 ? 128 : 256;
     ks = g.width <= 128 ? 2 : 1;
   }
-  g.box = g.width / 2 < 32 ? g.width / 2 : 32;
   g.tiles_p = cdiv(g.P, 2 * kRows);
   g.tiles_q = cdiv(g.Q, g.width);
   g.KB = cdiv(contraction, BK * ks);
   const int stage = ks * (kRows + g.width / 2) * 128;
-  g.stages = kStageBudget / stage < kMaxStages ? kStageBudget / stage : kMaxStages;
+  g.stages = stage_budget(kMode) / stage < kMaxStages ? stage_budget(kMode) / stage : kMaxStages;
   const int run = out32 ? kRunFP32 : fp16 ? kRunFP16 : kRunBF16;
-  const bool promote = cdiv(contraction, BK) > run;
+  // (the general epilogue of a gradient keeps its sums in fp32 registers)
+  const bool promote = cdiv(contraction, BK) > run || out32 || accumulate;
   g.chunk = run / ks;
   g.idesc = make_idesc(fp16 ? 0 : 1, 2 * kRows, 0) | (kMode != kForward ? 1u << 15 : 0) | (kMode == kDw ? 1u << 16 : 0);
   const long long units =
       kMode == kDw ? (long long)E * g.tiles_p * g.tiles_q : (long long)g.tiles_p * (S / g.width + (S < E ? S : E));
   if (units > 1073741823LL) return MOE_ERR_UNSUPPORTED;
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mo;
+  Maps mb;
+  const int type = fp16 ? MOE_DT_FP16 : MOE_DT_BF16;
   bool ok;
-  if (kMode == kDw)
-    ok = make_map(&ma, a, fp16, N, S, 0, BK) && make_map(&mb, b, fp16, K, S, 0, BK);
-  else
-    ok = make_map(&ma, a, fp16, K, N, E, kMode == kForward ? kRows : BK * ks) &&
-         make_map(&mb, b, fp16, kMode == kForward ? K : N, S, 0, g.box);
+  if (kMode == kDw) {
+    ok = make_map(&mo, out, out32 ? (int)MOE_DT_FP32 : type, K, N, E, 32);
+    ma = mo;  // (not used)
+  } else {
+    ok = make_map(&ma, a, type, K, N, E, kMode == kForward ? kRows : BK * ks);
+    for (int i = 0; i < g.width / 32; ++i)
+      ok = ok && make_map(&mb.b[i], b, type, kMode == kForward ? K : N, S, 0, 16 * (i + 1));
+    mo = ma;  // (not used)
+  }
   if (!ok) return MOE_ERR_CUDA;
-  const cudaError_t err = promote ? launch<kMode, true>(ks, ma, mb, g, units, overlap, s)
-                                  : launch<kMode, false>(ks, ma, mb, g, units, overlap, s);
+  const cudaError_t err = promote ? launch<kMode, true>(ks, ma, mb, mo, g, units, overlap, s)
+                                  : launch<kMode, false>(ks, ma, mb, mo, g, units, overlap, s);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 // Rows in `order` -> sorted rows at `to` (the caller's where they are sorted already).
 const void* sorted_rows(const void* from, int order, const int32_t* offsets, const int32_t* slots, int S, int E, int cols,
-                        int top_k, void* to, cudaStream_t s) {
+                        int top_k, void* to, bool& overlap, cudaStream_t s) {
   if (order == MOE_ROWS_SORTED) return from;
-  gather_rows_kernel<<<cdiv(S, 8), 256, 0, s>>>(static_cast<const uint4*>(from), slots, offsets, E, S,
-                                                order == MOE_ROWS_TOKEN ? top_k : 1, cols / 8, static_cast<uint4*>(to));
-  return to;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cdiv(S, 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1] = {overlap_attr()};
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  overlap = true;
+  const cudaError_t err =
+      cudaLaunchKernelEx(&cfg, gather_rows_kernel, static_cast<const uint4*>(from), slots, offsets, E, S,
+                         order == MOE_ROWS_TOKEN ? top_k : 1, cols / 8, static_cast<uint4*>(to));
+  return err == cudaSuccess ? to : nullptr;
 }
 
 size_t rows_bytes(long long S, long long cols, int order) {
   return order == MOE_ROWS_SORTED ? 0 : ((size_t)S * cols * 2 + 255) / 256 * 256;
 }
+
+// The groups' maps, and room to start them on 128 bytes.
+size_t maps_bytes(int E) { return (size_t)E * 2 * sizeof(CUtensorMap) + 128; }
 
 bool order_ok(int order, const int32_t* slots, int S, int top_k, bool token) {
   if (order < MOE_ROWS_SORTED || order > (token ? MOE_ROWS_TOKEN : MOE_ROWS_SLOT)) return false;
@@ -765,16 +796,18 @@ extern "C" moe_status_t moe_grouped_linear(const void* x, int x_rows, const void
   const size_t need = rows_bytes(S, K, x_rows);
   if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const void* xs = sorted_rows(x, x_rows, expert_offsets, sorted_slot, S, E, K, top_k, ws, s);
+  bool overlap = false;
+  const void* xs = sorted_rows(x, x_rows, expert_offsets, sorted_slot, S, E, K, top_k, ws, overlap, s);
+  if (!xs) return MOE_ERR_CUDA;
   const moe_status_t got =
       run<kForward>(w, xs, expert_offsets, out_rows == MOE_ROWS_SLOT ? sorted_slot : nullptr, S, E, N, K,
-                    dtype == MOE_DT_FP16, out, 0, 0, xs != x, s);
+                    dtype == MOE_DT_FP16, out, 0, 0, nullptr, overlap, s);
   return got == MOE_OK ? launch_status() : got;
 }
 
 extern "C" size_t moe_grouped_linear_backward_workspace_size(int S, int E, int N, int K, int dout_rows, int x_rows) {
   if (S <= 0 || E <= 0 || N <= 0 || K <= 0) return 0;
-  return rows_bytes(S, N, dout_rows) + rows_bytes(S, K, x_rows);
+  return rows_bytes(S, N, dout_rows) + rows_bytes(S, K, x_rows) + maps_bytes(E);
 }
 
 extern "C" moe_status_t moe_grouped_linear_backward(const void* dout, int dout_rows, const void* x, int x_rows,
@@ -800,21 +833,35 @@ extern "C" moe_status_t moe_grouped_linear_backward(const void* dout, int dout_r
                 order_ok(dx_rows, sorted_slot, S, top_k, false));
   MOE_CHECK_ARG(aligned16(dout) && aligned16(x) && aligned16(w) && aligned16(expert_offsets) && aligned16(sorted_slot) &&
                 aligned16(ws));
-  const size_t first = rows_bytes(S, N, dout_rows), need = first + (dw ? rows_bytes(S, K, x_rows) : 0);
+  const size_t first = rows_bytes(S, N, dout_rows), need = first + (dw ? rows_bytes(S, K, x_rows) + maps_bytes(E) : 0);
   if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   const int fp16 = dtype == MOE_DT_FP16;
-  const void* d = sorted_rows(dout, dout_rows, expert_offsets, sorted_slot, S, E, N, top_k, ws, s);
-  const void* xs =
-      dw ? sorted_rows(x, x_rows, expert_offsets, sorted_slot, S, E, K, top_k, static_cast<uint8_t*>(ws) + first, s) : x;
-  bool overlap = d != dout || xs != x;
+  bool overlap = false;
+  uint8_t* next = static_cast<uint8_t*>(ws) + first;  // behind dout's rows
+  const void* xs = x;
+  CUtensorMap* ends = nullptr;
+  if (dw) {
+    const int type = fp16 ? MOE_DT_FP16 : MOE_DT_BF16;
+    if (x_rows != MOE_ROWS_SORTED) xs = next;
+    next += rows_bytes(S, K, x_rows);
+    ends = reinterpret_cast<CUtensorMap*>((reinterpret_cast<uintptr_t>(next) + 127) & ~uintptr_t(127));
+    CUtensorMap md, mx;
+    if (!make_map(&md, dout_rows == MOE_ROWS_SORTED ? dout : ws, type, N, S, 0, BK) || !make_map(&mx, xs, type, K, S, 0, BK))
+      return MOE_ERR_CUDA;
+    group_maps_kernel<<<2 * E, 32, 0, s>>>(md, mx, expert_offsets, S, ends);
+    overlap = true;
+  }
+  const void* d = sorted_rows(dout, dout_rows, expert_offsets, sorted_slot, S, E, N, top_k, ws, overlap, s);
+  if (dw) xs = sorted_rows(x, x_rows, expert_offsets, sorted_slot, S, E, K, top_k, const_cast<void*>(xs), overlap, s);
+  if (!d || (dw && !xs)) return MOE_ERR_CUDA;
   if (dx) {
     st = run<kDx>(w, d, expert_offsets, dx_rows == MOE_ROWS_SLOT ? sorted_slot : nullptr, S, E, N, K, fp16, dx, 0, 0,
-                  overlap, s);
+                  nullptr, overlap, s);
     if (st != MOE_OK) return st;
     overlap = true;
   }
   if (dw) {
-    st = run<kDw>(d, xs, expert_offsets, nullptr, S, E, N, K, fp16, dw, out32, accumulate != 0, overlap, s);
+    st = run<kDw>(d, xs, expert_offsets, nullptr, S, E, N, K, fp16, dw, out32, accumulate != 0, ends, overlap, s);
     if (st != MOE_OK) return st;
   }
   return launch_status();

@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kMaxThreads = 1024;
 constexpr int kMaxH = 16384;
+constexpr int kRegs = 65536;  // of an SM
 
 struct Norm {
   const __nv_bfloat16 *x, *res, *gamma;
@@ -26,51 +27,97 @@ struct Norm {
   int threads;  // of a row: 16 or a multiple of 32
 };
 
-// Over the `threads` lanes of a row (16, or whole warps); the same value in each.
+// Over the `threads` lanes of a row (16, or whole warps); the same value in each.  Every thread of the CTA comes.
 template <bool kMax>
-__device__ __forceinline__ float row_reduce(float a, int threads, float (&red)[2][kMaxThreads / 32], int which) {
+__device__ __forceinline__ float row_reduce(float a, int threads, float* red) {
   auto op = [](float p, float q) { return kMax ? fmaxf(p, q) : p + q; };
 #pragma unroll
   for (int off = 8; off > 0; off >>= 1) a = op(a, __shfl_xor_sync(0xffffffffu, a, off));
-  if (threads == 16) return a;
-  a = op(a, __shfl_xor_sync(0xffffffffu, a, 16));
-  const int warps = threads >> 5;
-  if (warps == 1) return a;
-  const int warp = threadIdx.x >> 5, first = warp / warps * warps;
-  if ((threadIdx.x & 31) == 0) red[which][warp] = a;
+  if (threads > 16) a = op(a, __shfl_xor_sync(0xffffffffu, a, 16));
+  const int warp = threadIdx.x >> 5, warps = threads >> 5;
+  if (warps > 1 && (threadIdx.x & 31) == 0) red[warp] = a;
   __syncthreads();
-  a = red[which][first];
-  for (int i = 1; i < warps; ++i) a = op(a, red[which][first + i]);
+  if (warps > 1) {
+    const int first = warp / warps * warps;
+    a = red[first];
+    for (int i = 1; i < warps; ++i) a = op(a, red[first + i]);
+  }
   return a;
 }
 
-// NV: vectors of 8 columns a thread holds of a row.
-template <int NV>
-__global__ void rmsnorm_kernel(const Norm p) {
-  __shared__ float red[2][kMaxThreads / 32];
+__device__ __forceinline__ void unpack8(const uint4 w, float (&v)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) Word<__nv_bfloat16>::get(u[i], v + 2 * i);
+}
+
+__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(smem_dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// NV: vectors of 8 columns a thread holds of a row.  kRing: the rows come through two stages of shared memory by bulk
+// copies, the next turn's under this turn's work (loads by the threads themselves left HBM idle through each row's
+// sum and outputs: 16384 x 7168 with all outputs 301 us).
+template <int NV, bool kRing>
+__global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const Norm p) {
+  extern __shared__ __align__(128) uint8_t stages[];
+  __shared__ float red[2][2][kMaxThreads / 32];
+  __shared__ uint64_t full[2];
   const int threads = p.threads, rows = blockDim.x / threads;  // rows of a CTA at a time
-  const int i = threadIdx.x % threads, nvec = p.H / 8;
-  float gamma[NV][8];
+  const int i = threadIdx.x % threads, mine = threadIdx.x / threads, nvec = p.H / 8;
+  const size_t tensor = (size_t)rows * p.H * 2;  // bytes of one tensor's rows in a stage
+  const int step = gridDim.x * rows;
+  bool ok = true;
+  auto fetch = [&](int t0, int stage) {  // by one thread
+    if (t0 >= p.T) return;
+    const uint32_t bytes = (uint32_t)min(rows, p.T - t0) * p.H * 2;
+    uint8_t* to = stages + stage * tensor * (p.res ? 2 : 1);
+    mbar_arrive_expect_tx(&full[stage], p.res ? 2 * bytes : bytes);
+    bulk_load(to, p.x + (size_t)t0 * p.H, bytes, &full[stage]);
+    if (p.res) bulk_load(to + tensor, p.res + (size_t)t0 * p.H, bytes, &full[stage]);
+  };
+  if (kRing) {
+    if (threadIdx.x == 0) {
+      mbar_init(&full[0], 1);
+      mbar_init(&full[1], 1);
+      fence_mbar_init();
+      fetch(blockIdx.x * rows, 0);
+      fetch(blockIdx.x * rows + step, 1);
+    }
+    __syncthreads();
+  }
+  uint4 gamma[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int v = j * threads + i;
-    if (v < nvec) load8(p.gamma + v * 8, gamma[j]);
+    if (v < nvec) gamma[j] = __ldg(reinterpret_cast<const uint4*>(p.gamma) + v);
   }
   // (every thread of the CTA makes every turn: the sums meet at barriers)
-  for (int t0 = blockIdx.x * rows; t0 < p.T; t0 += gridDim.x * rows) {
-    const int t = t0 + threadIdx.x / threads;
+  int turn = 0;
+  for (int t0 = blockIdx.x * rows; t0 < p.T; t0 += step, ++turn) {
+    const int t = t0 + mine, stage = turn & 1;
     const size_t at = (size_t)t * p.H;
     float n[NV][8], sum = 0.f;
     bool on[NV];
+    // a wait that gives up (recorded) leaves wrong values, but every barrier is still met
+    if (kRing) ok &= mbar_wait(&full[stage], turn >> 1 & 1);
+    const uint8_t* row = stages + stage * tensor * (p.res ? 2 : 1) + (size_t)mine * p.H * 2;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int v = j * threads + i;
       on[j] = t < p.T && v < nvec;
       if (on[j]) {
-        load8(p.x + at + v * 8, n[j]);
+        const uint4 a = kRing ? *reinterpret_cast<const uint4*>(row + v * 16)
+                              : *reinterpret_cast<const uint4*>(p.x + at + v * 8);
+        unpack8(a, n[j]);
         if (p.res) {
+          const uint4 b = kRing ? *reinterpret_cast<const uint4*>(row + tensor + v * 16)
+                                : *reinterpret_cast<const uint4*>(p.res + at + v * 8);
           float r[8];
-          load8(p.res + at + v * 8, r);
+          unpack8(b, r);
 #pragma unroll
           for (int c = 0; c < 8; ++c) n[j][c] += r[c];
         }
@@ -83,25 +130,29 @@ __global__ void rmsnorm_kernel(const Norm p) {
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int c = 0; c < 8; ++c) sum = fmaf(n[j][c], n[j][c], sum);
+    sum = row_reduce<false>(sum, threads, red[0][stage]);
+    if (kRing && threadIdx.x == 0) fetch(t0 + 2 * step, stage);  // (all threads have read the stage)
     if (p.res_out) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (on[j]) store8(p.res_out + at + (size_t)(j * threads + i) * 8, n[j]);
     }
-    const float r = __frsqrt_rn(row_reduce<false>(sum, threads, red, 0) / (float)p.H + p.eps);
-    float most = 0.f;
+    const float r = __frsqrt_rn(sum / (float)p.H + p.eps);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (on[j]) {
+        float g[8];
+        unpack8(gamma[j], g);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) n[j][c] = n[j][c] * r * gamma[j][c];
+        for (int c = 0; c < 8; ++c) n[j][c] = n[j][c] * r * g[c];
         if (p.out) store8(p.out + at + (size_t)(j * threads + i) * 8, n[j]);
       }
     }
     if (p.group == MOE_GROUP_TOKEN) {
+      float most = 0.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) most = fmaxf(most, amax8(n[j]));
-      const float s = __fdiv_rn(fmaxf(row_reduce<true>(most, threads, red, 1), 1e-10f), 448.f);
+      const float s = __fdiv_rn(fmaxf(row_reduce<true>(most, threads, red[1][stage]), 1e-10f), 448.f);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (on[j]) *reinterpret_cast<uint2*>(p.q + at + (size_t)(j * threads + i) * 8) = e4m3x8(n[j], s);
@@ -121,11 +172,19 @@ __global__ void rmsnorm_kernel(const Norm p) {
         }
       }
     }
-    __syncthreads();  // (red is written again)
   }
+  // copies that a wait did not see land (bounded) before the shared memory goes
+  if (kRing && !ok && threadIdx.x == 0)
+    for (int s = 0; s < 2; ++s) {
+      const int last = turn - 1 - ((turn - 1 - s) & 1);  // the stage's last turn
+      if (last >= 0) mbar_wait(&full[s], last >> 1 & 1, false, 100000000ull);
+    }
 }
 
 }  // namespace
+
+MOE_DEFINE_STATUS_READER(rmsnorm_status)
+
 }  // namespace moe
 
 using namespace moe;
@@ -148,19 +207,31 @@ extern "C" moe_status_t moe_rmsnorm(const void* x, const void* residual, const v
   using B = __nv_bfloat16;
   Norm p{static_cast<const B*>(x), static_cast<const B*>(residual), static_cast<const B*>(weight), static_cast<B*>(out),
          static_cast<B*>(residual_out), static_cast<uint8_t*>(q), q_scale, eps, T, H, group, 0};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int nvec = H / 8;
-  auto go = [&](auto nv) {
+  auto go = [&](auto nv, auto ring) {
     constexpr int NV = decltype(nv)::value;
+    constexpr bool kRing = decltype(ring)::value;
     const int need = (nvec + NV - 1) / NV;
     p.threads = need <= 16 ? 16 : (need + 31) / 32 * 32;
     const int rows = p.threads >= 128 ? 1 : 128 / p.threads, block = rows * p.threads;
-    const int turns = (T + rows - 1) / rows, most = num_sms() * (2048 / block);
-    rmsnorm_kernel<NV><<<turns < most ? turns : most, block, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    const int turns = (T + rows - 1) / rows;
+    const int smem = kRing ? 2 * rows * H * 2 * (residual ? 2 : 1) : 0;
+    int ctas = 2048 / block;  // of an SM
+    if (kRing) {
+      const int by_regs = kRegs / (block * 64), by_smem = 232448 / (smem + 2048);
+      ctas = by_regs < by_smem ? by_regs : by_smem;
+      if (ctas < 1) ctas = 1;
+      if (cudaFuncSetAttribute(rmsnorm_kernel<NV, kRing>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    }
+    const int most = num_sms() * ctas;
+    rmsnorm_kernel<NV, kRing><<<turns < most ? turns : most, block, smem, s>>>(p);
+    return launch_status();
   };
-  // a row's loads in one round where there are few rows, fewer threads to a row where there are many
-  if (nvec <= kMaxThreads && T <= num_sms())
-    go(std::integral_constant<int, 1>());
-  else
-    go(std::integral_constant<int, 4>());
-  return launch_status();
+  // Few rows: one round of loads a thread and no ring.  [1, 7168] with all outputs 4.4 us in a graph, by the ring 5.1.
+  if (nvec <= kMaxThreads && T <= num_sms()) return go(std::integral_constant<int, 1>(), std::false_type());
+  // Two vectors a thread.  With 1 / 2 / 4 of them, all outputs: [16384, 7168] 207 / 185 / 179 us, [16384, 1024] 28 / 29 /
+  // 28, [65536, 128] 14 / 16 / 24, [1024, 7168] 17 / 13.5 / 15 (by the threads' own loads 300, 39, 32, 23).
+  return go(std::integral_constant<int, 2>(), std::true_type());
 }

@@ -12,6 +12,7 @@ namespace moe {
 moe_status_t route_grouped_status(int clear);
 moe_status_t linear_status(int clear);
 moe_status_t grouped_status(int clear);
+moe_status_t rmsnorm_status(int clear);
 moe_status_t finalize_backward_status(int clear);
 
 // ---- launches that overlap the end of the launch before them on the stream

@@ -960,7 +960,7 @@ def moe_grouped_linear_backward(dout: torch.Tensor, x: Optional[torch.Tensor], w
     wdt = dt if dw is None else dw.dtype
     if wdt is not dt and wdt is not torch.float32 or dw is not None and dw_dtype not in (None, wdt):
         raise TypeError(f"dw: expected {dt} or float32 as dw_dtype says, got {wdt}")
-    if ws is None and (dout_rows != "sorted" or x_rows != "sorted"):
+    if ws is None and (dw is not None or dout_rows != "sorted"):
         ws = _empty((max(grouped_linear_backward_workspace_size(S, E, N, K, dout_rows, x_rows), 16),), torch.uint8,
                     dout.device, stream)
     dev, s = _launch(stream)

@@ -67,9 +67,10 @@ def test_grouped_linear_backward_refusals(moelib):
     for kw in (dict(dt=FP32), dict(wdt=FP16), dict(dt=FP16, wdt=BF16), dict(wdt=FP8)):
         assert call(**kw) == UNSUP, kw
     size = moe.grouped_linear_backward_workspace_size
-    assert size(12, 4, 16, 32) == 0
-    assert size(12, 4, 16, 32, "slot", "token") >= 12 * 16 * 2 + 12 * 32 * 2
-    assert call(dr=SLOT, ws=None) == WS and call(xr=TOKEN, n=100) == WS
+    assert size(0, 4, 16, 32) == 0 and size(12, 4, 16, 32) >= 4 * 256
+    assert size(12, 4, 16, 32, "slot", "token") >= 12 * 16 * 2 + 12 * 32 * 2 + 4 * 256
+    assert call(dr=SLOT, ws=None) == WS and call(xr=TOKEN, n=100) == WS and call(ws=None) == WS and call(n=1000) == WS
+    assert call(dw=None, dr=SLOT, n=12 * 32 - 1) == WS
 
 
 def test_activation_refusals(moelib):
