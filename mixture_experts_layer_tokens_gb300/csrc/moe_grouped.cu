@@ -32,20 +32,20 @@ constexpr int kEpiWarps = 8;
 constexpr int kMaxStages = 8;
 constexpr int kMaxE = 1024;
 constexpr int kCtrlBytes = 512;
-constexpr int kTableBytes = 2 * (kMaxE + 4) * 4;
+constexpr int kSmemMost = 232448;
 enum Mode { kForward, kDx, kDw };
-// Shared memory: the stages, a buffer for each epilogue warp, barriers, the groups' table.
-constexpr int stage_budget(Mode m) { return (m == kDw ? 160 : 192) * 1024; }
+// Shared memory: the stages (as many as fit), a buffer for each epilogue warp, barriers, the groups' table.
 constexpr int buf_bytes(Mode m) { return m == kDw ? 4096 : 2048; }
-constexpr int smem_bytes(Mode m) {
-  return 1024 + stage_budget(m) + kEpiWarps * buf_bytes(m) + kCtrlBytes + kTableBytes;
+constexpr int table_bytes(Mode m, int E) { return (m == kDw ? 1 : 2) * ((E + 4) & ~3) * 4; }
+constexpr int smem_bytes(Mode m, int E, int stages, int stage) {
+  return 1024 + stages * stage + kEpiWarps * buf_bytes(m) + kCtrlBytes + table_bytes(m, E);
 }
 // K blocks of a sum in tensor memory, whose additions truncate, by the output's type; longer ones are added up in
 // fp32 registers with rounding (kPromote), as moe_linear's are
 constexpr int kRunFP32 = 8, kRunFP16 = 128, kRunBF16 = 256;
 constexpr int kLaunchRegs = 168, kLowRegs = 40, kHighRegs = 232;
 static_assert(128 * kLowRegs + 256 * kHighRegs == kThreads * kLaunchRegs, "register split must balance");
-static_assert((2 * kMaxStages + 5) * 8 + 4 <= kCtrlBytes && smem_bytes(kForward) <= 232448 && smem_bytes(kDw) <= 232448, "shared memory layout");
+static_assert((2 * kMaxStages + 5) * 8 + 4 <= kCtrlBytes && smem_bytes(kForward, kMaxE, 6, 32768) <= kSmemMost && smem_bytes(kDw, kMaxE, 5, 32768) <= kSmemMost, "shared memory layout");
 
 struct Grouped {
   const CUtensorMap* ends;         // dw: maps of dout and x that end with each group
@@ -58,6 +58,7 @@ struct Grouped {
   int width;             // columns of a tile at most
   int stages, chunk;     // chunk: stages added up in the tensor memory (kPromote)
   int fp16, out32, accumulate;
+  int wide_a, wide_b;    // dw: an operand's 128 columns are one copy (see make_rows_map)
   uint32_t idesc;        // but for the columns
 };
 
@@ -234,7 +235,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kAStage = kRows * 128;  // bytes of a K block of A
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  char* bufs = reinterpret_cast<char*>(smem + stage_budget(kMode));
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int stages = p.stages, half_width = p.width / 2;
+  const int b_stage = half_width * 128;  // bytes of a K block of B at most
+  const int stage_bytes = KS * (kAStage + b_stage);
+  char* bufs = reinterpret_cast<char*>(smem + stages * stage_bytes);
   uint8_t* ctrl = reinterpret_cast<uint8_t*>(bufs + kEpiWarps * buf_bytes(kMode));
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
   uint64_t* empty = full + kMaxStages;
@@ -243,11 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* start = reinterpret_cast<int*>(ctrl + kCtrlBytes);  // [E + 1] first sorted row of each group
-  int* pre = start + kMaxE + 4;                                       // [E + 1] tiles of the groups before it
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int stages = p.stages, half_width = p.width / 2;
-  const int b_stage = half_width * 128;  // bytes of a K block of B at most
-  const int stage_bytes = KS * (kAStage + b_stage);
+  int* pre = start + ((p.E + 4) & ~3);                     // [E + 1] tiles of the groups before it (not dw's)
   const int half = (int)cluster_rank() & 1;
   const uint16_t pair_mask = 3;
 
@@ -297,7 +298,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();  // the pair's barriers are set up, the tiles counted
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  depend_wait();
 
   const int units = kMode == kDw ? p.E * p.tiles_p * p.tiles_q : p.tiles_p * pre[p.E];
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
@@ -320,45 +320,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = first; u < units; u += step) {
         const Unit t = unit_of<kMode>(p, start, pre, u);
         const int arow = (t.p * 2 + half) * kRows;
-        const int boxes = kBMN ? half_width / 64 : 1;
         const int brow = kBMN ? t.q * p.width + half * half_width : t.row0 + half * (t.width / 2);
-        const uint32_t bytes = KS * (kAStage + (kBMN ? b_stage : t.width / 2 * 128));
+        const uint32_t bytes = KS * (kAStage + (kBMN ? b_stage : t.width / 2 * 128));  // a CTA's of a stage
         const CUtensorMap* mA = kMode == kDw ? p.ends + 2 * t.e : &tmA;
         const CUtensorMap* mB = kMode == kDw ? mA + 1 : &maps.b[t.width / 32 - 1];
         if (elect_one()) {
-          if (kMode == kDw && seen != t.e && t.stages) {
-            acquire_map(mA);
-            acquire_map(mB);
-          }
           int st = stage;
           uint32_t ph = phase;
-          for (int kb = 0; kb < t.stages; ++kb) {
-            if (!lane_wait(&empty[st], ph ^ 1)) {
-              failed = true;
-              break;
-            }
-            uint8_t* sA = smem + st * stage_bytes;
-            uint8_t* sB = sA + KS * kAStage;
-            const uint32_t bar = full0 + st * 8;
-            if (half == 0) mbar_arrive_expect_tx(&full[st], 2 * bytes);
+          auto load_a = [&](int kb, int at) {  // K blocks of the stage kb into the ring's stage `at`
+            uint8_t* sA = smem + at * stage_bytes;
+            const uint32_t bar = full0 + at * 8;
+            if (half == 0) mbar_arrive_expect_tx(&full[at], 2 * bytes);
             const int k = kMode == kDw ? t.row0 + kb * BK : kb * KS * BK;
             if constexpr (kMode == kForward) {
 #pragma unroll
               for (int i = 0; i < KS; ++i)
                 tma_load_pair_3d(sA + i * kAStage, mA, k + i * BK, arow, (int)t.e, bar, pol);
-            } else if constexpr (kMode == kDx) {
-#pragma unroll
-              for (int g = 0; g < 2; ++g) tma_load_pair_3d(sA + g * KS * 8192, mA, arow + g * 64, k, (int)t.e, bar, pol);
+            } else if (kMode == kDw && p.wide_a) {
+              tma_load_pair_3d(sA, mA, 0, k, arow / 64, bar, pol);
             } else {
 #pragma unroll
-              for (int g = 0; g < 2; ++g) tma_load<2>(sA + g * 8192, mA, arow + g * 64, k, bar, pol);
-              for (int g = 0; g < boxes; ++g) tma_load<2>(sB + g * 8192, mB, brow + g * 64, k, bar, pol);
+              for (int g = 0; g < 2; ++g) {
+                if (kMode == kDx)
+                  tma_load_pair_3d(sA + g * KS * 8192, mA, arow + g * 64, k, (int)t.e, bar, pol);
+                else
+                  tma_load<2>(sA + g * 8192, mA, arow + g * 64, k, bar, pol);
+              }
             }
+          };
+          auto load_b = [&](int kb, int at) {
+            uint8_t* sB = smem + at * stage_bytes + KS * kAStage;
+            const uint32_t bar = full0 + at * 8;
+            const int k = kMode == kDw ? t.row0 + kb * BK : kb * KS * BK;
             if constexpr (!kBMN) {
 #pragma unroll
-              for (int i = 0; i < KS; ++i)
-                tma_load<2>(sB + i * b_stage, mB, k + i * BK, brow, bar, pol);
+              for (int i = 0; i < KS; ++i) tma_load<2>(sB + i * b_stage, mB, k + i * BK, brow, bar, pol);
+            } else if (p.wide_b) {
+              tma_load_pair_3d(sB, mB, 0, k, brow / 64, bar, pol);
+            } else {
+              for (int g = 0; g < half_width / 64; ++g) tma_load<2>(sB + g * 8192, mB, brow + g * 64, k, bar, pol);
             }
+          };
+          int early = 0;
+          if (u == first) {
+            // The weights do not wait for what came before in this call (rows put in order): the first stages'
+            // are on their way meanwhile.
+            if (kMode != kDw)
+              for (; early < min(t.stages, stages); ++early) load_a(early, early);
+            depend_wait();
+          }
+          if (kMode == kDw && seen != t.e && t.stages) {
+            acquire_map(mA);
+            acquire_map(mB);
+          }
+          for (int kb = 0; kb < t.stages; ++kb) {
+            if (!lane_wait(&empty[st], ph ^ 1)) {
+              failed = true;
+              break;
+            }
+            if (kb >= early) load_a(kb, st);
+            load_b(kb, st);
             if (++st == stages) {
               st = 0;
               ph ^= 1;
@@ -557,6 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (kMode == kDw && lane == 0) tma_store_wait();
   }
 
+  // (whoever had nothing to wait for: what comes after this kernel comes after the one before it, too)
+  depend_wait();
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -634,9 +657,27 @@ bool make_map(CUtensorMap* m, const void* base, int dtype, long long inner, long
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of dout or x [S, cols] as dw takes them, in boxes of 64 rows x 64 columns.  wide: columns in 64s, as [cols / 64][64],
+// so that a box takes two neighbouring groups (one behind the other in shared memory) and the two operands of a K block
+// are two copies, whose issue bounds the K loop, and not four: 4096 x 14336 over groups of 1024 rows 698 -> 640 us.
+// (dx's weights the same way: no difference.)
+bool wide(long long cols) { return cols % 64 == 0 && cols > 128; }
+bool make_rows_map(CUtensorMap* m, const void* base, int dtype, long long cols, long long S) {
+  if (!wide(cols)) return make_map(m, base, dtype, cols, S, 0, BK);
+  auto enc = get_encode();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {64, (cuuint64_t)S, (cuuint64_t)cols / 64};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, 128};
+  cuuint32_t boxes[3] = {64, BK, 2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, dtype == MOE_DT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<void*>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <Mode kMode, bool kPromote, int KS>
 cudaError_t launch(const CUtensorMap& ma, const Maps& mb, const CUtensorMap& mo, const Grouped& g, long long units,
-                   bool overlap, cudaStream_t s) {
+                   int smem, bool overlap, cudaStream_t s) {
   auto kern = grouped_gemm_kernel<kMode, kPromote, KS>;
   if (kPromote) {
     // The epilogue's warps take registers that the first warpgroup gives back (setmaxnreg): a build with another
@@ -650,11 +691,11 @@ cudaError_t launch(const CUtensorMap& ma, const Maps& mb, const CUtensorMap& mo,
       checked.store(true, std::memory_order_relaxed);
     }
   }
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kMode));
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes(kMode);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -670,10 +711,10 @@ cudaError_t launch(const CUtensorMap& ma, const Maps& mb, const CUtensorMap& mo,
 }
 template <Mode kMode, bool kPromote>
 cudaError_t launch(int ks, const CUtensorMap& ma, const Maps& mb, const CUtensorMap& mo, const Grouped& g,
-                   long long units, bool overlap, cudaStream_t s) {
+                   long long units, int smem, bool overlap, cudaStream_t s) {
   if constexpr (kMode != kDw)
-    if (ks == 2) return launch<kMode, kPromote, 2>(ma, mb, mo, g, units, overlap, s);
-  return launch<kMode, kPromote, 1>(ma, mb, mo, g, units, overlap, s);
+    if (ks == 2) return launch<kMode, kPromote, 2>(ma, mb, mo, g, units, smem, overlap, s);
+  return launch<kMode, kPromote, 1>(ma, mb, mo, g, units, smem, overlap, s);
 }
 
 // One product.  a: the weights [E, N, K] (dw: dout, sorted), b: sorted rows.
@@ -692,6 +733,8 @@ moe_status_t run(const void* a, const void* b, const int32_t* offsets, const int
   g.fp16 = fp16;
   g.out32 = out32;
   g.accumulate = accumulate;
+  g.wide_a = kMode == kDw && wide(N);
+  g.wide_b = kMode == kDw && wide(K);
   const int contraction = kMode == kForward ? K : kMode == kDx ? N : S;
   const long long mean = cdiv(S, E);
   int ks = 1;
@@ -705,7 +748,9 @@ moe_status_t run(const void* a, const void* b, const int32_t* offsets, const int
   g.tiles_q = cdiv(g.Q, g.width);
   g.KB = cdiv(contraction, BK * ks);
   const int stage = ks * (kRows + g.width / 2) * 128;
-  g.stages = stage_budget(kMode) / stage < kMaxStages ? stage_budget(kMode) / stage : kMaxStages;
+  g.stages = (kSmemMost - smem_bytes(kMode, E, 0, 0)) / stage;
+  if (g.stages > kMaxStages) g.stages = kMaxStages;
+  const int smem = smem_bytes(kMode, E, g.stages, stage);
   const int run = out32 ? kRunFP32 : fp16 ? kRunFP16 : kRunBF16;
   // (the general epilogue of a gradient keeps its sums in fp32 registers)
   const bool promote = cdiv(contraction, BK) > run || out32 || accumulate;
@@ -728,8 +773,8 @@ moe_status_t run(const void* a, const void* b, const int32_t* offsets, const int
     mo = ma;  // (not used)
   }
   if (!ok) return MOE_ERR_CUDA;
-  const cudaError_t err = promote ? launch<kMode, true>(ks, ma, mb, mo, g, units, overlap, s)
-                                  : launch<kMode, false>(ks, ma, mb, mo, g, units, overlap, s);
+  const cudaError_t err = promote ? launch<kMode, true>(ks, ma, mb, mo, g, units, smem, overlap, s)
+                                  : launch<kMode, false>(ks, ma, mb, mo, g, units, smem, overlap, s);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -846,7 +891,7 @@ extern "C" moe_status_t moe_grouped_linear_backward(const void* dout, int dout_r
     next += rows_bytes(S, K, x_rows);
     ends = reinterpret_cast<CUtensorMap*>((reinterpret_cast<uintptr_t>(next) + 127) & ~uintptr_t(127));
     CUtensorMap md, mx;
-    if (!make_map(&md, dout_rows == MOE_ROWS_SORTED ? dout : ws, type, N, S, 0, BK) || !make_map(&mx, xs, type, K, S, 0, BK))
+    if (!make_rows_map(&md, dout_rows == MOE_ROWS_SORTED ? dout : ws, type, N, S) || !make_rows_map(&mx, xs, type, K, S))
       return MOE_ERR_CUDA;
     group_maps_kernel<<<2 * E, 32, 0, s>>>(md, mx, expert_offsets, S, ends);
     overlap = true;
