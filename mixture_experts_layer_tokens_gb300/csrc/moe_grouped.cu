@@ -45,11 +45,14 @@ constexpr int smem_bytes(Mode m, int E, int stages, int stage) {
 constexpr int kRunFP32 = 8, kRunFP16 = 128, kRunBF16 = 256;
 constexpr int kLaunchRegs = 168, kLowRegs = 40, kHighRegs = 232;
 static_assert(128 * kLowRegs + 256 * kHighRegs == kThreads * kLaunchRegs, "register split must balance");
-static_assert((2 * kMaxStages + 5) * 8 + 4 <= kCtrlBytes && smem_bytes(kForward, kMaxE, 6, 32768) <= kSmemMost && smem_bytes(kDw, kMaxE, 5, 32768) <= kSmemMost, "shared memory layout");
+static_assert((2 * kMaxStages + 5) * 8 + 4 <= 256 && 256 + 32 * 4 <= kCtrlBytes && smem_bytes(kForward, kMaxE, 6, 32768) <= kSmemMost && smem_bytes(kDw, kMaxE, 5, 32768) <= kSmemMost, "shared memory layout");
 
 struct Grouped {
   const CUtensorMap* ends;         // dw: maps of dout and x that end with each group
-  const int32_t *offsets, *slots;  // slots: rows of out are the slots of the sorted rows (NULL: the sorted rows)
+  const int32_t *offsets, *slots;  // slots: NULL where no order needs them
+  int to_slots;                    // rows of out are the slots of the sorted rows (else the sorted rows)
+  const int32_t* from;             // forward, small groups: B's rows are those of slots / from_div, fetched one by one
+  int from_div;
   void* out;
   int S, E;
   int P, Q;              // rows of A's tensor (forward N, dx K, dw N); dw: columns of B's (K)
@@ -124,6 +127,15 @@ __device__ __forceinline__ void tma_load_pair_3d(void* smem_dst, const CUtensorM
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(smem_dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+      : "memory");
+}
+// Four rows of a tensor (a box is one row of 64 elements).
+__device__ __forceinline__ void tma_gather4_pair(void* smem_dst, const CUtensorMap* map, int x, int4 rows, uint32_t bar,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar), "l"(policy)
       : "memory");
 }
 // A tensor map in global memory that an earlier kernel wrote.
@@ -247,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* tempty = tfull + 2;          // [2] accumulator read
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* rows4 = reinterpret_cast<int*>(ctrl + 256);  // B's rows of the producer's tile (p.from)
   int* start = reinterpret_cast<int*>(ctrl + kCtrlBytes);  // [E + 1] first sorted row of each group
   int* pre = start + ((p.E + 4) & ~3);                     // [E + 1] tiles of the groups before it (not dw's)
   const int half = (int)cluster_rank() & 1;
@@ -258,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tensormap(&tmOut);
     } else {
       prefetch_tensormap(&tmA);
-      for (int i = 0; i < p.width / 32; ++i) prefetch_tensormap(&maps.b[i]);
+      for (int i = 0; i < (p.from ? 1 : p.width / 32); ++i) prefetch_tensormap(&maps.b[i]);
     }
   }
   // (offsets out of order or range would be the caller's mistake; no row outside [0, S) is touched)
@@ -321,16 +334,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Unit t = unit_of<kMode>(p, start, pre, u);
         const int arow = (t.p * 2 + half) * kRows;
         const int brow = kBMN ? t.q * p.width + half * half_width : t.row0 + half * (t.width / 2);
-        const uint32_t bytes = KS * (kAStage + (kBMN ? b_stage : t.width / 2 * 128));  // a CTA's of a stage
+        uint32_t bytes = 2 * KS * (kAStage + (kBMN ? b_stage : t.width / 2 * 128));  // both CTAs' of a stage
+        int fours = 0;  // p.from: this CTA's rows, by four
         const CUtensorMap* mA = kMode == kDw ? p.ends + 2 * t.e : &tmA;
-        const CUtensorMap* mB = kMode == kDw ? mA + 1 : &maps.b[t.width / 32 - 1];
+        const CUtensorMap* mB = kMode == kDw ? mA + 1 : &maps.b[kMode == kForward && p.from ? 0 : t.width / 32 - 1];
+        if (kMode == kForward && p.from) {
+          // (the columns of the tile that have no row keep what the stage held; nobody looks at their sums)
+          const int n = t.width / 2, have = max(0, min(t.rows - half * n, n));
+          fours = (have + 3) / 4;
+          bytes = KS * (2 * kAStage + ((min(t.rows, n) + 3) / 4 + (max(0, t.rows - n) + 3) / 4) * 512);
+          __syncwarp();
+          int slot = have ? __ldg(p.from + t.row0 + half * n + min(lane, have - 1)) : 0;
+          if (slot < 0 || slot >= p.S) {
+            record_status((int)MOE_ERR_INVALID_ARG);
+            slot = 0;
+          }
+          rows4[lane] = slot / p.from_div;
+          __syncwarp();
+        }
         if (elect_one()) {
           int st = stage;
           uint32_t ph = phase;
           auto load_a = [&](int kb, int at) {  // K blocks of the stage kb into the ring's stage `at`
             uint8_t* sA = smem + at * stage_bytes;
             const uint32_t bar = full0 + at * 8;
-            if (half == 0) mbar_arrive_expect_tx(&full[at], 2 * bytes);
+            if (half == 0) mbar_arrive_expect_tx(&full[at], bytes);
             const int k = kMode == kDw ? t.row0 + kb * BK : kb * KS * BK;
             if constexpr (kMode == kForward) {
 #pragma unroll
@@ -352,7 +380,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* sB = smem + at * stage_bytes + KS * kAStage;
             const uint32_t bar = full0 + at * 8;
             const int k = kMode == kDw ? t.row0 + kb * BK : kb * KS * BK;
-            if constexpr (!kBMN) {
+            if (kMode == kForward && p.from) {
+              for (int g = 0; g < fours; ++g) {
+                const int4 rows = reinterpret_cast<const int4*>(rows4)[g];
+#pragma unroll
+                for (int i = 0; i < KS; ++i) tma_gather4_pair(sB + i * b_stage + g * 512, mB, k + i * BK, rows, bar, pol);
+              }
+            } else if constexpr (!kBMN) {
 #pragma unroll
               for (int i = 0; i < KS; ++i) tma_load<2>(sB + i * b_stage, mB, k + i * BK, brow, bar, pol);
             } else if (p.wide_b) {
@@ -490,11 +524,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = at(c) + lane;
           to[c] = row < cols ? t.row0 + row : -1;
           if (p.slots && to[c] >= 0) {
-            to[c] = __ldg(p.slots + to[c]);
-            if (to[c] < 0 || to[c] >= p.S) {
-              record_status((int)MOE_ERR_INVALID_ARG);
-              to[c] = -1;
-            }
+            const int slot = __ldg(p.slots + to[c]);
+            const bool bad = slot < 0 || slot >= p.S;
+            if (bad) record_status((int)MOE_ERR_INVALID_ARG);
+            to[c] = bad ? -1 : p.to_slots ? slot : to[c];
           }
         }
       }
@@ -717,14 +750,23 @@ cudaError_t launch(int ks, const CUtensorMap& ma, const Maps& mb, const CUtensor
   return launch<kMode, kPromote, 1>(ma, mb, mo, g, units, smem, overlap, s);
 }
 
+// Columns of a tile at most: narrow ones leave room for more stages where the groups are small.
+int widest(int S, int E) {
+  const int mean = cdiv(S, E);
+  return S <= 32 ? 32 : mean <= 24 ? 64 : mean <= 48 ? 128 : 256;
+}
+
 // One product.  a: the weights [E, N, K] (dw: dout, sorted), b: sorted rows.
 template <Mode kMode>
-moe_status_t run(const void* a, const void* b, const int32_t* offsets, const int32_t* slots, int S, int E, int N, int K,
-                 int fp16, void* out, int out32, int accumulate, const CUtensorMap* ends, bool overlap, cudaStream_t s) {
+moe_status_t run(const void* a, const void* b, const int32_t* offsets, const int32_t* slots, int to_slots, const int32_t* from,
+                 int from_div, int S, int E, int N, int K, int fp16, void* out, int out32, int accumulate, const CUtensorMap* ends, bool overlap, cudaStream_t s) {
   Grouped g = {};
   g.ends = ends;
   g.offsets = offsets;
   g.slots = slots;
+  g.to_slots = to_slots;
+  g.from = from;
+  g.from_div = from_div;
   g.out = out;
   g.S = S;
   g.E = E;
@@ -736,12 +778,11 @@ moe_status_t run(const void* a, const void* b, const int32_t* offsets, const int
   g.wide_a = kMode == kDw && wide(N);
   g.wide_b = kMode == kDw && wide(K);
   const int contraction = kMode == kForward ? K : kMode == kDx ? N : S;
-  const long long mean = cdiv(S, E);
   int ks = 1;
   if (kMode == kDw) {
     g.width = K <= 128 ? 128 : 256;
   } else {
-    g.width = S <= 32 ? 32 : mean <= 24 ? 64 : mean <= 48 ? 128 : 256;
+    g.width = widest(S, E);
     ks = g.width <= 128 ? 2 : 1;
   }
   g.tiles_p = cdiv(g.P, 2 * kRows);
@@ -768,7 +809,8 @@ moe_status_t run(const void* a, const void* b, const int32_t* offsets, const int
     ma = mo;  // (not used)
   } else {
     ok = make_map(&ma, a, type, K, N, E, kMode == kForward ? kRows : BK * ks);
-    for (int i = 0; i < g.width / 32; ++i)
+    if (from) ok = ok && make_map(&mb.b[0], b, type, K, S / from_div, 0, 1);
+    for (int i = 0; !from && i < g.width / 32; ++i)
       ok = ok && make_map(&mb.b[i], b, type, kMode == kForward ? K : N, S, 0, 16 * (i + 1));
     mo = ma;  // (not used)
   }
@@ -841,12 +883,16 @@ extern "C" moe_status_t moe_grouped_linear(const void* x, int x_rows, const void
   const size_t need = rows_bytes(S, K, x_rows);
   if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // Small groups fetch x's rows by four as they are; putting the rows in order first costs a launch.
+  const bool direct = x_rows != MOE_ROWS_SORTED && widest(S, E) <= 64;
+  const int div = x_rows == MOE_ROWS_TOKEN ? top_k : 1;
   bool overlap = false;
-  const void* xs = sorted_rows(x, x_rows, expert_offsets, sorted_slot, S, E, K, top_k, ws, overlap, s);
+  const void* xs = direct ? x : sorted_rows(x, x_rows, expert_offsets, sorted_slot, S, E, K, top_k, ws, overlap, s);
   if (!xs) return MOE_ERR_CUDA;
+  const bool slots = x_rows != MOE_ROWS_SORTED || out_rows == MOE_ROWS_SLOT;
   const moe_status_t got =
-      run<kForward>(w, xs, expert_offsets, out_rows == MOE_ROWS_SLOT ? sorted_slot : nullptr, S, E, N, K,
-                    dtype == MOE_DT_FP16, out, 0, 0, nullptr, overlap, s);
+      run<kForward>(w, xs, expert_offsets, slots ? sorted_slot : nullptr, out_rows == MOE_ROWS_SLOT,
+                    direct ? sorted_slot : nullptr, div, S, E, N, K, dtype == MOE_DT_FP16, out, 0, 0, nullptr, overlap, s);
   return got == MOE_OK ? launch_status() : got;
 }
 
@@ -900,13 +946,14 @@ extern "C" moe_status_t moe_grouped_linear_backward(const void* dout, int dout_r
   if (dw) xs = sorted_rows(x, x_rows, expert_offsets, sorted_slot, S, E, K, top_k, const_cast<void*>(xs), overlap, s);
   if (!d || (dw && !xs)) return MOE_ERR_CUDA;
   if (dx) {
-    st = run<kDx>(w, d, expert_offsets, dx_rows == MOE_ROWS_SLOT ? sorted_slot : nullptr, S, E, N, K, fp16, dx, 0, 0,
-                  nullptr, overlap, s);
+    const bool slots = dout_rows != MOE_ROWS_SORTED || dx_rows == MOE_ROWS_SLOT;
+    st = run<kDx>(w, d, expert_offsets, slots ? sorted_slot : nullptr, dx_rows == MOE_ROWS_SLOT, nullptr, 1, S, E, N, K, fp16,
+                  dx, 0, 0, nullptr, overlap, s);
     if (st != MOE_OK) return st;
     overlap = true;
   }
   if (dw) {
-    st = run<kDw>(d, xs, expert_offsets, nullptr, S, E, N, K, fp16, dw, out32, accumulate != 0, ends, overlap, s);
+    st = run<kDw>(d, xs, expert_offsets, nullptr, 0, nullptr, 1, S, E, N, K, fp16, dw, out32, accumulate != 0, ends, overlap, s);
     if (st != MOE_OK) return st;
   }
   return launch_status();

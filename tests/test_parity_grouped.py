@@ -190,18 +190,28 @@ def test_not_a_number_stays(cuda_dev):
     assert not torch.isfinite(dw[3]).all()
 
 
-def test_slots_out_of_range_are_left_out(cuda_dev):
-    """A slot outside [0, S) is recorded, its row read as zeros and not written; the others are as they were."""
-    p = Problem([40, 25], 136, 72, 1, BF, "slot", "slot", "slot")
-    good, bad = p.slots.clone(), [3, 50]
+@pytest.mark.parametrize("rows", ["sorted", "slot"])
+@pytest.mark.parametrize("counts", [[40, 25], [5, 7, 0, 1], [200, 300]])
+def test_slots_out_of_range_are_left_out(cuda_dev, counts, rows):
+    """A slot outside [0, S) is recorded, its rows are not written and have no share in dw; the others are as they were."""
+    p = Problem(counts, 136, 72, 1, BF, "slot", rows, "slot")
+    good, bad = p.slots.clone(), [3, sum(counts) - 1]
     ref = p.forward(cuda_dev).clone()
+    dref, _ = (t.clone() for t in p.backward(cuda_dev))
     p.slots[bad[0]], p.slots[bad[1]] = -1, p.S
     out = p.forward(cuda_dev)
     assert moe.moe_device_status() == moe.MOE_ERR_INVALID_ARG and moe.moe_device_status() == moe.MOE_OK
-    left = good[bad].long().to(cuda_dev)
+    dx, dw = p.backward(cuda_dev)
+    assert moe.moe_device_status() == moe.MOE_ERR_INVALID_ARG
+    left = good[bad].long().to(cuda_dev) if rows == "slot" else torch.tensor(bad, device=cuda_dev)
     keep = torch.ones(p.S, dtype=torch.bool, device=cuda_dev)
     keep[left] = False
     assert torch.equal(out[keep], ref[keep]) and bool((out[left] == 7).all())
+    assert torch.equal(dx[keep], dref[keep]) and bool((dx[left] == 7).all())
+    p.slots = good
+    p.dout[good[bad].long()] = 0
+    _, want = p.backward(cuda_dev)
+    assert torch.equal(dw, want) and moe.moe_device_status() == moe.MOE_OK
 
 
 def test_parts_of_the_gradients(cuda_dev):
