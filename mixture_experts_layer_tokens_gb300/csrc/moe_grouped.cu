@@ -58,7 +58,7 @@ struct Grouped {
   int P, Q;              // rows of A's tensor (forward N, dx K, dw N); dw: columns of B's (K)
   int KB;                // stages of the contraction (dw: by the group's rows)
   int tiles_p, tiles_q;  // of 256 rows of A; dw: of `width` columns
-  int width;             // columns of a tile at most
+  int width, log2_width; // columns of a tile at most (a power of two)
   int stages, chunk;     // chunk: stages added up in the tensor memory (kPromote)
   int fp16, out32, accumulate;
   int wide_a, wide_b;    // dw: an operand's 128 columns are one copy (see make_rows_map)
@@ -274,8 +274,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < (p.from ? 1 : p.width / 32); ++i) prefetch_tensormap(&maps.b[i]);
     }
   }
-  // (offsets out of order or range would be the caller's mistake; no row outside [0, S) is touched)
-  for (int e = threadIdx.x; e <= p.E; e += kThreads) start[e] = min(max(__ldg(p.offsets + e), 0), p.S);
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
@@ -288,27 +286,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain, 1);
     fence_mbar_init();
   }
+  // The pair meets twice: here, with its barriers set up, and (half a microsecond later, under the rest) below.
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   if (warp == 1) tmem_take<2>(tmem_slot);
-  tc_fence_before();
-  __syncthreads();
-  if (kMode != kDw && warp == 3) {  // tiles of the groups
+  if (warp == 3) {  // the groups' rows and tiles
     int before = 0;
-    for (int b = 0; b < p.E; b += 32) {
-      const int e = b + lane;
-      int n = e < p.E ? (max(0, start[e + 1] - start[e]) + p.width - 1) / p.width : 0;
-      const int own = n;
+    for (int b = 0; b < p.E; b += 128) {
+      int first[4], end[4];
+      // (offsets out of order or range would be the caller's mistake; no row outside [0, S) is touched)
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, n, off);
-        if (lane >= off) n += v;
+      for (int j = 0; j < 4; ++j) {
+        const int e = b + j * 32 + lane;
+        first[j] = e < p.E ? min(max(__ldg(p.offsets + e), 0), p.S) : 0;
+        end[j] = e < p.E ? min(max(__ldg(p.offsets + e + 1), 0), p.S) : 0;
       }
-      if (e < p.E) pre[e] = before + n - own;
-      before += __shfl_sync(0xffffffffu, n, 31);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int e = b + j * 32 + lane;
+        if (b + j * 32 >= p.E) break;
+        int n = (max(0, end[j] - first[j]) + p.width - 1) >> p.log2_width;
+        if (e < p.E) start[e] = first[j];
+        if (e == p.E - 1) start[p.E] = end[j];
+        if (kMode == kDw) continue;
+        const int own = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, n, off);
+          if (lane >= off) n += v;
+        }
+        if (e < p.E) pre[e] = before + n - own;
+        before += __shfl_sync(0xffffffffu, n, 31);
+      }
     }
-    if (lane == 0) pre[p.E] = before;
+    if (kMode != kDw && lane == 0) pre[p.E] = before;
     __syncwarp();
   }
-  cluster_sync();  // the pair's barriers are set up, the tiles counted
+  tc_fence_before();
+  __syncthreads();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -785,6 +800,7 @@ moe_status_t run(const void* a, const void* b, const int32_t* offsets, const int
     g.width = widest(S, E);
     ks = g.width <= 128 ? 2 : 1;
   }
+  while ((1 << g.log2_width) < g.width) ++g.log2_width;
   g.tiles_p = cdiv(g.P, 2 * kRows);
   g.tiles_q = cdiv(g.Q, g.width);
   g.KB = cdiv(contraction, BK * ks);
