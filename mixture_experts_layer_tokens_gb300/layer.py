@@ -1,6 +1,7 @@
 """One fused-MoE layer step composed from the C-ABI calls, with every buffer
 allocated once up front (PyTorch allocates, the library computes); the gradients of the
-finalize alone are made by each MoELayer.router_backward call.
+finalize alone are made by each MoELayer.router_backward call, and the buffers of the experts'
+gradients by the first MoELayer.experts_backward call.
 
 Step: moe_route -> moe_align -> moe_prepare -> moe_experts [-> shared expert via
   moe_experts with one expert and the identity permutation] -> moe_finalize, on the
@@ -14,6 +15,10 @@ late because the shared expert still holds their SMs take fewer units).
 A layer with a MoERouter makes its logits itself (moe_linear on the hidden states, then
 moe_route_grouped in place of moe_route), and its router can be trained beside fixed
 experts: moe_finalize_backward, moe_route_grouped_backward, moe_linear_backward.
+A layer with input_norm normalises what it is given first (moe_rmsnorm, with the residual's
+addition), and an fp8 layer's quantised rows come from the same launch in place of moe_prepare.
+The experts of a bf16 layer are trained by MoEExperts: moe_grouped_linear and moe_activation
+with their gradients.
 NVFP4 layers use moe_prepare_nvfp4 and moe_experts_nvfp4 (the shared expert
 stays bf16).  Single-launch layers run the whole step as one moe_layer_fused launch.
 
@@ -80,13 +85,70 @@ class MoERouter:
         return dgate_w, dgate_bias, da1, self._dlogits
 
 
+class MoEExperts:
+    """The experts as separate calls that keep what lies between their products, and their gradients: [g | u] =
+    x w13^T (``moe_grouped_linear``), h = act(g) u (``moe_activation``), y = h w2^T, and back; every buffer allocated
+    once.
+
+    w13 [E, 2I, H] (the *_no_mul activations [E, I, H]) and w2 [E, H, I] bf16 or fp16; T tokens of top_k experts each;
+    dw_dtype: the weights' gradients', fp32 or (None) the weights' type."""
+
+    def __init__(self, w13: torch.Tensor, w2: torch.Tensor, T: int, top_k: int, activation: str = "silu",
+                 dw_dtype: Optional[torch.dtype] = None, stream=None):
+        (E, rows13, H), I, S = w13.shape, w2.shape[2], T * top_k
+        if tuple(w2.shape) != (E, H, I) or rows13 != (I if activation.endswith("_no_mul") else 2 * I):
+            raise ValueError("w13 and w2: expected [E, 2I, H] (*_no_mul: [E, I, H]) and [E, H, I]")
+        self.w13, self.w2, self.T, self.top_k, self.activation = w13, w2, T, top_k, activation
+        dt, dev = w13.dtype, w13.device
+        empty = lambda shape, dtype=dt: moe._empty(shape, dtype, dev, stream)  # noqa: E731
+        self.gu, self.h = empty((S, rows13)), empty((S, I))
+        self.y = empty((S, H))
+        self.dh, self.drows, self.da1 = empty((S, I)), empty((S, H)), empty((T, H))
+        self.dw13, self.dw2 = empty((E, rows13, H), dw_dtype or dt), empty((E, H, I), dw_dtype or dt)
+        self.ws = empty((max(moe.grouped_linear_workspace_size(S, E, rows13, H, "token"),
+                             moe.grouped_linear_backward_workspace_size(S, E, H, I, "slot", "sorted"),
+                             moe.grouped_linear_backward_workspace_size(S, E, rows13, H, "sorted", "token"), 16),),
+                        torch.uint8)
+
+    def hidden(self, a1: torch.Tensor, al: "moe.Alignment", stream=None) -> torch.Tensor:
+        """h [S, I] in sorted order, [g | u] kept beside it: the forward pass up to the second product."""
+        moe.moe_grouped_linear(a1, self.w13, al.expert_offsets, al.sorted_slot, self.top_k, x_rows="token", out=self.gu,
+                               ws=self.ws, stream=stream)
+        return moe.moe_activation(self.gu, self.activation, h=self.h, stream=stream)
+
+    def forward(self, a1: torch.Tensor, al: "moe.Alignment", stream=None) -> torch.Tensor:
+        """y [T * top_k, H], the unweighted rows by slots, of the hidden states a1 [T, H]."""
+        self.hidden(a1, al, stream)
+        return moe.moe_grouped_linear(self.h, self.w2, al.expert_offsets, al.sorted_slot, self.top_k, out_rows="slot",
+                                      out=self.y, ws=self.ws, stream=stream)
+
+    def backward(self, dy: torch.Tensor, a1: torch.Tensor, al: "moe.Alignment", accumulate: bool = False, stream=None):
+        """Gradients of the last forward (or hidden) call, once for each such call, given dy [T * top_k, H] by slots: (dw13, dw2, da1).
+        accumulate: dw13 and dw2 are added to.  da1 [T, H] is what reaches the hidden states through these experts
+        alone.  Buffers of this object, written again (or added to) by the next call; a bf16 da1 is summed by
+        moe_finalize, an fp16 one is not made (None)."""
+        kw = dict(accumulate=accumulate, ws=self.ws, stream=stream)
+        moe.moe_grouped_linear_backward(dy, self.h, self.w2, al.expert_offsets, al.sorted_slot, self.top_k,
+                                        dout_rows="slot", dx=self.dh, dw=self.dw2, **kw)
+        # (dgu takes the place of [g | u]'s copy: each value is read before it is written)
+        moe.moe_activation_backward(self.dh, self.gu, self.activation, dgu=self.gu, stream=stream)
+        moe.moe_grouped_linear_backward(self.gu, a1, self.w13, al.expert_offsets, al.sorted_slot, self.top_k,
+                                        x_rows="token", dx_rows="slot", dx=self.drows, dw=self.dw13, **kw)
+        if self.drows.dtype is not torch.bfloat16:
+            return self.dw13, self.dw2, None
+        moe.moe_finalize(self.drows, None, self.top_k, True, output=self.da1, stream=stream)
+        return self.dw13, self.dw2, self.da1
+
+
 class MoELayer:
     """router: a MoERouter of the same tokens, experts and top_k that takes the place of moe_route (the
     forward call's logits are then not read and may be None).  keep_residual: forward also writes the sum before
-    the RMSNorm to residual_out, which router_backward needs."""
+    the RMSNorm to residual_out, which router_backward needs.  input_norm: weight [H] bf16 of an RMSNorm (eps
+    1e-6) in front of the layer."""
 
     def __init__(self, inp: LayerInputs, stream: Optional[torch.cuda.Stream] = None,
-                 router: Optional[MoERouter] = None, keep_residual: bool = False):
+                 router: Optional[MoERouter] = None, keep_residual: bool = False,
+                 input_norm: Optional[torch.Tensor] = None):
         cfg = self.cfg = inp.cfg
         assert not cfg.finalize_only
         self.router = router
@@ -95,9 +157,17 @@ class MoELayer:
             raise ValueError("router: expected one of the layer's tokens, experts and top_k, and separate launches")
         if keep_residual and cfg.single_launch:
             raise ValueError("keep_residual: expected separate launches")
+        if input_norm is not None and cfg.single_launch:
+            raise ValueError("input_norm: expected separate launches")
         self.inp = inp
         dev = inp.logits.device
         T, H, I, E, k = cfg.T, cfg.H, cfg.I, cfg.E, cfg.top_k
+        self.input_norm, self.trainer = input_norm, None
+        if input_norm is not None:
+            self.a1 = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+            self.stream_sum = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        # the norm quantises for the experts, in place of moe_prepare
+        self.norm_quant = input_norm is not None and cfg.quant in ("fp8", "fp8_token") and not cfg.weight_on_input
         self.residual_out = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if keep_residual else None
         self.scoring = moe.MOE_SCORING_SIGMOID if cfg.scoring == "sigmoid" else moe.MOE_SCORING_SOFTMAX_RENORM
         self.topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
@@ -155,8 +225,14 @@ class MoELayer:
                  moe.experts_problem(a_dummy, None, inp.shared_w13, None, inp.shared_w2, None, self.al_shared,
                                      self.shared, identity=True)], H, "bf16"), 16), dtype=torch.uint8, device=dev)
 
-    def forward(self, logits: Optional[torch.Tensor], a1: torch.Tensor, stream=None) -> torch.Tensor:
+    def forward(self, logits: Optional[torch.Tensor], a1: torch.Tensor, stream=None,
+                residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """a1 [T, H] bf16: the hidden states; with input_norm what the norm takes.  residual (input_norm alone): the
+        residual stream [T, H], added to a1 before the norm; the sum is what the finalize adds in place of the
+        inputs' residual."""
         cfg, inp = self.cfg, self.inp
+        if residual is not None and self.input_norm is None:
+            raise ValueError("residual: expected with input_norm alone")
         if self.single:
             return moe.moe_layer_fused(
                 logits, a1, inp.w13, inp.w2, cfg.top_k, self.scoring, cfg.weight_on_input,
@@ -165,6 +241,12 @@ class MoELayer:
                 rms_weight=inp.rms_weight, eps=1e-6, topk_ids=self.topk_ids, topk_weights=self.topk_weights,
                 output=self.out, ws=self.ws_fused, stream=stream)
         main = stream if stream is not None else torch.cuda.current_stream()
+        if self.input_norm is not None:
+            moe.moe_rmsnorm(a1, self.input_norm, residual=residual, eps=1e-6, quant=cfg.quant if self.norm_quant else None,
+                            out=self.a1, residual_out=None if residual is None else self.stream_sum,
+                            q=self.a1q if self.norm_quant else None,
+                            q_scale=self.a1q_scale if self.norm_quant else None, stream=stream)
+            a1 = self.a1
         if self.shared_side:
             self.ev_fork.record(main)
             self.side.wait_event(self.ev_fork)
@@ -178,6 +260,8 @@ class MoELayer:
         moe.moe_align(self.topk_ids, cfg.E, out=self.al, stream=stream)
         if self.passthrough:
             a1q, a1q_scale = a1, None
+        elif self.norm_quant:
+            a1q, a1q_scale = self.a1q, self.a1q_scale
         elif self.nvfp4:
             a1q, a1q_scale = moe.moe_prepare_nvfp4(a1, self.topk_weights, cfg.top_k, cfg.weight_on_input, self.g_a,
                                                    self.a1q, self.a1q_scale, stream=stream)
@@ -188,13 +272,14 @@ class MoELayer:
         if self.shared_side:
             main.wait_event(self.ev_join)
         moe.moe_finalize(self.y, self.topk_weights, cfg.top_k, cfg.weight_on_input, shared=shared,
-                         residual=inp.residual, rms_weight=inp.rms_weight, output=self.out,
-                         residual_out=self.residual_out, stream=stream)
+                         residual=inp.residual if residual is None else self.stream_sum, rms_weight=inp.rms_weight,
+                         output=self.out, residual_out=self.residual_out, stream=stream)
         return self.out
 
     def router_backward(self, dout: torch.Tensor, a1: torch.Tensor, residual_out: Optional[torch.Tensor] = None,
-                        stream=None, dresidual_out: Optional[torch.Tensor] = None):
-        """Gradients that train the router of a layer whose experts are held fixed: dout [T, H] bf16, the
+                        stream=None, dresidual_out: Optional[torch.Tensor] = None, need_dy: bool = False):
+        """Gradients that train the router of a layer (whose experts are held fixed, or trained by experts_backward
+        from the finalize gradients' dy, made with need_dy): dout [T, H] bf16, the
         gradient of the last forward call's output -> (finalize gradients, router gradients), as
         moe_finalize_backward and MoERouter.backward return them.  residual_out: the sum before the RMSNorm (layers
         with one; None: what a keep_residual layer's forward call wrote).  The router weights of a layer that
@@ -206,9 +291,25 @@ class MoELayer:
         if residual_out is None and self.inp.rms_weight is not None:
             raise ValueError("router_backward under an RMSNorm needs residual_out, or a layer with keep_residual")
         fin = moe.moe_finalize_backward(dout, self.y, self.topk_weights, self.cfg.top_k, residual_out=residual_out,
-                                        rms_weight=self.inp.rms_weight, dresidual_out=dresidual_out, need_dy=False,
+                                        rms_weight=self.inp.rms_weight, dresidual_out=dresidual_out, need_dy=need_dy,
                                         stream=stream)
         return fin, self.router.backward(fin[1], a1, self.topk_ids, stream=stream)
+
+    def experts_backward(self, dy: torch.Tensor, a1: torch.Tensor, dw_dtype: Optional[torch.dtype] = None,
+                         accumulate: bool = False, stream=None):
+        """Gradients of the routed experts of a bf16 layer, given dy [T * top_k, H] bf16 (moe_finalize_backward's, by
+        slots) and the hidden states a1 of the last forward call (with input_norm: the layer's a1): (dw13, dw2, da1),
+        as MoEExperts.backward returns them.  [g | u] and h are made again from a1.  dw_dtype: as MoEExperts',
+        chosen by the first call."""
+        if self.cfg.quant != "bf16" or self.cfg.weight_on_input or self.single:
+            raise ValueError("experts_backward needs a bf16 layer of separate launches, its weights applied in the finalize")
+        if self.trainer is not None and dw_dtype not in (None, self.trainer.dw13.dtype):
+            raise ValueError(f"dw_dtype: the first call's was {self.trainer.dw13.dtype}")
+        if self.trainer is None:
+            self.trainer = MoEExperts(self.inp.w13, self.inp.w2, self.cfg.T, self.cfg.top_k, self.cfg.activation, dw_dtype,
+                                      stream)
+        self.trainer.hidden(a1, self.al, stream)
+        return self.trainer.backward(dy, a1, self.al, accumulate, stream)
 
     def experts(self, a1q, a1q_scale, a1, stream=None, shared_launched=False):
         """The routed experts into self.y and the shared expert (if any) into
