@@ -14,8 +14,8 @@
 // for what lies behind them.  (Zeroing those rows in shared memory between copy and MMAs stalled the K loop some 2500
 // clocks a tile: 4096 x 14336 over groups of 1024 rows 670 us.)
 //
-// Persistent, warp-specialised, pairs of CTAs: warp 0 copies stages of K blocks by TMA, warp 1 issues the MMAs, warps
-// 4-11 run the epilogue from one of two accumulators in tensor memory while the
+// Persistent, warp-specialised, pairs of CTAs: warps 0 and 2 copy stages of K blocks of A and of B by TMA (one warp for
+// both was busy 65 % of its time where K loops are short), warp 1 issues the MMAs, warps 4-11 run the epilogue from one of two accumulators in tensor memory while the
 // other fills.  Every CTA counts the tiles from the offsets itself; nothing comes back to the host.
 #include "moe_mma.cuh"
 
@@ -83,10 +83,15 @@ struct Unit {
 // the pairs that work at the same time share both operands in L2.
 constexpr int kRaster = 8;
 __device__ __forceinline__ void raster(int in, int many, int other, int& a, int& b) {
-  const int blocks = (many + kRaster - 1) / kRaster, r = (many + blocks - 1) / blocks;
-  const int g = in / (r * other), left = in - g * r * other, n = min(r, many - g * r);
-  a = g * r + left % n;
-  b = left / n;
+  int first = 0, n = many;
+  if (many > kRaster) {
+    const int blocks = (many + kRaster - 1) / kRaster, r = (many + blocks - 1) / blocks, g = in / (r * other);
+    first = g * r;
+    in -= first * other;
+    n = min(r, many - first);
+  }
+  b = n == 1 ? in : in / n;
+  a = first + in - b * n;
 }
 template <Mode kMode>
 __device__ __forceinline__ Unit unit_of(const Grouped& p, const int* start, const int* pre, int u) {
@@ -113,7 +118,7 @@ __device__ __forceinline__ Unit unit_of(const Grouped& p, const int* start, cons
     raster(u - p.tiles_p * pre[e], n, p.tiles_p, t.q, t.p);
     t.e = e;
     // the group's rows dealt evenly over its tiles (that many are needed, so none is empty)
-    t.width = ((rows + n - 1) / n + 31) & ~31;
+    t.width = ((n == 1 ? rows : (rows + n - 1) / n) + 31) & ~31;
     t.row0 = start[e] + t.q * t.width;
     t.rows = min(t.width, rows - t.q * t.width);
     t.stages = p.KB;
@@ -341,39 +346,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       stage %= stages;
     };
     if (warp == 0) {
-      // ---------------------------------------------------------- TMA producer
+      // ---------------------------------------------------------- TMA producer of A
       const uint64_t pol = policy_evict_normal();
       const uint32_t full0 = map_to_rank(smem_u32(full), 0);  // (both CTAs' copies complete there)
-      long long seen = -1;  // dw: the group whose maps were acquired
+      long long seen = -1;  // dw: the group whose map was acquired
+      if (kMode == kDw) depend_wait();  // (the weights are the caller's and wait for nothing in this call)
       for (int u = first; u < units; u += step) {
         const Unit t = unit_of<kMode>(p, start, pre, u);
         const int arow = (t.p * 2 + half) * kRows;
-        const int brow = kBMN ? t.q * p.width + half * half_width : t.row0 + half * (t.width / 2);
-        uint32_t bytes = 2 * KS * (kAStage + (kBMN ? b_stage : t.width / 2 * 128));  // both CTAs' of a stage
-        int fours = 0;  // p.from: this CTA's rows, by four
         const CUtensorMap* mA = kMode == kDw ? p.ends + 2 * t.e : &tmA;
-        const CUtensorMap* mB = kMode == kDw ? mA + 1 : &maps.b[kMode == kForward && p.from ? 0 : t.width / 32 - 1];
+        uint32_t bytes = 2 * KS * (kAStage + (kBMN ? b_stage : t.width / 2 * 128));  // of a stage, both CTAs', A and B
         if (kMode == kForward && p.from) {
-          // (the columns of the tile that have no row keep what the stage held; nobody looks at their sums)
-          const int n = t.width / 2, have = max(0, min(t.rows - half * n, n));
-          fours = (have + 3) / 4;
+          const int n = t.width / 2;
           bytes = KS * (2 * kAStage + ((min(t.rows, n) + 3) / 4 + (max(0, t.rows - n) + 3) / 4) * 512);
-          __syncwarp();
-          int slot = have ? __ldg(p.from + t.row0 + half * n + min(lane, have - 1)) : 0;
-          if (slot < 0 || slot >= p.S) {
-            record_status((int)MOE_ERR_INVALID_ARG);
-            slot = 0;
-          }
-          rows4[lane] = slot / p.from_div;
-          __syncwarp();
         }
         if (elect_one()) {
+          if (kMode == kDw && seen != t.e && t.stages) acquire_map(mA);
           int st = stage;
           uint32_t ph = phase;
-          auto load_a = [&](int kb, int at) {  // K blocks of the stage kb into the ring's stage `at`
-            uint8_t* sA = smem + at * stage_bytes;
-            const uint32_t bar = full0 + at * 8;
-            if (half == 0) mbar_arrive_expect_tx(&full[at], bytes);
+          for (int kb = 0; kb < t.stages; ++kb) {
+            if (!lane_wait(&empty[st], ph ^ 1)) {
+              failed = true;
+              break;
+            }
+            uint8_t* sA = smem + st * stage_bytes;
+            const uint32_t bar = full0 + st * 8;
+            if (half == 0) mbar_arrive_expect_tx(&full[st], bytes);
             const int k = kMode == kDw ? t.row0 + kb * BK : kb * KS * BK;
             if constexpr (kMode == kForward) {
 #pragma unroll
@@ -390,10 +388,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                   tma_load<2>(sA + g * 8192, mA, arow + g * 64, k, bar, pol);
               }
             }
-          };
-          auto load_b = [&](int kb, int at) {
-            uint8_t* sB = smem + at * stage_bytes + KS * kAStage;
-            const uint32_t bar = full0 + at * 8;
+            if (++st == stages) {
+              st = 0;
+              ph ^= 1;
+            }
+          }
+          if (failed) {
+            // wait (bounded) for the copies still in flight, B's too: each stage's phase that the ring was in
+            if (half == 0)
+              for (int i = 0; i < stages; ++i) mbar_wait(&full[i], i < st ? ph : ph ^ 1, false, 100000000ull);
+          }
+        }
+        __syncwarp();
+        if ((failed = __any_sync(0xffffffffu, failed))) break;
+        advance(t.stages);
+        seen = t.stages ? t.e : seen;
+      }
+    } else if (warp == 2) {
+      // ---------------------------------------------------------- TMA producer of B
+      const uint64_t pol = policy_evict_normal();
+      const uint32_t full0 = map_to_rank(smem_u32(full), 0);
+      long long seen = -1;
+      depend_wait();  // (rows put in order by an earlier kernel of this call)
+      for (int u = first; u < units; u += step) {
+        const Unit t = unit_of<kMode>(p, start, pre, u);
+        const int brow = kBMN ? t.q * p.width + half * half_width : t.row0 + half * (t.width / 2);
+        const CUtensorMap* mB =
+            kMode == kDw ? p.ends + 2 * t.e + 1 : &maps.b[kMode == kForward && p.from ? 0 : t.width / 32 - 1];
+        int fours = 0;  // p.from: this CTA's rows, by four
+        if (kMode == kForward && p.from) {
+          // (the columns of the tile that have no row keep what the stage held; nobody looks at their sums)
+          const int n = t.width / 2, have = max(0, min(t.rows - half * n, n));
+          fours = (have + 3) / 4;
+          __syncwarp();
+          int slot = have ? __ldg(p.from + t.row0 + half * n + min(lane, have - 1)) : 0;
+          if (slot < 0 || slot >= p.S) {
+            record_status((int)MOE_ERR_INVALID_ARG);
+            slot = 0;
+          }
+          rows4[lane] = slot / p.from_div;
+          __syncwarp();
+        }
+        if (elect_one()) {
+          if (kMode == kDw && seen != t.e && t.stages) acquire_map(mB);
+          int st = stage;
+          uint32_t ph = phase;
+          for (int kb = 0; kb < t.stages; ++kb) {
+            if (!lane_wait(&empty[st], ph ^ 1)) {
+              failed = true;
+              break;
+            }
+            uint8_t* sB = smem + st * stage_bytes + KS * kAStage;
+            const uint32_t bar = full0 + st * 8;
             const int k = kMode == kDw ? t.row0 + kb * BK : kb * KS * BK;
             if (kMode == kForward && p.from) {
               for (int g = 0; g < fours; ++g) {
@@ -409,35 +455,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               for (int g = 0; g < half_width / 64; ++g) tma_load<2>(sB + g * 8192, mB, brow + g * 64, k, bar, pol);
             }
-          };
-          int early = 0;
-          if (u == first) {
-            // The weights do not wait for what came before in this call (rows put in order): the first stages'
-            // are on their way meanwhile.
-            if (kMode != kDw)
-              for (; early < min(t.stages, stages); ++early) load_a(early, early);
-            depend_wait();
-          }
-          if (kMode == kDw && seen != t.e && t.stages) {
-            acquire_map(mA);
-            acquire_map(mB);
-          }
-          for (int kb = 0; kb < t.stages; ++kb) {
-            if (!lane_wait(&empty[st], ph ^ 1)) {
-              failed = true;
-              break;
-            }
-            if (kb >= early) load_a(kb, st);
-            load_b(kb, st);
             if (++st == stages) {
               st = 0;
               ph ^= 1;
             }
-          }
-          if (failed) {
-            // wait (bounded) for the copies still in flight: each stage's phase that the ring was in
-            if (half == 0)
-              for (int i = 0; i < stages; ++i) mbar_wait(&full[i], i < st ? ph : ph ^ 1, false, 100000000ull);
           }
         }
         __syncwarp();
