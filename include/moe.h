@@ -615,7 +615,8 @@ moe_status_t moe_rmsnorm(const void *x, const void *residual, const void *weight
  * x, w and out in dtype (MOE_DT_BF16 or MOE_DT_FP16).  expert_offsets [E + 1] int32 ascend within [0, S];
  * sorted_slot [S] int32, distinct values in [0, S), is read for the rows of a group alone (NULL where
  * every order is MOE_ROWS_SORTED); a value out of range is recorded as MOE_ERR_INVALID_ARG
- * in the device status word, its row of out (or dx) not written and its share in dw zero.  Rows of out that belong to no group (behind
+ * in the device status word, its row of out (or dx) not written and its share in dw zero; offsets out of
+ * order or range are recorded likewise, and nothing outside the buffers is touched.  Rows of out that belong to no group (behind
  * expert_offsets[E]) are left as they were.  0 <= S <= 2^30 (0: nothing is done), 1 <= E <= 1024, N and K
  * multiples of 8 up to 2^21, S % top_k == 0 where MOE_ROWS_TOKEN is used; more than 2^30 tiles may be
  * MOE_ERR_UNSUPPORTED.  A row of x that holds a NaN or an infinity affects its row of out alone.

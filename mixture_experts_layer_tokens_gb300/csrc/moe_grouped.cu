@@ -47,6 +47,10 @@ constexpr int kLaunchRegs = 168, kLowRegs = 40, kHighRegs = 232;
 static_assert(128 * kLowRegs + 256 * kHighRegs == kThreads * kLaunchRegs, "register split must balance");
 static_assert((2 * kMaxStages + 5) * 8 + 4 <= 256 && 256 + 32 * 4 <= kCtrlBytes && smem_bytes(kForward, kMaxE, 6, 32768) <= kSmemMost && smem_bytes(kDw, kMaxE, 5, 32768) <= kSmemMost, "shared memory layout");
 
+// Bad offsets and slots are kept apart from the status word: a wait gives up when that is set, and they are no reason to.
+static __device__ int g_invalid = 0;
+__device__ __forceinline__ void record_invalid() { atomicExch(&g_invalid, (int)MOE_ERR_INVALID_ARG); }
+
 struct Grouped {
   const CUtensorMap* ends;         // dw: maps of dout and x that end with each group
   const int32_t *offsets, *slots;  // slots: NULL where no order needs them
@@ -298,17 +302,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     int before = 0;
     for (int b = 0; b < p.E; b += 128) {
       int first[4], end[4];
-      // (offsets out of order or range would be the caller's mistake; no row outside [0, S) is touched)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int e = b + j * 32 + lane;
-        first[j] = e < p.E ? min(max(__ldg(p.offsets + e), 0), p.S) : 0;
-        end[j] = e < p.E ? min(max(__ldg(p.offsets + e + 1), 0), p.S) : 0;
+        first[j] = e < p.E ? __ldg(p.offsets + e) : 0;
+        end[j] = e < p.E ? __ldg(p.offsets + e + 1) : 0;
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int e = b + j * 32 + lane;
         if (b + j * 32 >= p.E) break;
+        // (the caller's mistake; no row outside [0, S) is touched)
+        if (first[j] < 0 || first[j] > end[j] || end[j] > p.S) record_invalid();
+        first[j] = min(max(first[j], 0), p.S);
+        end[j] = min(max(end[j], 0), p.S);
         int n = (max(0, end[j] - first[j]) + p.width - 1) >> p.log2_width;
         if (e < p.E) start[e] = first[j];
         if (e == p.E - 1) start[p.E] = end[j];
@@ -423,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           int slot = have ? __ldg(p.from + t.row0 + half * n + min(lane, have - 1)) : 0;
           if (slot < 0 || slot >= p.S) {
-            record_status((int)MOE_ERR_INVALID_ARG);
+            record_invalid();
             slot = 0;
           }
           rows4[lane] = slot / p.from_div;
@@ -562,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.slots && to[c] >= 0) {
             const int slot = __ldg(p.slots + to[c]);
             const bool bad = slot < 0 || slot >= p.S;
-            if (bad) record_status((int)MOE_ERR_INVALID_ARG);
+            if (bad) record_invalid();
             to[c] = bad ? -1 : p.to_slots ? slot : to[c];
           }
         }
@@ -661,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 __device__ __forceinline__ void gather_row(const uint4* __restrict__ from, int slot, int S, int div, int nvec,
                                            uint4* __restrict__ d, int lane) {
   if (slot < 0 || slot >= S) {
-    if (lane == 0) record_status((int)MOE_ERR_INVALID_ARG);
+    if (lane == 0) record_invalid();
     for (int i = lane; i < nvec; i += 32) d[i] = make_uint4(0, 0, 0, 0);
     return;
   }
@@ -895,7 +902,16 @@ moe_status_t check_sizes(int S, int E, int N, int K, int top_k, moe_dtype_t dtyp
 
 }  // namespace
 
-MOE_DEFINE_STATUS_READER(grouped_status)
+MOE_DEFINE_STATUS_READER(grouped_wait_status)
+
+moe_status_t grouped_status(int clear) {
+  int v = 0;
+  const int z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_invalid, sizeof(int)) != cudaSuccess) return MOE_ERR_CUDA;
+  if (clear && v && cudaMemcpyToSymbol(g_invalid, &z, sizeof(int)) != cudaSuccess) return MOE_ERR_CUDA;
+  const moe_status_t waits = grouped_wait_status(clear);
+  return waits != MOE_OK ? waits : (moe_status_t)v;
+}
 
 }  // namespace moe
 

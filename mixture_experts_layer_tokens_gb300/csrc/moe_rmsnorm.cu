@@ -15,6 +15,7 @@ namespace {
 constexpr int kMaxThreads = 1024;
 constexpr int kMaxH = 16384;
 constexpr int kRegs = 65536;  // of an SM
+constexpr int kMaxSmem = 2 * 2 * kMaxH * 2;  // two stages of two rows
 
 struct Norm {
   const __nv_bfloat16 *x, *res, *gamma;
@@ -62,7 +63,7 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint3
 // copies, the next turn's under this turn's work (loads by the threads themselves left HBM idle through each row's
 // sum and outputs: 16384 x 7168 with all outputs 301 us).
 template <int NV, bool kRing>
-__global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const Norm p) {
+__global__ void __launch_bounds__(NV == 4 ? kMaxThreads / 2 : kMaxThreads) rmsnorm_kernel(const Norm p) {
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ float red[2][2][kMaxThreads / 32];
   __shared__ uint64_t full[2];
@@ -219,10 +220,11 @@ extern "C" moe_status_t moe_rmsnorm(const void* x, const void* residual, const v
     const int smem = kRing ? 2 * rows * H * 2 * (residual ? 2 : 1) : 0;
     int ctas = 2048 / block;  // of an SM
     if (kRing) {
-      const int by_regs = kRegs / (block * 64), by_smem = 232448 / (smem + 2048);
+      const int by_regs = kRegs / (block * (NV == 4 ? 120 : 64)), by_smem = 232448 / (smem + 2048);
       ctas = by_regs < by_smem ? by_regs : by_smem;
       if (ctas < 1) ctas = 1;
-      if (cudaFuncSetAttribute(rmsnorm_kernel<NV, kRing>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      // (the same for every call: host threads may come at once)
+      if (cudaFuncSetAttribute(rmsnorm_kernel<NV, kRing>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
         return MOE_ERR_CUDA;
     }
     const int most = num_sms() * ctas;
@@ -231,7 +233,9 @@ extern "C" moe_status_t moe_rmsnorm(const void* x, const void* residual, const v
   };
   // Few rows: one round of loads a thread and no ring.  [1, 7168] with all outputs 4.4 us in a graph, by the ring 5.1.
   if (nvec <= kMaxThreads && T <= num_sms()) return go(std::integral_constant<int, 1>(), std::false_type());
-  // Two vectors a thread.  With 1 / 2 / 4 of them, all outputs: [16384, 7168] 207 / 185 / 179 us, [16384, 1024] 28 / 29 /
-  // 28, [65536, 128] 14 / 16 / 24, [1024, 7168] 17 / 13.5 / 15 (by the threads' own loads 300, 39, 32, 23).
+  // With 1 / 2 / 4 vectors a thread, all outputs: [16384, 7168] 207 / 185 / 179 us, [8192, 16384] 181 / 188 / 181,
+  // [4096, 7168] 55 / 46 / 45, [1024, 7168] 17 / 13.5 / 15, [16384, 1024] 28 / 29 / 28, [65536, 128] 14 / 16 / 24 (by the
+  // threads' own loads 300, 319, 79, 23, 39, 32).
+  if (nvec >= 512 && T >= 2048) return go(std::integral_constant<int, 4>(), std::true_type());
   return go(std::integral_constant<int, 2>(), std::true_type());
 }

@@ -214,6 +214,42 @@ def test_slots_out_of_range_are_left_out(cuda_dev, counts, rows):
     assert torch.equal(dw, want) and moe.moe_device_status() == moe.MOE_OK
 
 
+def test_a_bad_slot_stops_nothing_else(cuda_dev):
+    """A bad slot is recorded while the kernels' waits are long, and stays recorded through later calls: neither makes a
+    wait give up."""
+    g = torch.Generator(device=cuda_dev).manual_seed(0)
+    S, E, N, K = 16384, 8, 4096, 4096
+    x = torch.randn((S, K), generator=g, device=cuda_dev).to(BF)
+    w = (torch.randn((E, N, K), generator=g, device=cuda_dev) / 64).to(BF)
+    o = torch.arange(E + 1, dtype=torch.int32, device=cuda_dev) * (S // E)
+    slots = torch.randperm(S, generator=g, device=cuda_dev).to(torch.int32)
+    kw = dict(x_rows="slot", out_rows="slot")
+    want = moe.moe_grouped_linear(x, w, o, slots, **kw)
+    bad = slots.clone()
+    bad[5], bad[S - 7] = S + 3, -4
+    keep = torch.ones(S, dtype=torch.bool, device=cuda_dev)
+    keep[slots[[5, S - 7]].long()] = False
+    for _ in range(2):
+        assert torch.equal(moe.moe_grouped_linear(x, w, o, bad, **kw)[keep], want[keep])
+    assert torch.equal(moe.moe_grouped_linear(x, w, o, slots, **kw), want)
+    assert moe.moe_device_status() == moe.MOE_ERR_INVALID_ARG and moe.moe_device_status() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("offsets", [[0, 30, 20, 70], [-5, 30, 40, 70], [0, 30, 40, 90]])
+def test_offsets_out_of_order_are_recorded(cuda_dev, offsets):
+    """Groups that do not fit are cut to the rows there are, and the call says so; the rows of a sound group are right."""
+    p = Problem([30, 10, 30], 136, 72, 1, BF, "slot", "slot", "slot")
+    want, (dx, dw) = p.forward(cuda_dev).clone(), [t.clone() for t in p.backward(cuda_dev)]
+    p.offsets = torch.tensor(offsets, dtype=torch.int32)
+    out = p.forward(cuda_dev)
+    assert moe.moe_device_status() == moe.MOE_ERR_INVALID_ARG and bool((p.store[p.S] == 7).all())
+    dx2, dw2 = p.backward(cuda_dev)
+    assert moe.moe_device_status() == moe.MOE_ERR_INVALID_ARG
+    assert bool((p.dx_store[p.S] == 7).all()) and bool((p.dw_store[p.E] == 7).all())
+    rows = p.slots[:30 if offsets[0] == 0 and offsets[2] == 40 else 20].long().to(cuda_dev)
+    assert torch.equal(out[rows], want[rows]) and torch.equal(dx2[rows], dx[rows])
+
+
 def test_parts_of_the_gradients(cuda_dev):
     """dx or dw alone are what both together are; without rows dw is zeros, or what it was."""
     p = Problem([70, 0, 33], 136, 72, 1, BF, "slot", "slot", "slot")
