@@ -62,6 +62,8 @@ struct Grouped {
   int P, Q;              // rows of A's tensor (forward N, dx K, dw N); dw: columns of B's (K)
   int KB;                // stages of the contraction (dw: by the group's rows)
   int tiles_p, tiles_q;  // of 256 rows of A; dw: of `width` columns
+  int per;               // dw: tiles of an expert
+  unsigned long long per_inverse;  // floor(2^64 / per) + 1: the high word of u times it is u / per
   int width, log2_width; // columns of a tile at most (a power of two)
   int stages, chunk;     // chunk: stages added up in the tensor memory (kPromote)
   int fp16, out32, accumulate;
@@ -83,46 +85,51 @@ struct Unit {
   long long e;
 };
 
-// Tile of the unit u.  Blocks of up to 8 tile columns run through all tile rows (dw: the other way round), so that
-// the pairs that work at the same time share both operands in L2.
+// a / d: exact below 2^20 by way of the reciprocal, whose error there is a quarter of the distance to the next quotient
+// (an integer division would be most of a tile's bookkeeping, which short K loops do not hide).
+__device__ __forceinline__ int quotient(int a, int d) {
+  if (d == 1) return a;
+  return a < (1 << 20) ? (int)(((float)a + 0.5f) * __frcp_rn((float)d)) : a / d;
+}
+// Blocks of up to 8 tile columns run through all tile rows (dw: the other way round), so that the pairs that work at
+// the same time share both operands in L2.
 constexpr int kRaster = 8;
 __device__ __forceinline__ void raster(int in, int many, int other, int& a, int& b) {
   int first = 0, n = many;
   if (many > kRaster) {
-    const int blocks = (many + kRaster - 1) / kRaster, r = (many + blocks - 1) / blocks, g = in / (r * other);
+    const int blocks = (many + kRaster - 1) / kRaster, r = quotient(many + blocks - 1, blocks), g = quotient(in, r * other);
     first = g * r;
     in -= first * other;
     n = min(r, many - first);
   }
-  b = n == 1 ? in : in / n;
+  b = quotient(in, n);
   a = first + in - b * n;
 }
+// The tile of the unit u.  For a whole warp.
 template <Mode kMode>
-__device__ __forceinline__ Unit unit_of(const Grouped& p, const int* start, const int* pre, int u) {
+__device__ __forceinline__ Unit unit_of(const Grouped& p, const int* start, const int* pre, int u, int lane) {
   Unit t;
   if constexpr (kMode == kDw) {
-    const int per = p.tiles_p * p.tiles_q, e = u / per;
-    raster(u - e * per, p.tiles_p, p.tiles_q, t.p, t.q);
+    const int e = p.per == 1 ? u : (int)__umul64hi((unsigned long long)u, p.per_inverse);
+    raster(u - e * p.per, p.tiles_p, p.tiles_q, t.p, t.q);
     t.e = e;
     t.row0 = start[e];
     t.rows = max(0, start[e + 1] - t.row0);
     t.width = p.width;
     t.stages = (t.rows + BK - 1) / BK;
   } else {
-    const int at = u / p.tiles_p;
-    int e = 0, end = p.E;  // the last e with pre[e] <= at
-    while (end - e > 1) {
-      const int mid = (e + end) >> 1;
-      if (pre[mid] <= at)
-        e = mid;
-      else
-        end = mid;
+    int e = 0, span = p.E;  // the last e with pre[e] <= u is in [e, e + span)
+    while (span > 1) {
+      const int stride = (span + 31) >> 5, i = lane * stride;
+      const int last = __popc(__ballot_sync(0xffffffffu, i < span && pre[min(e + i, p.E)] <= u)) - 1;
+      e += last * stride;
+      span = min(stride, span - last * stride);
     }
-    const int n = pre[e + 1] - pre[e], rows = start[e + 1] - start[e];
-    raster(u - p.tiles_p * pre[e], n, p.tiles_p, t.q, t.p);
+    const int rows = start[e + 1] - start[e], n = (rows + p.width - 1) >> p.log2_width;
+    raster(u - pre[e], n, p.tiles_p, t.q, t.p);
     t.e = e;
     // the group's rows dealt evenly over its tiles (that many are needed, so none is empty)
-    t.width = ((n == 1 ? rows : (rows + n - 1) / n) + 31) & ~31;
+    t.width = (quotient(rows + n - 1, n) + 31) & ~31;
     t.row0 = start[e] + t.q * t.width;
     t.rows = min(t.width, rows - t.q * t.width);
     t.stages = p.KB;
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* rows4 = reinterpret_cast<int*>(ctrl + 256);  // B's rows of the producer's tile (p.from)
   int* start = reinterpret_cast<int*>(ctrl + kCtrlBytes);  // [E + 1] first sorted row of each group
-  int* pre = start + ((p.E + 4) & ~3);                     // [E + 1] tiles of the groups before it (not dw's)
+  int* pre = start + ((p.E + 4) & ~3);                     // [E + 1] units of the groups before it (not dw's)
   const int half = (int)cluster_rank() & 1;
   const uint16_t pair_mask = 3;
 
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (first[j] < 0 || first[j] > end[j] || end[j] > p.S) record_invalid();
         first[j] = min(max(first[j], 0), p.S);
         end[j] = min(max(end[j], 0), p.S);
-        int n = (max(0, end[j] - first[j]) + p.width - 1) >> p.log2_width;
+        int n = p.tiles_p * ((max(0, end[j] - first[j]) + p.width - 1) >> p.log2_width);
         if (e < p.E) start[e] = first[j];
         if (e == p.E - 1) start[p.E] = end[j];
         if (kMode == kDw) continue;
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int units = kMode == kDw ? p.E * p.tiles_p * p.tiles_q : p.tiles_p * pre[p.E];
+  const int units = kMode == kDw ? p.E * p.per : pre[p.E];
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (warp < kFirstEpi) {
@@ -359,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       long long seen = -1;  // dw: the group whose map was acquired
       if (kMode == kDw) depend_wait();  // (the weights are the caller's and wait for nothing in this call)
       for (int u = first; u < units; u += step) {
-        const Unit t = unit_of<kMode>(p, start, pre, u);
+        const Unit t = unit_of<kMode>(p, start, pre, u, lane);
         const int arow = (t.p * 2 + half) * kRows;
         const CUtensorMap* mA = kMode == kDw ? p.ends + 2 * t.e : &tmA;
         uint32_t bytes = 2 * KS * (kAStage + (kBMN ? b_stage : t.width / 2 * 128));  // of a stage, both CTAs', A and B
@@ -418,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       long long seen = -1;
       depend_wait();  // (rows put in order by an earlier kernel of this call)
       for (int u = first; u < units; u += step) {
-        const Unit t = unit_of<kMode>(p, start, pre, u);
+        const Unit t = unit_of<kMode>(p, start, pre, u, lane);
         const int brow = kBMN ? t.q * p.width + half * half_width : t.row0 + half * (t.width / 2);
         const CUtensorMap* mB =
             kMode == kDw ? p.ends + 2 * t.e + 1 : &maps.b[kMode == kForward && p.from ? 0 : t.width / 32 - 1];
@@ -481,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int acc = 0;
       uint32_t acc_phase = 0;
       for (int u = first; u < units && !failed; u += step) {
-        const Unit t = unit_of<kMode>(p, start, pre, u);
+        const Unit t = unit_of<kMode>(p, start, pre, u, lane);
         const uint32_t idesc = p.idesc | (uint32_t)(t.width >> 3) << 17;
         const int chunk = kPromote ? p.chunk : t.stages;
         for (int kc = 0; kc < t.stages; kc += chunk) {
@@ -553,103 +560,137 @@ __global__ void __launch_bounds__(kThreads, 1)
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     };
-    bool ok = true;
-    for (int u = first; ok && u < units; u += step) {
-      const Unit t = unit_of<kMode>(p, start, pre, u);
+    bool ok = true, zeroed = false;  // zeroed: dw's buffer holds zeros
+    // first column of the c-th 32 columns of this warp, in the tile
+    auto at = [&](int c) { return kMode == kDw ? side * (p.width / 2) + c * 32 : c * 64 + side * 32; };
+    // Rows of out of a tile's columns (see store_rows32).  (Asked for a tile ahead: their latency would be a good part
+    // of a short tile's time.)
+    auto rows_of = [&](const Unit& t, int (&to)[4]) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int row = at(c) + lane;
+        to[c] = row < t.rows ? t.row0 + row : -1;
+        if (p.slots && to[c] >= 0) {
+          const int slot = __ldg(p.slots + to[c]);
+          const bool bad = slot < 0 || slot >= p.S;
+          if (bad) record_invalid();
+          to[c] = bad ? -1 : p.to_slots ? slot : to[c];
+        }
+      }
+    };
+    Unit t = {};
+    int to[4] = {};
+    if (first < units) {
+      t = unit_of<kMode>(p, start, pre, first, lane);
+      if (kMode != kDw) rows_of(t, to);
+    }
+    for (int u = first; u < units; u += step) {
       const int n0 = (t.p * 2 + half) * kRows + quarter * 32;
-      // first column of the c-th 32 columns of this warp, in the tile; columns of the tile that are of use
-      auto at = [&](int c) { return kMode == kDw ? side * (p.width / 2) + c * 32 : c * 64 + side * 32; };
+      // columns of the tile that are of use
       const int cols = n0 >= p.P ? 0 : kMode == kDw ? min((side + 1) * (p.width / 2), p.Q - t.q * p.width) : t.rows;
-      int to[4];  // rows of out (see store_rows32), on their way before the accumulator is complete
-      if constexpr (kMode != kDw) {
+      uint32_t words[kPromote ? 1 : 4][16] = {};
+      float sums[kPromote ? 128 : 1] = {};
+      if (kMode != kDw || t.stages > 0) {
+        if constexpr (kPromote) {
+          for (int kc = 0; kc < t.stages; kc += p.chunk) {
+            if (!(ok = __all_sync(0xffffffffu, lane_wait(&tfull[acc], acc_phase)))) break;
+            tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int row = at(c) + lane;
-          to[c] = row < cols ? t.row0 + row : -1;
-          if (p.slots && to[c] >= 0) {
-            const int slot = __ldg(p.slots + to[c]);
-            const bool bad = slot < 0 || slot >= p.S;
-            if (bad) record_invalid();
-            to[c] = bad ? -1 : p.to_slots ? slot : to[c];
+            for (int c = 0; c < 4; ++c)
+              if (at(c) < cols) {
+#pragma unroll
+                for (int h = 0; h < 32; h += 16) {
+                  float v[16];
+                  tmem_ld16(tb + acc * kAccCols + at(c) + h, v);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) sums[c * 32 + h + i] += v[i];
+                }
+              }
+            release();
           }
-        }
-      }
-      auto finish = [&](const uint32_t (&w)[4][16]) {  // 16-bit words of all columns
-        if constexpr (kMode == kDw) {
-#pragma unroll
-          for (int c = 0; c < 4; c += 2)
-            if (at(c) < cols) store_grad(&tmOut, buf, &w[0][0] + c * 16, n0, t.q * p.width + at(c), (int)t.e, false, lane);
+          if (!ok) break;
         } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (at(c) < cols) store_rows32(p, buf, w[c], n0, to[c], lane);
-        }
-      };
-      uint32_t words[4][16] = {};
-      if (kMode == kDw && t.stages == 0) {  // an expert without rows
-        if (p.accumulate) continue;
-        if (!p.out32) {
-          finish(words);
-        } else {
-          const uint32_t zero[32] = {};
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (at(c) < cols) store_grad(&tmOut, buf, zero, n0, t.q * p.width + at(c), (int)t.e, false, lane);
-        }
-        continue;
-      }
-      if constexpr (kPromote) {
-        float sums[128] = {};
-        for (int kc = 0; kc < t.stages; kc += p.chunk) {
-          if (!(ok = __all_sync(0xffffffffu, lane_wait(&tfull[acc], acc_phase)))) break;
+          if (!(ok = warp_wait(&tfull[acc], acc_phase))) break;
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             if (at(c) < cols) {
+              float v[32];
+              tmem_ld32(tb + acc * kAccCols + at(c), v);
+              tmem_ld_wait();
 #pragma unroll
-              for (int h = 0; h < 32; h += 16) {
-                float v[16];
-                tmem_ld16(tb + acc * kAccCols + at(c) + h, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) sums[c * 32 + h + i] += v[i];
-              }
+              for (int i = 0; i < 16; ++i) words[c][i] = pack16(v[2 * i], v[2 * i + 1], p.fp16);
             }
           release();
         }
-        if (!ok) break;
-        if (kMode == kDw && (p.out32 || p.accumulate)) {
+      }
+      Unit next = {};
+      int next_to[4] = {};
+      if (u + step < units) {
+        next = unit_of<kMode>(p, start, pre, u + step, lane);
+        if (kMode != kDw) rows_of(next, next_to);
+      }
+      // the c-th 32 columns in 16 bits, two to a word
+      auto packed = [&](int c, uint32_t* w) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if constexpr (kPromote)
+            w[i] = pack16(sums[c * 32 + 2 * i], sums[c * 32 + 2 * i + 1], p.fp16);
+          else
+            w[i] = words[c][i];
+        }
+      };
+      if constexpr (kMode != kDw) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (at(c) < cols) {
+            uint32_t w[16];
+            packed(c, w);
+            store_rows32(p, buf, w, n0, to[c], lane);
+          }
+      } else {
+        const int k0 = t.q * p.width;
+        if (t.stages == 0) {  // an expert without rows: zeros, from one buffer
+          if (!p.accumulate) {
+            if (!zeroed) {
+              if (lane == 0) tma_store_wait();
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(grad_at(buf, lane, i)) = make_uint4(0, 0, 0, 0);
+              fence_async_smem();
+              __syncwarp();
+              zeroed = true;
+            }
+            for (int c = 0; c < 4; c += p.out32 ? 1 : 2)
+              if (lane == 0 && at(c) < cols) tma_store_3d(&tmOut, buf, k0 + at(c), n0, (int)t.e, false);
+          }
+        } else if (!(kPromote && (p.out32 || p.accumulate))) {
+          zeroed = false;
+#pragma unroll
+          for (int c = 0; c < 4; c += 2)
+            if (at(c) < cols) {
+              uint32_t w[32];
+              packed(c, w);
+              packed(c + 1, w + 16);
+              store_grad(&tmOut, buf, w, n0, k0 + at(c), (int)t.e, false, lane);
+            }
+        } else if constexpr (kPromote) {
+          zeroed = false;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             if (at(c) < cols) {
               if (p.out32)
-                store_grad(&tmOut, buf, reinterpret_cast<const uint32_t*>(sums + c * 32), n0, t.q * p.width + at(c),
-                           (int)t.e, p.accumulate, lane);
+                store_grad(&tmOut, buf, reinterpret_cast<const uint32_t*>(sums + c * 32), n0, k0 + at(c), (int)t.e,
+                           p.accumulate, lane);
               else
-                add_grad16(p, buf, sums + c * 32, n0, t.q * p.width + at(c), (size_t)t.e * p.P * p.Q, lane);
+                add_grad16(p, buf, sums + c * 32, n0, k0 + at(c), (size_t)t.e * p.P * p.Q, lane);
             }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) words[c][i] = pack16(sums[c * 32 + 2 * i], sums[c * 32 + 2 * i + 1], p.fp16);
-          finish(words);
         }
-      } else {
-        if (!(ok = warp_wait(&tfull[acc], acc_phase))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (at(c) < cols) {
-            float v[32];
-            tmem_ld32(tb + acc * kAccCols + at(c), v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) words[c][i] = pack16(v[2 * i], v[2 * i + 1], p.fp16);
-          }
-        release();
-        finish(words);
       }
+      t = next;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) to[c] = next_to[c];
     }
     if (kMode == kDw && lane == 0) tma_store_wait();
   }
@@ -686,10 +727,11 @@ __device__ __forceinline__ void gather_row(const uint4* __restrict__ from, int s
 // to[p] = from[slots[p] / div] for the sorted rows p that belong to a group: a warp a row.
 __global__ void __launch_bounds__(256)
     gather_rows_kernel(const uint4* __restrict__ from, const int32_t* __restrict__ slots,
-                       const int32_t* __restrict__ offsets, int E, int S, int div, int nvec, uint4* __restrict__ to) {
+                       const int32_t* __restrict__ offsets, int E, int S, int div, int nvec, int pitch,
+                       uint4* __restrict__ to) {
   depend_launch();
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row < S && row < __ldg(offsets + E)) gather_row(from, __ldg(slots + row), S, div, nvec, to + (size_t)row * nvec, lane);
+  if (row < S && row < __ldg(offsets + E)) gather_row(from, __ldg(slots + row), S, div, nvec, to + (size_t)row * pitch, lane);
   depend_wait();  // (not for its own sake: what comes after this kernel comes after the one before it, too)
 }
 
@@ -716,13 +758,14 @@ __global__ void __launch_bounds__(32)
 }
 
 // ------------------------------------------------------------------ host side
-// A tensor [outer][rows][inner] in boxes of 128 bytes x box rows of one matrix; outer 0: two dimensions.
-bool make_map(CUtensorMap* m, const void* base, int dtype, long long inner, long long rows, long long outer, int box) {
+// A tensor [outer][rows][inner] in boxes of 128 bytes x box rows of one matrix; outer 0: two dimensions, rows ld apart.
+bool make_map(CUtensorMap* m, const void* base, int dtype, long long inner, long long rows, long long outer, int box,
+              long long ld = 0) {
   auto enc = get_encode();
   if (!enc) return false;
   const int rank = outer ? 3 : 2, size = dtype == MOE_DT_FP32 ? 4 : 2;
   cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)outer};
-  cuuint64_t strides[2] = {(cuuint64_t)inner * size, (cuuint64_t)inner * rows * size};
+  cuuint64_t strides[2] = {(cuuint64_t)(ld ? ld : inner) * size, (cuuint64_t)inner * rows * size};
   cuuint32_t boxes[3] = {(cuuint32_t)(128 / size), (cuuint32_t)box, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType type = dtype == MOE_DT_FP32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
@@ -733,21 +776,29 @@ bool make_map(CUtensorMap* m, const void* base, int dtype, long long inner, long
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of dout or x [S, cols] as dw takes them, in boxes of 64 rows x 64 columns.  wide: columns in 64s, as [cols / 64][64],
+// Sorted rows: the caller's, or put in order in the workspace, there with a pitch of 128 bytes (rows that start on 128
+// bytes are copied at twice the rate of others).
+struct Rows {
+  const void* at;
+  long long ld;
+};
+long long pitch(long long cols) { return cols > 32 ? (cols + 63) / 64 * 64 : cols; }
+
+// Rows of dout or x [S, cols] as dw takes them, in boxes of 64 rows x 64 columns.  wide: columns in 64s, as [ld / 64][64],
 // so that a box takes two neighbouring groups (one behind the other in shared memory) and the two operands of a K block
 // are two copies, whose issue bounds the K loop, and not four: 4096 x 14336 over groups of 1024 rows 698 -> 640 us.
-// (dx's weights the same way: no difference.)
-bool wide(long long cols) { return cols % 64 == 0 && cols > 128; }
-bool make_rows_map(CUtensorMap* m, const void* base, int dtype, long long cols, long long S) {
-  if (!wide(cols)) return make_map(m, base, dtype, cols, S, 0, BK);
+// (What lies between cols and ld only reaches sums that are not stored.  dx's weights the same way: no difference.)
+bool wide(const Rows& r, long long cols) { return r.ld % 64 == 0 && cols > 128; }
+bool make_rows_map(CUtensorMap* m, const Rows& r, int dtype, long long cols, long long S) {
+  if (!wide(r, cols)) return make_map(m, r.at, dtype, cols, S, 0, BK, r.ld);
   auto enc = get_encode();
   if (!enc) return false;
-  cuuint64_t dims[3] = {64, (cuuint64_t)S, (cuuint64_t)cols / 64};
-  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, 128};
+  cuuint64_t dims[3] = {64, (cuuint64_t)S, (cuuint64_t)r.ld / 64};
+  cuuint64_t strides[2] = {(cuuint64_t)r.ld * 2, 128};
   cuuint32_t boxes[3] = {64, BK, 2};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, dtype == MOE_DT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-             const_cast<void*>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             const_cast<void*>(r.at), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -799,9 +850,9 @@ int widest(int S, int E) {
   return S <= 32 ? 32 : mean <= 24 ? 64 : mean <= 48 ? 128 : 256;
 }
 
-// One product.  a: the weights [E, N, K] (dw: dout, sorted), b: sorted rows.
+// One product.  a: the weights [E, N, K] (dw: not used), b: sorted rows (dw: x's; d: dout's).
 template <Mode kMode>
-moe_status_t run(const void* a, const void* b, const int32_t* offsets, const int32_t* slots, int to_slots, const int32_t* from,
+moe_status_t run(const void* a, const Rows& b, const Rows& d, const int32_t* offsets, const int32_t* slots, int to_slots, const int32_t* from,
                  int from_div, int S, int E, int N, int K, int fp16, void* out, int out32, int accumulate, const CUtensorMap* ends, bool overlap, cudaStream_t s) {
   Grouped g = {};
   g.ends = ends;
@@ -818,8 +869,8 @@ moe_status_t run(const void* a, const void* b, const int32_t* offsets, const int
   g.fp16 = fp16;
   g.out32 = out32;
   g.accumulate = accumulate;
-  g.wide_a = kMode == kDw && wide(N);
-  g.wide_b = kMode == kDw && wide(K);
+  g.wide_a = kMode == kDw && wide(d, N);
+  g.wide_b = kMode == kDw && wide(b, K);
   const int contraction = kMode == kForward ? K : kMode == kDx ? N : S;
   int ks = 1;
   if (kMode == kDw) {
@@ -831,6 +882,8 @@ moe_status_t run(const void* a, const void* b, const int32_t* offsets, const int
   while ((1 << g.log2_width) < g.width) ++g.log2_width;
   g.tiles_p = cdiv(g.P, 2 * kRows);
   g.tiles_q = cdiv(g.Q, g.width);
+  g.per = g.tiles_p * g.tiles_q;
+  g.per_inverse = g.per > 1 ? ~0ull / g.per + 1 : 0;  // (~0 / per is floor(2^64 / per) but for powers of two, where + 1 makes it exact)
   g.KB = cdiv(contraction, BK * ks);
   const int stage = ks * (kRows + g.width / 2) * 128;
   g.stages = (kSmemMost - smem_bytes(kMode, E, 0, 0)) / stage;
@@ -853,9 +906,9 @@ moe_status_t run(const void* a, const void* b, const int32_t* offsets, const int
     ma = mo;  // (not used)
   } else {
     ok = make_map(&ma, a, type, K, N, E, kMode == kForward ? kRows : BK * ks);
-    if (from) ok = ok && make_map(&mb.b[0], b, type, K, S / from_div, 0, 1);
+    if (from) ok = ok && make_map(&mb.b[0], b.at, type, K, S / from_div, 0, 1);
     for (int i = 0; !from && i < g.width / 32; ++i)
-      ok = ok && make_map(&mb.b[i], b, type, kMode == kForward ? K : N, S, 0, 16 * (i + 1));
+      ok = ok && make_map(&mb.b[i], b.at, type, kMode == kForward ? K : N, S, 0, 16 * (i + 1), b.ld);
     mo = ma;  // (not used)
   }
   if (!ok) return MOE_ERR_CUDA;
@@ -864,10 +917,14 @@ moe_status_t run(const void* a, const void* b, const int32_t* offsets, const int
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// Rows in `order` -> sorted rows at `to` (the caller's where they are sorted already).
-const void* sorted_rows(const void* from, int order, const int32_t* offsets, const int32_t* slots, int S, int E, int cols,
-                        int top_k, void* to, bool& overlap, cudaStream_t s) {
-  if (order == MOE_ROWS_SORTED) return from;
+// Where the rows of a tensor in `order` are once they are sorted: at `to` unless they are already.
+Rows placed(const void* from, int order, long long cols, void* to) {
+  return order == MOE_ROWS_SORTED ? Rows{from, cols} : Rows{to, pitch(cols)};
+}
+// Puts them there.
+bool put_in_order(const void* from, int order, const Rows& r, const int32_t* offsets, const int32_t* slots, int S, int E,
+                  int cols, int top_k, bool& overlap, cudaStream_t s) {
+  if (order == MOE_ROWS_SORTED) return true;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cdiv(S, 8));
   cfg.blockDim = dim3(256);
@@ -876,14 +933,13 @@ const void* sorted_rows(const void* from, int order, const int32_t* offsets, con
   cfg.attrs = attr;
   cfg.numAttrs = overlap ? 1 : 0;
   overlap = true;
-  const cudaError_t err =
-      cudaLaunchKernelEx(&cfg, gather_rows_kernel, static_cast<const uint4*>(from), slots, offsets, E, S,
-                         order == MOE_ROWS_TOKEN ? top_k : 1, cols / 8, static_cast<uint4*>(to));
-  return err == cudaSuccess ? to : nullptr;
+  return cudaLaunchKernelEx(&cfg, gather_rows_kernel, static_cast<const uint4*>(from), slots, offsets, E, S,
+                            order == MOE_ROWS_TOKEN ? top_k : 1, cols / 8, (int)(r.ld / 8),
+                            static_cast<uint4*>(const_cast<void*>(r.at))) == cudaSuccess;
 }
 
 size_t rows_bytes(long long S, long long cols, int order) {
-  return order == MOE_ROWS_SORTED ? 0 : ((size_t)S * cols * 2 + 255) / 256 * 256;
+  return order == MOE_ROWS_SORTED ? 0 : ((size_t)S * pitch(cols) * 2 + 255) / 256 * 256;
 }
 
 // The groups' maps, and room to start them on 128 bytes.
@@ -940,11 +996,11 @@ extern "C" moe_status_t moe_grouped_linear(const void* x, int x_rows, const void
   const bool direct = x_rows != MOE_ROWS_SORTED && widest(S, E) <= 64;
   const int div = x_rows == MOE_ROWS_TOKEN ? top_k : 1;
   bool overlap = false;
-  const void* xs = direct ? x : sorted_rows(x, x_rows, expert_offsets, sorted_slot, S, E, K, top_k, ws, overlap, s);
-  if (!xs) return MOE_ERR_CUDA;
+  const Rows xs = direct ? Rows{x, K} : placed(x, x_rows, K, ws);
+  if (!direct && !put_in_order(x, x_rows, xs, expert_offsets, sorted_slot, S, E, K, top_k, overlap, s)) return MOE_ERR_CUDA;
   const bool slots = x_rows != MOE_ROWS_SORTED || out_rows == MOE_ROWS_SLOT;
   const moe_status_t got =
-      run<kForward>(w, xs, expert_offsets, slots ? sorted_slot : nullptr, out_rows == MOE_ROWS_SLOT,
+      run<kForward>(w, xs, xs, expert_offsets, slots ? sorted_slot : nullptr, out_rows == MOE_ROWS_SLOT,
                     direct ? sorted_slot : nullptr, div, S, E, N, K, dtype == MOE_DT_FP16, out, 0, 0, nullptr, overlap, s);
   return got == MOE_OK ? launch_status() : got;
 }
@@ -982,31 +1038,28 @@ extern "C" moe_status_t moe_grouped_linear_backward(const void* dout, int dout_r
   const int fp16 = dtype == MOE_DT_FP16;
   bool overlap = false;
   uint8_t* next = static_cast<uint8_t*>(ws) + first;  // behind dout's rows
-  const void* xs = x;
+  const Rows d = placed(dout, dout_rows, N, ws), xs = placed(x, x_rows, K, next);
   CUtensorMap* ends = nullptr;
   if (dw) {
     const int type = fp16 ? MOE_DT_FP16 : MOE_DT_BF16;
-    if (x_rows != MOE_ROWS_SORTED) xs = next;
     next += rows_bytes(S, K, x_rows);
     ends = reinterpret_cast<CUtensorMap*>((reinterpret_cast<uintptr_t>(next) + 127) & ~uintptr_t(127));
     CUtensorMap md, mx;
-    if (!make_rows_map(&md, dout_rows == MOE_ROWS_SORTED ? dout : ws, type, N, S) || !make_rows_map(&mx, xs, type, K, S))
-      return MOE_ERR_CUDA;
+    if (!make_rows_map(&md, d, type, N, S) || !make_rows_map(&mx, xs, type, K, S)) return MOE_ERR_CUDA;
     group_maps_kernel<<<2 * E, 32, 0, s>>>(md, mx, expert_offsets, S, ends);
     overlap = true;
   }
-  const void* d = sorted_rows(dout, dout_rows, expert_offsets, sorted_slot, S, E, N, top_k, ws, overlap, s);
-  if (dw) xs = sorted_rows(x, x_rows, expert_offsets, sorted_slot, S, E, K, top_k, const_cast<void*>(xs), overlap, s);
-  if (!d || (dw && !xs)) return MOE_ERR_CUDA;
+  if (!put_in_order(dout, dout_rows, d, expert_offsets, sorted_slot, S, E, N, top_k, overlap, s)) return MOE_ERR_CUDA;
+  if (dw && !put_in_order(x, x_rows, xs, expert_offsets, sorted_slot, S, E, K, top_k, overlap, s)) return MOE_ERR_CUDA;
   if (dx) {
     const bool slots = dout_rows != MOE_ROWS_SORTED || dx_rows == MOE_ROWS_SLOT;
-    st = run<kDx>(w, d, expert_offsets, slots ? sorted_slot : nullptr, dx_rows == MOE_ROWS_SLOT, nullptr, 1, S, E, N, K, fp16,
+    st = run<kDx>(w, d, d, expert_offsets, slots ? sorted_slot : nullptr, dx_rows == MOE_ROWS_SLOT, nullptr, 1, S, E, N, K, fp16,
                   dx, 0, 0, nullptr, overlap, s);
     if (st != MOE_OK) return st;
     overlap = true;
   }
   if (dw) {
-    st = run<kDw>(d, xs, expert_offsets, nullptr, 0, nullptr, 1, S, E, N, K, fp16, dw, out32, accumulate != 0, ends, overlap, s);
+    st = run<kDw>(nullptr, xs, d, expert_offsets, nullptr, 0, nullptr, 1, S, E, N, K, fp16, dw, out32, accumulate != 0, ends, overlap, s);
     if (st != MOE_OK) return st;
   }
   return launch_status();
