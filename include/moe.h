@@ -622,7 +622,7 @@ moe_status_t moe_rmsnorm(const void *x, const void *residual, const void *weight
  * MOE_ERR_UNSUPPORTED.  A row of x that holds a NaN or an infinity affects its row of out alone.
  * Long sums are treated as moe_linear's are; the order of a sum is fixed by the sizes and
  * the group, so the same inputs give the same bits.  ws: moe_grouped_linear_workspace_size(...)
- * bytes (0 for MOE_ROWS_SORTED: ws may be NULL), for one call at a time.  Outputs overlap nothing. */
+ * bytes (may be 0 for MOE_ROWS_SORTED: ws may then be NULL), for one call at a time.  Outputs overlap nothing. */
 typedef enum { MOE_ROWS_SORTED = 0, MOE_ROWS_SLOT = 1, MOE_ROWS_TOKEN = 2 } moe_rows_t;
 
 moe_status_t moe_grouped_linear(const void *x, int x_rows, const void *w, const int32_t *expert_offsets,

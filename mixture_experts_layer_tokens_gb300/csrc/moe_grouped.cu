@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     };
-    bool ok = true, zeroed = false;  // zeroed: dw's buffer holds zeros
+    bool ok = true;
     // first column of the c-th 32 columns of this warp, in the tile
     auto at = [&](int c) { return kMode == kDw ? side * (p.width / 2) + c * 32 : c * 64 + side * 32; };
     // Rows of out of a tile's columns (see store_rows32).  (Asked for a tile ahead: their latency would be a good part
@@ -651,22 +651,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
       } else {
         const int k0 = t.q * p.width;
-        if (t.stages == 0) {  // an expert without rows: zeros, from one buffer
+        if (t.stages == 0) {
+          // An expert without rows: its gradient is zeros in one piece, of which this unit and warp take a share (by
+          // tiles, rows that start on no multiple of 32 bytes took twice the time).
           if (!p.accumulate) {
-            if (!zeroed) {
-              if (lane == 0) tma_store_wait();
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(grad_at(buf, lane, i)) = make_uint4(0, 0, 0, 0);
-              fence_async_smem();
-              __syncwarp();
-              zeroed = true;
-            }
-            for (int c = 0; c < 4; c += p.out32 ? 1 : 2)
-              if (lane == 0 && at(c) < cols) tma_store_3d(&tmOut, buf, k0 + at(c), n0, (int)t.e, false);
+            const long long all = (long long)p.P * p.Q / (p.out32 ? 4 : 8);  // 16-byte vectors
+            const int shares = p.per * 2 * kEpiWarps, mine = ((u - (int)t.e * p.per) * 2 + half) * kEpiWarps + warp - kFirstEpi;
+            const long long each = ((all + shares - 1) / shares + 7) & ~7ll, end = min(all, (mine + 1) * each);
+            uint4* d = static_cast<uint4*>(p.out) + t.e * all;
+            for (long long i = mine * each + lane; i < end; i += 32) d[i] = make_uint4(0, 0, 0, 0);
           }
         } else if (!(kPromote && (p.out32 || p.accumulate))) {
-          zeroed = false;
 #pragma unroll
           for (int c = 0; c < 4; c += 2)
             if (at(c) < cols) {
@@ -676,7 +671,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               store_grad(&tmOut, buf, w, n0, k0 + at(c), (int)t.e, false, lane);
             }
         } else if constexpr (kPromote) {
-          zeroed = false;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             if (at(c) < cols) {
@@ -731,7 +725,7 @@ __global__ void __launch_bounds__(256)
                        uint4* __restrict__ to) {
   depend_launch();
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row < S && row < __ldg(offsets + E)) gather_row(from, __ldg(slots + row), S, div, nvec, to + (size_t)row * pitch, lane);
+  if (row < S && row < __ldg(offsets + E)) gather_row(from, slots ? __ldg(slots + row) : row, S, div, nvec, to + (size_t)row * pitch, lane);
   depend_wait();  // (not for its own sake: what comes after this kernel comes after the one before it, too)
 }
 
@@ -918,13 +912,21 @@ moe_status_t run(const void* a, const Rows& b, const Rows& d, const int32_t* off
 }
 
 // Where the rows of a tensor in `order` are once they are sorted: at `to` unless they are already.
-Rows placed(const void* from, int order, long long cols, void* to) {
-  return order == MOE_ROWS_SORTED ? Rows{from, cols} : Rows{to, pitch(cols)};
+// Sorted rows that start on no multiple of 128 bytes are worth a copy, too, where there are many and each is read for
+// eight tiles or more (cost: two passes over HBM; gain: half of each later copy's time).  As they are / moved, us, forward,
+// dx, dw: [1683, 2920] to 13800 in 3 groups 173, 188, 184 / 135, 161, 154; [8192, 2920] to 4096 in 8 212, 164, 163 / 168,
+// 164, 150; [2048, 1000] to 2000 in 16 23, 20, 26 / 21, 22, 29; [24824, 5752] to 488 in 32 163 / 207 (forward).
+// other: the columns on the products' other side.
+bool moved(int order, int S, int cols, int other) {
+  return order != MOE_ROWS_SORTED || (pitch(cols) != cols && (long long)S * cols >= 1 << 22 && other >= 2048);
+}
+Rows placed(const void* from, int order, int S, int cols, int other, void* to) {
+  return moved(order, S, cols, other) ? Rows{to, pitch(cols)} : Rows{from, cols};
 }
 // Puts them there.
 bool put_in_order(const void* from, int order, const Rows& r, const int32_t* offsets, const int32_t* slots, int S, int E,
                   int cols, int top_k, bool& overlap, cudaStream_t s) {
-  if (order == MOE_ROWS_SORTED) return true;
+  if (r.at == from) return true;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cdiv(S, 8));
   cfg.blockDim = dim3(256);
@@ -933,13 +935,14 @@ bool put_in_order(const void* from, int order, const Rows& r, const int32_t* off
   cfg.attrs = attr;
   cfg.numAttrs = overlap ? 1 : 0;
   overlap = true;
-  return cudaLaunchKernelEx(&cfg, gather_rows_kernel, static_cast<const uint4*>(from), slots, offsets, E, S,
+  return cudaLaunchKernelEx(&cfg, gather_rows_kernel, static_cast<const uint4*>(from),
+                            order == MOE_ROWS_SORTED ? nullptr : slots, offsets, E, S,
                             order == MOE_ROWS_TOKEN ? top_k : 1, cols / 8, (int)(r.ld / 8),
                             static_cast<uint4*>(const_cast<void*>(r.at))) == cudaSuccess;
 }
 
-size_t rows_bytes(long long S, long long cols, int order) {
-  return order == MOE_ROWS_SORTED ? 0 : ((size_t)S * pitch(cols) * 2 + 255) / 256 * 256;
+size_t rows_bytes(int S, int cols, int other, int order) {
+  return !moved(order, S, cols, other) ? 0 : ((size_t)S * pitch(cols) * 2 + 255) / 256 * 256;
 }
 
 // The groups' maps, and room to start them on 128 bytes.
@@ -975,7 +978,7 @@ using namespace moe;
 
 extern "C" size_t moe_grouped_linear_workspace_size(int S, int E, int N, int K, int x_rows) {
   if (S <= 0 || E <= 0 || N <= 0 || K <= 0) return 0;
-  return rows_bytes(S, K, x_rows);
+  return rows_bytes(S, K, N, x_rows);
 }
 
 extern "C" moe_status_t moe_grouped_linear(const void* x, int x_rows, const void* w, const int32_t* expert_offsets,
@@ -989,14 +992,14 @@ extern "C" moe_status_t moe_grouped_linear(const void* x, int x_rows, const void
   MOE_CHECK_ARG(order_ok(x_rows, sorted_slot, S, top_k, true) && order_ok(out_rows, sorted_slot, S, top_k, false));
   MOE_CHECK_ARG(aligned16(x) && aligned16(w) && aligned16(expert_offsets) && aligned16(sorted_slot) && aligned16(out) &&
                 aligned16(ws));
-  const size_t need = rows_bytes(S, K, x_rows);
+  const size_t need = rows_bytes(S, K, N, x_rows);
   if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // Small groups fetch x's rows by four as they are; putting the rows in order first costs a launch.
   const bool direct = x_rows != MOE_ROWS_SORTED && widest(S, E) <= 64;
   const int div = x_rows == MOE_ROWS_TOKEN ? top_k : 1;
   bool overlap = false;
-  const Rows xs = direct ? Rows{x, K} : placed(x, x_rows, K, ws);
+  const Rows xs = direct ? Rows{x, K} : placed(x, x_rows, S, K, N, ws);
   if (!direct && !put_in_order(x, x_rows, xs, expert_offsets, sorted_slot, S, E, K, top_k, overlap, s)) return MOE_ERR_CUDA;
   const bool slots = x_rows != MOE_ROWS_SORTED || out_rows == MOE_ROWS_SLOT;
   const moe_status_t got =
@@ -1007,7 +1010,7 @@ extern "C" moe_status_t moe_grouped_linear(const void* x, int x_rows, const void
 
 extern "C" size_t moe_grouped_linear_backward_workspace_size(int S, int E, int N, int K, int dout_rows, int x_rows) {
   if (S <= 0 || E <= 0 || N <= 0 || K <= 0) return 0;
-  return rows_bytes(S, N, dout_rows) + rows_bytes(S, K, x_rows) + maps_bytes(E);
+  return rows_bytes(S, N, K, dout_rows) + rows_bytes(S, K, N, x_rows) + maps_bytes(E);
 }
 
 extern "C" moe_status_t moe_grouped_linear_backward(const void* dout, int dout_rows, const void* x, int x_rows,
@@ -1033,16 +1036,16 @@ extern "C" moe_status_t moe_grouped_linear_backward(const void* dout, int dout_r
                 order_ok(dx_rows, sorted_slot, S, top_k, false));
   MOE_CHECK_ARG(aligned16(dout) && aligned16(x) && aligned16(w) && aligned16(expert_offsets) && aligned16(sorted_slot) &&
                 aligned16(ws));
-  const size_t first = rows_bytes(S, N, dout_rows), need = first + (dw ? rows_bytes(S, K, x_rows) + maps_bytes(E) : 0);
+  const size_t first = rows_bytes(S, N, K, dout_rows), need = first + (dw ? rows_bytes(S, K, N, x_rows) + maps_bytes(E) : 0);
   if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   const int fp16 = dtype == MOE_DT_FP16;
   bool overlap = false;
   uint8_t* next = static_cast<uint8_t*>(ws) + first;  // behind dout's rows
-  const Rows d = placed(dout, dout_rows, N, ws), xs = placed(x, x_rows, K, next);
+  const Rows d = placed(dout, dout_rows, S, N, K, ws), xs = placed(x, x_rows, S, K, N, next);
   CUtensorMap* ends = nullptr;
   if (dw) {
     const int type = fp16 ? MOE_DT_FP16 : MOE_DT_BF16;
-    next += rows_bytes(S, K, x_rows);
+    next += rows_bytes(S, K, N, x_rows);
     ends = reinterpret_cast<CUtensorMap*>((reinterpret_cast<uintptr_t>(next) + 127) & ~uintptr_t(127));
     CUtensorMap md, mx;
     if (!make_rows_map(&md, d, type, N, S) || !make_rows_map(&mx, xs, type, K, S)) return MOE_ERR_CUDA;

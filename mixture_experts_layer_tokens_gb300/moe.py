@@ -925,8 +925,9 @@ def moe_grouped_linear(x: torch.Tensor, w: torch.Tensor, expert_offsets: torch.T
     rx, ro = _rows("x_rows", x_rows, S, top_k), _rows("out_rows", out_rows, S, top_k, False)
     if out is None:
         out = _empty((ro, N), dt, x.device, stream)
-    if ws is None and x_rows != "sorted":
-        ws = _empty((max(grouped_linear_workspace_size(S, E, N, K, x_rows), 16),), torch.uint8, x.device, stream)
+    if ws is None:
+        size = grouped_linear_workspace_size(S, E, N, K, x_rows)
+        ws = _empty((size,), torch.uint8, x.device, stream) if size else None
     dev, s = _launch(stream)
     i32 = torch.int32
     _check("moe_grouped_linear", lib().moe_grouped_linear(
@@ -960,7 +961,7 @@ def moe_grouped_linear_backward(dout: torch.Tensor, x: Optional[torch.Tensor], w
     wdt = dt if dw is None else dw.dtype
     if wdt is not dt and wdt is not torch.float32 or dw is not None and dw_dtype not in (None, wdt):
         raise TypeError(f"dw: expected {dt} or float32 as dw_dtype says, got {wdt}")
-    if ws is None and (dw is not None or dout_rows != "sorted"):
+    if ws is None:
         ws = _empty((max(grouped_linear_backward_workspace_size(S, E, N, K, dout_rows, x_rows), 16),), torch.uint8,
                     dout.device, stream)
     dev, s = _launch(stream)

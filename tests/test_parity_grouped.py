@@ -164,6 +164,24 @@ def test_long_sums(cuda_dev, counts, N, K, dtype, wdt):
     p.check_backward(*p.backward(cuda_dev, wdt))
 
 
+@pytest.mark.parametrize("counts,N,K,over", [([2000, 0, 40], 2056, 2072, 0), ([1000, 1045], 2072, 2056, 9)])
+def test_many_rows_off_128_bytes(cuda_dev, counts, N, K, over):
+    """Sorted rows that start on no multiple of 128 bytes, enough of them that they are moved to such a pitch first."""
+    p = Problem(counts, N, K, 1, BF, over=over)
+    assert moe.grouped_linear_workspace_size(p.S, p.E, N, K) == (p.S * 2112 * 2 + 255) // 256 * 256
+    p.check_forward(p.forward(cuda_dev))
+    p.check_backward(*p.backward(cuda_dev, F32))
+
+
+@pytest.mark.parametrize("dtype,wdt", [(BF, BF), (HF, F32)])
+@pytest.mark.parametrize("N,K", [(8, 8), (264, 1000), (72, 136)])
+def test_gradient_of_experts_without_rows(cuda_dev, N, K, dtype, wdt):
+    """Zeros in every place and nowhere else, whatever the sizes leave over."""
+    for counts in ([0, 3, 0], [0, 0, 0, 0, 9], [1, 0]):
+        p = Problem(counts, N, K, 1, dtype)
+        p.check_backward(*p.backward(cuda_dev, wdt))
+
+
 def test_sums_of_one_sign(cuda_dev):
     """Terms of one sign, where truncation would add up: 32 steps of 16 terms lose at most 2^-23 of the part so far
     each, 16.5 2^-23 of a part of 512, and 40 parts are added in fp32 with a half step of the sum so far each, 20.5
