@@ -12,7 +12,9 @@
  * with the experts also in other forms: moe_experts_act (other activations),
  * moe_experts_multi (routed and shared experts in the same launches),
  * moe_prepare_nvfp4 / moe_experts_nvfp4 (every operand NVFP4); and the whole
- * bf16 step as one launch for decode-sized problems: moe_layer_fused.
+ * bf16 step as one launch for decode-sized problems: moe_layer_fused.  Around it: the
+ * norm in front (moe_rmsnorm), projections and routers (moe_linear, moe_route_grouped), the
+ * experts as separate calls (moe_grouped_linear, moe_activation), and the gradients.
  *
  * Sources: "[vLLM] MoE Oracle & Prepare/Finalize" blog, section "No DP/EP: the
  * simplest case" (prepare and finalize of MoEPrepareAndFinalizeNoDPEPModular);
