@@ -14,6 +14,10 @@
 // for what lies behind them.  (Zeroing those rows in shared memory between copy and MMAs stalled the K loop some 2500
 // clocks a tile: 4096 x 14336 over groups of 1024 rows 670 us.)
 //
+// Where there are few tiles, forward and dx split the contraction over two or four pairs of a cluster: each leaves its
+// fp32 partial tile in its own shared memory, and after one cluster barrier every pair adds its share of the columns
+// over distributed shared memory, in rank order.
+//
 // Persistent, warp-specialised, pairs of CTAs: warps 0 and 2 copy stages of K blocks of A and of B by TMA (one warp for
 // both was busy 65 % of its time where K loops are short), warp 1 issues the MMAs, warps 4-11 run the epilogue from one of two accumulators in tensor memory while the
 // other fills.  Every CTA counts the tiles from the offsets itself; nothing comes back to the host.
@@ -43,6 +47,10 @@ constexpr int smem_bytes(Mode m, int E, int stages, int stage) {
 // K blocks of a sum in tensor memory, whose additions truncate, by the output's type; longer ones are added up in
 // fp32 registers with rounding (kPromote), as moe_linear's are
 constexpr int kRunFP32 = 8, kRunFP16 = 128, kRunBF16 = 256;
+// stages that splitting a tile's contraction has to save to be worth its cluster barrier and joining: not split / split, 306
+// rows of 9 experts, 256 over 9512 37 / 19 us; 2 of 8, 1024 over 4096 13 / 10.4; 512 of 2, 512 over 2048 16 / 13; 17 of 4,
+// 1472 over 3168 (saves 19) 11.9 / 13.0
+constexpr int kSplitGain = 20;
 constexpr int kLaunchRegs = 168, kLowRegs = 40, kHighRegs = 232;
 static_assert(128 * kLowRegs + 256 * kHighRegs == kThreads * kLaunchRegs, "register split must balance");
 static_assert((2 * kMaxStages + 5) * 8 + 4 <= 256 && 256 + 32 * 4 <= kCtrlBytes && smem_bytes(kForward, kMaxE, 6, 32768) <= kSmemMost && smem_bytes(kDw, kMaxE, 5, 32768) <= kSmemMost, "shared memory layout");
@@ -61,6 +69,7 @@ struct Grouped {
   int S, E;
   int P, Q;              // rows of A's tensor (forward N, dx K, dw N); dw: columns of B's (K)
   int KB;                // stages of the contraction (dw: by the group's rows)
+  int splits;            // pairs of a cluster that share a tile's (forward, dx; more than one: a tile a cluster)
   int tiles_p, tiles_q;  // of 256 rows of A; dw: of `width` columns
   int per;               // dw: tiles of an expert
   unsigned long long per_inverse;  // floor(2^64 / per) + 1: the high word of u times it is u / per
@@ -81,7 +90,7 @@ struct Unit {
   int p, q;        // tile of A; dw: of B
   int row0, rows;  // sorted rows: of the tile (forward, dx), of the group (dw)
   int width;       // columns of the tile
-  int stages;      // of its contraction
+  int stage0, stages;  // of its contraction, this pair's
   long long e;
 };
 
@@ -106,8 +115,8 @@ __device__ __forceinline__ void raster(int in, int many, int other, int& a, int&
   a = first + in - b * n;
 }
 // The tile of the unit u.  For a whole warp.
-template <Mode kMode>
-__device__ __forceinline__ Unit unit_of(const Grouped& p, const int* start, const int* pre, int u, int lane) {
+template <Mode kMode, bool kSplit>
+__device__ __forceinline__ Unit unit_of(const Grouped& p, const int* start, const int* pre, int u, int lane, int split) {
   Unit t;
   if constexpr (kMode == kDw) {
     const int e = p.per == 1 ? u : (int)__umul64hi((unsigned long long)u, p.per_inverse);
@@ -116,6 +125,7 @@ __device__ __forceinline__ Unit unit_of(const Grouped& p, const int* start, cons
     t.row0 = start[e];
     t.rows = max(0, start[e + 1] - t.row0);
     t.width = p.width;
+    t.stage0 = 0;
     t.stages = (t.rows + BK - 1) / BK;
   } else {
     int e = 0, span = p.E;  // the last e with pre[e] <= u is in [e, e + span)
@@ -132,7 +142,8 @@ __device__ __forceinline__ Unit unit_of(const Grouped& p, const int* start, cons
     t.width = (quotient(rows + n - 1, n) + 31) & ~31;
     t.row0 = start[e] + t.q * t.width;
     t.rows = min(t.width, rows - t.q * t.width);
-    t.stages = p.KB;
+    t.stage0 = kSplit ? p.KB * split / p.splits : 0;
+    t.stages = kSplit ? p.KB * (split + 1) / p.splits - t.stage0 : p.KB;
   }
   return t;
 }
@@ -254,8 +265,9 @@ __device__ __forceinline__ void add_grad16(const Grouped& p, char* buf, const fl
   __syncwarp();
 }
 
-// KS: K blocks of a stage.  kPromote: see moe_linear's kernel.
-template <Mode kMode, bool kPromote, int KS>
+// KS: K blocks of a stage.  kPromote: see moe_linear's kernel.  kSplit: p.splits pairs share a tile's contraction (in the
+// other kernels its branches cost 2 % of short tiles).
+template <Mode kMode, bool kPromote, int KS, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ Maps maps,
                         const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ Grouped p) {
@@ -278,8 +290,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* rows4 = reinterpret_cast<int*>(ctrl + 256);  // B's rows of the producer's tile (p.from)
   int* start = reinterpret_cast<int*>(ctrl + kCtrlBytes);  // [E + 1] first sorted row of each group
   int* pre = start + ((p.E + 4) & ~3);                     // [E + 1] units of the groups before it (not dw's)
-  const int half = (int)cluster_rank() & 1;
-  const uint16_t pair_mask = 3;
+  // cluster: the pairs that share a tile; the even CTA of a pair issues its MMAs
+  const int rank = (int)cluster_rank(), half = rank & 1, split = rank >> 1;
+  const uint32_t leader = rank - half;
+  const uint16_t pair_mask = (uint16_t)(3u << leader);
 
   depend_launch();
   if (warp == 2 && elect_one()) {
@@ -302,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain, 1);
     fence_mbar_init();
   }
+  __syncwarp();
   // The pair meets twice: here, with its barriers set up, and (half a microsecond later, under the rest) below.
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   if (warp == 1) tmem_take<2>(tmem_slot);
@@ -347,7 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   const int units = kMode == kDw ? p.E * p.per : pre[p.E];
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int splits = kSplit ? p.splits : 1;
+  const int first = blockIdx.x / (2 * splits), step = kSplit ? units : gridDim.x >> 1;
 
   if (warp < kFirstEpi) {
     if (kPromote) setmaxnreg_dec<kLowRegs>();
@@ -362,11 +378,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       // ---------------------------------------------------------- TMA producer of A
       const uint64_t pol = policy_evict_normal();
-      const uint32_t full0 = map_to_rank(smem_u32(full), 0);  // (both CTAs' copies complete there)
+      const uint32_t full0 = map_to_rank(smem_u32(full), leader);  // (both CTAs' copies complete there)
       long long seen = -1;  // dw: the group whose map was acquired
       if (kMode == kDw) depend_wait();  // (the weights are the caller's and wait for nothing in this call)
       for (int u = first; u < units; u += step) {
-        const Unit t = unit_of<kMode>(p, start, pre, u, lane);
+        const Unit t = unit_of<kMode, kSplit>(p, start, pre, u, lane, split);
         const int arow = (t.p * 2 + half) * kRows;
         const CUtensorMap* mA = kMode == kDw ? p.ends + 2 * t.e : &tmA;
         uint32_t bytes = 2 * KS * (kAStage + (kBMN ? b_stage : t.width / 2 * 128));  // of a stage, both CTAs', A and B
@@ -386,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* sA = smem + st * stage_bytes;
             const uint32_t bar = full0 + st * 8;
             if (half == 0) mbar_arrive_expect_tx(&full[st], bytes);
-            const int k = kMode == kDw ? t.row0 + kb * BK : kb * KS * BK;
+            const int k = kMode == kDw ? t.row0 + kb * BK : (t.stage0 + kb) * KS * BK;
             if constexpr (kMode == kForward) {
 #pragma unroll
               for (int i = 0; i < KS; ++i)
@@ -421,11 +437,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 2) {
       // ---------------------------------------------------------- TMA producer of B
       const uint64_t pol = policy_evict_normal();
-      const uint32_t full0 = map_to_rank(smem_u32(full), 0);
+      const uint32_t full0 = map_to_rank(smem_u32(full), leader);
       long long seen = -1;
       depend_wait();  // (rows put in order by an earlier kernel of this call)
       for (int u = first; u < units; u += step) {
-        const Unit t = unit_of<kMode>(p, start, pre, u, lane);
+        const Unit t = unit_of<kMode, kSplit>(p, start, pre, u, lane, split);
         const int brow = kBMN ? t.q * p.width + half * half_width : t.row0 + half * (t.width / 2);
         const CUtensorMap* mB =
             kMode == kDw ? p.ends + 2 * t.e + 1 : &maps.b[kMode == kForward && p.from ? 0 : t.width / 32 - 1];
@@ -454,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             uint8_t* sB = smem + st * stage_bytes + KS * kAStage;
             const uint32_t bar = full0 + st * 8;
-            const int k = kMode == kDw ? t.row0 + kb * BK : kb * KS * BK;
+            const int k = kMode == kDw ? t.row0 + kb * BK : (t.stage0 + kb) * KS * BK;
             if (kMode == kForward && p.from) {
               for (int g = 0; g < fours; ++g) {
                 const int4 rows = reinterpret_cast<const int4*>(rows4)[g];
@@ -488,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int acc = 0;
       uint32_t acc_phase = 0;
       for (int u = first; u < units && !failed; u += step) {
-        const Unit t = unit_of<kMode>(p, start, pre, u, lane);
+        const Unit t = unit_of<kMode, kSplit>(p, start, pre, u, lane, split);
         const uint32_t idesc = p.idesc | (uint32_t)(t.width >> 3) << 17;
         const int chunk = kPromote ? p.chunk : t.stages;
         for (int kc = 0; kc < t.stages; kc += chunk) {
@@ -536,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+    if (kSplit) cluster_sync();  // (the partial tiles are in shared memory)
     // Every stage comes back before this CTA leaves: the commits of the pair's MMAs arrive on the barriers here.
     if (warp == 0 && elect_one() && !failed)
       for (int i = 0; i < stages && lane_wait<false>(&empty[stage], phase ^ 1); ++i)
@@ -550,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int side = (warp - kFirstEpi) >> 2;  // forward, dx: every other 32 columns; dw: half of them
     char* buf = bufs + (warp - kFirstEpi) * buf_bytes(kMode);
     const uint32_t tb = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t freed = map_to_rank(smem_u32(tempty), 0);
+    const uint32_t freed = map_to_rank(smem_u32(tempty), leader);
     int acc = 0;
     uint32_t acc_phase = 0;
     auto release = [&]() {  // this warp is done with the accumulator
@@ -565,23 +582,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto at = [&](int c) { return kMode == kDw ? side * (p.width / 2) + c * 32 : c * 64 + side * 32; };
     // Rows of out of a tile's columns (see store_rows32).  (Asked for a tile ahead: their latency would be a good part
     // of a short tile's time.)
+    auto row_of = [&](const Unit& t, int col) {
+      const int row = col < t.rows ? t.row0 + col : -1;
+      if (!p.slots || row < 0) return row;
+      const int slot = __ldg(p.slots + row);
+      const bool bad = slot < 0 || slot >= p.S;
+      if (bad) record_invalid();
+      return bad ? -1 : p.to_slots ? slot : row;
+    };
     auto rows_of = [&](const Unit& t, int (&to)[4]) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int row = at(c) + lane;
-        to[c] = row < t.rows ? t.row0 + row : -1;
-        if (p.slots && to[c] >= 0) {
-          const int slot = __ldg(p.slots + to[c]);
-          const bool bad = slot < 0 || slot >= p.S;
-          if (bad) record_invalid();
-          to[c] = bad ? -1 : p.to_slots ? slot : to[c];
-        }
-      }
+      for (int c = 0; c < 4; ++c) to[c] = row_of(t, at(c) + lane);
     };
+    // A split tile's sums, by columns: a column's 128 rows are neighbours (this CTA's stages: every copy has landed and
+    // every MMA has read it when the accumulator is complete).
+    float* part = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
     Unit t = {};
     int to[4] = {};
     if (first < units) {
-      t = unit_of<kMode>(p, start, pre, first, lane);
+      t = unit_of<kMode, kSplit>(p, start, pre, first, lane, split);
       if (kMode != kDw) rows_of(t, to);
     }
     for (int u = first; u < units; u += step) {
@@ -621,6 +640,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 16; ++i) words[c][i] = pack16(v[2 * i], v[2 * i + 1], p.fp16);
+              if (kSplit) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) part[(at(c) + i) * kRows] = v[i];
+              }
             }
           release();
         }
@@ -628,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Unit next = {};
       int next_to[4] = {};
       if (u + step < units) {
-        next = unit_of<kMode>(p, start, pre, u + step, lane);
+        next = unit_of<kMode, kSplit>(p, start, pre, u + step, lane, split);
         if (kMode != kDw) rows_of(next, next_to);
       }
       // the c-th 32 columns in 16 bits, two to a word
@@ -641,6 +664,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[i] = words[c][i];
         }
       };
+      if (kSplit) {  // (joined below)
+        if constexpr (kPromote) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (at(c) < cols) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) part[(at(c) + i) * kRows] = sums[c * 32 + i];
+            }
+        }
+        break;
+      }
       if constexpr (kMode != kDw) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -687,6 +721,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 4; ++c) to[c] = next_to[c];
     }
     if (kMode == kDw && lane == 0) tma_store_wait();
+    if (kSplit) {
+      __syncwarp();
+      cluster_sync();  // every pair's partial tile is in its shared memory
+      const int n0 = (t.p * 2 + half) * kRows + quarter * 32, cols = first < units && n0 < p.P ? t.rows : 0;
+      const uint32_t mine = smem_u32(part);
+      // (a wait that gave up, here or in another CTA, leaves wrong values, and is recorded)
+      for (int c = (side * splits + split) * 32; c < cols; c += 64 * splits) {
+        const int row = row_of(t, c + lane);
+        uint32_t w[16];
+#pragma unroll
+        for (int h = 0; h < 32; h += 8) {
+          float z[8] = {};
+          for (int s = 0; s < splits; ++s) {
+            const uint32_t from = map_to_rank(mine + (uint32_t)((c + h) * kRows * 4), 2 * s + half);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = ld_cluster1(from + i * kRows * 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] += v[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) w[(h + i) / 2] = pack16(z[i], z[i + 1], p.fp16);
+        }
+        store_rows32(p, buf, w, n0, row, lane);
+      }
+    }
   }
 
   // (whoever had nothing to wait for: what comes after this kernel comes after the one before it, too)
@@ -796,10 +856,10 @@ bool make_rows_map(CUtensorMap* m, const Rows& r, int dtype, long long cols, lon
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <Mode kMode, bool kPromote, int KS>
+template <Mode kMode, bool kPromote, int KS, bool kSplit>
 cudaError_t launch(const CUtensorMap& ma, const Maps& mb, const CUtensorMap& mo, const Grouped& g, long long units,
                    int smem, bool overlap, cudaStream_t s) {
-  auto kern = grouped_gemm_kernel<kMode, kPromote, KS>;
+  auto kern = grouped_gemm_kernel<kMode, kPromote, KS, kSplit>;
   if (kPromote) {
     // The epilogue's warps take registers that the first warpgroup gives back (setmaxnreg): a build with another
     // count than the split assumes would wait for them without an end, so it never launches.
@@ -820,22 +880,57 @@ cudaError_t launch(const CUtensorMap& ma, const Maps& mb, const CUtensorMap& mo,
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = 2 * g.splits;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1] = overlap_attr();
   cfg.attrs = attr;
   const long long pairs = num_sms() / 2;
-  cfg.gridDim = dim3((unsigned)(2 * (units < pairs ? units : pairs)));
+  cfg.gridDim = dim3((unsigned)(2 * (g.splits > 1 ? units * g.splits : units < pairs ? units : pairs)));
   cfg.numAttrs = overlap ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, ma, mb, mo, g);
 }
 template <Mode kMode, bool kPromote>
 cudaError_t launch(int ks, const CUtensorMap& ma, const Maps& mb, const CUtensorMap& mo, const Grouped& g,
                    long long units, int smem, bool overlap, cudaStream_t s) {
-  if constexpr (kMode != kDw)
-    if (ks == 2) return launch<kMode, kPromote, 2>(ma, mb, mo, g, units, smem, overlap, s);
-  return launch<kMode, kPromote, 1>(ma, mb, mo, g, units, smem, overlap, s);
+  if constexpr (kMode != kDw) {
+    if (g.splits > 1)
+      return ks == 2 ? launch<kMode, kPromote, 2, true>(ma, mb, mo, g, units, smem, overlap, s)
+                     : launch<kMode, kPromote, 1, true>(ma, mb, mo, g, units, smem, overlap, s);
+    if (ks == 2) return launch<kMode, kPromote, 2, false>(ma, mb, mo, g, units, smem, overlap, s);
+  }
+  return launch<kMode, kPromote, 1, false>(ma, mb, mo, g, units, smem, overlap, s);
+}
+
+// Clusters of `size` CTAs that fit the device at once (a cluster lies within one group of SMs), asked once per device and
+// size.
+int cluster_slots(int size) {
+  static std::atomic<int> cached[64][4];  // (host threads may come at once)
+  int dev = 0, log2 = 0;
+  while ((1 << log2) < size) ++log2;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = cached[dev][log2].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemMost;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto kern = grouped_gemm_kernel<kForward, false, 1, true>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      n = -1;
+    }
+    cached[dev][log2].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 // Columns of a tile at most: narrow ones leave room for more stages where the groups are small.
@@ -891,6 +986,10 @@ moe_status_t run(const void* a, const Rows& b, const Rows& d, const int32_t* off
   const long long units =
       kMode == kDw ? (long long)E * g.tiles_p * g.tiles_q : (long long)g.tiles_p * (S / g.width + (S < E ? S : E));
   if (units > 1073741823LL) return MOE_ERR_UNSUPPORTED;
+  g.splits = 1;
+  if (kMode != kDw)
+    for (int s = 4; s > 1 && g.splits == 1; s /= 2)
+      if (units <= cluster_slots(2 * s) && g.KB - g.KB / s >= kSplitGain) g.splits = s;
   CUtensorMap ma, mo;
   Maps mb;
   const int type = fp16 ? MOE_DT_FP16 : MOE_DT_BF16;

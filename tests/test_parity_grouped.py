@@ -129,6 +129,26 @@ def test_grouped(cuda_dev, shape, orders, dtype):
 
 
 @pytest.mark.parametrize("orders", ORDERS)
+@pytest.mark.parametrize("counts,N,K", [([30, 0, 50], 264, 4104), ([200, 130], 72, 1600), ([30, 1, 49], 4104, 136),
+                                        ([3], 520, 8200), ([700, 300], 16, 3080)])
+def test_few_tiles(cuda_dev, counts, N, K, orders):
+    """Tiles so few, and sums so long, that several CTAs share a tile's sum (forward, dx or both): right, and the same bits
+    each time."""
+    x_rows, rows, d_rows = orders
+    p = Problem(counts, N, K, 1, HF, x_rows, rows, d_rows)
+    out = p.forward(cuda_dev)
+    p.check_forward(out)
+    first = out.clone()
+    for _ in range(3):
+        assert torch.equal(p.forward(cuda_dev), first)
+    dx, dw = p.backward(cuda_dev)
+    p.check_backward(dx, dw)
+    first = dx.clone()
+    assert torch.equal(p.backward(cuda_dev)[0], first)
+    assert moe.moe_device_status() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("orders", ORDERS)
 def test_rows_of_no_group(cuda_dev, orders):
     """Sorted rows behind the last group, NaN here, are neither used nor written."""
     x_rows, rows, d_rows = orders
