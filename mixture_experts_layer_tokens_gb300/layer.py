@@ -106,6 +106,7 @@ class MoEExperts:
         self.dh, self.drows, self.da1 = empty((S, I)), empty((S, H)), empty((T, H))
         self.dw13, self.dw2 = empty((E, rows13, H), dw_dtype or dt), empty((E, H, I), dw_dtype or dt)
         self.ws = empty((max(moe.grouped_linear_workspace_size(S, E, rows13, H, "token"),
+                             moe.grouped_linear_workspace_size(S, E, H, I, "sorted"),
                              moe.grouped_linear_backward_workspace_size(S, E, H, I, "slot", "sorted"),
                              moe.grouped_linear_backward_workspace_size(S, E, rows13, H, "sorted", "token"), 16),),
                         torch.uint8)

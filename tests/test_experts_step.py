@@ -71,6 +71,23 @@ def test_experts_training_step(cuda_dev, act, dtype):
     assert moe.moe_device_status() == moe.MOE_OK
 
 
+def test_workspace_of_many_rows_off_128_bytes(cuda_dev):
+    """Enough rows of an odd width that the products move them first: the object's one workspace is enough for each."""
+    T, k, E, H, I = 2100, 1, 2, 2056, 2072
+    ids, a1, w13, w2, dy = (t.to(cuda_dev) for t in _experts(T, k, E, H, I, "silu_no_mul", BF, seed=4))
+    assert moe.grouped_linear_workspace_size(T, E, H, I) > 0
+    al = moe.moe_align(ids, E)
+    ex = MoEExperts(w13, w2, T, k, "silu_no_mul")
+    y = ex.forward(a1, al)
+    assert torch.equal(y, moe.moe_grouped_linear(ex.h, w2, al.expert_offsets, al.sorted_slot, k, out_rows="slot"))
+    h = ex.h.clone()
+    dw13, dw2, _ = ex.backward(dy, a1, al)
+    dh, want = moe.moe_grouped_linear_backward(dy, h, w2, al.expert_offsets, al.sorted_slot, k, dout_rows="slot")
+    assert torch.equal(dw2, want) and torch.equal(ex.dh, dh)
+    _, want = moe.moe_grouped_linear_backward(ex.gu, a1, w13, al.expert_offsets, al.sorted_slot, k, x_rows="token")
+    assert torch.equal(dw13, want)
+
+
 def test_layer_step_trains_router_and_experts(cuda_dev):
     """forward, the finalize's gradients, the router's and the experts': the experts' against autograd over the whole
     sum (dy is rounded once more on the way)."""
@@ -109,7 +126,7 @@ def test_experts_backward_refuses(cuda_dev, quant):
 
 
 @pytest.mark.parametrize("residual", [False, True])
-@pytest.mark.parametrize("quant", ["bf16", "fp8", "fp8_token", "fp8_tensor"])
+@pytest.mark.parametrize("quant", ["bf16", "fp8", "fp8_token", "fp8_tensor", "nvfp4"])
 def test_layer_with_input_norm(cuda_dev, quant, residual):
     """The layer on what the norm gives, bit for bit: the same calls on moe_rmsnorm's outputs."""
     T, H = 37, 512

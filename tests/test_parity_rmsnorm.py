@@ -97,8 +97,9 @@ def test_rmsnorm_rows_are_their_own(cuda_dev, T, H):
     assert torch.isnan(odd[0][T // 2]).all() and torch.isnan(odd[2].view(torch.float8_e4m3fn)[T // 2].float()).all()
 
 
-def test_rmsnorm_in_place(cuda_dev):
-    x, res, w = _inputs(64, 1024)
+@pytest.mark.parametrize("T,H", [(64, 1024), (3000, 1024), (2500, 4096)])
+def test_rmsnorm_in_place(cuda_dev, T, H):
+    x, res, w = _inputs(T, H)
     a, b, c = x.to(cuda_dev), res.to(cuda_dev), w.to(cuda_dev)
     outs = moe.moe_rmsnorm(a, c, residual=b, out=a, residual_out=b, quant="fp8")
     assert outs[0] is a and outs[1] is b
