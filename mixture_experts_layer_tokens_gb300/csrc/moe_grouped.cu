@@ -759,56 +759,73 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_release<2>(tmem);
 }
 
-// ------------------------------------------------------------------ rows into sorted order
-__device__ __forceinline__ void gather_row(const uint4* __restrict__ from, int slot, int S, int div, int nvec,
-                                           uint4* __restrict__ d, int lane) {
-  if (slot < 0 || slot >= S) {
+// ------------------------------------------------------------------ what comes before the products
+// Rows put into sorted order, and the maps that end with each group, in one launch.
+struct Move {
+  const uint4* from;
+  uint4* to;
+  int rows;           // 0: nothing is moved
+  int nvec, pitch;    // 16-byte vectors of a row, and between rows of `to`
+  int div, by_slots;  // row p of `to` is row slots[p] / div of `from`, or p
+};
+struct Setup {
+  CUtensorMap d, x;   // maps of dout's and x's sorted rows
+  CUtensorMap* ends;  // [2 e] and [2 e + 1]: d and x with their rows cut at the end of group e
+  const int32_t *slots, *offsets;
+  int E, S;
+  int map_blocks, first_blocks;  // blocks (of 8 warps, a warp a map or a row) of the maps, of move[0]
+  Move move[2];
+};
+
+__device__ __forceinline__ void move_row(const Move& m, const Setup& p, int row, int lane) {
+  if (row >= m.rows || row >= __ldg(p.offsets + p.E)) return;
+  const int slot = m.by_slots ? __ldg(p.slots + row) : row;
+  uint4* d = m.to + (size_t)row * m.pitch;
+  if (slot < 0 || slot >= p.S) {
     if (lane == 0) record_invalid();
-    for (int i = lane; i < nvec; i += 32) d[i] = make_uint4(0, 0, 0, 0);
+    for (int i = lane; i < m.nvec; i += 32) d[i] = make_uint4(0, 0, 0, 0);
     return;
   }
-  const uint4* s = from + (size_t)(slot / div) * nvec;
+  const uint4* s = m.from + (size_t)(slot / m.div) * m.nvec;
   int i = lane;
-  for (; i + 96 < nvec; i += 128) {
+  for (; i + 96 < m.nvec; i += 128) {
     uint4 v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = __ldg(s + i + j * 32);
 #pragma unroll
     for (int j = 0; j < 4; ++j) d[i + j * 32] = v[j];
   }
-  for (; i < nvec; i += 32) d[i] = __ldg(s + i);
-}
-// to[p] = from[slots[p] / div] for the sorted rows p that belong to a group: a warp a row.
-__global__ void __launch_bounds__(256)
-    gather_rows_kernel(const uint4* __restrict__ from, const int32_t* __restrict__ slots,
-                       const int32_t* __restrict__ offsets, int E, int S, int div, int nvec, int pitch,
-                       uint4* __restrict__ to) {
-  depend_launch();
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row < S && row < __ldg(offsets + E)) gather_row(from, slots ? __ldg(slots + row) : row, S, div, nvec, to + (size_t)row * pitch, lane);
-  depend_wait();  // (not for its own sake: what comes after this kernel comes after the one before it, too)
+  for (; i < m.nvec; i += 32) d[i] = __ldg(s + i);
 }
 
-// ------------------------------------------------------------------ maps that end with a group
-// ends[2 e] and ends[2 e + 1]: the maps of dout and x with their rows cut at the end of group e.  A warp a map.
-__global__ void __launch_bounds__(32)
-    group_maps_kernel(const __grid_constant__ CUtensorMap d, const __grid_constant__ CUtensorMap x,
-                      const int32_t* __restrict__ offsets, int S, CUtensorMap* ends) {
-  __shared__ __align__(128) CUtensorMap map;
+__global__ void __launch_bounds__(256) grouped_setup_kernel(const __grid_constant__ Setup p) {
+  __shared__ __align__(128) CUtensorMap maps[8];
   depend_launch();
-  const int end = min(max(__ldg(offsets + (blockIdx.x >> 1) + 1), 0), S), lane = threadIdx.x;
-  const CUtensorMap& from = blockIdx.x & 1 ? x : d;
-  reinterpret_cast<uint32_t*>(&map)[lane] = reinterpret_cast<const uint32_t*>(&from)[lane];
-  __syncwarp();
-  if (lane == 0)
-    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(smem_u32(&map)), "r"(max(end, 1))
-                 : "memory");
-  __syncwarp();
-  asm volatile(
-      "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
-          reinterpret_cast<uint64_t>(ends + blockIdx.x)),
-      "r"(smem_u32(&map))
-      : "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int block = blockIdx.x;
+  if (block < p.map_blocks) {
+    const int i = block * 8 + warp;
+    if (i >= 2 * p.E) return;
+    const int end = min(max(__ldg(p.offsets + (i >> 1) + 1), 0), p.S);
+    CUtensorMap* map = &maps[warp];
+    reinterpret_cast<uint32_t*>(map)[lane] = reinterpret_cast<const uint32_t*>(i & 1 ? &p.x : &p.d)[lane];
+    __syncwarp();
+    if (lane == 0)
+      asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(smem_u32(map)), "r"(max(end, 1))
+                   : "memory");
+    __syncwarp();
+    asm volatile(
+        "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
+            reinterpret_cast<uint64_t>(p.ends + i)),
+        "r"(smem_u32(map))
+        : "memory");
+    return;
+  }
+  block -= p.map_blocks;
+  if (block < p.first_blocks)
+    move_row(p.move[0], p, block * 8 + warp, lane);
+  else
+    move_row(p.move[1], p, (block - p.first_blocks) * 8 + warp, lane);
 }
 
 // ------------------------------------------------------------------ host side
@@ -1022,22 +1039,18 @@ bool moved(int order, int S, int cols, int other) {
 Rows placed(const void* from, int order, int S, int cols, int other, void* to) {
   return moved(order, S, cols, other) ? Rows{to, pitch(cols)} : Rows{from, cols};
 }
-// Puts them there.
-bool put_in_order(const void* from, int order, const Rows& r, const int32_t* offsets, const int32_t* slots, int S, int E,
-                  int cols, int top_k, bool& overlap, cudaStream_t s) {
-  if (r.at == from) return true;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)cdiv(S, 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1] = {overlap_attr()};
-  cfg.attrs = attr;
-  cfg.numAttrs = overlap ? 1 : 0;
-  overlap = true;
-  return cudaLaunchKernelEx(&cfg, gather_rows_kernel, static_cast<const uint4*>(from),
-                            order == MOE_ROWS_SORTED ? nullptr : slots, offsets, E, S,
-                            order == MOE_ROWS_TOKEN ? top_k : 1, cols / 8, (int)(r.ld / 8),
-                            static_cast<uint4*>(const_cast<void*>(r.at))) == cudaSuccess;
+// What puts them there.
+Move move_of(const void* from, int order, const Rows& r, int S, int cols, int top_k) {
+  return Move{static_cast<const uint4*>(from), static_cast<uint4*>(const_cast<void*>(r.at)), r.at == from ? 0 : S, cols / 8,
+              (int)(r.ld / 8), order == MOE_ROWS_TOKEN ? top_k : 1, order != MOE_ROWS_SORTED};
+}
+// Its launch, if there is anything to do; the next one may then overlap it.
+bool set_up(Setup& p, cudaStream_t s) {
+  p.map_blocks = p.ends ? cdiv(2 * p.E, 8) : 0;
+  p.first_blocks = cdiv(p.move[0].rows, 8);
+  const int blocks = p.map_blocks + p.first_blocks + cdiv(p.move[1].rows, 8);
+  if (blocks) grouped_setup_kernel<<<blocks, 256, 0, s>>>(p);
+  return blocks > 0;
 }
 
 size_t rows_bytes(int S, int cols, int other, int order) {
@@ -1097,9 +1110,14 @@ extern "C" moe_status_t moe_grouped_linear(const void* x, int x_rows, const void
   // Small groups fetch x's rows by four as they are; putting the rows in order first costs a launch.
   const bool direct = x_rows != MOE_ROWS_SORTED && widest(S, E) <= 64;
   const int div = x_rows == MOE_ROWS_TOKEN ? top_k : 1;
-  bool overlap = false;
   const Rows xs = direct ? Rows{x, K} : placed(x, x_rows, S, K, N, ws);
-  if (!direct && !put_in_order(x, x_rows, xs, expert_offsets, sorted_slot, S, E, K, top_k, overlap, s)) return MOE_ERR_CUDA;
+  Setup setup = {};
+  setup.slots = sorted_slot;
+  setup.offsets = expert_offsets;
+  setup.E = E;
+  setup.S = S;
+  setup.move[0] = move_of(x, x_rows, xs, S, K, top_k);
+  const bool overlap = set_up(setup, s);
   const bool slots = x_rows != MOE_ROWS_SORTED || out_rows == MOE_ROWS_SLOT;
   const moe_status_t got =
       run<kForward>(w, xs, xs, expert_offsets, slots ? sorted_slot : nullptr, out_rows == MOE_ROWS_SLOT,
@@ -1138,21 +1156,22 @@ extern "C" moe_status_t moe_grouped_linear_backward(const void* dout, int dout_r
   const size_t first = rows_bytes(S, N, K, dout_rows), need = first + (dw ? rows_bytes(S, K, N, x_rows) + maps_bytes(E) : 0);
   if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   const int fp16 = dtype == MOE_DT_FP16;
-  bool overlap = false;
   uint8_t* next = static_cast<uint8_t*>(ws) + first;  // behind dout's rows
   const Rows d = placed(dout, dout_rows, S, N, K, ws), xs = placed(x, x_rows, S, K, N, next);
-  CUtensorMap* ends = nullptr;
+  Setup setup = {};
+  setup.slots = sorted_slot;
+  setup.offsets = expert_offsets;
+  setup.E = E;
+  setup.S = S;
+  setup.move[0] = move_of(dout, dout_rows, d, S, N, top_k);
   if (dw) {
     const int type = fp16 ? MOE_DT_FP16 : MOE_DT_BF16;
     next += rows_bytes(S, K, N, x_rows);
-    ends = reinterpret_cast<CUtensorMap*>((reinterpret_cast<uintptr_t>(next) + 127) & ~uintptr_t(127));
-    CUtensorMap md, mx;
-    if (!make_rows_map(&md, d, type, N, S) || !make_rows_map(&mx, xs, type, K, S)) return MOE_ERR_CUDA;
-    group_maps_kernel<<<2 * E, 32, 0, s>>>(md, mx, expert_offsets, S, ends);
-    overlap = true;
+    setup.ends = reinterpret_cast<CUtensorMap*>((reinterpret_cast<uintptr_t>(next) + 127) & ~uintptr_t(127));
+    setup.move[1] = move_of(x, x_rows, xs, S, K, top_k);
+    if (!make_rows_map(&setup.d, d, type, N, S) || !make_rows_map(&setup.x, xs, type, K, S)) return MOE_ERR_CUDA;
   }
-  if (!put_in_order(dout, dout_rows, d, expert_offsets, sorted_slot, S, E, N, top_k, overlap, s)) return MOE_ERR_CUDA;
-  if (dw && !put_in_order(x, x_rows, xs, expert_offsets, sorted_slot, S, E, K, top_k, overlap, s)) return MOE_ERR_CUDA;
+  bool overlap = set_up(setup, s);
   if (dx) {
     const bool slots = dout_rows != MOE_ROWS_SORTED || dx_rows == MOE_ROWS_SLOT;
     st = run<kDx>(w, d, d, expert_offsets, slots ? sorted_slot : nullptr, dx_rows == MOE_ROWS_SLOT, nullptr, 1, S, E, N, K, fp16,
@@ -1161,7 +1180,7 @@ extern "C" moe_status_t moe_grouped_linear_backward(const void* dout, int dout_r
     overlap = true;
   }
   if (dw) {
-    st = run<kDw>(nullptr, xs, d, expert_offsets, nullptr, 0, nullptr, 1, S, E, N, K, fp16, dw, out32, accumulate != 0, ends, overlap, s);
+    st = run<kDw>(nullptr, xs, d, expert_offsets, nullptr, 0, nullptr, 1, S, E, N, K, fp16, dw, out32, accumulate != 0, setup.ends, overlap, s);
     if (st != MOE_OK) return st;
   }
   return launch_status();
