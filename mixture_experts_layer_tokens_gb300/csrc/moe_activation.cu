@@ -5,15 +5,16 @@
 //   dg = dh act'(g) u,  du = dh act(g)  (swigluoai: 0 for what a clamp holds, the border itself passes)
 //
 // Bound by HBM: 6 bytes read and written a column pair forward, 10 backward (12 with h made again), some 30
-// operations.  A thread takes two vectors of 8 columns, all loads before the first use; each value is read and
-// written once, in fp32 in between.
+// operations.  A thread takes one vector of 8 columns, its loads before their first use; each value is read and
+// written once, in fp32 in between.  Vectors a thread 1 / 2 / 4 in blocks of 128 threads: SiLU of 16384 x 14336 194 / 219
+// / 277 us, its gradient with h of 8192 x 14336 199 / 212 / 263; one vector in blocks of 256 196 and 199, of 512 201 and 197
+// (1.41 GB each: 7.2 TB/s).
 #include "moe_act.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kVecs = 2;  // vectors a thread
+constexpr int kThreads = 128;
 
 __device__ __forceinline__ float at_least(float z, float low) { return z < low ? low : z; }  // (a NaN stays)
 __device__ __forceinline__ float at_most(float z, float high) { return z > high ? high : z; }
@@ -58,51 +59,39 @@ template <class T, int kAct, bool kBackward>
 __global__ void __launch_bounds__(kThreads) activation_kernel(const Act p) {
   constexpr bool kMul = kAct != MOE_ACT_SILU_NO_MUL && kAct != MOE_ACT_GELU_NO_MUL;
   const T* gu = static_cast<const T*>(p.gu);
-  const long long I = (long long)p.nv * 8, v0 = (long long)blockIdx.x * (kThreads * kVecs) + threadIdx.x;
-  float g[kVecs][8], u[kVecs][8], d[kVecs][8];
-  long long at[kVecs], to[kVecs];  // in gu and dgu; in h and dh
+  const long long I = (long long)p.nv * 8, v = (long long)blockIdx.x * kThreads + threadIdx.x;
+  if (v >= p.total) return;
+  long long row;
+  int col;
+  place(p, v, row, col);
+  const long long to = v * 8, at = kMul ? row * 2 * I + col : to;  // in h and dh; in gu and dgu
+  float g[8], u[8], d[8], h[8], dg[8], du[8];
+  load8(gu + at, g);
+  if (kMul) load8(gu + at + I, u);
+  if (kBackward) load8(static_cast<const T*>(p.dh) + to, d);
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const long long v = v0 + i * kThreads;
-    if (v >= p.total) continue;
-    long long row;
-    int col;
-    place(p, v, row, col);
-    to[i] = v * 8;
-    at[i] = kMul ? row * 2 * I + col : to[i];
-    load8(gu + at[i], g[i]);
-    if (kMul) load8(gu + at[i] + I, u[i]);
-    if (kBackward) load8(static_cast<const T*>(p.dh) + to[i], d[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    if (v0 + i * kThreads >= p.total) continue;
-    float h[8], dg[8], du[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float slope = 0.f;
-      const float a = gate<kAct, kBackward>(g[i][j], slope);
-      float m = 1.f;  // what act(g) is multiplied by
-      if (kMul) m = kAct == MOE_ACT_SWIGLUOAI ? at_least(at_most(u[i][j], 7.f), -7.f) + 1.f : u[i][j];
-      h[j] = kMul ? a * m : a;
-      if (kBackward) {
-        dg[j] = kMul ? d[i][j] * slope * m : d[i][j] * slope;
-        du[j] = kAct == MOE_ACT_SWIGLUOAI && fabsf(u[i][j]) > 7.f ? 0.f : d[i][j] * a;
-      }
-    }
+  for (int j = 0; j < 8; ++j) {
+    float slope = 0.f;
+    const float a = gate<kAct, kBackward>(g[j], slope);
+    float m = 1.f;  // what act(g) is multiplied by
+    if (kMul) m = kAct == MOE_ACT_SWIGLUOAI ? at_least(at_most(u[j], 7.f), -7.f) + 1.f : u[j];
+    h[j] = kMul ? a * m : a;
     if (kBackward) {
-      T* dgu = static_cast<T*>(p.dgu);
-      store8(dgu + at[i], dg);
-      if (kMul) store8(dgu + at[i] + I, du);
+      dg[j] = kMul ? d[j] * slope * m : d[j] * slope;
+      du[j] = kAct == MOE_ACT_SWIGLUOAI && fabsf(u[j]) > 7.f ? 0.f : d[j] * a;
     }
-    if (!kBackward || p.h) store8(static_cast<T*>(p.h) + to[i], h);
   }
+  if (kBackward) {
+    T* dgu = static_cast<T*>(p.dgu);
+    store8(dgu + at, dg);
+    if (kMul) store8(dgu + at + I, du);
+  }
+  if (!kBackward || p.h) store8(static_cast<T*>(p.h) + to, h);
 }
 
 template <class T, bool kBackward>
 void launch(int act, const Act& p, cudaStream_t s) {
-  const long long per = kThreads * kVecs;
-  const unsigned grid = (unsigned)((p.total + per - 1) / per);
+  const unsigned grid = (unsigned)((p.total + kThreads - 1) / kThreads);
   switch (act) {
     case MOE_ACT_SILU: activation_kernel<T, MOE_ACT_SILU, kBackward><<<grid, kThreads, 0, s>>>(p); break;
     case MOE_ACT_GELU: activation_kernel<T, MOE_ACT_GELU, kBackward><<<grid, kThreads, 0, s>>>(p); break;
@@ -123,7 +112,7 @@ moe_status_t run(const void* dh, const void* gu, int S, int I, moe_dtype_t dtype
   MOE_CHECK_ARG(gu && (kBackward ? dh && dgu : h != nullptr));
   MOE_CHECK_ARG(aligned16(gu) && aligned16(dh) && aligned16(dgu) && aligned16(h));
   const Act p{gu, dh, h, dgu, (long long)S * (I / 8), I / 8};
-  if (p.total > (1ll << 39)) return MOE_ERR_UNSUPPORTED;  // (the grid's limit; 2^42 values)
+  if (p.total > (1ll << 37)) return MOE_ERR_UNSUPPORTED;  // (the grid's limit; 2^40 values)
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == MOE_DT_FP16)
     launch<__half, kBackward>(act, p, s);

@@ -12,7 +12,7 @@
 // token's experts read their weights once over narrow tiles.  dw has no ragged side but its contraction: a small
 // kernel makes tensor maps that end with each group, so that the copies of a group's last rows bring zeros
 // for what lies behind them.  (Zeroing those rows in shared memory between copy and MMAs stalled the K loop some 2500
-// clocks a tile: 4096 x 14336 over groups of 1024 rows 670 us.)
+// clocks a tile: both gradients of 4096 x 14336 over groups of 1024 rows 1338 us, like this 1207.)
 //
 // Where there are few tiles, forward and dx split the contraction over two or four pairs of a cluster: each leaves its
 // fp32 partial tile in its own shared memory, and after one cluster barrier every pair adds its share of the columns
