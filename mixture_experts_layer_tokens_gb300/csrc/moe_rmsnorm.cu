@@ -215,12 +215,15 @@ extern "C" moe_status_t moe_rmsnorm(const void* x, const void* residual, const v
     constexpr bool kRing = decltype(ring)::value;
     const int need = (nvec + NV - 1) / NV;
     p.threads = need <= 16 ? 16 : (need + 31) / 32 * 32;
-    const int rows = p.threads >= 128 ? 1 : 128 / p.threads, block = rows * p.threads;
+    int rows = p.threads >= 128 ? 1 : 128 / p.threads;
+    if (NV == 4)
+      while (2 * rows * p.threads <= 512 && (long long)2 * rows * num_sms() <= T) rows *= 2;
+    const int block = rows * p.threads;
     const int turns = (T + rows - 1) / rows;
     const int smem = kRing ? 2 * rows * H * 2 * (residual ? 2 : 1) : 0;
     int ctas = 2048 / block;  // of an SM
     if (kRing) {
-      const int by_regs = kRegs / (block * (NV == 4 ? 120 : 64)), by_smem = 232448 / (smem + 2048);
+      const int by_regs = kRegs / (block * (NV == 4 ? 104 : 64)), by_smem = 232448 / (smem + 2048);
       ctas = by_regs < by_smem ? by_regs : by_smem;
       if (ctas < 1) ctas = 1;
       // (the same for every call: host threads may come at once)
@@ -233,9 +236,11 @@ extern "C" moe_status_t moe_rmsnorm(const void* x, const void* residual, const v
   };
   // Few rows: one round of loads a thread and no ring.  [1, 7168] with all outputs 4.4 us in a graph, by the ring 5.1.
   if (nvec <= kMaxThreads && T <= num_sms()) return go(std::integral_constant<int, 1>(), std::false_type());
-  // With 1 / 2 / 4 vectors a thread, all outputs: [16384, 7168] 207 / 185 / 179 us, [8192, 16384] 181 / 188 / 181,
-  // [4096, 7168] 55 / 46 / 45, [1024, 7168] 17 / 13.5 / 15, [16384, 1024] 28 / 29 / 28, [65536, 128] 14 / 16 / 24 (by the
-  // threads' own loads 300, 319, 79, 23, 39, 32).
-  if (nvec >= 512 && T >= 2048) return go(std::integral_constant<int, 4>(), std::true_type());
+  // Many long rows: four vectors a thread and one CTA of up to 512 threads an SM, whose copies are long and neighbours in
+  // memory; else two vectors, and CTAs of one row or 128 threads.  All outputs, two vectors / four in CTAs of one row or
+  // 128 threads / four in CTAs of 512: [16384, 7168] 185 / 179 / 162 us, [16384, 2048] 57 / 55 / 49, [16384, 1024] 29 / 28 /
+  // 27, [16384, 256] 9.0 / 12 / 12, [65536, 128] 15 / 24 / 25, [1024, 7168] 13.4 / 15 / 16 (by the threads' own loads 300,
+  // 76, 39, 15, 32, 23).
+  if (nvec >= 64 && T >= 2048) return go(std::integral_constant<int, 4>(), std::true_type());
   return go(std::integral_constant<int, 2>(), std::true_type());
 }
