@@ -234,7 +234,8 @@ extern "C" moe_status_t moe_rmsnorm(const void* x, const void* residual, const v
     rmsnorm_kernel<NV, kRing><<<turns < most ? turns : most, block, smem, s>>>(p);
     return launch_status();
   };
-  // Few rows: one round of loads a thread and no ring.  [1, 7168] with all outputs 4.4 us in a graph, by the ring 5.1.
+  // Few rows: one round of loads a thread and no ring.  All outputs, so / by the ring, us in a graph: [1, 2048] 2.3 / 2.6,
+  // [150, 2048] 2.7 / 3.1, [150, 256] 2.3 / 2.8, [1, 7168] 3.3 either way, [100, 7168] 3.7 / 3.6.
   if (nvec <= kMaxThreads && T <= num_sms()) return go(std::integral_constant<int, 1>(), std::false_type());
   // Many long rows: four vectors a thread and one CTA of up to 512 threads an SM, whose copies are long and neighbours in
   // memory; else two vectors, and CTAs of one row or 128 threads.  All outputs, two vectors / four in CTAs of one row or
