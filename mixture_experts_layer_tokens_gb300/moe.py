@@ -830,6 +830,9 @@ def moe_finalize_backward(dout: torch.Tensor, fused_expert_output: Optional[torc
 
 
 # ------------------------------------------------------------------ RMSNorm
+_NORM_QUANTS = {q: ctypes.byref(QUANT_CONFIGS[q or "bf16"]) for q in (None, "bf16", "fp8", "fp8_token")}
+
+
 def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
                 quant: Optional[str] = None, out: Optional[torch.Tensor] = None,
                 residual_out: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
@@ -840,32 +843,33 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
     fp32), None where not needed.  quant: None or "bf16" (no q), "fp8" (a scale per 128 columns, [T, ceil(H / 128)]) or
     "fp8_token" ([T]), as moe_prepare's.  Gradients: ``moe_finalize_backward(dout, None, None, 1,
     residual_out=..., rms_weight=weight, need_dy=False)`` gives dsum (of x and of the residual) and drms."""
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x: expected [T, H]")
-    T, H = x.shape
+    T, H = shape
     if T > _INT_MAX or H > _INT_MAX:
         raise ValueError("x: expected sizes up to 2^31 - 1")
-    quant = "bf16" if quant is None else quant
-    if quant not in ("bf16", "fp8", "fp8_token"):
+    if quant not in _NORM_QUANTS:
         raise ValueError(f"quant: expected None, 'bf16', 'fp8' or 'fp8_token', got {quant!r}")
-    bf, d, fp8 = torch.bfloat16, x.device, quant != "bf16"
+    bf = torch.bfloat16
     if out is None and need_out:
-        out = _empty((T, H), bf, d, stream)
+        out = _empty(shape, bf, x.device, stream)
     if residual_out is None and need_residual_out and residual is not None:
-        residual_out = _empty((T, H), bf, d, stream)
+        residual_out = _empty(shape, bf, x.device, stream)
     groups = (T, (H + 127) // 128) if quant == "fp8" else (T,)
-    if fp8 and q is None:
-        q = _empty((T, H), torch.uint8, d, stream)
-    if fp8 and q_scale is None:
-        q_scale = _empty(groups, torch.float32, d, stream)
-    if not fp8 and (q is not None or q_scale is not None):
+    if quant == "fp8" or quant == "fp8_token":
+        if q is None:
+            q = _empty(shape, torch.uint8, x.device, stream)
+        if q_scale is None:
+            q_scale = _empty(groups, torch.float32, x.device, stream)
+    elif q is not None or q_scale is not None:
         raise ValueError("q and q_scale: expected None without a quant")
     dev, s = _launch(stream)
     _check("moe_rmsnorm", lib().moe_rmsnorm(
-        _tensor(x, bf, (T, H), "x", dev), _tensor(residual, bf, (T, H), "residual", dev),
-        _tensor(weight, bf, (H,), "weight", dev), eps, T, H, ctypes.byref(QUANT_CONFIGS[quant]),
-        _tensor(out, bf, (T, H), "out", dev), _tensor(residual_out, bf, (T, H), "residual_out", dev),
-        _tensor(q, torch.uint8, (T, H), "q", dev), _tensor(q_scale, torch.float32, groups, "q_scale", dev), s))
+        _tensor(x, bf, shape, "x", dev), _tensor(residual, bf, shape, "residual", dev),
+        _tensor(weight, bf, (H,), "weight", dev), eps, T, H, _NORM_QUANTS[quant],
+        _tensor(out, bf, shape, "out", dev), _tensor(residual_out, bf, shape, "residual_out", dev),
+        _tensor(q, torch.uint8, shape, "q", dev), _tensor(q_scale, torch.float32, groups, "q_scale", dev), s))
     return out, residual_out, q, q_scale
 
 

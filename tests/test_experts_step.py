@@ -202,3 +202,46 @@ def test_training_step_captured(cuda_dev):
     for e in ex:
         assert all(torch.equal(a, b) for a, b in zip((e.y, e.dw13, e.dw2, e.da1), want))
     assert moe.moe_device_status() == moe.MOE_OK
+
+
+def test_two_threads_on_two_streams(cuda_dev):
+    """Host threads that call at once, each on its stream with buffers of its own, get what one gets alone (the first calls
+    of a kernel's several forms among them)."""
+    import threading
+
+    T, k, E, H, I = 90, 2, 6, 264, 136
+    sets = [[t.to(cuda_dev) for t in _experts(T, k, E, H, I, "silu", BF, seed=s)] for s in (21, 22)]
+    gamma = torch.ones(H, dtype=BF, device=cuda_dev)
+
+    def step(ids, a1, w13, w2, dy, stream):
+        n, _, q, sc = moe.moe_rmsnorm(a1, gamma, quant="fp8", stream=stream)
+        al = moe.Alignment(T, k, E, cuda_dev)
+        moe.moe_align(ids, E, out=al, stream=stream)
+        ex = MoEExperts(w13, w2, T, k, dw_dtype=torch.float32, stream=stream)
+        y = ex.forward(n, al, stream=stream)
+        return (n, q, sc, y, *ex.backward(dy, n, al, stream=stream))
+
+    alone = [[t.clone() for t in step(*v, None)] for v in sets]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(i):
+        try:
+            torch.cuda.set_device(cuda_dev)
+            side = torch.cuda.Stream()
+            with torch.cuda.stream(side):
+                for _ in range(30):
+                    got[i] = step(*sets[i], side)
+            side.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for a, b in zip(alone, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert moe.moe_device_status() == moe.MOE_OK
