@@ -91,7 +91,8 @@ class MoEExperts:
     once.
 
     w13 [E, 2I, H] (the *_no_mul activations [E, I, H]) and w2 [E, H, I] bf16 or fp16; T tokens of top_k experts each;
-    dw_dtype: the weights' gradients', fp32 or (None) the weights' type."""
+    dw_dtype: the weights' gradients', fp32 or (None) the weights' type.  dw13 and dw2 start as zeros, so that the first
+    backward call may add to them; an object that is made under capture has to write them first."""
 
     def __init__(self, w13: torch.Tensor, w2: torch.Tensor, T: int, top_k: int, activation: str = "silu",
                  dw_dtype: Optional[torch.dtype] = None, stream=None):
@@ -104,7 +105,10 @@ class MoEExperts:
         self.gu, self.h = empty((S, rows13)), empty((S, I))
         self.y = empty((S, H))
         self.dh, self.drows, self.da1 = empty((S, I)), empty((S, H)), empty((T, H))
-        self.dw13, self.dw2 = empty((E, rows13, H), dw_dtype or dt), empty((E, H, I), dw_dtype or dt)
+        # (zeros set in a graph would be set again by each of its replays)
+        self._summed = not (w13.is_cuda and moe._capturing(stream))
+        grad = moe._zeros if self._summed else moe._empty
+        self.dw13, self.dw2 = (grad(shape, dw_dtype or dt, dev, stream) for shape in ((E, rows13, H), (E, H, I)))
         self.ws = empty((max(moe.grouped_linear_workspace_size(S, E, rows13, H, "token"),
                              moe.grouped_linear_workspace_size(S, E, H, I, "sorted"),
                              moe.grouped_linear_backward_workspace_size(S, E, H, I, "slot", "sorted"),
@@ -128,6 +132,8 @@ class MoEExperts:
         accumulate: dw13 and dw2 are added to.  da1 [T, H] is what reaches the hidden states through these experts
         alone.  Buffers of this object, written again (or added to) by the next call; a bf16 da1 is summed by
         moe_finalize, an fp16 one is not made (None)."""
+        if accumulate and not self._summed:
+            raise ValueError("accumulate: expected after a call that writes, for gradients made under capture")
         kw = dict(accumulate=accumulate, ws=self.ws, stream=stream)
         moe.moe_grouped_linear_backward(dy, self.h, self.w2, al.expert_offsets, al.sorted_slot, self.top_k,
                                         dout_rows="slot", dx=self.dh, dw=self.dw2, **kw)
@@ -135,6 +141,7 @@ class MoEExperts:
         moe.moe_activation_backward(self.dh, self.gu, self.activation, dgu=self.gu, stream=stream)
         moe.moe_grouped_linear_backward(self.gu, a1, self.w13, al.expert_offsets, al.sorted_slot, self.top_k,
                                         x_rows="token", dx_rows="slot", dx=self.drows, dw=self.dw13, **kw)
+        self._summed = True
         if self.drows.dtype is not torch.bfloat16:
             return self.dw13, self.dw2, None
         moe.moe_finalize(self.drows, None, self.top_k, True, output=self.da1, stream=stream)
@@ -301,7 +308,8 @@ class MoELayer:
         """Gradients of the routed experts of a bf16 layer, given dy [T * top_k, H] bf16 (moe_finalize_backward's, by
         slots) and the hidden states a1 of the last forward call (with input_norm: the layer's a1): (dw13, dw2, da1),
         as MoEExperts.backward returns them.  [g | u] and h are made again from a1.  dw_dtype: as MoEExperts',
-        chosen by the first call."""
+        chosen by the first call.  accumulate: dw13 and dw2 are added to, by the first call to zeros (which has to write
+        where it is captured)."""
         if self.cfg.quant != "bf16" or self.cfg.weight_on_input or self.single:
             raise ValueError("experts_backward needs a bf16 layer of separate launches, its weights applied in the finalize")
         if self.trainer is not None and dw_dtype not in (None, self.trainer.dw13.dtype):

@@ -647,6 +647,22 @@ def _empty(shape, dtype, device, stream: Optional[torch.cuda.Stream]):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _zeros(shape, dtype, device, stream: Optional[torch.cuda.Stream]):
+    """As _empty, but zeros, set on that stream."""
+    if stream is None:
+        return torch.zeros(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.zeros(shape, dtype=dtype, device=device)
+
+
+def _capturing(stream: Optional[torch.cuda.Stream]) -> bool:
+    """The stream's work goes into a graph, whose replays the host does not see."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _linear_args(x: torch.Tensor, w: torch.Tensor, activation: str):
     if activation not in LINEAR_ACTIVATIONS:
         raise ValueError(f"unknown activation {activation!r}")

@@ -1,0 +1,88 @@
+"""What MoEExperts and MoELayer.experts_backward hold between calls: gradients that a first call adds to, weights that are
+replaced, a forward pass that a backward call has used up."""
+import pytest
+import torch
+
+from mixture_experts_layer_tokens_gb300 import moe
+from mixture_experts_layer_tokens_gb300.inputs import CONFIGS, make_inputs, scaled
+from mixture_experts_layer_tokens_gb300.layer import MoEExperts, MoELayer
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+T, K, E, H, I = 45, 2, 5, 264, 136
+
+
+def _inputs(seed=0, dtype=BF):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.rand((T, E), generator=g).argsort(1)[:, :K].to(torch.int32),
+            torch.randn((T, H), generator=g).to(dtype),
+            (torch.randn((E, 2 * I, H), generator=g) / H ** 0.5).to(dtype),
+            (torch.randn((E, H, I), generator=g) / I ** 0.5).to(dtype),
+            torch.randn((T * K, H), generator=g).to(dtype))
+
+
+def _layer(dev, seed=3):
+    cfg = scaled(CONFIGS["tiny"], name="state", T=64, H=256, I=128, E=8, top_k=2)
+    layer = MoELayer(make_inputs(cfg, seed=seed).to(dev))
+    layer.forward(layer.inp.logits, layer.inp.a1)
+    dy = torch.randn((128, 256), generator=torch.Generator().manual_seed(seed)).to(BF).to(dev)
+    return layer, dy
+
+
+def _spoil(dev):
+    """What the allocator hands out next holds NaN."""
+    torch.cuda.synchronize()
+    for size in (1 << 10, 1 << 16, 1 << 19, 1 << 20, 1 << 22, 1 << 24):
+        held = [torch.full((size // 4,), float("nan"), device=dev) for _ in range(8)]
+        del held
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,wdt", [(BF, None), (BF, F32), (HF, F32)])
+def test_first_call_adds_to_zeros(cuda_dev, dtype, wdt):
+    ids, a1, w13, w2, dy = (t.to(cuda_dev) for t in _inputs(1, dtype))
+    al = moe.moe_align(ids, E)
+    ex = MoEExperts(w13, w2, T, K, dw_dtype=wdt)
+    ex.forward(a1, al)
+    want = [t.clone() for t in ex.backward(dy, a1, al)[:2]]
+    _spoil(cuda_dev)
+    ex = MoEExperts(w13, w2, T, K, dw_dtype=wdt)
+    ex.forward(a1, al)
+    # (a group's rows are one run of the sums, added to 0)
+    assert all(torch.equal(a, b) for a, b in zip(ex.backward(dy, a1, al, accumulate=True)[:2], want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wdt", [None, F32])
+def test_first_call_of_a_layer_adds_to_zeros(cuda_dev, wdt):
+    layer, dy = _layer(cuda_dev)
+    want = [t.clone() for t in layer.experts_backward(dy, layer.inp.a1, dw_dtype=wdt)]
+    other, _ = _layer(cuda_dev)
+    _spoil(cuda_dev)
+    got = other.experts_backward(dy, other.inp.a1, dw_dtype=wdt, accumulate=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+def test_gradients_made_under_capture(cuda_dev):
+    """Zeros set in a graph would be set again by every replay, so there the first call has to write."""
+    ids, a1, w13, w2, dy = (t.to(cuda_dev) for t in _inputs(2))
+    al = moe.moe_align(ids, E)
+    ex = MoEExperts(w13, w2, T, K, dw_dtype=F32)
+    ex.forward(a1, al)
+    one = [t.clone() for t in ex.backward(dy, a1, al)[:2]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph, held = torch.cuda.CUDAGraph(), []
+    with torch.cuda.graph(graph, stream=side):
+        held.append(MoEExperts(w13, w2, T, K, dw_dtype=F32, stream=side))
+        held[0].forward(a1, al, stream=side)
+        with pytest.raises(ValueError, match="accumulate"):
+            held[0].backward(dy, a1, al, accumulate=True, stream=side)
+        held[0].backward(dy, a1, al, stream=side)
+        held[0].forward(a1, al, stream=side)
+        held[0].backward(dy, a1, al, accumulate=True, stream=side)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, w in zip((held[0].dw13, held[0].dw2), one):
+            assert torch.equal(got, 2 * w)
