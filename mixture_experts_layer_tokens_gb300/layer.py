@@ -317,6 +317,8 @@ class MoELayer:
         if self.trainer is None:
             self.trainer = MoEExperts(self.inp.w13, self.inp.w2, self.cfg.T, self.cfg.top_k, self.cfg.activation, dw_dtype,
                                       stream)
+        # (the weights that the forward call read, not those of the first call here)
+        self.trainer.w13, self.trainer.w2 = self.inp.w13, self.inp.w2
         self.trainer.hidden(a1, self.al, stream)
         return self.trainer.backward(dy, a1, self.al, accumulate, stream)
 

@@ -86,3 +86,17 @@ def test_gradients_made_under_capture(cuda_dev):
         torch.cuda.synchronize()
         for got, w in zip((held[0].dw13, held[0].dw2), one):
             assert torch.equal(got, 2 * w)
+
+
+@pytest.mark.gpu
+def test_layer_uses_the_weights_it_has_now(cuda_dev):
+    layer, dy = _layer(cuda_dev)
+    layer.experts_backward(dy, layer.inp.a1)
+    g = torch.Generator().manual_seed(9)
+    layer.inp.w13 = (torch.randn(layer.inp.w13.shape, generator=g) / 16).to(BF).to(cuda_dev)
+    layer.inp.w2 = (torch.randn(layer.inp.w2.shape, generator=g) / 11).to(BF).to(cuda_dev)
+    layer.forward(layer.inp.logits, layer.inp.a1)
+    got = [t.clone() for t in layer.experts_backward(dy, layer.inp.a1)]
+    ex = MoEExperts(layer.inp.w13, layer.inp.w2, 64, 2)
+    ex.forward(layer.inp.a1, layer.al)
+    assert all(torch.equal(a, b) for a, b in zip(got, ex.backward(dy, layer.inp.a1, layer.al)))
