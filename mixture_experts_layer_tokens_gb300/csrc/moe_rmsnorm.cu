@@ -16,6 +16,10 @@ constexpr int kMaxThreads = 1024;
 constexpr int kMaxH = 16384;
 constexpr int kRegs = 65536;  // of an SM
 constexpr int kMaxSmem = 2 * 2 * kMaxH * 2;  // two stages of two rows
+// A sum of squares below 2^-80 has lost digits to those that vanish in fp32 (each is off by up to 2^-150, by 2^-136 in
+// all), which counts where eps is no larger: such a row is multiplied by 2^100, exactly, and summed again.  (A kernel of
+// its own: the branch cost the others 1.3 %, 16384 x 7168 162.8 -> 165.0 us.)
+constexpr float kSmall = 0x1p-80f, kRaise = 0x1p100f;
 
 struct Norm {
   const __nv_bfloat16 *x, *res, *gamma;
@@ -61,11 +65,11 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint3
 
 // NV: vectors of 8 columns a thread holds of a row.  kRing: the rows come through two stages of shared memory by bulk
 // copies, the next turn's under this turn's work (loads by the threads themselves left HBM idle through each row's
-// sum and outputs: 16384 x 7168 with all outputs 301 us).
-template <int NV, bool kRing>
+// sum and outputs: 16384 x 7168 with all outputs 301 us).  kSmallEps: eps is below kSmall.
+template <int NV, bool kRing, bool kSmallEps>
 __global__ void __launch_bounds__(NV == 4 ? kMaxThreads / 2 : kMaxThreads) rmsnorm_kernel(const Norm p) {
   extern __shared__ __align__(128) uint8_t stages[];
-  __shared__ float red[2][2][kMaxThreads / 32];
+  __shared__ float red[kSmallEps ? 3 : 2][2][kMaxThreads / 32];
   __shared__ uint64_t full[2];
   const int threads = p.threads, rows = blockDim.x / threads;  // rows of a CTA at a time
   const int i = threadIdx.x % threads, mine = threadIdx.x / threads, nvec = p.H / 8;
@@ -138,7 +142,21 @@ __global__ void __launch_bounds__(NV == 4 ? kMaxThreads / 2 : kMaxThreads) rmsno
       for (int j = 0; j < NV; ++j)
         if (on[j]) store8(p.res_out + at + (size_t)(j * threads + i) * 8, n[j]);
     }
-    const float r = __frsqrt_rn(sum / (float)p.H + p.eps);
+    float eps = p.eps;
+    if constexpr (kSmallEps) {
+      const float raise = sum < kSmall ? kRaise : 1.f;
+      eps = eps * raise * raise;
+      sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          n[j][c] *= raise;
+          sum = fmaf(n[j][c], n[j][c], sum);
+        }
+      sum = row_reduce<false>(sum, threads, red[2][stage]);
+    }
+    const float r = __frsqrt_rn(sum / (float)p.H + eps);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (on[j]) {
@@ -210,9 +228,10 @@ extern "C" moe_status_t moe_rmsnorm(const void* x, const void* residual, const v
          static_cast<B*>(residual_out), static_cast<uint8_t*>(q), q_scale, eps, T, H, group, 0};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int nvec = H / 8;
-  auto go = [&](auto nv, auto ring) {
+  auto go = [&](auto nv, auto ring, auto small_eps) {
     constexpr int NV = decltype(nv)::value;
     constexpr bool kRing = decltype(ring)::value;
+    constexpr auto kernel = rmsnorm_kernel<NV, kRing, decltype(small_eps)::value>;
     const int need = (nvec + NV - 1) / NV;
     p.threads = need <= 16 ? 16 : (need + 31) / 32 * 32;
     int rows = p.threads >= 128 ? 1 : 128 / p.threads;
@@ -227,21 +246,22 @@ extern "C" moe_status_t moe_rmsnorm(const void* x, const void* residual, const v
       ctas = by_regs < by_smem ? by_regs : by_smem;
       if (ctas < 1) ctas = 1;
       // (the same for every call: host threads may come at once)
-      if (cudaFuncSetAttribute(rmsnorm_kernel<NV, kRing>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
         return MOE_ERR_CUDA;
     }
     const int most = num_sms() * ctas;
-    rmsnorm_kernel<NV, kRing><<<turns < most ? turns : most, block, smem, s>>>(p);
+    kernel<<<turns < most ? turns : most, block, smem, s>>>(p);
     return launch_status();
   };
+  if (eps < kSmall) return go(std::integral_constant<int, 2>(), std::true_type(), std::true_type());
   // Few rows: one round of loads a thread and no ring.  All outputs, so / by the ring, us in a graph: [1, 2048] 2.3 / 2.6,
   // [150, 2048] 2.7 / 3.1, [150, 256] 2.3 / 2.8, [1, 7168] 3.3 either way, [100, 7168] 3.7 / 3.6.
-  if (nvec <= kMaxThreads && T <= num_sms()) return go(std::integral_constant<int, 1>(), std::false_type());
+  if (nvec <= kMaxThreads && T <= num_sms()) return go(std::integral_constant<int, 1>(), std::false_type(), std::false_type());
   // Many long rows: four vectors a thread and one CTA of up to 512 threads an SM, whose copies are long and neighbours in
   // memory; else two vectors, and CTAs of one row or 128 threads.  All outputs, two vectors / four in CTAs of one row or
   // 128 threads / four in CTAs of 512: [16384, 7168] 185 / 179 / 162 us, [16384, 2048] 57 / 55 / 49, [16384, 1024] 29 / 28 /
   // 27, [16384, 256] 9.0 / 12 / 12, [65536, 128] 15 / 24 / 25, [1024, 7168] 13.4 / 15 / 16 (by the threads' own loads 300,
   // 76, 39, 15, 32, 23).
-  if (nvec >= 64 && T >= 2048) return go(std::integral_constant<int, 4>(), std::true_type());
-  return go(std::integral_constant<int, 2>(), std::true_type());
+  if (nvec >= 64 && T >= 2048) return go(std::integral_constant<int, 4>(), std::true_type(), std::false_type());
+  return go(std::integral_constant<int, 2>(), std::true_type(), std::false_type());
 }
