@@ -619,10 +619,10 @@ moe_status_t moe_rmsnorm(const void *x, const void *residual, const void *weight
  * sorted_slot [S] int32, distinct values in [0, S), is read for the rows of a group alone (NULL where
  * every order is MOE_ROWS_SORTED); a value out of range is recorded as MOE_ERR_INVALID_ARG
  * in the device status word, its row of out (or dx) not written and its share in dw zero; offsets out of
- * order or range are recorded likewise, and nothing outside the buffers is touched.  Rows of out that belong to no group (behind
- * expert_offsets[E]) are left as they were.  0 <= S <= 2^30 (0: nothing is done), 1 <= E <= 1024, N and K
- * multiples of 8 up to 2^21, S % top_k == 0 where MOE_ROWS_TOKEN is used; more than 2^30 tiles may be
- * MOE_ERR_UNSUPPORTED.  A row of x that holds a NaN or an infinity affects its row of out alone.
+ * order or range are recorded likewise, and nothing outside the buffers is touched.  Rows of out that belong to no group
+ * (in front of expert_offsets[0] or behind expert_offsets[E]) are left as they were.  0 <= S <= 2^30 (0: nothing
+ * is done), 1 <= E <= 1024, N and K multiples of 8 up to 2^21, S % top_k == 0 where MOE_ROWS_TOKEN is used; more
+ * than 2^30 tiles may be MOE_ERR_UNSUPPORTED.  A row of x that holds a NaN or an infinity affects its row of out alone.
  * Long sums are treated as moe_linear's are; the order of a sum is fixed by the sizes and
  * the group, so the same inputs give the same bits.  ws: moe_grouped_linear_workspace_size(...)
  * bytes (may be 0 for MOE_ROWS_SORTED: ws may then be NULL), for one call at a time.  Outputs overlap nothing. */

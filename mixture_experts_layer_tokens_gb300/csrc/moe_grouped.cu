@@ -778,7 +778,7 @@ struct Setup {
 };
 
 __device__ __forceinline__ void move_row(const Move& m, const Setup& p, int row, int lane) {
-  if (row >= m.rows || row >= __ldg(p.offsets + p.E)) return;
+  if (row >= m.rows || row < __ldg(p.offsets) || row >= __ldg(p.offsets + p.E)) return;  // (a row of no group)
   const int slot = m.by_slots ? __ldg(p.slots + row) : row;
   uint4* d = m.to + (size_t)row * m.pitch;
   if (slot < 0 || slot >= p.S) {

@@ -940,7 +940,8 @@ def moe_grouped_linear(x: torch.Tensor, w: torch.Tensor, expert_offsets: torch.T
     rows p in [expert_offsets[e], expert_offsets[e + 1]); w [E, N, K] bf16 or fp16, expert_offsets [E + 1] and
     sorted_slot [S] int32 as moe_align writes them (sorted_slot may be None where every order is "sorted").
     x_rows, out_rows: the order of a tensor's rows (``ROWS``): "sorted" and "slot" have S rows, "token" (x alone)
-    S / top_k.  out [S, N] in the operands' type; rows behind expert_offsets[E] are left as they were."""
+    S / top_k.  out [S, N] in the operands' type; rows in front of the first group or behind the last are
+    left as they were."""
     S, E, N, K, dt, code = _grouped_args(x, w, expert_offsets, sorted_slot, top_k, (x_rows, out_rows))
     rx, ro = _rows("x_rows", x_rows, S, top_k), _rows("out_rows", out_rows, S, top_k, False)
     if out is None:
