@@ -107,6 +107,7 @@ class MoEExperts:
         self.dh, self.drows, self.da1 = empty((S, I)), empty((S, H)), empty((T, H))
         # (zeros set in a graph would be set again by each of its replays)
         self._summed = not (w13.is_cuda and moe._capturing(stream))
+        self._kept: Optional[bool] = False  # [g | u] is a hidden call's (None: calls were captured, and replays go unseen)
         grad = moe._zeros if self._summed else moe._empty
         self.dw13, self.dw2 = (grad(shape, dw_dtype or dt, dev, stream) for shape in ((E, rows13, H), (E, H, I)))
         self.ws = empty((max(moe.grouped_linear_workspace_size(S, E, rows13, H, "token"),
@@ -119,7 +120,9 @@ class MoEExperts:
         """h [S, I] in sorted order, [g | u] kept beside it: the forward pass up to the second product."""
         moe.moe_grouped_linear(a1, self.w13, al.expert_offsets, al.sorted_slot, self.top_k, x_rows="token", out=self.gu,
                                ws=self.ws, stream=stream)
-        return moe.moe_activation(self.gu, self.activation, h=self.h, stream=stream)
+        h = moe.moe_activation(self.gu, self.activation, h=self.h, stream=stream)
+        self._kept = None if self._kept is None or moe._capturing(stream) else True
+        return h
 
     def forward(self, a1: torch.Tensor, al: "moe.Alignment", stream=None) -> torch.Tensor:
         """y [T * top_k, H], the unweighted rows by slots, of the hidden states a1 [T, H]."""
@@ -128,16 +131,24 @@ class MoEExperts:
                                       out=self.y, ws=self.ws, stream=stream)
 
     def backward(self, dy: torch.Tensor, a1: torch.Tensor, al: "moe.Alignment", accumulate: bool = False, stream=None):
-        """Gradients of the last forward (or hidden) call, once for each such call, given dy [T * top_k, H] by slots: (dw13, dw2, da1).
+        """Gradients of the last forward (or hidden) call, given dy [T * top_k, H] by slots: (dw13, dw2, da1).  Once for each
+        such call, whose [g | u] it replaces by its gradient: a second call is refused, but not where the object's calls
+        were captured, since a replay may have made [g | u] again.
         accumulate: dw13 and dw2 are added to.  da1 [T, H] is what reaches the hidden states through these experts
         alone.  Buffers of this object, written again (or added to) by the next call; a bf16 da1 is summed by
         moe_finalize, an fp16 one is not made (None)."""
+        if moe._capturing(stream):
+            self._kept = None
+        if self._kept is False:
+            raise ValueError("backward: expected a forward (or hidden) call since the last backward call, which used it up")
         if accumulate and not self._summed:
             raise ValueError("accumulate: expected after a call that writes, for gradients made under capture")
         kw = dict(accumulate=accumulate, ws=self.ws, stream=stream)
         moe.moe_grouped_linear_backward(dy, self.h, self.w2, al.expert_offsets, al.sorted_slot, self.top_k,
                                         dout_rows="slot", dx=self.dh, dw=self.dw2, **kw)
         # (dgu takes the place of [g | u]'s copy: each value is read before it is written)
+        if self._kept:
+            self._kept = False
         moe.moe_activation_backward(self.dh, self.gu, self.activation, dgu=self.gu, stream=stream)
         moe.moe_grouped_linear_backward(self.gu, a1, self.w13, al.expert_offsets, al.sorted_slot, self.top_k,
                                         x_rows="token", dx_rows="slot", dx=self.drows, dw=self.dw13, **kw)

@@ -100,3 +100,47 @@ def test_layer_uses_the_weights_it_has_now(cuda_dev):
     ex = MoEExperts(layer.inp.w13, layer.inp.w2, 64, 2)
     ex.forward(layer.inp.a1, layer.al)
     assert all(torch.equal(a, b) for a, b in zip(got, ex.backward(dy, layer.inp.a1, layer.al)))
+
+
+@pytest.mark.gpu
+def test_backward_needs_a_forward_of_its_own(cuda_dev):
+    ids, a1, w13, w2, dy = (t.to(cuda_dev) for t in _inputs(3))
+    al = moe.moe_align(ids, E)
+    ex = MoEExperts(w13, w2, T, K)
+    with pytest.raises(ValueError, match="forward"):
+        ex.backward(dy, a1, al)
+    ex.hidden(a1, al)
+    with pytest.raises(ValueError, match="dout"):  # (refused before anything is used up)
+        ex.backward(dy[:, :8], a1, al)
+    want = [t.clone() for t in ex.backward(dy, a1, al)]
+    with pytest.raises(ValueError):
+        ex.forward(a1[:, :8], al)
+    with pytest.raises(ValueError, match="forward"):
+        ex.backward(dy, a1, al)
+    ex.forward(a1, al)
+    assert all(torch.equal(a, b) for a, b in zip(ex.backward(dy, a1, al), want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("first", [0, 1])
+def test_parts_of_a_step_in_graphs(cuda_dev, first):
+    """A captured forward pass with eager gradients, and the other way round, whichever is captured first: the host does
+    not see a replay, and refuses neither."""
+    ids, a1, w13, w2, dy = (t.to(cuda_dev) for t in _inputs(4))
+    al = moe.moe_align(ids, E)
+    ex = MoEExperts(w13, w2, T, K)
+    ex.forward(a1, al)
+    want = [t.clone() for t in ex.backward(dy, a1, al)]
+    side = torch.cuda.Stream()
+    calls = (lambda: ex.forward(a1, al, stream=side), lambda: ex.backward(dy, a1, al, stream=side))
+    graphs = [torch.cuda.CUDAGraph() for _ in calls]
+    for i in (first, 1 - first):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graphs[i], stream=side):
+            calls[i]()
+    for _ in range(2):
+        graphs[0].replay()
+        assert all(torch.equal(a, b) for a, b in zip(ex.backward(dy, a1, al), want))
+        ex.forward(a1, al)
+        graphs[1].replay()
+        assert all(torch.equal(a, b) for a, b in zip((ex.dw13, ex.dw2, ex.da1), want))
