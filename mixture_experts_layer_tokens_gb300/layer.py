@@ -101,6 +101,8 @@ class MoEExperts:
             raise ValueError("w13 and w2: expected [E, 2I, H] (*_no_mul: [E, I, H]) and [E, H, I]")
         self.w13, self.w2, self.T, self.top_k, self.activation = w13, w2, T, top_k, activation
         dt, dev = w13.dtype, w13.device
+        if dw_dtype not in (None, dt, torch.float32):
+            raise TypeError(f"dw_dtype: expected {dt} or float32, got {dw_dtype}")
         empty = lambda shape, dtype=dt: moe._empty(shape, dtype, dev, stream)  # noqa: E731
         self.gu, self.h = empty((S, rows13)), empty((S, I))
         self.y = empty((S, H))

@@ -144,3 +144,18 @@ def test_parts_of_a_step_in_graphs(cuda_dev, first):
         ex.forward(a1, al)
         graphs[1].replay()
         assert all(torch.equal(a, b) for a, b in zip((ex.dw13, ex.dw2, ex.da1), want))
+
+
+@pytest.mark.parametrize("dtype,wdt", [(BF, HF), (HF, BF), (BF, torch.float64)])
+def test_gradient_types_are_refused_first(dtype, wdt):
+    _, _, w13, w2, _ = _inputs(5, dtype)
+    with pytest.raises(TypeError, match="dw_dtype"):
+        MoEExperts(w13, w2, T, K, dw_dtype=wdt)
+
+
+@pytest.mark.gpu
+def test_a_refused_gradient_type_leaves_the_layer_as_it_was(cuda_dev):
+    layer, dy = _layer(cuda_dev)
+    with pytest.raises(TypeError):
+        layer.experts_backward(dy, layer.inp.a1, dw_dtype=HF)
+    assert layer.experts_backward(dy, layer.inp.a1, dw_dtype=F32)[0].dtype is F32
