@@ -118,9 +118,12 @@ class MoEExperts:
                              moe.grouped_linear_backward_workspace_size(S, E, rows13, H, "sorted", "token"), 16),),
                         torch.uint8)
 
+    def _slots(self, al: "moe.Alignment") -> torch.Tensor:
+        return al.sorted_slot if self.T else al.sorted_slot[:0]  # (an Alignment of no tokens holds room for one slot)
+
     def hidden(self, a1: torch.Tensor, al: "moe.Alignment", stream=None) -> torch.Tensor:
         """h [S, I] in sorted order, [g | u] kept beside it: the forward pass up to the second product."""
-        moe.moe_grouped_linear(a1, self.w13, al.expert_offsets, al.sorted_slot, self.top_k, x_rows="token", out=self.gu,
+        moe.moe_grouped_linear(a1, self.w13, al.expert_offsets, self._slots(al), self.top_k, x_rows="token", out=self.gu,
                                ws=self.ws, stream=stream)
         h = moe.moe_activation(self.gu, self.activation, h=self.h, stream=stream)
         self._kept = None if self._kept is None or moe._capturing(stream) else True
@@ -129,7 +132,7 @@ class MoEExperts:
     def forward(self, a1: torch.Tensor, al: "moe.Alignment", stream=None) -> torch.Tensor:
         """y [T * top_k, H], the unweighted rows by slots, of the hidden states a1 [T, H]."""
         self.hidden(a1, al, stream)
-        return moe.moe_grouped_linear(self.h, self.w2, al.expert_offsets, al.sorted_slot, self.top_k, out_rows="slot",
+        return moe.moe_grouped_linear(self.h, self.w2, al.expert_offsets, self._slots(al), self.top_k, out_rows="slot",
                                       out=self.y, ws=self.ws, stream=stream)
 
     def backward(self, dy: torch.Tensor, a1: torch.Tensor, al: "moe.Alignment", accumulate: bool = False, stream=None):
@@ -146,13 +149,13 @@ class MoEExperts:
         if accumulate and not self._summed:
             raise ValueError("accumulate: expected after a call that writes, for gradients made under capture")
         kw = dict(accumulate=accumulate, ws=self.ws, stream=stream)
-        moe.moe_grouped_linear_backward(dy, self.h, self.w2, al.expert_offsets, al.sorted_slot, self.top_k,
+        moe.moe_grouped_linear_backward(dy, self.h, self.w2, al.expert_offsets, self._slots(al), self.top_k,
                                         dout_rows="slot", dx=self.dh, dw=self.dw2, **kw)
         # (dgu takes the place of [g | u]'s copy: each value is read before it is written)
         if self._kept:
             self._kept = False
         moe.moe_activation_backward(self.dh, self.gu, self.activation, dgu=self.gu, stream=stream)
-        moe.moe_grouped_linear_backward(self.gu, a1, self.w13, al.expert_offsets, al.sorted_slot, self.top_k,
+        moe.moe_grouped_linear_backward(self.gu, a1, self.w13, al.expert_offsets, self._slots(al), self.top_k,
                                         x_rows="token", dx_rows="slot", dx=self.drows, dw=self.dw13, **kw)
         self._summed = True
         if self.drows.dtype is not torch.bfloat16:

@@ -159,3 +159,21 @@ def test_a_refused_gradient_type_leaves_the_layer_as_it_was(cuda_dev):
     with pytest.raises(TypeError):
         layer.experts_backward(dy, layer.inp.a1, dw_dtype=HF)
     assert layer.experts_backward(dy, layer.inp.a1, dw_dtype=F32)[0].dtype is F32
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("top_k", [1, 2])
+def test_no_tokens(cuda_dev, top_k):
+    """Nothing to do but the weights' gradients, which are zeros, or stay."""
+    _, _, w13, w2, _ = (t.to(cuda_dev) for t in _inputs(6))
+    none = lambda *s: torch.empty((0,) + s, dtype=BF, device=cuda_dev)  # noqa: E731
+    al = moe.moe_align(torch.empty((0, top_k), dtype=torch.int32, device=cuda_dev), E)
+    ex = MoEExperts(w13, w2, 0, top_k)
+    assert ex.forward(none(H), al).shape == (0, H)
+    ex.dw2.fill_(7)
+    dw13, dw2, da1 = ex.backward(none(H), none(H), al)
+    assert bool((dw13 == 0).all()) and bool((dw2 == 0).all()) and da1.shape == (0, H)
+    ex.forward(none(H), al)
+    dw2.fill_(7)
+    assert bool((ex.backward(none(H), none(H), al, accumulate=True)[1] == 7).all())
+    assert moe.moe_device_status() == moe.MOE_OK
