@@ -112,6 +112,10 @@ class MoEExperts:
         self._kept: Optional[bool] = False  # [g | u] is a hidden call's (None: calls were captured, and replays go unseen)
         grad = moe._zeros if self._summed else moe._empty
         self.dw13, self.dw2 = (grad(shape, dw_dtype or dt, dev, stream) for shape in ((E, rows13, H), (E, H, I)))
+        self._zeroed = None  # the zeros are there: for a first backward call on another stream than this one
+        if w13.is_cuda and self._summed:
+            self._zeroed = torch.cuda.Event()
+            self._zeroed.record(stream if stream is not None else torch.cuda.current_stream())
         self.ws = empty((max(moe.grouped_linear_workspace_size(S, E, rows13, H, "token"),
                              moe.grouped_linear_workspace_size(S, E, H, I, "sorted"),
                              moe.grouped_linear_backward_workspace_size(S, E, H, I, "slot", "sorted"),
@@ -142,12 +146,16 @@ class MoEExperts:
         accumulate: dw13 and dw2 are added to.  da1 [T, H] is what reaches the hidden states through these experts
         alone.  Buffers of this object, written again (or added to) by the next call; a bf16 da1 is summed by
         moe_finalize, an fp16 one is not made (None)."""
-        if moe._capturing(stream):
+        capturing = moe._capturing(stream)
+        if capturing:
             self._kept = None
         if self._kept is False:
             raise ValueError("backward: expected a forward (or hidden) call since the last backward call, which used it up")
         if accumulate and not self._summed:
             raise ValueError("accumulate: expected after a call that writes, for gradients made under capture")
+        if self._zeroed is not None and not capturing:  # (what is captured cannot wait for what is not)
+            (stream if stream is not None else torch.cuda.current_stream()).wait_event(self._zeroed)
+            self._zeroed = None
         kw = dict(accumulate=accumulate, ws=self.ws, stream=stream)
         moe.moe_grouped_linear_backward(dy, self.h, self.w2, al.expert_offsets, self._slots(al), self.top_k,
                                         dout_rows="slot", dx=self.dh, dw=self.dw2, **kw)

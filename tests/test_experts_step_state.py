@@ -63,6 +63,25 @@ def test_first_call_of_a_layer_adds_to_zeros(cuda_dev, wdt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_zeros_are_set_before_another_stream_adds(cuda_dev, accumulate):
+    """An object made on a stream that is busy, and used at once on another."""
+    ids, a1, w13, w2, dy = (t.to(cuda_dev) for t in _inputs(7))
+    al = moe.moe_align(ids, E)
+    ex = MoEExperts(w13, w2, T, K, dw_dtype=F32)
+    ex.forward(a1, al)
+    want = [t.clone() for t in ex.backward(dy, a1, al)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # (a tenth of a second)
+    ex = MoEExperts(w13, w2, T, K, dw_dtype=F32)
+    ex.forward(a1, al, stream=side)
+    got = ex.backward(dy, a1, al, accumulate=accumulate, stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
 def test_gradients_made_under_capture(cuda_dev):
     """Zeros set in a graph would be set again by every replay, so there the first call has to write."""
     ids, a1, w13, w2, dy = (t.to(cuda_dev) for t in _inputs(2))
