@@ -597,8 +597,9 @@ size_t moe_finalize_backward_workspace_size(int T, int H);
  * (q_scale [T, ceil(H / 128)]; a last group may be shorter) or MOE_GROUP_TOKEN (q_scale [T]); other
  * groups are MOE_ERR_UNSUPPORTED.  x, residual, residual_out, out [T, H] and weight [H] bf16, q
  * [T, H] E4M3 codes.  0 <= T <= 2^30, H % 8 == 0, 8 <= H <= 16384, eps >= 0; out or q is required.
- * The squares are summed in fp32 in a fixed order (|v| beyond 1e19 / sqrt(H) overflows them; small values keep
- * their digits whatever eps is, and a row of zeros is NaN where eps is 0); a row with a NaN or
+ * The squares are summed in fp32 in an order that T, H, eps and the device fix: the same call gives the same bits, and a
+ * row in a call with another T may differ by an fp32 rounding.  |v| beyond 1e19 / sqrt(H) overflows the sum; small
+ * values keep their digits whatever eps is, and a row of zeros is NaN where eps is 0.  A row with a NaN or
  * an infinity affects that row alone.  residual_out may be residual or x, and out x or residual, itself (a row
  * is read before it is written); no other overlap.  The gradients, from residual_out (x without a residual),
  * are moe_finalize_backward's dsum and drms (topk_weights, dy and dweights NULL, top_k 1). */

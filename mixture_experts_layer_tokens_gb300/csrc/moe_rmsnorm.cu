@@ -261,7 +261,9 @@ extern "C" moe_status_t moe_rmsnorm(const void* x, const void* residual, const v
   // memory; else two vectors, and CTAs of one row or 128 threads.  All outputs, two vectors / four in CTAs of one row or
   // 128 threads / four in CTAs of 512: [16384, 7168] 185 / 179 / 162 us, [16384, 2048] 57 / 55 / 49, [16384, 1024] 29 / 28 /
   // 27, [16384, 256] 9.0 / 12 / 12, [65536, 128] 15 / 24 / 25, [1024, 7168] 13.4 / 15 / 16 (by the threads' own loads 300,
-  // 76, 39, 15, 32, 23).
+  // 76, 39, 15, 32, 23).  Around the cut, two / four in CTAs of 512: [2048, 512] 3.4 / 3.8, [2048, 7168] 22.7 / 25.5,
+  // [4096, 2048] 13.0 / 16.5, [4096, 7168] 47.6 / 46.0, [6000, 512] 5.6 / 7.9, [8192, 2048] 26.7 / 27.4, [8192, 7168] 94 / 84,
+  // [12000, 2048] 41.4 / 36.6: four pay from some 2^24 values on, and cost up to 40 % between the cut and there.
   if (nvec >= 64 && T >= 2048) return go(std::integral_constant<int, 4>(), std::true_type(), std::false_type());
   return go(std::integral_constant<int, 2>(), std::true_type(), std::false_type());
 }

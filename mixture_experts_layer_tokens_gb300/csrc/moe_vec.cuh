@@ -18,9 +18,12 @@ moe_status_t finalize_backward_status(int clear);
 // ---- launches that overlap the end of the launch before them on the stream
 // A call's second and later kernels are launched with overlap_attr(): the device may start their
 // CTAs when every CTA of the kernel before has called depend_launch() (or ended) and there is room
-// for them.  depend_wait() then waits until that kernel has ended and its writes are visible; each
-// kernel of a call waits before it touches memory, so the whole chain is ordered.  The first
-// kernel of a call is launched plainly and waits for nothing.
+// for them.  depend_wait() then waits until that kernel has ended and its writes are visible.  Each
+// kernel of a call waits before it touches what another kernel of the call writes, or writes what
+// another one reads, and in any case before it ends, so the whole chain is ordered.  The first
+// kernel of a call is launched plainly and waits for nothing; so the caller's own inputs (weights,
+// offsets, slots) are complete, and outputs that this kernel alone touches are free, for every kernel of
+// the call without a wait.
 __device__ __forceinline__ void depend_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

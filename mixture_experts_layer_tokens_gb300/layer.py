@@ -176,7 +176,7 @@ class MoELayer:
     """router: a MoERouter of the same tokens, experts and top_k that takes the place of moe_route (the
     forward call's logits are then not read and may be None).  keep_residual: forward also writes the sum before
     the RMSNorm to residual_out, which router_backward needs.  input_norm: weight [H] bf16 of an RMSNorm (eps
-    1e-6) in front of the layer."""
+    1e-6) in front of the layer; its gradient is moe_finalize_backward's, from the sum that was normalised."""
 
     def __init__(self, inp: LayerInputs, stream: Optional[torch.cuda.Stream] = None,
                  router: Optional[MoERouter] = None, keep_residual: bool = False,
@@ -261,7 +261,8 @@ class MoELayer:
                 residual: Optional[torch.Tensor] = None) -> torch.Tensor:
         """a1 [T, H] bf16: the hidden states; with input_norm what the norm takes.  residual (input_norm alone): the
         residual stream [T, H], added to a1 before the norm; the sum is what the finalize adds in place of the
-        inputs' residual."""
+        inputs' residual.  Without it the finalize adds the inputs' residual as it does without a norm, not a1: where a1
+        is itself the residual stream (a first block), it has to be the inputs' residual too."""
         cfg, inp = self.cfg, self.inp
         if residual is not None and self.input_norm is None:
             raise ValueError("residual: expected with input_norm alone")
@@ -312,7 +313,8 @@ class MoELayer:
                         stream=None, dresidual_out: Optional[torch.Tensor] = None, need_dy: bool = False):
         """Gradients that train the router of a layer (whose experts are held fixed, or trained by experts_backward
         from the finalize gradients' dy, made with need_dy): dout [T, H] bf16, the
-        gradient of the last forward call's output -> (finalize gradients, router gradients), as
+        gradient of the last forward call's output, and a1, the hidden states that the router saw in it (with input_norm
+        the layer's a1, not what forward was given) -> (finalize gradients, router gradients), as
         moe_finalize_backward and MoERouter.backward return them.  residual_out: the sum before the RMSNorm (layers
         with one; None: what a keep_residual layer's forward call wrote).  The router weights of a layer that
         applies them on the input have no gradient here."""
