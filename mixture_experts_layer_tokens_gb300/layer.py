@@ -115,7 +115,7 @@ class MoEExperts:
         self._zeroed = None  # the zeros are there: for a first backward call on another stream than this one
         if w13.is_cuda and self._summed:
             self._zeroed = torch.cuda.Event()
-            self._zeroed.record(stream if stream is not None else torch.cuda.current_stream())
+            self._zeroed.record(stream if stream is not None else torch.cuda.current_stream(dev))
         self.ws = empty((max(moe.grouped_linear_workspace_size(S, E, rows13, H, "token"),
                              moe.grouped_linear_workspace_size(S, E, H, I, "sorted"),
                              moe.grouped_linear_backward_workspace_size(S, E, H, I, "slot", "sorted"),
